@@ -55,7 +55,7 @@ typedef enum {
 } vt_status;
 
 /* Storage types.  VT_E4M3 is an FP8 K/V cache (with bf16 q and out) and is
- * taken only by vt_paged_attn_decode_fp8 and vt_paged_attn_decode_multi_fp8. */
+ * taken only by the entry points whose names end in _fp8. */
 typedef enum { VT_BF16 = 0, VT_F32 = 1, VT_E4M3 = 2 } vt_dtype;
 
 /*
@@ -232,7 +232,171 @@ VT_API vt_status vt_paged_attn_decode_multi_fp8(void* out, const void* q, const 
                                                 vt_stream_t stream, int max_blocks_per_seq,
                                                 int num_blocks);
 
-/* What the last successful decode call on this host thread launched. */
+/*
+ * Rotary positions.  Each rotated pair j (0 <= j < rot_dim / 2) of a head's
+ * row is turned by the angle position * inv_freq[j] and scaled by amplitude:
+ *   a' = amplitude * (a cos - b sin)      b' = amplitude * (b cos + a sin)
+ * with (a, b) = (x[j], x[j + rot_dim / 2]) in the half layout
+ * (interleaved = 0) and (x[2j], x[2j + 1]) in the interleaved one; elements
+ * at and past rot_dim are copied.  The angle is reduced exactly (the turn per
+ * token is held as a 64-bit fraction of a full turn), so far positions are as
+ * accurate as near ones; sin, cos and the products are fp32, rounded once to
+ * the storage type.  Any int32 position is taken; a negative one turns back,
+ * so the call with -position is the gradient of the call with position.
+ */
+
+/* How vt_rope_frequencies stretches the frequencies for contexts longer than
+ * the one a model was trained on.  Frequencies are f_j = base^(-2j / rot_dim)
+ * radians per token before that. */
+typedef enum {
+  VT_ROPE_PLAIN = 0,  /* f_j as they are; amplitude 1 */
+  VT_ROPE_LINEAR = 1, /* f_j / factor (position interpolation) */
+  VT_ROPE_NTK = 2,    /* base * factor^(rot_dim / (rot_dim - 2)) instead of base: the slowest pair is stretched
+                         by factor, the fastest not at all (rot_dim >= 4) */
+  VT_ROPE_YARN = 3,   /* f_j / factor where a pair makes fewer than beta_slow turns in original_context tokens,
+                         f_j where it makes more than beta_fast, a linear ramp over j between; amplitude
+                         0.1 ln(factor) + 1 for factor > 1 */
+  VT_ROPE_BANDED = 4  /* the same bounds, the ramp linear in the number of turns; amplitude 1 */
+} vt_rope_kind;
+
+typedef struct {
+  vt_rope_kind kind;
+  double factor;           /* > 0 (all kinds but plain) */
+  double original_context; /* tokens, > 0 (YaRN, banded) */
+  double beta_fast;        /* turns, > beta_slow (YaRN: 32 is usual; banded: 4) */
+  double beta_slow;        /* turns, > 0 (usually 1) */
+} vt_rope_stretch;
+
+/*
+ * vt_rope_frequencies -- fills host arrays for the calls below: inv_freq
+ * [rot_dim / 2] (radians per token, fp64) and *amplitude.  rot_dim even and
+ * positive, base finite and > 1; stretch NULL is VT_ROPE_PLAIN.  Host
+ * arithmetic only; copy inv_freq to the device once.
+ */
+VT_API vt_status vt_rope_frequencies(double* inv_freq, float* amplitude, int rot_dim, double base,
+                                     const vt_rope_stretch* stretch);
+
+/*
+ * vt_rope -- rotary positions on packed rows.
+ *
+ *   out, x      [num_tokens] rows of [num_heads][head_dim], consecutive rows out_stride and x_stride elements
+ *               apart (>= num_heads * head_dim; e.g. the queries inside the rows of a fused projection).  Row
+ *               starts 16-byte aligned.  out == x with equal strides rotates in place; other overlaps are not
+ *               allowed.
+ *   positions   [num_tokens] int32.
+ *   inv_freq    [rot_dim / 2] device fp64, finite, 8-byte aligned.
+ *   num_tokens >= 0 (0 is a no-op), head_dim a multiple of 8 and at most 1024 (else VT_ERR_UNSUPPORTED), rot_dim
+ *   even, 0 < rot_dim <= head_dim; interleaved 0 or 1; amplitude finite; dtype VT_BF16 or VT_F32.
+ * Needs no workspace.
+ */
+VT_API vt_status vt_rope(void* out, const void* x, const int32_t* positions, const double* inv_freq, int num_tokens,
+                         int num_heads, int head_dim, int rot_dim, int interleaved, float amplitude,
+                         long long x_stride, long long out_stride, vt_stream_t stream, vt_dtype dtype);
+
+/*
+ * vt_paged_kv_append -- writes the keys and values of new tokens into the
+ * paged cache and rotates keys and queries on the way.
+ *
+ * A ragged batch: the rows of all sequences are packed, sequence b owns rows
+ * [q_starts[b], q_starts[b + 1]), which are the last
+ * n_b = q_starts[b + 1] - q_starts[b] (0 or more) of its context_lens[b]
+ * tokens.  Row j of sequence b goes to token t = context_lens[b] - n_b + j:
+ *   k_cache[bt[b][t/32]][t%32][h] = rotated k row,   v_cache[...] = v row,
+ *   q_out row = rotated q row,
+ * at position t, or positions[row] where positions is not NULL.
+ *
+ *   k_cache, v_cache  as for vt_paged_attn_decode, written; no other slot is touched.
+ *   q_out, q    [num_tokens][num_q_heads][head_dim], q_out contiguous, q rows q_stride elements apart; both NULL
+ *               to append alone.  q_out == q with q_stride == num_q_heads * head_dim rotates in place.
+ *   k, v        [num_tokens] rows of [num_kv_heads][head_dim], k_stride and v_stride elements apart.
+ *   q_starts    [num_seqs + 1] int32, q_starts[0] = 0, not decreasing, last entry <= num_tokens.  Rows behind the
+ *               last sequence (a padded batch) are left as they were.
+ *   inv_freq, rot_dim, interleaved, amplitude  as for vt_rope; rot_dim 0 (inv_freq NULL) rotates nothing.
+ *   num_tokens  rows that q, k, v and q_out hold; num_seqs or num_tokens 0 is a no-op.
+ *   head_dim    64, 128, 256 or 512 (fp32: up to 256).
+ * All pointers 16-byte aligned (int32 arrays 4, inv_freq 8), strides multiples of 16 bytes.
+ *
+ * Invalid device data never faults: a sequence with a context outside [n_b, max_blocks_per_seq * 32] writes nothing
+ * to the cache and gets NaN q_out rows; a token whose page id is outside [0, num_blocks) is not written.  Two rows
+ * of one call that name the same slot leave one of the two there.  Needs no workspace.
+ */
+VT_API vt_status vt_paged_kv_append(void* k_cache, void* v_cache, void* q_out, const void* k, const void* v,
+                                    const void* q, const int32_t* q_starts, const int32_t* block_tables,
+                                    const int32_t* context_lens, const int32_t* positions, const double* inv_freq,
+                                    int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                    int block_size, int rot_dim, int interleaved, float amplitude,
+                                    long long q_stride, long long k_stride, long long v_stride, vt_stream_t stream,
+                                    int max_blocks_per_seq, int num_blocks, vt_dtype dtype);
+
+/*
+ * vt_paged_kv_append_fp8 -- the append into an FP8 (E4M3) cache: q, k, v and
+ * q_out bf16, a cached code is the E4M3 value nearest to row / k_scale[h]
+ * (v_scale[h]), ties to even, magnitudes past 448 held at 448, NaN kept.
+ * head_dim 64, 128 or 256; k_scale, v_scale device float32 [num_kv_heads].
+ */
+VT_API vt_status vt_paged_kv_append_fp8(void* k_cache, void* v_cache, void* q_out, const void* k, const void* v,
+                                        const void* q, const float* k_scale, const float* v_scale,
+                                        const int32_t* q_starts, const int32_t* block_tables,
+                                        const int32_t* context_lens, const int32_t* positions,
+                                        const double* inv_freq, int num_seqs, int num_tokens, int num_q_heads,
+                                        int num_kv_heads, int head_dim, int block_size, int rot_dim,
+                                        int interleaved, float amplitude, long long q_stride, long long k_stride,
+                                        long long v_stride, vt_stream_t stream, int max_blocks_per_seq,
+                                        int num_blocks);
+
+/*
+ * vt_paged_attn_prefill -- attention of a ragged batch of chunks of new
+ * tokens (whole prompts, chunks of prompts, draft tokens, single tokens
+ * beside them) over the paged cache that already holds their keys and values.
+ *
+ * Rows are packed as for vt_paged_kv_append; row j of sequence b stands at
+ * p = context_lens[b] - n_b + j and attends to the tokens
+ *   t0 <= t <= p,   t0 = window > 0 ? max(0, p + 1 - window) : 0
+ * which is the operation of vt_paged_attn_decode_multi with a chunk length of
+ * its own for each sequence and no bound on it.
+ *
+ *   out, q      [num_tokens][num_q_heads][head_dim]; out rows behind the last sequence are left as they were.
+ *   q_starts, num_seqs, num_tokens  as for vt_paged_kv_append.
+ *   num_q_heads / num_kv_heads at most 128, fp32 64 (else VT_ERR_UNSUPPORTED); the other arguments, layouts and
+ *   limits as for vt_paged_attn_decode.
+ * bf16 runs on the tensor cores: scores and sums in fp32, softmax weights rounded to bf16 before the product with
+ * V.  fp32 runs on CUDA cores.
+ *
+ * The values of slots outside [0, context_lens[b]) of a sequence's pages are never used, whatever they hold.
+ * Invalid device data never faults: rows of a sequence with a context outside [n_b, max_blocks_per_seq * 32] are
+ * NaN, and so are rows that attend to a page whose id is outside [0, num_blocks) (other rows of that sequence may be
+ * too).  q_starts that decrease or pass num_tokens are read as sequences without rows.
+ *
+ * Workspace: as for vt_paged_attn_decode, but the library's own prefill scratch is apart from the decode's; it is
+ * sized by the head_dim and the device, not by the batch, and a call that would have to allocate it inside a stream
+ * capture returns VT_ERR_SCRATCH_LIMIT (make one call before capturing).  With vt_paged_attn_set_workspace the
+ * caller's area is used instead and must hold vt_paged_attn_prefill_workspace_bytes() beyond the decodes' counters.
+ * vt_paged_attn_set_override and vt_paged_attn_set_test_wait apply; vt_paged_attn_device_status reports.
+ */
+VT_API vt_status vt_paged_attn_prefill(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                       const int32_t* q_starts, const int32_t* block_tables,
+                                       const int32_t* context_lens, int num_seqs, int num_tokens, int num_q_heads,
+                                       int num_kv_heads, int head_dim, int block_size, float scale, int window,
+                                       vt_stream_t stream, int max_blocks_per_seq, int num_blocks, vt_dtype dtype);
+
+/*
+ * vt_paged_attn_prefill_fp8 -- the same over an FP8 (E4M3) cache (bf16 q and
+ * out; codes times per-kv-head scales, as for vt_paged_attn_decode_fp8);
+ * head_dim 64, 128 or 256.
+ */
+VT_API vt_status vt_paged_attn_prefill_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                           const float* k_scale, const float* v_scale, const int32_t* q_starts,
+                                           const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+                                           int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                           int block_size, float scale, int window, vt_stream_t stream,
+                                           int max_blocks_per_seq, int num_blocks);
+
+/* Bytes of workspace a prefill call with this head_dim and cache type uses on the current device (0: not taken). */
+VT_API size_t vt_paged_attn_prefill_workspace_bytes(int head_dim, vt_dtype dtype);
+
+/* What the last successful decode or prefill call on this host thread
+ * launched (a prefill: group_tile is the query rows of a work item, subgroups
+ * 1, min_units_per_cta in 128-key blocks, q_len 0). */
 typedef struct {
   int grid_ctas;          /* CTAs launched (persistent, balanced split of the work) */
   int ctas_per_sm;        /* resident CTAs per SM for this kernel variant */

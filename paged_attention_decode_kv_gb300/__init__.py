@@ -22,6 +22,8 @@ BLOCK_SIZE = 32
 
 EXPORTED = ("vt_paged_attn_decode", "vt_paged_attn_decode_noalloc", "vt_paged_attn_decode_fp8",
             "vt_paged_attn_decode_multi", "vt_paged_attn_decode_multi_fp8",
+            "vt_rope_frequencies", "vt_rope", "vt_paged_kv_append", "vt_paged_kv_append_fp8",
+            "vt_paged_attn_prefill", "vt_paged_attn_prefill_fp8", "vt_paged_attn_prefill_workspace_bytes",
             "vt_paged_attn_last_plan",
             "vt_paged_attn_set_override", "vt_paged_attn_set_overlap", "vt_paged_attn_set_segment_cost",
             "vt_paged_attn_set_workspace", "vt_paged_attn_set_test_wait",
@@ -29,6 +31,7 @@ EXPORTED = ("vt_paged_attn_decode", "vt_paged_attn_decode_noalloc", "vt_paged_at
             "vt_paged_attn_release", "vt_status_string", "vt_last_cuda_error", "vt_paged_attn_version")
 VT_NOALLOC_SCRATCH_BYTES = 8 << 20
 VT_MIN_WORKSPACE_BYTES = 4096
+(VT_ROPE_PLAIN, VT_ROPE_LINEAR, VT_ROPE_NTK, VT_ROPE_YARN, VT_ROPE_BANDED) = range(5)
 
 
 class VtError(RuntimeError):
@@ -50,6 +53,11 @@ class vt_plan(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class vt_rope_stretch(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_double), ("original_context", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double)]
 
 
 _lib = None
@@ -83,6 +91,24 @@ def library() -> ctypes.CDLL:
             lib.vt_paged_attn_decode_multi_fp8.argtypes = [c_void] * 8 + [c_int] * 6 + [c_float, c_int, c_void,
                                                                                          c_int, c_int]
             lib.vt_paged_attn_decode_multi_fp8.restype = c_int
+            c_long, c_double = ctypes.c_longlong, ctypes.c_double
+            lib.vt_rope_frequencies.argtypes = [ctypes.POINTER(c_double), ctypes.POINTER(c_float), c_int, c_double,
+                                                ctypes.POINTER(vt_rope_stretch)]
+            lib.vt_rope_frequencies.restype = c_int
+            lib.vt_rope.argtypes = [c_void] * 4 + [c_int] * 5 + [c_float, c_long, c_long, c_void, c_int]
+            lib.vt_rope.restype = c_int
+            tail = [c_int] * 8 + [c_float, c_long, c_long, c_long, c_void, c_int, c_int]
+            lib.vt_paged_kv_append.argtypes = [c_void] * 11 + tail + [c_int]
+            lib.vt_paged_kv_append.restype = c_int
+            lib.vt_paged_kv_append_fp8.argtypes = [c_void] * 13 + tail
+            lib.vt_paged_kv_append_fp8.restype = c_int
+            tail = [c_int] * 6 + [c_float, c_int, c_void, c_int, c_int]
+            lib.vt_paged_attn_prefill.argtypes = [c_void] * 7 + tail + [c_int]
+            lib.vt_paged_attn_prefill.restype = c_int
+            lib.vt_paged_attn_prefill_fp8.argtypes = [c_void] * 9 + tail
+            lib.vt_paged_attn_prefill_fp8.restype = c_int
+            lib.vt_paged_attn_prefill_workspace_bytes.argtypes = [c_int, c_int]
+            lib.vt_paged_attn_prefill_workspace_bytes.restype = c_size
             lib.vt_paged_attn_last_plan.argtypes = [ctypes.POINTER(vt_plan)]
             lib.vt_paged_attn_last_plan.restype = c_int
             lib.vt_paged_attn_set_override.argtypes = [c_int, c_int]
@@ -173,6 +199,69 @@ def vt_paged_attn_decode_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_t
                                               context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim,
                                               block_size, float(scale), int(window), stream, max_blocks_per_seq,
                                               num_blocks)
+
+
+def vt_rope_frequencies(rot_dim, base, stretch=None):
+    """(status, list of rot_dim // 2 radians per token, amplitude); stretch is
+    a vt_rope_stretch or None."""
+    inv = (ctypes.c_double * max(1, rot_dim // 2))()
+    amplitude = ctypes.c_float(0.0)
+    st = library().vt_rope_frequencies(inv, ctypes.byref(amplitude), rot_dim, float(base),
+                                       ctypes.byref(stretch) if stretch is not None else None)
+    return st, list(inv)[:max(0, rot_dim // 2)], float(amplitude.value)
+
+
+def vt_rope(out, x, positions, inv_freq, num_tokens, num_heads, head_dim, rot_dim, interleaved, amplitude, x_stride,
+            out_stride, stream, dtype) -> int:
+    """Raw call of the rotary positions; returns the status code."""
+    return library().vt_rope(out, x, positions, inv_freq, num_tokens, num_heads, head_dim, rot_dim, int(interleaved),
+                             float(amplitude), x_stride, out_stride, stream, dtype)
+
+
+def vt_paged_kv_append(k_cache, v_cache, q_out, k, v, q, q_starts, block_tables, context_lens, positions, inv_freq,
+                       num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, rot_dim, interleaved,
+                       amplitude, q_stride, k_stride, v_stride, stream, max_blocks_per_seq, num_blocks, dtype) -> int:
+    """Raw call of the append to the paged cache; returns the status code."""
+    return library().vt_paged_kv_append(k_cache, v_cache, q_out, k, v, q, q_starts, block_tables, context_lens,
+                                        positions, inv_freq, num_seqs, num_tokens, num_q_heads, num_kv_heads,
+                                        head_dim, block_size, rot_dim, int(interleaved), float(amplitude), q_stride,
+                                        k_stride, v_stride, stream, max_blocks_per_seq, num_blocks, dtype)
+
+
+def vt_paged_kv_append_fp8(k_cache, v_cache, q_out, k, v, q, k_scale, v_scale, q_starts, block_tables, context_lens,
+                           positions, inv_freq, num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
+                           rot_dim, interleaved, amplitude, q_stride, k_stride, v_stride, stream, max_blocks_per_seq,
+                           num_blocks) -> int:
+    """Raw call of the append to an FP8 (E4M3) cache; returns the status code."""
+    return library().vt_paged_kv_append_fp8(k_cache, v_cache, q_out, k, v, q, k_scale, v_scale, q_starts,
+                                            block_tables, context_lens, positions, inv_freq, num_seqs, num_tokens,
+                                            num_q_heads, num_kv_heads, head_dim, block_size, rot_dim,
+                                            int(interleaved), float(amplitude), q_stride, k_stride, v_stride, stream,
+                                            max_blocks_per_seq, num_blocks)
+
+
+def vt_paged_attn_prefill(out, q, k_cache, v_cache, q_starts, block_tables, context_lens, num_seqs, num_tokens,
+                          num_q_heads, num_kv_heads, head_dim, block_size, scale, window, stream, max_blocks_per_seq,
+                          num_blocks, dtype) -> int:
+    """Raw call of the ragged prefill; returns the status code."""
+    return library().vt_paged_attn_prefill(out, q, k_cache, v_cache, q_starts, block_tables, context_lens, num_seqs,
+                                           num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, float(scale),
+                                           int(window), stream, max_blocks_per_seq, num_blocks, dtype)
+
+
+def vt_paged_attn_prefill_fp8(out, q, k_cache, v_cache, k_scale, v_scale, q_starts, block_tables, context_lens,
+                              num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, scale, window,
+                              stream, max_blocks_per_seq, num_blocks) -> int:
+    """Raw call of the ragged prefill over an FP8 (E4M3) cache; returns the
+    status code."""
+    return library().vt_paged_attn_prefill_fp8(out, q, k_cache, v_cache, k_scale, v_scale, q_starts, block_tables,
+                                               context_lens, num_seqs, num_tokens, num_q_heads, num_kv_heads,
+                                               head_dim, block_size, float(scale), int(window), stream,
+                                               max_blocks_per_seq, num_blocks)
+
+
+def vt_paged_attn_prefill_workspace_bytes(head_dim, dtype) -> int:
+    return int(library().vt_paged_attn_prefill_workspace_bytes(head_dim, dtype))
 
 
 def vt_paged_attn_last_plan() -> dict:
@@ -388,3 +477,251 @@ def decode_multi(q, k_cache, v_cache, block_tables, context_lens, scale=None, wi
                                     dtype_code(q))
     _check(st, "vt_paged_attn_decode_multi")
     return out
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, kind: int = VT_ROPE_PLAIN, factor: float = 1.0,
+                     original_context: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """Frequencies for ``rope`` and ``append``: (inv_freq float64 [rot_dim / 2]
+    on ``device``, amplitude).  ``kind`` is a VT_ROPE_* stretch for contexts
+    longer than the trained one (vt_rope_frequencies)."""
+    import torch
+    st, inv, amplitude = vt_rope_frequencies(
+        rot_dim, base, vt_rope_stretch(kind, factor, original_context, beta_fast, beta_slow))
+    _check(st, "vt_rope_frequencies")
+    return torch.tensor(inv, dtype=torch.float64, device=device), amplitude
+
+
+def _rows(name, t, heads=None, head_dim=None, dtype=None, like=None):
+    """Checks packed rows [T][H][D] whose heads are contiguous; the token
+    stride in elements."""
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (head_dim is not None and t.shape[2] != head_dim):
+        raise ValueError(f"{name} must be [tokens][heads][head_dim]")
+    _cuda(name, t, like, contiguous=False)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    T, H, D = t.shape
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name} must have contiguous heads (only the token stride is free)")
+    return t.stride(0) if T > 1 else max(H * D, t.stride(0))
+
+
+def _cuda(name, t, like=None, contiguous=True):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _ragged(q_starts, block_tables, context_lens, like):
+    import torch
+    for name, t in (("q_starts", q_starts), ("block_tables", block_tables), ("context_lens", context_lens)):
+        _cuda(name, t, like)
+        if t.dtype != torch.int32:
+            raise TypeError("q_starts, block_tables and context_lens must be int32")
+    B = context_lens.numel()
+    if q_starts.numel() != B + 1 or block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("q_starts must be [num_seqs + 1] and block_tables [num_seqs][max_blocks]")
+    return B
+
+
+def _frequencies(inv_freq, like):
+    import torch
+    if inv_freq is None or inv_freq.numel() == 0:
+        return None, 0
+    _cuda("inv_freq", inv_freq, like)
+    if inv_freq.dtype != torch.float64:
+        raise TypeError("inv_freq must be float64")
+    return inv_freq.data_ptr(), 2 * inv_freq.numel()
+
+
+def _codes(t):
+    import torch
+    t = t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t
+    if t.dtype != torch.uint8:
+        raise TypeError("the caches must be uint8 or float8_e4m3fn E4M3 codes")
+    return t
+
+
+def _scales(k_scale, v_scale, heads, like):
+    import torch
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _cuda(name, t, like)
+        if t.dtype != torch.float32 or t.numel() != heads:
+            raise TypeError("k_scale and v_scale must be float32 [num_kv_heads]")
+
+
+def _on(t, stream):
+    """The tensors' device made current, and the stream handle on it."""
+    import torch
+
+    class _Guard:
+        def __enter__(self):
+            self.guard = torch.cuda.device(t.device)
+            self.guard.__enter__()
+            return _stream_handle(stream)
+
+        def __exit__(self, *exc):
+            return self.guard.__exit__(*exc)
+
+    return _Guard()
+
+
+def rope(x, positions, inv_freq, interleaved: bool = False, amplitude: float = 1.0, out=None, stream=None):
+    """Rotary positions on torch CUDA tensors.
+
+    x [T][H][D] bf16 or fp32 (token stride free, e.g. the queries of a fused
+    projection); positions [T] int32; inv_freq float64 [rot_dim / 2] (see
+    ``rope_frequencies``).  Returns out [T][H][D] (allocated unless given; x
+    itself rotates in place).  A negative position turns back, so the gradient
+    of ``rope(x, p)`` is ``rope(grad, -p)``.  Asynchronous on ``stream``."""
+    import torch
+    x_stride = _rows("x", x)
+    T, H, D = x.shape
+    code = dtype_code(x)
+    _cuda("positions", positions, x)
+    if positions.dtype != torch.int32 or positions.numel() != T:
+        raise TypeError("positions must be int32 [tokens]")
+    freq, rot = _frequencies(inv_freq, x)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+    out_stride = _rows("out", out, H, D, x.dtype, x)
+    if out.shape[0] != T:
+        raise ValueError("out must have x's shape")
+    with _on(x, stream) as handle:
+        st = vt_rope(out.data_ptr(), x.data_ptr(), positions.data_ptr(), freq, T, H, D, rot, interleaved, amplitude,
+                     x_stride, out_stride, handle, code)
+        _check(st, "vt_rope")
+    return out
+
+
+def _append(k, v, k_cache, v_cache, scales, q_starts, block_tables, context_lens, q, q_out, positions, inv_freq,
+            interleaved, amplitude, stream):
+    import torch
+    T, Hkv, D = k.shape
+    io = torch.bfloat16 if scales is not None else k_cache.dtype
+    code = VT_E4M3 if scales is not None else dtype_code(k_cache)
+    ks = _rows("k", k, dtype=io)
+    vs = _rows("v", v, Hkv, D, io, k)
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same rows")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _cuda(name, t, k)
+        if t.dim() != 4 or tuple(t.shape[2:]) != (Hkv, D) or t.shape != k_cache.shape or t.dtype != k_cache.dtype:
+            raise ValueError("k_cache/v_cache must be [num_blocks][32][Hkv][head_dim] matching k")
+    nb, P = k_cache.shape[:2]
+    B = _ragged(q_starts, block_tables, context_lens, k)
+    freq, rot = _frequencies(inv_freq, k)
+    Hq = qs = 0
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        qs = _rows("q", q, Hq, D, io, k)
+        if q.shape[0] != T:
+            raise ValueError("q must have k's rows")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=io, device=k.device)
+        _cuda("q_out", q_out, k)
+        if q_out.shape != q.shape or q_out.dtype != io:
+            raise ValueError("q_out must be a contiguous tensor shaped and typed like q")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if positions is not None:
+        _cuda("positions", positions, k)
+        if positions.dtype != torch.int32 or positions.numel() != T:
+            raise TypeError("positions must be int32 [tokens]")
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    head = (k_cache.data_ptr(), v_cache.data_ptr(), ptr(q_out), k.data_ptr(), v.data_ptr(), ptr(q))
+    mid = (q_starts.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), ptr(positions), freq, B, T, Hq, Hkv,
+           D, P, rot, interleaved, amplitude, qs, ks, vs)
+    with _on(k, stream) as handle:
+        tail = (handle, block_tables.shape[1], nb)
+        if scales is not None:
+            st = vt_paged_kv_append_fp8(*head, scales[0].data_ptr(), scales[1].data_ptr(), *mid, *tail)
+            _check(st, "vt_paged_kv_append_fp8")
+        else:
+            st = vt_paged_kv_append(*head, *mid, *tail, code)
+            _check(st, "vt_paged_kv_append")
+    return q_out
+
+
+def append(k, v, k_cache, v_cache, q_starts, block_tables, context_lens, q=None, q_out=None, positions=None,
+           inv_freq=None, interleaved: bool = False, amplitude: float = 1.0, stream=None):
+    """Writes the keys and values of new tokens into the paged cache, keys and
+    queries rotated on the way.
+
+    k, v [T][Hkv][D] and q [T][Hq][D] (token strides free); sequence b owns
+    rows q_starts[b]:q_starts[b + 1], the last of its context_lens[b] tokens;
+    caches [num_blocks][32][Hkv][D] of the rows' type.  Rotates at each
+    token's place in its context, or at positions [T]; without inv_freq it
+    rotates nothing.  Returns the rotated queries [T][Hq][D] (q_out, allocated
+    unless given; None without q).  Asynchronous on ``stream``."""
+    return _append(k, v, k_cache, v_cache, None, q_starts, block_tables, context_lens, q, q_out, positions, inv_freq,
+                   interleaved, amplitude, stream)
+
+
+def append_fp8(k, v, k_codes, v_codes, k_scale, v_scale, q_starts, block_tables, context_lens, q=None, q_out=None,
+               positions=None, inv_freq=None, interleaved: bool = False, amplitude: float = 1.0, stream=None):
+    """``append`` into an FP8 (E4M3) cache of codes with a scale per kv head
+    (rows bf16; codes uint8 or torch.float8_e4m3fn)."""
+    _scales(k_scale, v_scale, k.shape[1], k)
+    return _append(k, v, _codes(k_codes), _codes(v_codes), (k_scale, v_scale), q_starts, block_tables, context_lens,
+                   q, q_out, positions, inv_freq, interleaved, amplitude, stream)
+
+
+def _prefill(q, k_cache, v_cache, scales, q_starts, block_tables, context_lens, scale, window, out, stream):
+    import torch
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens][heads][head_dim]")
+    T, Hq, D = q.shape
+    _cuda("q", q)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _cuda(name, t, q)
+        if t.dim() != 4 or t.shape[3] != D or t.shape != k_cache.shape:
+            raise ValueError("k_cache/v_cache must be [num_blocks][32][Hkv][head_dim] matching q")
+    nb, P, Hkv, _ = k_cache.shape
+    if scales is None and (k_cache.dtype != q.dtype or v_cache.dtype != q.dtype):
+        raise TypeError("q, k_cache and v_cache must share one dtype")
+    if scales is not None:
+        if q.dtype != torch.bfloat16:
+            raise TypeError("q must be bfloat16")
+        _scales(*scales, Hkv, q)
+    B = _ragged(q_starts, block_tables, context_lens, q)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != q.device:
+        raise ValueError("out must be a contiguous CUDA tensor shaped and typed like q")
+    if scale is None:
+        scale = D ** -0.5
+    mid = (q_starts.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), B, T, Hq, Hkv, D, P, scale, window)
+    with _on(q, stream) as handle:
+        tail = (handle, block_tables.shape[1], nb)
+        head = (out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr())
+        if scales is not None:
+            st = vt_paged_attn_prefill_fp8(*head, scales[0].data_ptr(), scales[1].data_ptr(), *mid, *tail)
+            _check(st, "vt_paged_attn_prefill_fp8")
+        else:
+            st = vt_paged_attn_prefill(*head, *mid, *tail, dtype_code(q))
+            _check(st, "vt_paged_attn_prefill")
+    return out
+
+
+def prefill(q, k_cache, v_cache, q_starts, block_tables, context_lens, scale=None, window: int = 0, out=None,
+            stream=None):
+    """Attention of a ragged batch of chunks of new tokens over the paged
+    cache (which holds their keys and values already, see ``append``).
+
+    q [T][Hq][D]: sequence b owns rows q_starts[b]:q_starts[b + 1], the last of
+    its context_lens[b] tokens, attending causally; q_starts [B + 1] int32, the
+    rest as for ``decode``.  Returns out [T][Hq][D] (allocated unless given;
+    rows behind the last sequence are not written).  Asynchronous on
+    ``stream``."""
+    return _prefill(q, k_cache, v_cache, None, q_starts, block_tables, context_lens, scale, window, out, stream)
+
+
+def prefill_fp8(q, k_codes, v_codes, k_scale, v_scale, q_starts, block_tables, context_lens, scale=None,
+                window: int = 0, out=None, stream=None):
+    """``prefill`` over an FP8 (E4M3) cache (q and out bf16; codes uint8 or
+    torch.float8_e4m3fn with a float32 scale per kv head)."""
+    return _prefill(q, _codes(k_codes), _codes(v_codes), (k_scale, v_scale), q_starts, block_tables, context_lens,
+                    scale, window, out, stream)

@@ -28,6 +28,10 @@ SOURCES = [
     "decode_d128_f32.cu",
     "decode_d256_f32.cu",
     "decode_e4m3.cu",
+    "rope_append.cu",
+    "prefill_api.cu",
+    "prefill_simt.cu",
+    "prefill_bf16.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -21,10 +21,66 @@
 #include <vector>
 
 #include "../../include/vt_paged_attn.h"
+#include "host_state.cuh"
 #include "kernel_variants.cuh"
+
+// ---------------------------------------------------------------------------
+// Host state shared with the other entry points (declared in host_state.cuh)
+// ---------------------------------------------------------------------------
+namespace vt {
+namespace host {
+
+thread_local std::string g_last_cuda_error;
+thread_local long long g_test_wait_limit = 0;
+thread_local int g_test_withhold_cta = -1;
+thread_local int g_test_withhold_tile = -1;
+thread_local int g_override_grid = 0;
+thread_local int g_override_min_units = 0;
+thread_local vt_plan g_last_plan{};
+thread_local bool g_have_plan = false;
+std::mutex g_mutex;
+std::vector<DeviceState> g_devices;
+
+vt_status cuda_fail(cudaError_t e, const char* where) {
+  g_last_cuda_error = std::string(where) + ": " + cudaGetErrorString(e);
+  return VT_ERR_CUDA;
+}
+
+DeviceState& device_state(int dev) {
+  if (static_cast<int>(g_devices.size()) <= dev) g_devices.resize(dev + 1);
+  return g_devices[dev];
+}
+
+vt_status prepare_device(int dev, DeviceState& ds) {
+  if (ds.init) return VT_OK;
+  int sms = 0;
+  cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+  ds.num_sms = sms;
+  ds.init = true;
+  return VT_OK;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+}  // namespace host
+}  // namespace vt
 
 namespace {
 
+using namespace vt::host;
 using vt::DecodeArgs;
 using vt::VariantInfo;
 
@@ -36,23 +92,9 @@ constexpr int kDefaultMinUnits = 2;
 // is worth less against it: measured best at six.
 constexpr int kDefaultSegCost = 2;
 constexpr int kDefaultSegCostFp8OrMulti = 6;
-constexpr size_t kStatusBytes = 256;
 
-thread_local int g_override_grid = 0;
 thread_local bool g_overlap = false;
-thread_local int g_override_min_units = 0;
 thread_local int g_seg_cost = -1;  // < 0: default
-thread_local long long g_test_wait_limit = 0;  // <= 0: kWaitLimitCycles
-thread_local int g_test_withhold_cta = -1;
-thread_local int g_test_withhold_tile = -1;
-thread_local vt_plan g_last_plan{};
-thread_local bool g_have_plan = false;
-thread_local std::string g_last_cuda_error;
-
-vt_status cuda_fail(cudaError_t e, const char* where) {
-  g_last_cuda_error = std::string(where) + ": " + cudaGetErrorString(e);
-  return VT_ERR_CUDA;
-}
 
 // ---------------------------------------------------------------------------
 // Variant lookup
@@ -87,8 +129,6 @@ int group_tile_for(int group, vt_dtype dtype, int head_dim) {
   return g;
 }
 
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
 // Split scratch layout: [status words (256 B) | arrival counters | partial
 // records].  Arrival counters are zero between calls (every kernel leaves
 // them so; vt_paged_attn_device_status clears them after a give-up), so the
@@ -108,42 +148,6 @@ WsNeed ws_need(int num_seqs, int nvh, int grid, int group_tile, int head_dim) {
 }
 
 size_t ws_total(const WsNeed& n) { return kStatusBytes + align_up(n.counters_bytes, 256) + n.part_bytes; }
-
-struct Scratch {
-  char* base = nullptr;
-  size_t bytes = 0;
-  size_t counters_cap = 0;  // bytes after the status words that hold zeroed counters
-};
-
-// ---------------------------------------------------------------------------
-// Per-device state
-// ---------------------------------------------------------------------------
-struct DeviceState {
-  bool init = false;
-  int num_sms = 0;
-  Scratch lib;               // library-owned (cudaMallocAsync, grows)
-  Scratch user;              // caller-owned (vt_paged_attn_set_workspace)
-  char* noalloc = nullptr;   // device address of the static array, once looked up
-  std::vector<std::pair<const void*, int>> occupancy;
-};
-
-std::mutex g_mutex;
-std::vector<DeviceState> g_devices;
-
-DeviceState& device_state(int dev) {
-  if (static_cast<int>(g_devices.size()) <= dev) g_devices.resize(dev + 1);
-  return g_devices[dev];
-}
-
-vt_status prepare_device(int dev, DeviceState& ds) {
-  if (ds.init) return VT_OK;
-  int sms = 0;
-  cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
-  ds.num_sms = sms;
-  ds.init = true;
-  return VT_OK;
-}
 
 vt_status prepare_variant(DeviceState& ds, const VariantInfo& v, int* ctas_per_sm) {
   for (auto& p : ds.occupancy)
@@ -224,20 +228,6 @@ vt_status fit_user_scratch(Scratch& w, const WsNeed& n, cudaStream_t stream) {
 // ---------------------------------------------------------------------------
 // TMA descriptors: tiled views of a page pool (4-D for bf16, 3-D for fp32).
 // ---------------------------------------------------------------------------
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
 struct MapKey {
   const void* ptr;
   int head_dim, num_kv_heads, num_blocks, dtype, device;
@@ -327,8 +317,6 @@ vt_status tensor_map(const MapKey& k, CUtensorMap* out) {
   *out = m;
   return VT_OK;
 }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // ---------------------------------------------------------------------------
 // The shared call path
@@ -514,6 +502,7 @@ std::vector<std::pair<char*, size_t>> status_areas(DeviceState& ds) {
   if (ds.lib.base) areas.emplace_back(ds.lib.base, kStatusBytes + ds.lib.counters_cap);
   if (ds.user.base) areas.emplace_back(ds.user.base, kStatusBytes + ds.user.counters_cap);
   if (ds.noalloc) areas.emplace_back(ds.noalloc, kStatusBytes);  // its calls clear their counters themselves
+  if (ds.prefill.base) areas.emplace_back(ds.prefill.base, kStatusBytes);  // no counters
   return areas;
 }
 
@@ -787,6 +776,13 @@ void vt_paged_attn_release(void) {
       cudaSetDevice(static_cast<int>(d));
       cudaFree(ds.lib.base);
       ds.lib = Scratch{};
+    }
+    if (ds.prefill.base) {
+      cudaSetDevice(static_cast<int>(d));
+      cudaFree(ds.prefill.base);
+      for (char* p : ds.prefill_retired) cudaFree(p);
+      ds.prefill = Scratch{};
+      ds.prefill_retired.clear();
     }
   }
   cudaSetDevice(cur);

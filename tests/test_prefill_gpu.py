@@ -1,0 +1,323 @@
+"""Ragged prefill over the paged cache against its 64-bit form (GPU).
+
+Tolerances, from the kernel's arithmetic, with w = sum_t p_t |v_t| of an
+output element: the softmax weights are rounded to bf16 (2^-8 of each, so at
+most 2^-8 w), or for codes to two E4M3 terms (the same 2^-8, and 2^-17 of the
+largest weight each), the output to bf16 (2^-8 of it); scores, their
+exponentials and sums are fp32, whose errors over D products and a few
+thousand keys stay below 2^-12 w at these magnitudes.  fp32 storage: a score
+sums D products of magnitude up to sum |q k| with 2^-24 each, the output up
+to n of them.
+"""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import paged_attention_decode_kv_gb300 as vt
+from ragged import attention, make_batch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    from paged_attention_decode_kv_gb300 import build_lib
+    build_lib.build()
+    vt.library()
+    return torch.device("cuda:0")
+
+
+@pytest.fixture(autouse=True)
+def _reset():
+    yield
+    if vt._lib is not None:
+        vt.vt_paged_attn_set_override(0, 0)
+        vt.vt_paged_attn_set_test_wait(0, -1, -1)
+        vt.vt_paged_attn_set_workspace(0, 0)
+
+
+def run(batch, scale=None, window=0, out=None, grid=0, blocks=0, stream=None):
+    vt.vt_paged_attn_set_override(grid, blocks)
+    if batch.dtype == "e4m3":
+        out = vt.prefill_fp8(batch.q, batch.k_cache, batch.v_cache, batch.k_scale, batch.v_scale, batch.q_starts,
+                             batch.block_tables, batch.context_lens, scale, window, out=out, stream=stream)
+    else:
+        out = vt.prefill(batch.q, batch.k_cache, batch.v_cache, batch.q_starts, batch.block_tables,
+                         batch.context_lens, scale, window, out=out, stream=stream)
+    vt.vt_paged_attn_set_override(0, 0)
+    return out
+
+
+def check(batch, got, scale=None, window=0):
+    live, D = batch.starts[-1], batch.q.shape[2]
+    torch.cuda.synchronize()
+    assert vt.vt_paged_attn_device_status() == 0
+    plan = vt.vt_paged_attn_last_plan()
+    assert plan["tensor_cores"] == (0 if batch.dtype == "f32" else 1)
+    ref, reach = attention(batch, D ** -0.5 if scale is None else scale, window)
+    ref, reach, got = ref[:live], reach[:live], got[:live].double()
+    assert torch.isfinite(got).all()
+    err = (got - ref).abs()
+    if batch.dtype == "f32":
+        n = max(batch.ctx)
+        span = float(batch.q[:live].double().norm(dim=-1).max()) * 1.5 * D ** 0.5 * abs(
+            D ** -0.5 if scale is None else scale)   # no |q||k| scale is above it (k rows: 1.5 sqrt(D) at most)
+        tol = ((2 * D * span + n + 16) * 2.0 ** -24) * reach
+    else:
+        tol = (2.0 ** -8 + 2.0 ** -12) * reach + 2.0 ** -8 * ref.abs() + 1e-30
+        if batch.dtype == "e4m3":
+            tol = tol + 2.0 ** -9 * reach
+    assert (err <= tol).all(), (float((err - tol).max()), float(err.max()))
+    if live:
+        nmse = float((err ** 2).sum() / (ref ** 2).sum())
+        assert nmse <= (1e-10 if batch.dtype == "f32" else 2e-5), nmse
+
+
+#: (type, head_dim): every kernel
+KINDS = [("bf16", 64), ("bf16", 128), ("bf16", 256), ("bf16", 512), ("f32", 64), ("f32", 128), ("f32", 256)]
+SHAPES = {
+    "one_token": ([1], [1]),
+    "first_tokens": ([2, 3], [2, 3]),
+    "decode_rows": ([1, 1, 1], [33, 100, 257]),
+    "page_edges": ([31, 32, 33, 64], [31, 64, 97, 300]),
+    "empty_between": ([0, 7, 0, 0, 130, 0], [5, 7, 0, 300, 131, 64]),
+    "block_edges": ([127, 128, 129], [128, 256, 385]),
+    "long": ([300, 1, 65], [300, 1025, 900]),
+}
+
+
+@pytest.mark.parametrize("shape", list(SHAPES))
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_shapes(dev, dtype, D, shape):
+    new, ctx = SHAPES[shape]
+    batch = make_batch(new, ctx, 8, 2, D, dtype, seed=D)
+    check(batch, run(batch))
+
+
+@pytest.mark.parametrize("q_heads,kv_heads", [(1, 1), (8, 8), (6, 2), (5, 1), (14, 2), (16, 2), (33, 1), (64, 1)])
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f32", 64)])
+def test_groups(dev, dtype, D, q_heads, kv_heads):
+    batch = make_batch([70, 3, 131], [200, 3, 131], q_heads, kv_heads, D, dtype, seed=q_heads)
+    check(batch, run(batch))
+
+
+@pytest.mark.parametrize("window", [1, 2, 31, 33, 128, 200, 1000])
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_windows(dev, dtype, D, window):
+    batch = make_batch([150, 1, 40], [500, 300, 40], 4, 2, D, dtype, seed=window)
+    check(batch, run(batch, window=window), window=window)
+
+
+@pytest.mark.parametrize("grid", [1, 2, 3, 7, 40, 152, 400])
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_forced_partitions(dev, dtype, D, grid):
+    """Any number of CTAs, down to shares of two blocks, so that items are cut everywhere."""
+    batch = make_batch([100, 260, 5, 1], [1200, 260, 900, 2000], 8, 2, D, dtype, seed=1)
+    got = run(batch, grid=grid, blocks=2)
+    assert vt.vt_paged_attn_last_plan()["grid_ctas"] == grid
+    check(batch, got)
+    assert torch.equal(got, run(batch, grid=grid, blocks=2))  # the same bits every time
+
+
+@pytest.mark.parametrize("grid", [7, 152])
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_forced_partitions_with_a_window(dev, dtype, D, grid):
+    batch = make_batch([100, 260, 5, 1], [1200, 260, 900, 2000], 8, 2, D, dtype, seed=2)
+    check(batch, run(batch, grid=grid, blocks=2, window=333), window=333)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, 0.5, 2.0])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 256), ("f32", 128)])
+def test_scales(dev, dtype, D, scale):
+    """Flat, reversed and peaked softmax (peaked: scores up to about 150, so a score error of 2^-20 of that is
+    2^-12)."""
+    batch = make_batch([200, 9], [300, 70], 4, 2, D, dtype, seed=3)
+    check(batch, run(batch, scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_growing_scores(dev, dtype, D):
+    """Keys that grow along the context move the running maximum at every block."""
+    batch = make_batch([64, 10], [1000, 800], 4, 2, D, dtype, seed=4)
+    if dtype == "e4m3":
+        batch.k_scale = batch.k_scale * 2
+    else:
+        for b, L in enumerate(batch.ctx):
+            for i in range((L + 31) // 32):
+                batch.k_cache[batch.block_tables[b, i].long()] *= 2.0 ** min(3, i // 8)
+    check(batch, run(batch, scale=D ** -0.5 / 2), scale=D ** -0.5 / 2)
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_padding_rows_are_kept(dev, dtype, D):
+    batch = make_batch([5, 0, 140], [5, 9, 200], 4, 2, D, dtype, pad=19)
+    out = torch.full_like(batch.q, 3.0)
+    check(batch, run(batch, out=out))
+    assert (out[145:] == 3).all()
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_bad_device_data(dev, dtype, D):
+    batch = make_batch([20, 20, 20, 20, 20], [100] * 5, 4, 2, D, dtype)
+    good, _ = attention(batch, D ** -0.5)
+    batch.context_lens[1] = 19
+    batch.context_lens[2] = 10 ** 6
+    batch.context_lens[4] = -5
+    batch.block_tables[3, 1] = batch.k_cache.shape[0]
+    for grid in (0, 11):
+        out = run(batch, grid=grid, blocks=2 if grid else 0)
+        torch.cuda.synchronize()
+        assert vt.vt_paged_attn_device_status() == 0
+        assert torch.isnan(out[20:]).all()
+        assert (out[:20].double() - good[:20]).abs().max() < 0.02
+
+
+def test_bad_row_starts(dev):
+    """Starts that decrease or pass the rows: those sequences have no rows; nothing faults."""
+    batch = make_batch([8, 8, 8], [40, 40, 40], 4, 2, 128, "bf16")
+    good, _ = attention(batch, 128 ** -0.5)
+    out = torch.full_like(batch.q, 3.0)
+    batch.q_starts.copy_(torch.tensor([0, 8, 4, 400], dtype=torch.int32))
+    run(batch, out=out)
+    torch.cuda.synchronize()
+    assert (out[8:] == 3).all() and (out[:8].double() - good[:8]).abs().max() < 0.02
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_values_that_are_not_finite_in_masked_places(dev, dtype, D):
+    """A value of a later new token that is not finite does not reach the rows before it; rows that attend to it
+    are not finite there."""
+    batch = make_batch([60], [150], 2, 1, D, dtype)
+    ref, _ = attention(batch, D ** -0.5)
+    t = 120                                        # position of new token 30
+    page = batch.block_tables[0, t // 32].long()
+    for col, bits in ((3, float("nan")), (D - 1, float("inf"))):
+        if dtype == "e4m3":
+            batch.v_cache[page, t % 32, 0, col] = 0x7F
+        else:
+            batch.v_cache[page, t % 32, 0, col] = bits
+    out = run(batch)
+    torch.cuda.synchronize()
+    assert torch.isfinite(out[:30]).all()
+    assert (out[:30].double() - ref[:30]).abs().max() < 0.02
+    assert not torch.isfinite(out[30:, :, 3]).any() and not torch.isfinite(out[30:, :, D - 1]).any()
+    clean = [c for c in range(D) if c not in (3, D - 1)]
+    assert (out[30:][..., clean].double() - ref[30:][..., clean]).abs().max() < 0.02
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f32", 64)])
+def test_workspace_of_the_caller(dev, dtype, D):
+    batch = make_batch([100, 30], [900, 2000], 8, 2, D, dtype)
+    need = vt.vt_paged_attn_prefill_workspace_bytes(D, vt.VT_BF16 if dtype == "bf16" else vt.VT_F32)
+    area = torch.empty(need + 256, dtype=torch.uint8, device=dev)
+    vt.vt_paged_attn_set_workspace(area.data_ptr(), need)
+    got = run(batch)
+    assert vt.vt_paged_attn_last_plan()["scratch_source"] == 1
+    check(batch, got)
+    vt.vt_paged_attn_set_workspace(area.data_ptr(), need - 256)
+    with pytest.raises(vt.VtError) as e:
+        run(batch)
+    assert e.value.status == vt.VT_ERR_SCRATCH_LIMIT
+
+
+def test_captured_and_replayed_with_other_lengths(dev):
+    """The plan is made on the device: a replay follows the lengths as they then are."""
+    batch = make_batch([100, 30], [900, 2000], 8, 2, 128, "bf16")
+    out = torch.zeros_like(batch.q)
+    run(batch, out=out)
+    other = make_batch([60, 70], [400, 1500], 8, 2, 128, "bf16", seed=8)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(batch, out=out)
+    graph.replay()
+    check(batch, out)
+    pages = min(batch.k_cache.shape[0], other.k_cache.shape[0])
+    assert other.k_cache.shape[0] <= batch.k_cache.shape[0] and pages == other.k_cache.shape[0]
+    batch.k_cache[:pages].copy_(other.k_cache)
+    batch.v_cache[:pages].copy_(other.v_cache)
+    batch.q.copy_(other.q)
+    batch.q_starts.copy_(other.q_starts)
+    batch.context_lens.copy_(other.context_lens)
+    batch.block_tables[:, : other.block_tables.shape[1]].copy_(other.block_tables)
+    batch.new, batch.ctx = other.new, other.ctx
+    graph.replay()
+    check(batch, out)
+
+
+def test_other_stream(dev):
+    batch = make_batch([64], [700], 8, 2, 128, "bf16")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = run(batch, stream=s)
+    s.synchronize()
+    check(batch, got)
+
+
+def test_many_sequences(dev):
+    """More sequences than threads of a CTA, one to four new tokens each."""
+    g = torch.Generator().manual_seed(0)
+    new = torch.randint(0, 5, (900,), generator=g).tolist()
+    ctx = [n + int(c) for n, c in zip(new, torch.randint(0, 200, (900,), generator=g))]
+    batch = make_batch(new, ctx, 4, 1, 64, "bf16")
+    check(batch, run(batch))
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 256)])
+def test_one_chunk_for_all_is_the_multi_token_decode(dev, dtype, D):
+    """Uniform chunks, against the decode entry points on the same cache."""
+    batch = make_batch([6] * 5, [100, 37, 500, 6, 64], 8, 2, D, dtype)
+    got = run(batch)
+    q = batch.q.view(5, 6, 8, D)
+    args = (batch.block_tables, batch.context_lens)
+    if dtype == "e4m3":
+        ref = vt.decode_fp8(q, batch.k_cache, batch.v_cache, batch.k_scale, batch.v_scale, *args)
+    else:
+        ref = vt.decode_multi(q, batch.k_cache, batch.v_cache, *args)
+    _, reach = attention(batch, D ** -0.5)
+    # both are within their own bounds of the same value
+    assert ((got.double() - ref.view_as(got).double()).abs() <= 2.0 ** -5 * reach + 1e-6).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_serving_steps(dev, dtype):
+    """Append, prefill, append one token, decode: what a serving loop runs, against dense attention on rotated
+    rows."""
+    D, Hq, Hkv = 128, 8, 2
+    new, ctx = [50, 3, 64], [50, 90, 64]
+    batch = make_batch(new, ctx, Hq, Hkv, D, dtype, seed=11)
+    io = batch.q.dtype
+    inv, amp = vt.rope_frequencies(D, 10000.0, vt.VT_ROPE_YARN, 4.0, 4096)
+    g = torch.Generator().manual_seed(2)
+    scales = (batch.k_scale, batch.v_scale) if dtype == "e4m3" else ()
+    # room for one more token in each sequence
+    pool = torch.cat([batch.block_tables, torch.zeros((3, 1), dtype=torch.int32, device=dev)], 1)
+    extra = batch.k_cache.shape[0]
+    grow = [torch.cat([c, torch.zeros_like(c[:3])]) for c in (batch.k_cache, batch.v_cache)]
+    for b, L in enumerate(ctx):
+        if L % 32 == 0:
+            pool[b, L // 32] = extra + b
+    batch.k_cache, batch.v_cache, batch.block_tables = *grow, pool
+
+    def append(rows, starts, lens):
+        qkv = torch.randn((rows, Hq + 2 * Hkv, D), generator=g).to(io).to(dev)
+        q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        fn = vt.append_fp8 if dtype == "e4m3" else vt.append
+        return fn(k, v, batch.k_cache, batch.v_cache, *scales, starts, batch.block_tables, lens, q=q, inv_freq=inv,
+                  amplitude=amp)
+
+    batch.q = append(117, batch.q_starts, batch.context_lens)
+    check(batch, run(batch))
+    lens = batch.context_lens + 1
+    q = append(3, torch.arange(4, dtype=torch.int32, device=dev), lens)
+    step = batch
+    step.q, step.new, step.ctx = q, [1, 1, 1], [L + 1 for L in ctx]
+    step.q_starts, step.context_lens = torch.arange(4, dtype=torch.int32, device=dev), lens
+    got = run(step)
+    check(step, got)
+    dec = vt.decode_fp8(q, step.k_cache, step.v_cache, *scales, step.block_tables, lens) if dtype == "e4m3" else \
+        vt.decode(q, step.k_cache, step.v_cache, step.block_tables, lens)
+    _, reach = attention(step, D ** -0.5)
+    assert ((got.double() - dec.double()).abs() <= 2.0 ** -5 * reach + 1e-6).all()
