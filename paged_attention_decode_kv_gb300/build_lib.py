@@ -32,6 +32,7 @@ SOURCES = [
     "prefill_api.cu",
     "prefill_simt.cu",
     "prefill_bf16.cu",
+    "prefill_e4m3.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

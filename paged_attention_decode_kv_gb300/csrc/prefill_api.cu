@@ -36,10 +36,10 @@ struct PrefillCall {
 const PrefillVariant* find_prefill(int head_dim, vt_dtype dtype) {
   if (dtype == VT_F32) return prefill_simt_variant(head_dim);
   if (dtype == VT_BF16) return prefill_bf16_variant(head_dim);
-  return nullptr;
+  return prefill_e4m3_variant(head_dim);
 }
 
-vt_status encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+vt_status encode(CUtensorMap* m, CUtensorMapDataType type, bool wide_rows, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
                  const cuuint32_t* box) {
   auto fn = encode_fn();
   if (!fn) {
@@ -47,9 +47,10 @@ vt_status encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* di
     return VT_ERR_CUDA;
   }
   const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = fn(m, type, rank, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        wide_rows ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     g_last_cuda_error = "cuTensorMapEncodeTiled failed (code " + std::to_string(static_cast<int>(r)) + ")";
     return VT_ERR_CUDA;
@@ -65,18 +66,22 @@ vt_status query_map(CUtensorMap* m, const PrefillCall& c, int group) {
                               static_cast<cuuint64_t>(c.num_kv_heads)};
   const cuuint64_t strides[4] = {D * 2, row, 128, static_cast<cuuint64_t>(group) * D * 2};
   const cuuint32_t box[5] = {64u, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(128 / group), 1u, 1u};
-  return encode(m, c.q, 5, dims, strides, box);
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, true, c.q, 5, dims, strides, box);
 }
 
-// A bf16 pool as (64 columns, token, column block, kv head): one box is one
-// column block of a page, so that a stage's four pages lie one after another.
+// A pool as (columns of a block, token, column block, kv head), blocks of 64
+// bf16 columns or 128 codes (64 at head_dim 64): one box is one column block of
+// a page, so that a stage's four pages lie one after another.
 vt_status pool_map(CUtensorMap* m, const void* pool, const PrefillCall& c) {
-  const cuuint64_t D = c.head_dim, row = static_cast<cuuint64_t>(c.num_kv_heads) * D * 2;
-  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(c.num_blocks) * kPfPage, D / 64,
+  const bool fp8 = c.dtype == VT_E4M3;
+  const cuuint64_t es = fp8 ? 1 : 2, D = c.head_dim, cols = fp8 && D >= 128 ? 128 : 64;
+  const cuuint64_t row = static_cast<cuuint64_t>(c.num_kv_heads) * D * es;
+  const cuuint64_t dims[4] = {cols, static_cast<cuuint64_t>(c.num_blocks) * kPfPage, D / cols,
                               static_cast<cuuint64_t>(c.num_kv_heads)};
-  const cuuint64_t strides[3] = {row, 128, D * 2};
-  const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(kPfPage), 1u, 1u};
-  return encode(m, pool, 4, dims, strides, box);
+  const cuuint64_t strides[3] = {row, cols * es, D * es};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(kPfPage), 1u, 1u};
+  return encode(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cols * es == 128, pool, 4,
+                dims, strides, box);
 }
 
 vt_status validate(const PrefillCall& c) {

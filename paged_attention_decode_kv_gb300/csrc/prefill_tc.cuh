@@ -33,15 +33,24 @@
 
 namespace vt {
 
-template <int D, int NT, int DV, int CW, int NS>
+template <bool FP8, int D, int NT, int DV, int CW, int NS>
 struct TcConfig {
+  static constexpr bool kFp8 = FP8;                    // E4M3 codes in the cache, else bf16
   static constexpr int kD = D, kNT = NT, kDV = DV;
+  static constexpr int kElem = FP8 ? 1 : 2;            // bytes of a cached element
+  // One TMA box and one swizzled block are kCols columns wide: 128-byte rows,
+  // or 64-byte ones for the 64 codes of an FP8 head_dim 64.
+  static constexpr int kCols = FP8 ? (D < 128 ? D : 128) : 64;
+  static constexpr int kRow = kCols * kElem;
+  static constexpr uint32_t kSwizzle = kRow == 128 ? 2 : 4;
+  static constexpr int kKStep = 32 / kElem;            // k extent of an MMA
   static constexpr int kCW = CW;                       // columns of a stage
   static constexpr int kStages = NS;
   static constexpr int kKChunks = D / CW, kVChunks = DV / CW;
-  static constexpr int kStageBytes = kPfBlock * CW * 2;
-  static constexpr int kBlockBytes = kPfBlock * 128;   // one 64-column block of a stage
-  static constexpr int kQBytes = 128 * D * 2;
+  static constexpr int kBlocks = CW / kCols;           // swizzled blocks of a stage
+  static constexpr int kBlockBytes = kPfBlock * kRow;
+  static constexpr int kStageBytes = kBlocks * kBlockBytes;
+  static constexpr int kQBytes = 128 * D * 2;          // FP8: two E4M3 terms of each element, high terms first
   static constexpr int kThreads = NT * 128 + 128;
   static constexpr int kTmemO = 256;                   // S of tile (or buffer) i at 128 i
   static constexpr int kNumS = 2;                      // tiles, or buffers of one tile
@@ -66,6 +75,14 @@ struct TcSmem {
   volatile int flags[C::kNT];          // of the item whose O is full: 1 bad, 2 fix
   volatile int abort_flag;
 };
+
+// Weights are 2^(score - m + kWeightExp) with m at most kLazy below the largest
+// score: at most 2^8 in bf16, 2^8.5 as E4M3 terms (largest 448), whose
+// absolute step of 2^-10 is then 2^-17 of a row's largest weight.
+template <bool FP8>
+constexpr float lazy_bound() { return FP8 ? 1.5f : 8.f; }
+template <bool FP8>
+constexpr float weight_exp() { return FP8 ? 7.f : 0.f; }
 
 enum : int { kItemBad = 1, kItemFix = 2 };
 
@@ -107,6 +124,7 @@ struct Ring {
 
 // Adds the values that preparation took out to the output columns [c0, c0 + 32)
 // of a row at `pos`: they are not finite, so neither is the result.
+template <bool FP8>
 __device__ __forceinline__ void add_taken_values(const PrefillArgs& a, const PfItem& it, int head_dim, int pos, int c0,
                                                  float (&o)[32]) {
   const int first = max(it.lo_exact, it.lo + it.kb0 * kPfBlock);
@@ -118,24 +136,53 @@ __device__ __forceinline__ void add_taken_values(const PrefillArgs& a, const PfI
     if (t > pos || (a.window > 0 && t <= pos - a.window)) continue;
     const int page = a.block_tables[static_cast<long long>(it.b) * a.max_blocks + t / kPfPage];
     if (page < 0 || page >= a.num_blocks) continue;
-    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v_cache) +
-                             ((static_cast<long long>(page) * kPfPage + t % kPfPage) * a.num_kv_heads + it.head) *
-                                 head_dim + c0;
+    const long long at = ((static_cast<long long>(page) * kPfPage + t % kPfPage) * a.num_kv_heads + it.head) *
+                             head_dim + c0;
+    if constexpr (FP8) {
+      const uint8_t* v = static_cast<const uint8_t*>(a.v_cache) + at;
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(v + c);
-      if ((w & 0x7f80u) == 0x7f80u) o[c] += bf16_lo_f(w);
-      if ((w & 0x7f800000u) == 0x7f800000u) o[c + 1] += bf16_hi_f(w);
+      for (int c = 0; c < 32; ++c)
+        if ((v[c] & 0x7f) == 0x7f) o[c] = CUDART_NAN_F;
+    } else {
+      const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v_cache) + at;
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(v + c);
+        if ((w & 0x7f80u) == 0x7f80u) o[c] += bf16_lo_f(w);
+        if ((w & 0x7f800000u) == 0x7f800000u) o[c + 1] += bf16_hi_f(w);
+      }
     }
   }
 }
 
-// Non-finite bf16 halves of a word: 0xffff in their place.
-__device__ __forceinline__ uint32_t not_finite_bf16x2(uint32_t w) {
+// All ones in the place of a word's elements that are not finite.
+template <bool FP8>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   uint32_t m = 0;
+  if constexpr (FP8) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+      if (((w >> i) & 0x7fu) == 0x7fu) m |= 0xffu << i;
+    return m;
+  }
   if ((w & 0x7f80u) == 0x7f80u) m |= 0xffffu;
   if ((w & 0x7f800000u) == 0x7f800000u) m |= 0xffff0000u;
   return m;
+}
+
+// Two floats as E4M3 terms, hi + lo: lo is the rest that hi leaves, itself
+// rounded, so together they keep 8 significant bits (and 2^-10 absolutely).
+// The rest is taken in f16, whose 11 bits hold it exactly.
+__device__ __forceinline__ void e4m3x2_terms(float x, float y, uint32_t& hi, uint32_t& lo) {
+  uint32_t h, back, rest;
+  uint16_t a, b;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(h));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(a));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(back));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b) : "r"(rest));
+  hi = a;
+  lo = b;
 }
 
 template <typename C>
@@ -144,6 +191,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ PrefillArgs a) {
   constexpr int D = C::kD, NT = C::kNT, DV = C::kDV, CW = C::kCW, NS = C::kStages;
   constexpr int NKC = C::kKChunks, NVC = C::kVChunks;
+  constexpr bool FP8 = C::kFp8;
+  constexpr int ROW = C::kRow, KS = C::kKStep;
+  constexpr float kLazy = lazy_bound<FP8>(), kWeightExp = weight_exp<FP8>();
   extern __shared__ unsigned char raw[];
   TcSmem<C>& s = *reinterpret_cast<TcSmem<C>*>(
       raw + ((1024 - (static_cast<uint32_t>(__cvta_generic_to_shared(raw)) & 1023)) & 1023));
@@ -160,7 +210,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       mbar_init(&s.vready[i], 1);
     }
     for (int i = 0; i < NT; ++i) {
-      mbar_init(&s.q_full[i], 1);
+      mbar_init(&s.q_full[i], FP8 ? 128 : 1);
       mbar_init(&s.q_empty[i], 1);
       mbar_init(&s.o_full[i], 2);  // the commit, and the issuer's flags
       mbar_init(&s.o_free[i], 128);
@@ -210,7 +260,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           ids = at < a.max_blocks ? a.block_tables[static_cast<long long>(item_b) * a.max_blocks + at] : 0;
         }
         int page = __shfl_sync(0xffffffffu, ids, p0 - ids_at + (lane & 3));
-        const bool use = (lane & 3) < pages && lane < 4 * (CW / 64);
+        const bool use = (lane & 3) < pages && lane < 4 * C::kBlocks;
         const bool bad = use && (page < 0 || page >= a.num_blocks);
         const bool any_bad = __any_sync(0xffffffffu, bad);
         if (bad) page = 0;
@@ -220,12 +270,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           if (!live) break;
           if (lane == 0) {
             s.stage_bad[r.stage] = any_bad;
-            mbar_arrive_expect_tx(&s.full[r.stage], pages * (CW / 64) * kPfPage * 128);
+            mbar_arrive_expect_tx(&s.full[r.stage], pages * C::kBlocks * kPfPage * ROW);
           }
           __syncwarp();
           if (use)
-            tma_load_4d(s.ring[r.stage] + (lane >> 2) * C::kBlockBytes + (lane & 3) * kPfPage * 128, map, 0,
-                        page * kPfPage, chunk0 + c * (CW / 64) + (lane >> 2), head, &s.full[r.stage]);
+            tma_load_4d(s.ring[r.stage] + (lane >> 2) * C::kBlockBytes + (lane & 3) * kPfPage * ROW, map, 0,
+                        page * kPfPage, chunk0 + c * C::kBlocks + (lane >> 2), head, &s.full[r.stage]);
           ++issued;
           r.next();
         }
@@ -233,7 +283,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       while (live && w.next(a, it)) {
         if (it.kb1 <= it.kb0) continue;
         ids_at = -1;
-        for (int t = 0; t < NT && live; ++t) {
+        for (int t = 0; t < NT && live && !FP8; ++t) {
           const TileSpan sp = tile_span(a, it, t, tile_toks);
           if (sp.je <= sp.jb) continue;
           live = wait_phase(&s.q_empty[t], (nq[t] & 1u) ^ 1u, &s.abort_flag, a.status, kStatusEmpty, a.wait_limit);
@@ -251,7 +301,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                   : "memory");
           }
         }
-        const int vc0 = it.part * (DV / 64);
+        const int vc0 = it.part * (DV / C::kCols);
         for (int j = it.kb0; j < it.kb1 && live; ++j) {
           if (static_cast<int>(blockIdx.x) == a.withhold_cta && blocks >= a.withhold_block) {
             live = false;  // test hook: the issuer's wait for this block runs out
@@ -287,8 +337,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       uint32_t nq[NT] = {}, np[C::kNumS] = {}, no[NT] = {};
       uint32_t vphase = 0;  // one bit a stage
       bool live = true;
-      const uint32_t idesc_qk = umma_idesc_f16(true, kPfBlock, false) | (a.neg_scale ? kUmmaNegateA : 0u);
-      const uint32_t idesc_pv = umma_idesc_f16(true, CW, true);
+      const uint32_t idesc_qk = FP8 ? umma_idesc_e4m3(kPfBlock, false)
+                                    : umma_idesc_f16(true, kPfBlock, false) | (a.neg_scale ? kUmmaNegateA : 0u);
+      const uint32_t idesc_pv = FP8 ? umma_idesc_e4m3(CW, true) : umma_idesc_f16(true, CW, true);
       auto wait = [&](unsigned long long* bar, uint32_t parity, unsigned code) {
         if (live) live = wait_phase(bar, parity, &s.abort_flag, a.status, code, a.wait_limit);
         return live;
@@ -297,20 +348,27 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       auto qk = [&](int t, int buf, int c, int stage) {
         if (lane != 0) return;
         const uint32_t qa = smem_addr(s.q[t]), kb = smem_addr(s.ring[stage]);
+        constexpr int kSteps = ROW / 32;  // MMAs of a block's columns
 #pragma unroll
-        for (int k = 0; k < CW / 16; ++k) {
-          const int col = c * CW + k * 16;
-          umma_ss<false>(tmem + buf * 128, umma_desc(qa + (col / 64) * 128 * 128 + (col % 64) * 2, 16, 1024, 2),
-                         umma_desc(kb + (k / 4) * C::kBlockBytes + (k % 4) * 32, 16, 1024, 2), idesc_qk, c > 0 || k > 0);
-        }
+        for (int term = 0; term < (FP8 ? 2 : 1); ++term)
+#pragma unroll
+          for (int k = 0; k < C::kBlocks * kSteps; ++k) {
+            const uint32_t at = (k / kSteps) * C::kBlockBytes + (k % kSteps) * 32;
+            umma_ss<FP8>(tmem + buf * 128,
+                         umma_desc(qa + term * (128 * D) + c * C::kStageBytes + at, 16, 8 * ROW, C::kSwizzle),
+                         umma_desc(kb + at, 16, 8 * ROW, C::kSwizzle), idesc_qk, c > 0 || term > 0 || k > 0);
+          }
       };
-      // O_t chunk c (+)= P(buf) x V chunk in the stage, over ksteps of 16 keys
+      // O_t chunk c (+)= P(buf) x V chunk in the stage, over ksteps of KS keys
       auto pv = [&](int t, int buf, int c, int stage, int ksteps, bool acc) {
         if (lane != 0) return;
         const uint32_t vb = smem_addr(s.ring[stage]);
-        for (int k = 0; k < ksteps; ++k)
-          umma_ts<false>(tmem + C::kTmemO + t * DV + c * CW, tmem + buf * 128 + k * 8,
-                         umma_desc(vb + k * 16 * 128, C::kBlockBytes, 1024, 2), idesc_pv, acc || k > 0);
+        const uint32_t d = tmem + C::kTmemO + t * DV + c * CW, p = tmem + buf * 128;
+        for (int k = 0; k < ksteps; ++k) {
+          const uint64_t v = umma_desc(vb + k * KS * ROW, C::kBlockBytes, 8 * ROW, C::kSwizzle);
+          umma_ts<FP8>(d, p + k * 8, v, idesc_pv, acc || k > 0);
+          if constexpr (FP8) umma_ts<FP8>(d, p + 32 + k * 8, v, idesc_pv, true);  // P's low terms
+        }
       };
       while (live && w.next(a, it)) {
         if (it.kb1 <= it.kb0) continue;
@@ -347,7 +405,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         };
         auto keys_to = [&](int t, int j) {  // k-steps of block j that tile t's rows need
           const int n = it.pos0 + sp[t].tok0 + sp[t].ntok - (it.lo + j * kPfBlock);
-          return (min(n, kPfBlock) + 15) / 16;
+          return (min(n, kPfBlock) + KS - 1) / KS;
         };
         if constexpr (NT == 2) {
           Ring<NS> k = r;  // K of block j + 1
@@ -470,25 +528,26 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           if (!live) break;
           ++ngo;
           const int k0 = it.lo + j * kPfBlock;
-          const int end = min(kPfBlock, (it.hi - k0 + 15) / 16 * 16);  // slots the products read
+          const int end = min(kPfBlock, (it.hi - k0 + KS - 1) / KS * KS);  // slots the products read
           for (int c = 0; c < NVC && live; ++c) {
             live = wait_phase(&s.full[r.stage], r.phase, &s.abort_flag, a.status, kStatusFull, a.wait_limit);
             live = __all_sync(0xffffffffu, live);
             if (!live) break;
             bool fix = false;
-            for (int i = lane; i < end * 8; i += 32) {  // a 16-byte piece of a slot's 128-byte row
-              const int slot = i >> 3, t = k0 + slot;
+            constexpr int kPieces = ROW / 16;
+            for (int i = lane; i < end * kPieces; i += 32) {  // a 16-byte piece of a slot's row
+              const int slot = i / kPieces, t = k0 + slot;
               const bool none = t < it.lo_exact || t >= it.hi;
               const bool all = t <= it.pos0 && (a.window == 0 || t >= it.hi - a.window);
               if (all && !none) continue;
-              for (int cb = 0; cb < CW / 64; ++cb) {
-                uint4* p = reinterpret_cast<uint4*>(s.ring[r.stage] + cb * C::kBlockBytes + slot * 128 + (i & 7) * 16);
+              for (int cb = 0; cb < C::kBlocks; ++cb) {
+                uint4* p = reinterpret_cast<uint4*>(s.ring[r.stage] + cb * C::kBlockBytes + i * 16);
                 if (none) {
                   *p = make_uint4(0, 0, 0, 0);
                 } else {
                   uint4 x = *p;
-                  const uint32_t m0 = not_finite_bf16x2(x.x), m1 = not_finite_bf16x2(x.y),
-                                 m2 = not_finite_bf16x2(x.z), m3 = not_finite_bf16x2(x.w);
+                  const uint32_t m0 = not_finite<FP8>(x.x), m1 = not_finite<FP8>(x.y), m2 = not_finite<FP8>(x.z),
+                                 m3 = not_finite<FP8>(x.w);
                   if (m0 | m1 | m2 | m3) {
                     fix = true;
                     x.x &= ~m0, x.y &= ~m1, x.z &= ~m2, x.w &= ~m3;
@@ -524,6 +583,58 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const bool valid = tok < tile_toks && tok < sp.ntok;
       const int pos = it.pos0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1);
       float m = -CUDART_INF_F, l = 0.f;
+      float scale = a.scale_log2;  // from a score in tensor memory to the log2 domain
+      if constexpr (FP8) {
+        // This row of Q as two E4M3 terms in the layout TMA gives K.  (The
+        // previous item's last scores are here, so its Q is done with.)
+        if (sp.je > sp.jb) {
+          const float ks = a.k_scale[it.head] * (a.neg_scale ? -1.f : 1.f);
+          const uint4* src = reinterpret_cast<const uint4*>(
+              static_cast<const __nv_bfloat16*>(a.q) +
+              (static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads + it.head * a.group + g) * D);
+          uint32_t most = 0;  // largest magnitude, as bf16 bits
+          if (valid) {
+#pragma unroll 8
+            for (int i = 0; i < D / 8; ++i) {
+              const uint4 x = src[i];
+              most = __vmaxu2(most, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                             __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+            }
+          }
+          most = max(most & 0xffffu, most >> 16);
+          // the largest magnitude goes to [2^7, 2^8); rows below 2^-100 count as zero
+          const int e = min(max(static_cast<int>(most >> 7) - 127, -100), 127);
+          const float up = pow2f(7 - max(e, -119));
+          scale = a.scale_log2 * fabsf(ks) * pow2f(max(e, -119) - 7);
+          if (scale == 0.f) scale = 1e-37f;
+          const float mul = ks < 0.f ? -up : up;
+#pragma unroll 2
+          for (int i = 0; i < D / 16; ++i) {
+            uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+            if (valid) {
+              x0 = src[2 * i];
+              x1 = src[2 * i + 1];
+            }
+            const uint32_t in[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t h0, h1, l0, l1;
+              e4m3x2_terms(bf16_lo_f(in[2 * k]) * mul, bf16_hi_f(in[2 * k]) * mul, h0, l0);
+              e4m3x2_terms(bf16_lo_f(in[2 * k + 1]) * mul, bf16_hi_f(in[2 * k + 1]) * mul, h1, l1);
+              hi[k] = h0 | (h1 << 16);
+              lo[k] = l0 | (l1 << 16);
+            }
+            const int blk = i / (ROW / 16), ch = i % (ROW / 16);
+            const int swz = ROW == 128 ? (ch ^ (row & 7)) : (ch ^ ((row >> 1) & 3));
+            unsigned char* dst = s.q[t] + blk * C::kBlockBytes + row * ROW + swz * 16;
+            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(dst + 128 * D) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+          fence_proxy_async_shared();
+          mbar_arrive(&s.q_full[t]);
+        }
+      }
       for (int j = sp.jb; j < sp.je; ++j) {
         const int buf = NT == 2 ? t : static_cast<int>(blocks & 1u);
         const uint32_t tS = tmem + lane_base + buf * 128;
@@ -552,8 +663,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           top0 = fmaxf(top0, x[c]);
           top1 = fmaxf(top1, x[c + 1]);
         }
-        const float top = fmaxf(top0, top1) * a.scale_log2;
-        if (__any_sync(0xffffffffu, top > m + 8.f)) {
+        const float top = fmaxf(top0, top1) * scale;
+        if (__any_sync(0xffffffffu, top > m + kLazy)) {
           const float mn = fmaxf(m, top);
           const float keep = m == -CUDART_INF_F ? 0.f : ex2(m - mn);
           if (j > sp.jb) {
@@ -578,20 +689,38 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           l *= keep;
           m = mn;
         }
-        const float mb = m == -CUDART_INF_F ? 0.f : m;
+        const float mb = (m == -CUDART_INF_F ? 0.f : m) - kWeightExp;
         float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t p[32];
+        if constexpr (FP8) {
+          uint32_t hi[32], lo[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float p0 = ex2(fmaf(x[64 * h + 2 * e], a.scale_log2, -mb));
-            const float p1 = ex2(fmaf(x[64 * h + 2 * e + 1], a.scale_log2, -mb));
-            sum0 += p0;
-            sum1 += p1;
-            p[e] = pack_bf16(p0, p1);
+            const float p0 = ex2(fmaf(x[4 * e], scale, -mb)), p1 = ex2(fmaf(x[4 * e + 1], scale, -mb));
+            const float p2 = ex2(fmaf(x[4 * e + 2], scale, -mb)), p3 = ex2(fmaf(x[4 * e + 3], scale, -mb));
+            sum0 += p0 + p2;
+            sum1 += p1 + p3;
+            uint32_t h0, h1, l0, l1;
+            e4m3x2_terms(p0, p1, h0, l0);
+            e4m3x2_terms(p2, p3, h1, l1);
+            hi[e] = h0 | (h1 << 16);
+            lo[e] = l0 | (l1 << 16);
           }
-          tmem_st32(tS + 32 * h, p);
+          tmem_st32(tS, hi);
+          tmem_st32(tS + 32, lo);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t p[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float p0 = ex2(fmaf(x[64 * h + 2 * e], scale, -mb));
+              const float p1 = ex2(fmaf(x[64 * h + 2 * e + 1], scale, -mb));
+              sum0 += p0;
+              sum1 += p1;
+              p[e] = pack_bf16(p0, p1);
+            }
+            tmem_st32(tS + 32 * h, p);
+          }
         }
         l += sum0 + sum1;
         tmem_wait_st();
@@ -616,7 +745,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         a.splits[blockIdx.x] = PrefillSplit{it.pieces, it.row0, it.ntok, it.head, it.part};
       const long long rec = (2ll * blockIdx.x + (it.kb0 > 0 ? 1 : 0)) * (NT * 128) + t * 128 + row;
       const bool bad = it.bad || (flags & kItemBad);
-      const float inv = bad ? CUDART_NAN_F : 1.f / l;
+      const float vs = FP8 ? a.v_scale[it.head] : 1.f;
+      const float inv = bad ? CUDART_NAN_F : vs / l;
       const uint32_t tO = tmem + lane_base + C::kTmemO + t * DV;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
                            (static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads + it.head * a.group + g) *
@@ -629,7 +759,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
           tmem_wait_ld();
           if (flags & kItemFix) {
-            add_taken_values(a, it, D, pos, it.part * DV + c, o);
+            add_taken_values<FP8>(a, it, D, pos, it.part * DV + c, o);
             __syncwarp();
           }
         } else {
@@ -639,7 +769,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (valid && split && l != 0.f) {  // (the combine reads no sums of a row without weight)
           float4* p = reinterpret_cast<float4*>(a.part + rec * DV + c);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int e = 0; e < 8; ++e) p[e] = make_float4(o[4 * e] * vs, o[4 * e + 1] * vs, o[4 * e + 2] * vs, o[4 * e + 3] * vs);
         } else if (valid && !split) {
           uint4* p = reinterpret_cast<uint4*>(dst + c);
 #pragma unroll

@@ -24,6 +24,7 @@ struct PrefillVariant {
 // nullptr: not taken.
 const PrefillVariant* prefill_simt_variant(int head_dim);  // fp32
 const PrefillVariant* prefill_bf16_variant(int head_dim);
+const PrefillVariant* prefill_e4m3_variant(int head_dim);
 
 // Joins the pieces of split items (see prefill_plan.cuh).  dtype_out: 0 bf16, 1 fp32.
 cudaError_t launch_prefill_combine(const PrefillArgs& a, int grid, int rows, int tile_rows, int cols, int head_dim,

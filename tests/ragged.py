@@ -86,12 +86,14 @@ def make_batch(new, ctx, q_heads, kv_heads, head_dim, dtype="bf16", seed=0, pad=
                  *(s.to(device) for s in scales))
 
 
-def attention(batch: Batch, scale, window=0):
+def attention(batch: Batch, scale, window=0, flat=False):
     """(out, weight) float64 [T][Hq][D]: softmax attention row by row of the
-    definition, and sum_t p_t |v_t|, what an error in the weights can move."""
+    definition, and sum_t p_t |v_t|, what a relative error in the weights can
+    move; with `flat` also max_t p_t sum_t |v_t|, what an absolute one can."""
     T, Hq, D = batch.q.shape
     out = torch.full((T, Hq, D), float("nan"), dtype=torch.float64, device=batch.q.device)
     reach = out.clone()
+    even = out.clone()
     ks, vs, st = batch.dense("k"), batch.dense("v"), batch.starts
     for b, (n, L) in enumerate(zip(batch.new, batch.ctx)):
         if n == 0:
@@ -110,7 +112,9 @@ def attention(batch: Batch, scale, window=0):
             p = p / p.sum(-1, keepdim=True)
             out[st[b]:st[b + 1], h] = p @ v
             reach[st[b]:st[b + 1], h] = p @ v.abs()
-    return out, reach
+            if flat:
+                even[st[b]:st[b + 1], h] = p.amax(-1, keepdim=True) * (seen.double() @ v.abs())
+    return (out, reach, even) if flat else (out, reach)
 
 
 def rotate(x, positions, inv_freq, interleaved, amplitude):
