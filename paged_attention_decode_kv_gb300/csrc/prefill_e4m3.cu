@@ -8,9 +8,9 @@ namespace vt {
 
 const PrefillVariant* prefill_e4m3_variant(int head_dim) {
   static const PrefillVariant table[] = {
-      TcVariant<TcConfig<true, 64, 2, 64, 64, 12>>::info(),
-      TcVariant<TcConfig<true, 128, 2, 128, 128, 10>>::info(),
-      TcVariant<TcConfig<true, 256, 1, 256, 128, 10>>::info(),
+      TcVariant<TcConfig<true, 64, 2, 64, 64, 6, 128, 6>>::info(),
+      TcVariant<TcConfig<true, 128, 2, 128, 128, 5, 128, 5>>::info(),
+      TcVariant<TcConfig<true, 256, 1, 256, 128, 5, 64, 4>>::info(),
   };
   return head_dim == 64 ? &table[0] : head_dim == 128 ? &table[1] : head_dim == 256 ? &table[2] : nullptr;
 }

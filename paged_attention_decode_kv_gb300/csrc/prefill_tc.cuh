@@ -11,13 +11,16 @@
 // 2^8 (weights then stay below 2^8, sums below 2^8 n, and the quotient is
 // the same), so O is rescaled a few times an item and not once a block.
 //
-// Roles, one warp each: loader (Q tiles, and K and V pages through the block
-// table, TMA into a ring of stages), MMA issuer, V preparation (below); and
-// one warpgroup of softmax threads a tile.  With two tiles (head_dim 64 and
-// 128) the issuer alternates them, P V and the next Q K^T of one tile running
-// while the other's softmax does; with one (head_dim 256 and 512, whose O
-// takes half of tensor memory) S is double-buffered and the next block's
-// Q K^T runs during the softmax.
+// Roles: one warp loads (walks the CTA's share, passes its items on through a
+// queue, and fetches Q tiles and K and V pages by TMA into two rings of
+// stages), two issue MMAs, one prepares V (below); one warpgroup of softmax
+// threads a tile.  With two tiles (head_dim 64 and 128) each has an issuer of
+// its own, and one tile's products run while the other's softmax does: an
+// issuing thread needs 50 to 70 cycles for an MMA of 64, so one thread for
+// both left the tensor cores idle half of the time (8192-token prompt, 32 q /
+// 8 kv heads, head_dim 128: 758 us with one issuer).  With one tile (head_dim
+// 256 and 512, whose O takes half of tensor memory) S is double-buffered, one
+// warp issues Q K^T, a block ahead, and the other P V.
 //
 // V preparation: in blocks that some row of the item may see only in part,
 // slots outside the item's keys are zeroed (0 * NaN is NaN, whatever P is),
@@ -33,7 +36,7 @@
 
 namespace vt {
 
-template <bool FP8, int D, int NT, int DV, int CW, int NS>
+template <bool FP8, int D, int NT, int DV, int KCW, int NSK, int VK, int NSV>
 struct TcConfig {
   static constexpr bool kFp8 = FP8;                    // E4M3 codes in the cache, else bf16
   static constexpr int kD = D, kNT = NT, kDV = DV;
@@ -44,35 +47,41 @@ struct TcConfig {
   static constexpr int kRow = kCols * kElem;
   static constexpr uint32_t kSwizzle = kRow == 128 ? 2 : 4;
   static constexpr int kKStep = 32 / kElem;            // k extent of an MMA
-  static constexpr int kCW = CW;                       // columns of a stage
-  static constexpr int kStages = NS;
-  static constexpr int kKChunks = D / CW, kVChunks = DV / CW;
-  static constexpr int kBlocks = CW / kCols;           // swizzled blocks of a stage
-  static constexpr int kBlockBytes = kPfBlock * kRow;
-  static constexpr int kStageBytes = kBlocks * kBlockBytes;
+  // A K stage: 128 keys x KCW columns.  A V stage: VK keys x all DV columns,
+  // so that an MMA of P V is as wide as O (one MMA, not several narrow ones).
+  static constexpr int kStagesK = NSK, kStagesV = NSV, kVK = VK;
+  static constexpr int kKBlocks = KCW / kCols, kVBlocks = DV / kCols;  // swizzled blocks of a stage
+  static constexpr int kKChunks = D / KCW;             // K stages of a block of keys
+  static constexpr int kKBlockBytes = kPfBlock * kRow, kVBlockBytes = VK * kRow;
+  static constexpr int kKBytes = kKBlocks * kKBlockBytes, kVBytes = kVBlocks * kVBlockBytes;
   static constexpr int kQBytes = 128 * D * 2;          // FP8: two E4M3 terms of each element, high terms first
   static constexpr int kThreads = NT * 128 + 128;
   static constexpr int kTmemO = 256;                   // S of tile (or buffer) i at 128 i
   static constexpr int kNumS = 2;                      // tiles, or buffers of one tile
+  static constexpr int kItems = 4;                     // queue of items
+  static_assert(VK == 128 || VK == 64 || VK == 32, "whole pages, whole halves of a block");
+  static_assert(4 * kKBlocks <= 32 && VK / kPfPage * kVBlocks <= 32, "a lane for each box of a stage");
 };
 
 template <typename C>
 struct TcSmem {
   alignas(1024) unsigned char q[C::kNT][C::kQBytes];
-  alignas(1024) unsigned char ring[C::kStages][C::kStageBytes];
-  alignas(8) unsigned long long full[C::kStages];
-  unsigned long long empty[C::kStages];
-  unsigned long long vready[C::kStages];
+  alignas(1024) unsigned char k[C::kStagesK][C::kKBytes];
+  alignas(1024) unsigned char v[C::kStagesV][C::kVBytes];
+  alignas(8) unsigned long long k_full[C::kStagesK], k_empty[C::kStagesK];
+  unsigned long long v_full[C::kStagesV], v_empty[C::kStagesV], v_ready[C::kStagesV];
   unsigned long long q_full[C::kNT], q_empty[C::kNT];
-  unsigned long long s_full[C::kNumS], p_ready[C::kNumS];
+  unsigned long long s_full[C::kNumS], s_free[C::kNumS];  // s_free: one tile only
+  unsigned long long p_ready[2][C::kNumS];                // weights of the block's first and second 64 keys
   unsigned long long o_full[C::kNT], o_free[C::kNT];
-  unsigned long long prep_go;
-  unsigned long long pv_done, drain;
+  unsigned long long item_full[C::kItems], item_empty[C::kItems];
+  unsigned long long drain[2];
   long long scan[C::kThreads / 32 + 4];
+  PfItem items[C::kItems];
   uint32_t tmem;
-  volatile int stage_bad[C::kStages];  // a page id of this stage was out of range
-  volatile int stage_fix[C::kStages];  // V preparation took out a value that is not finite
-  volatile int flags[C::kNT];          // of the item whose O is full: 1 bad, 2 fix
+  volatile int stage_bad[C::kStagesV];  // a page id of this stage was out of range
+  volatile int stage_fix[C::kStagesV];  // V preparation took out a value that is not finite
+  volatile int flags[C::kNT];           // of the item whose O is full
   volatile int abort_flag;
 };
 
@@ -109,13 +118,19 @@ __device__ __forceinline__ bool needs_prep(const PrefillArgs& a, const PfItem& i
   return k0 + kPfBlock > it.pos0 + 1 || (a.window > 0 && k0 < it.hi - a.window);
 }
 
-// Position in the ring of stages.
-template <int NS>
+// V stages of block j.
+template <typename C>
+__device__ __forceinline__ int v_stages(const PfItem& it, int j) {
+  return (min(kPfBlock, it.hi - (it.lo + j * kPfBlock)) + C::kVK - 1) / C::kVK;
+}
+
+// Position in a ring of stages.
+template <int N>
 struct Ring {
   int stage = 0;
   uint32_t phase = 0;
   __device__ __forceinline__ void next() {
-    if (++stage == NS) {
+    if (++stage == N) {
       stage = 0;
       phase ^= 1u;
     }
@@ -185,43 +200,656 @@ __device__ __forceinline__ void e4m3x2_terms(float x, float y, uint32_t& hi, uin
   lo = b;
 }
 
+// a + b and a * b + c on pairs of floats.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 c, a, b;\n\t"
+      "mov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Everything a role needs besides its own state.
+template <typename C>
+struct TcRole {
+  const PrefillArgs& a;
+  TcSmem<C>& s;
+  int lane;
+  bool live = true;  // false once a bounded wait has given up; uniform over a warp
+
+  __device__ __forceinline__ bool wait(unsigned long long* bar, uint32_t parity, unsigned code) {
+    if (live) live = wait_phase(bar, parity & 1u, &s.abort_flag, a.status, code, a.wait_limit);
+    live = __all_sync(0xffffffffu, live);
+    return live;
+  }
+  // Item n of the CTA's share; false at the end.
+  __device__ __forceinline__ bool item(uint32_t n, PfItem& it) {
+    if (!wait(&s.item_full[n % C::kItems], n / C::kItems, kStatusSync)) return false;
+    it = s.items[n % C::kItems];
+    return it.b >= 0;
+  }
+  __device__ __forceinline__ void item_done(uint32_t n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.item_empty[n % C::kItems]);
+  }
+};
+
+// --------------------------------------------------------------------- loader
+template <typename C>
+__device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                          const PrefillArgs& a, TcSmem<C>& s, PfWalk& w, int lane) {
+  TcRole<C> role{a, s, lane};
+  Ring<C::kStagesK> rk;
+  Ring<C::kStagesV> rv;
+  uint32_t nq[C::kNT] = {}, items = 0;
+  long long nk = 0, nv = 0;
+  int blocks = 0;
+  const int tile_toks = 128 / a.group;
+  int ids = 0, ids_at = -1;  // 32 table entries, one a lane, from page index ids_at
+  PfItem it{};
+  // This lane's box of a stage whose first page is the item's page p0: page
+  // p0 + box % pages, column block box / pages.
+  auto page_of = [&](int p0, int i) {
+    if (ids_at < 0 || p0 < ids_at || p0 + 4 > ids_at + 32) {
+      ids_at = max(0, p0 - 4);  // K runs a block ahead of V
+      const int at = ids_at + lane;
+      ids = at < a.max_blocks ? a.block_tables[static_cast<long long>(it.b) * a.max_blocks + at] : 0;
+    }
+    return __shfl_sync(0xffffffffu, ids, p0 - ids_at + i);
+  };
+  auto load_k = [&](int j) {
+    const int k0 = it.lo + j * kPfBlock;
+    const int pages = min(kPfBlock, it.hi - k0 + kPfPage - 1) / kPfPage;  // those that hold keys of the item
+    int page = page_of(k0 / kPfPage, lane & 3);
+    const bool use = (lane & 3) < pages && lane < 4 * C::kKBlocks;
+    if (page < 0 || page >= a.num_blocks) page = 0;  // (load_v reports it)
+    for (int c = 0; c < C::kKChunks; ++c) {
+      if (!role.wait(&s.k_empty[rk.stage], rk.phase ^ 1u, kStatusEmpty)) return;
+      if (lane == 0) mbar_arrive_expect_tx(&s.k_full[rk.stage], pages * C::kKBlocks * kPfPage * C::kRow);
+      __syncwarp();
+      if (use)
+        tma_load_4d(s.k[rk.stage] + (lane >> 2) * C::kKBlockBytes + (lane & 3) * kPfPage * C::kRow, &tk, 0,
+                    page * kPfPage, c * C::kKBlocks + (lane >> 2), it.head, &s.k_full[rk.stage]);
+      ++nk;
+      rk.next();
+    }
+  };
+  auto load_v = [&](int j) {
+    constexpr int kPages = C::kVK / kPfPage;  // of a stage
+    const int stages = v_stages<C>(it, j);
+    for (int i = 0; i < stages; ++i) {
+      const int k0 = it.lo + j * kPfBlock + i * C::kVK;
+      const int pages = min(C::kVK, it.hi - k0 + kPfPage - 1) / kPfPage;
+      int page = page_of((it.lo + j * kPfBlock) / kPfPage, i * kPages + lane % kPages);
+      const bool use = lane % kPages < pages && lane < kPages * C::kVBlocks;
+      const bool bad = use && (page < 0 || page >= a.num_blocks);
+      const bool any_bad = __any_sync(0xffffffffu, bad);
+      if (bad) page = 0;
+      if (!role.wait(&s.v_empty[rv.stage], rv.phase ^ 1u, kStatusEmpty)) return;
+      if (lane == 0) {
+        s.stage_bad[rv.stage] = any_bad;
+        mbar_arrive_expect_tx(&s.v_full[rv.stage], pages * C::kVBlocks * kPfPage * C::kRow);
+      }
+      __syncwarp();
+      if (use)
+        tma_load_4d(s.v[rv.stage] + (lane / kPages) * C::kVBlockBytes + (lane % kPages) * kPfPage * C::kRow, &tv, 0,
+                    page * kPfPage, it.part * C::kVBlocks + lane / kPages, it.head, &s.v_full[rv.stage]);
+      ++nv;
+      rv.next();
+    }
+  };
+  while (role.live) {
+    const bool more = w.next(a, it);
+    if (!role.wait(&s.item_empty[items % C::kItems], (items / C::kItems) ^ 1u, kStatusEmpty)) break;
+    if (!more) it.b = -1;
+    if (lane == 0) {
+      s.items[items % C::kItems] = it;
+      mbar_arrive(&s.item_full[items % C::kItems]);
+    }
+    __syncwarp();
+    ++items;
+    if (!more) break;
+    ids_at = -1;
+    for (int t = 0; t < C::kNT && !C::kFp8; ++t) {
+      const TileSpan sp = tile_span(a, it, t, tile_toks);
+      if (sp.je <= sp.jb) continue;
+      if (!role.wait(&s.q_empty[t], nq[t] ^ 1u, kStatusEmpty)) break;
+      ++nq[t];
+      if (lane == 0) mbar_arrive_expect_tx(&s.q_full[t], tile_toks * a.group * C::kD * 2);
+      __syncwarp();
+      if (lane < C::kD / 64)
+        asm volatile(
+            "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(s.q[t] + lane * 128 * 128)),
+            "l"(reinterpret_cast<uint64_t>(&tq)), "r"(0), "r"(0), "r"(it.row0 + sp.tok0), "r"(lane), "r"(it.head),
+            "r"(smem_addr(&s.q_full[t]))
+            : "memory");
+    }
+    for (int j = it.kb0; j < it.kb1 && role.live; ++j) {
+      if (static_cast<int>(blockIdx.x) == a.withhold_cta && blocks >= a.withhold_block) {
+        role.live = false;  // test hook: an issuer's wait for this block runs out
+        break;
+      }
+      ++blocks;
+      if (j == it.kb0) load_k(j);
+      if (role.live && j + 1 < it.kb1) load_k(j + 1);
+      if (role.live) load_v(j);
+    }
+  }
+  if (!role.live) {
+    // let this CTA's copies land before it exits
+    volatile int never = 0;
+    auto drain = [&](unsigned long long* bars, long long n, int stages) {
+      for (long long k = 1; k <= (n < stages ? n : stages); ++k)
+        if (!wait_phase(&bars[(n - k) % stages], static_cast<uint32_t>(((n - k) / stages) & 1), &never, a.status,
+                        kStatusDrain, kDrainLimitCycles))
+          break;
+    };
+    drain(s.k_full, nk, C::kStagesK);
+    drain(s.v_full, nv, C::kStagesV);
+    for (int t = 0; t < C::kNT; ++t)
+      if (nq[t])
+        wait_phase(&s.q_full[t], (nq[t] - 1) & 1u, &never, a.status, kStatusDrain, kDrainLimitCycles);
+  }
+}
+
+// --------------------------------------------------------------------- MMA issue
+// With two tiles, issuer `who` owns tile `who`: Q K^T of block j + 1 follows
+// P V of block j on the same thread, which orders them (P lies over S).  With
+// one tile, issuer 0 runs Q K^T a block ahead into the other S buffer and
+// issuer 1 runs P V; s_free hands the buffers back.
+template <typename C>
+__device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, uint32_t tmem, int who, int lane) {
+  constexpr int NT = C::kNT, KS = C::kKStep, ROW = C::kRow;
+  constexpr bool FP8 = C::kFp8;
+  constexpr uint32_t kHi = umma_desc_hi(8 * ROW, C::kSwizzle);
+  constexpr int kHalf = kPfBlock / 2 / KS;  // k-steps of half a block
+  TcRole<C> role{a, s, lane};
+  Ring<C::kStagesK> rk;
+  Ring<C::kStagesV> rv;
+  uint32_t vphase = 0;  // of v_ready, one bit a stage
+  uint32_t items = 0, nq = 0, no = 0, np[2] = {};
+  uint32_t nblk = 0;    // one tile: blocks so far, whose parity is the buffer
+  const int t = NT == 2 ? who : 0;
+  const bool do_qk = NT == 2 || who == 0, do_pv = NT == 2 || who == 1;
+  const int tile_toks = 128 / a.group;
+  PfItem it{};
+
+  // S(buf) = Q K^T for block j's keys
+  auto qk = [&](int j, int buf, const TileSpan& sp) {
+    const bool active = j >= sp.jb && j < sp.je;
+    const int keys = min(kPfBlock, it.hi - (it.lo + j * kPfBlock));
+    const uint32_t idesc = (FP8 ? umma_idesc_e4m3(0, false)
+                                : umma_idesc_f16(true, 0, false) | (a.neg_scale ? kUmmaNegateA : 0u)) |
+                           (static_cast<uint32_t>((keys + 15) / 16 * 2) << 17);
+    for (int c = 0; c < C::kKChunks; ++c) {
+      if (!role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) return;
+      tc_fence_after();
+      const uint32_t qa = umma_desc_lo(smem_addr(s.q[t]) + c * C::kKBytes, 16);
+      const uint32_t kb = umma_desc_lo(smem_addr(s.k[rk.stage]), 16);
+      const uint32_t d = tmem + buf * 128, more = c > 0;
+      if (elect_one()) {
+        if (active) {
+          constexpr int kSteps = ROW / 32;  // MMAs of a block's columns
+#pragma unroll
+          for (int term = 0; term < (FP8 ? 2 : 1); ++term)
+#pragma unroll
+            for (int k = 0; k < C::kKBlocks * kSteps; ++k) {
+              const uint32_t at = ((k / kSteps) * C::kKBlockBytes + (k % kSteps) * 32) >> 4;
+              umma_ss<FP8>(d, qa + ((term * 128 * C::kD) >> 4) + at, kHi, kb + at, kHi, idesc,
+                           term > 0 || k > 0 ? 1u : more);
+            }
+        }
+        umma_commit(&s.k_empty[rk.stage]);
+        if (active && c == C::kKChunks - 1) {
+          umma_commit(&s.s_full[buf]);
+          if (j == sp.je - 1) umma_commit(&s.q_empty[t]);
+        }
+      }
+      __syncwarp();
+      rk.next();
+    }
+  };
+  // O (+)= P(buf) V for block j's keys; adds to `flags`
+  auto pv = [&](int j, int buf, const TileSpan& sp, int& flags) {
+    const bool active = j >= sp.jb && j < sp.je;
+    const bool prepared = needs_prep(a, it, j);
+    const int stages = v_stages<C>(it, j);
+    const int n = it.pos0 + sp.tok0 + sp.ntok - (it.lo + j * kPfBlock);
+    const int steps = active ? (min(n, kPfBlock) + KS - 1) / KS : 0;  // that the tile's rows need
+    const uint32_t idesc = FP8 ? umma_idesc_e4m3(C::kDV, true) : umma_idesc_f16(true, C::kDV, true);
+    const uint32_t d = tmem + C::kTmemO + t * C::kDV, p = tmem + buf * 128;
+    uint32_t acc = j > sp.jb;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (active) {
+        if (!role.wait(&s.p_ready[h][buf], np[buf], kStatusSync)) return;
+        if (h == 0 && j == sp.jb && !role.wait(&s.o_free[t], no ^ 1u, kStatusSync)) return;
+      }
+      constexpr int kPer = C::kVK == 128 ? 1 : 64 / C::kVK;  // stages of half a block (one stage holds both: 128)
+      constexpr int kSteps = C::kVK == 128 ? kHalf : C::kVK / KS;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int first = h * kHalf + i * kSteps;  // k-step of the block
+        if (C::kVK == 128 ? h == 0 : h * kPer + i < stages) {
+          if (!role.wait(&s.v_full[rv.stage], rv.phase, kStatusFull)) return;
+          if (prepared) {
+            if (!role.wait(&s.v_ready[rv.stage], vphase >> rv.stage, kStatusSync)) return;
+            vphase ^= 1u << rv.stage;
+            if (s.stage_fix[rv.stage]) flags |= kItemFix;
+          }
+          if (s.stage_bad[rv.stage]) flags |= kItemBad;
+        } else if (C::kVK != 128) {
+          continue;
+        }
+        tc_fence_after();
+        const uint32_t vb = umma_desc_lo(smem_addr(s.v[rv.stage]), C::kVBlockBytes) +
+                            (C::kVK == 128 ? (h * kHalf * KS * ROW) >> 4 : 0);
+        const bool last = C::kVK != 128 || h == 1;  // of the stage
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            if (first + k < steps) {
+              const uint32_t b = vb + ((k * KS * ROW) >> 4);
+              umma_ts<FP8>(d, p + (first + k) * 8, b, kHi, idesc, first + k > 0 ? 1u : acc);
+              if constexpr (FP8) umma_ts<FP8>(d, p + 32 + (first + k) * 8, b, kHi, idesc, 1u);  // P's low terms
+            }
+          }
+          if (last) umma_commit(&s.v_empty[rv.stage]);
+        }
+        __syncwarp();
+        if (last) rv.next();
+      }
+    }
+    if (active) {
+      ++np[buf];
+      if (elect_one()) {
+        if constexpr (NT == 1) umma_commit(&s.s_free[buf]);
+        if (j == sp.je - 1) {
+          s.flags[t] = flags;
+          umma_commit(&s.o_full[t]);
+          mbar_arrive(&s.o_full[t]);
+        }
+      }
+      __syncwarp();
+      if (j == sp.je - 1) ++no;
+    }
+  };
+
+  for (; role.item(items, it); ++items) {
+    if (it.kb1 > it.kb0) {
+      const TileSpan sp = tile_span(a, it, t, tile_toks);
+      int flags = 0;
+      if (do_qk && sp.je > sp.jb) {
+        if (!role.wait(&s.q_full[t], nq, kStatusFull)) break;
+        ++nq;
+      }
+      if constexpr (NT == 2) {
+        qk(it.kb0, t, sp);
+        for (int j = it.kb0; j < it.kb1 && role.live; ++j) {
+          pv(j, t, sp, flags);
+          if (role.live && j + 1 < it.kb1) qk(j + 1, t, sp);
+        }
+      } else {
+        for (int j = it.kb0; j < it.kb1 && role.live; ++j, ++nblk) {
+          const int buf = nblk & 1u;
+          if (do_qk) {
+            if (!role.wait(&s.s_free[buf], (nblk >> 1) ^ 1u, kStatusSync)) break;
+            qk(j, buf, sp);
+          }
+          if (do_pv) pv(j, buf, sp, flags);
+        }
+      }
+    }
+    if (!role.live) break;
+    role.item_done(items);
+  }
+  // every MMA has to be done before tensor memory is given back
+  __syncwarp();
+  if (elect_one()) umma_commit(&s.drain[who]);
+  __syncwarp();
+  volatile int never = 0;
+  wait_phase(&s.drain[who], 0, &never, a.status, kStatusDrain, kDrainLimitCycles);
+}
+
+// --------------------------------------------------------------------- V preparation
+template <typename C>
+__device__ __forceinline__ void tc_prepare(const PrefillArgs& a, TcSmem<C>& s, int lane) {
+  constexpr bool FP8 = C::kFp8;
+  constexpr int KS = C::kKStep;
+  TcRole<C> role{a, s, lane};
+  Ring<C::kStagesV> rv;
+  PfItem it{};
+  uint32_t items = 0;
+  for (; role.item(items, it); ++items) {
+    for (int j = it.kb0; j < it.kb1 && role.live; ++j) {
+      const bool prepare = needs_prep(a, it, j);
+      const int stages = v_stages<C>(it, j);
+      for (int i = 0; i < stages; ++i, rv.next()) {
+        // (stages are passed over in order too: a wait tells phases apart by parity only)
+        if (!role.wait(&s.v_full[rv.stage], rv.phase, kStatusFull)) break;
+        if (prepare) {
+          const int k0 = it.lo + j * kPfBlock + i * C::kVK;
+          const int end = min(C::kVK, (it.hi - k0 + KS - 1) / KS * KS);  // slots the products read
+          constexpr int kPieces = C::kRow / 16;
+          bool fix = false;
+          for (int p = lane; p < end * kPieces; p += 32) {  // a 16-byte piece of a slot's row
+            const int t = k0 + p / kPieces;
+            const bool none = t < it.lo_exact || t >= it.hi;
+            const bool all = t <= it.pos0 && (a.window == 0 || t >= it.hi - a.window);
+            if (all && !none) continue;
+            for (int cb = 0; cb < C::kVBlocks; ++cb) {
+              uint4* at = reinterpret_cast<uint4*>(s.v[rv.stage] + cb * C::kVBlockBytes + p * 16);
+              if (none) {
+                *at = make_uint4(0, 0, 0, 0);
+              } else {
+                uint4 x = *at;
+                const uint32_t m0 = not_finite<FP8>(x.x), m1 = not_finite<FP8>(x.y), m2 = not_finite<FP8>(x.z),
+                               m3 = not_finite<FP8>(x.w);
+                if (m0 | m1 | m2 | m3) {
+                  fix = true;
+                  x.x &= ~m0, x.y &= ~m1, x.z &= ~m2, x.w &= ~m3;
+                  *at = x;
+                }
+              }
+            }
+          }
+          fix = __any_sync(0xffffffffu, fix);
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            s.stage_fix[rv.stage] = fix;
+            mbar_arrive(&s.v_ready[rv.stage]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.v_empty[rv.stage]);
+      }
+    }
+    if (!role.live) break;
+    role.item_done(items);
+  }
+}
+
+// --------------------------------------------------------------------- softmax: one row a thread
+template <typename C>
+__device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, uint32_t tmem, int tid) {
+  constexpr int D = C::kD, NT = C::kNT, DV = C::kDV, ROW = C::kRow;
+  constexpr bool FP8 = C::kFp8;
+  constexpr float kLazy = lazy_bound<FP8>(), kWeightExp = weight_exp<FP8>();
+  const int warp = tid >> 5, lane = tid & 31;
+  const int tile_toks = 128 / a.group;
+  const int t = NT == 2 ? warp >> 2 : 0;
+  const int row = tid & 127;
+  const int tok = row / a.group, g = row - tok * a.group;
+  const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes a warp, lane in bits 16..
+  const uint32_t tO = tmem + lane_base + C::kTmemO + t * DV;
+  TcRole<C> role{a, s, lane};
+  PfItem it{};
+  uint32_t items = 0, no = 0;
+  uint32_t blocks = 0;  // of this tile; one tile: the parity is the buffer
+  for (; role.item(items, it); ++items) {
+    const TileSpan sp = tile_span(a, it, t, tile_toks);
+    const bool valid = tok < tile_toks && tok < sp.ntok;
+    const int pos = it.pos0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1);
+    float m = -CUDART_INF_F, l = 0.f;
+    float scale = a.scale_log2;  // from a score in tensor memory to the log2 domain
+    if constexpr (FP8) {
+      // This row of Q as two E4M3 terms in the layout TMA gives K.  (The
+      // previous item's last scores are here, so its Q is done with.)
+      if (sp.je > sp.jb) {
+        const float ks = a.k_scale[it.head] * (a.neg_scale ? -1.f : 1.f);
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(a.q) +
+            (static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads + it.head * a.group + g) * D);
+        uint32_t most = 0;  // largest magnitude, as bf16 bits
+        if (valid) {
+#pragma unroll 8
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 x = src[i];
+            most = __vmaxu2(most, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                           __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+          }
+        }
+        most = max(most & 0xffffu, most >> 16);
+        // the largest magnitude goes to [2^7, 2^8); rows below 2^-100 count as zero
+        const int e = min(max(static_cast<int>(most >> 7) - 127, -100), 127);
+        const float up = pow2f(7 - max(e, -119));
+        scale = a.scale_log2 * fabsf(ks) * pow2f(max(e, -119) - 7);
+        if (scale == 0.f) scale = 1e-37f;
+        const float mul = ks < 0.f ? -up : up;
+#pragma unroll 2
+        for (int i = 0; i < D / 16; ++i) {
+          uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+          if (valid) {
+            x0 = src[2 * i];
+            x1 = src[2 * i + 1];
+          }
+          const uint32_t in[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t h0, h1, l0, l1;
+            e4m3x2_terms(bf16_lo_f(in[2 * k]) * mul, bf16_hi_f(in[2 * k]) * mul, h0, l0);
+            e4m3x2_terms(bf16_lo_f(in[2 * k + 1]) * mul, bf16_hi_f(in[2 * k + 1]) * mul, h1, l1);
+            hi[k] = h0 | (h1 << 16);
+            lo[k] = l0 | (l1 << 16);
+          }
+          const int blk = i / (ROW / 16), ch = i % (ROW / 16);
+          const int swz = ROW == 128 ? (ch ^ (row & 7)) : (ch ^ ((row >> 1) & 3));
+          unsigned char* dst = s.q[t] + blk * C::kKBlockBytes + row * ROW + swz * 16;
+          *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(dst + 128 * D) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async_shared();
+        mbar_arrive(&s.q_full[t]);
+      }
+    }
+    for (int j = sp.jb; j < sp.je; ++j, ++blocks) {
+      const int buf = NT == 2 ? t : static_cast<int>(blocks & 1u);
+      const uint32_t tS = tmem + lane_base + buf * 128;
+      if (!role.wait(&s.s_full[buf], NT == 2 ? blocks : blocks >> 1, kStatusSync)) break;
+      tc_fence_after();
+      float x[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
+      tmem_wait_ld();
+      const int k0 = it.lo + j * kPfBlock;
+      // rows see keys (pos - window, pos]; block columns [from, upto]
+      const bool masked = k0 + kPfBlock > it.pos0 + sp.tok0 + 1 ||
+                          (a.window > 0 && k0 < it.pos0 + sp.tok0 + sp.ntok - a.window);
+      if (masked) {
+        const int upto = pos - k0, from = a.window > 0 ? pos - a.window + 1 - k0 : 0;
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c > upto || c < from) x[c] = -CUDART_INF_F;
+      }
+      float top[4] = {x[0], x[1], x[2], x[3]};  // independent chains
+#pragma unroll
+      for (int c = 4; c < 124; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top[e] = max3(top[e], x[c + 2 * e], x[c + 2 * e + 1]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], x[124 + e]);
+      const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+      if (__any_sync(0xffffffffu, most > m + kLazy)) {
+        const float mn = fmaxf(m, most);
+        const float keep = m == -CUDART_INF_F ? 0.f : ex2(m - mn);
+        if (j > sp.jb) {
+          // The accumulator is still: two tiles, S came after this tile's
+          // earlier products on the same thread; one, they are waited for.
+          if constexpr (NT == 1) {
+            if (!role.wait(&s.s_free[buf ^ 1], (blocks - 1) >> 1, kStatusSync)) break;
+            tc_fence_after();
+          }
+#pragma unroll 1
+          for (int c = 0; c < DV; c += 32) {
+            float o[32];
+            tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= keep;
+            tmem_st32(tO + c, reinterpret_cast<const uint32_t*>(o));
+          }
+        }
+        l *= keep;
+        m = mn;
+      }
+      const float mb = kWeightExp - (m == -CUDART_INF_F ? 0.f : m);
+      const float2 scale2 = make_float2(scale, scale), mb2 = make_float2(mb, mb);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // weights of keys 64 h .. 64 h + 63; the issuer starts on the first half at once
+        uint32_t p[32];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float2 w[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int c = 64 * h + 4 * e + 2 * i;
+            w[i] = fma2(make_float2(x[c], x[c + 1]), scale2, mb2);
+            w[i].x = ex2(w[i].x);
+            w[i].y = ex2(w[i].y);
+            sum[i] = add2(sum[i], w[i]);
+          }
+          if constexpr (FP8) {
+            uint32_t h0, h1, l0, l1;
+            e4m3x2_terms(w[0].x, w[0].y, h0, l0);
+            e4m3x2_terms(w[1].x, w[1].y, h1, l1);
+            p[e] = h0 | (h1 << 16);
+            p[16 + e] = l0 | (l1 << 16);
+          } else {
+            p[2 * e] = pack_bf16(w[0].x, w[0].y);
+            p[2 * e + 1] = pack_bf16(w[1].x, w[1].y);
+          }
+        }
+        if constexpr (FP8) {
+          tmem_st16(tS + 16 * h, p);
+          tmem_st16(tS + 32 + 16 * h, p + 16);
+        } else {
+          tmem_st32(tS + 32 * h, p);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&s.p_ready[h][buf]);
+      }
+      const float2 both = add2(sum[0], sum[1]);
+      l += both.x + both.y;
+    }
+    if (!role.live) break;
+
+    const bool any = sp.je > sp.jb;  // O holds sums of this tile
+    int flags = 0;
+    if (any) {
+      if (!role.wait(&s.o_full[t], no, kStatusSync)) break;
+      ++no;
+      tc_fence_after();
+      flags = s.flags[t];
+    }
+    const bool split = it.kb0 > 0 || it.pieces > 0;
+    if (it.pieces > 0 && tid == 0)
+      a.splits[blockIdx.x] = PrefillSplit{it.pieces, it.row0, it.ntok, it.head, it.part};
+    const long long rec = (2ll * blockIdx.x + (it.kb0 > 0 ? 1 : 0)) * (NT * 128) + t * 128 + row;
+    const bool bad = it.bad || (flags & kItemBad);
+    const float vs = FP8 ? a.v_scale[it.head] : 1.f;
+    const float inv = bad ? CUDART_NAN_F : vs / l;
+    const uint32_t tO = tmem + lane_base + C::kTmemO + t * DV;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
+                         (static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads + it.head * a.group + g) *
+                             D + it.part * DV;
+    if (split && valid) a.ml[rec] = make_float2(bad ? CUDART_NAN_F : m, l);
+#pragma unroll 1
+    for (int c = 0; c < DV; c += 32) {
+      float o[32];
+      if (any) {
+        tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
+        tmem_wait_ld();
+        if (flags & kItemFix) {
+          add_taken_values<FP8>(a, it, D, pos, it.part * DV + c, o);
+          __syncwarp();
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+      }
+      if (valid && split && l != 0.f) {  // (the combine reads no sums of a row without weight)
+        float4* p = reinterpret_cast<float4*>(a.part + rec * DV + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = make_float4(o[4 * e] * vs, o[4 * e + 1] * vs, o[4 * e + 2] * vs, o[4 * e + 3] * vs);
+      } else if (valid && !split) {
+        uint4* p = reinterpret_cast<uint4*>(dst + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          p[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
+                            pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                            pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                            pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+      }
+      __syncwarp();  // the next load of tensor memory is the whole warp's
+    }
+    if (any) {
+      tc_fence_before();
+      mbar_arrive(&s.o_free[t]);
+    }
+    role.item_done(items);
+  }
+}
+
 template <typename C>
 __global__ void __launch_bounds__(C::kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ PrefillArgs a) {
-  constexpr int D = C::kD, NT = C::kNT, DV = C::kDV, CW = C::kCW, NS = C::kStages;
-  constexpr int NKC = C::kKChunks, NVC = C::kVChunks;
-  constexpr bool FP8 = C::kFp8;
-  constexpr int ROW = C::kRow, KS = C::kKStep;
-  constexpr float kLazy = lazy_bound<FP8>(), kWeightExp = weight_exp<FP8>();
+  constexpr int NT = C::kNT;
   extern __shared__ unsigned char raw[];
   TcSmem<C>& s = *reinterpret_cast<TcSmem<C>*>(
       raw + ((1024 - (static_cast<uint32_t>(__cvta_generic_to_shared(raw)) & 1023)) & 1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kLoader = NT * 4, kIssuer = kLoader + 1, kPrep = kLoader + 2;
-  const int tile_toks = 128 / a.group;
+  constexpr int kLoader = NT * 4, kIssuer = kLoader + 1, kPrep = kLoader + 3;
 
   if (tid == 0) {
     a.splits[blockIdx.x].pieces = 0;
     s.abort_flag = 0;
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], 1);
-      mbar_init(&s.vready[i], 1);
+    for (int i = 0; i < C::kStagesK; ++i) {
+      mbar_init(&s.k_full[i], 1);
+      mbar_init(&s.k_empty[i], NT);      // the issuers of Q K^T
+    }
+    for (int i = 0; i < C::kStagesV; ++i) {
+      mbar_init(&s.v_full[i], 1);
+      mbar_init(&s.v_empty[i], NT + 1);  // the issuers of P V, and preparation
+      mbar_init(&s.v_ready[i], 1);
     }
     for (int i = 0; i < NT; ++i) {
-      mbar_init(&s.q_full[i], FP8 ? 128 : 1);
+      mbar_init(&s.q_full[i], C::kFp8 ? 128 : 1);
       mbar_init(&s.q_empty[i], 1);
-      mbar_init(&s.o_full[i], 2);  // the commit, and the issuer's flags
+      mbar_init(&s.o_full[i], 2);        // the commit, and the issuer's flags
       mbar_init(&s.o_free[i], 128);
     }
     for (int i = 0; i < C::kNumS; ++i) {
       mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.p_ready[i], 128);
+      mbar_init(&s.s_free[i], 1);
+      mbar_init(&s.p_ready[0][i], 128);
+      mbar_init(&s.p_ready[1][i], 128);
+      mbar_init(&s.drain[i], 1);
     }
-    mbar_init(&s.prep_go, 1);
-    mbar_init(&s.pv_done, 1);
-    mbar_init(&s.drain, 1);
+    for (int i = 0; i < C::kItems; ++i) {
+      mbar_init(&s.item_full[i], 1);
+      mbar_init(&s.item_empty[i], 3 + 4 * NT);  // issuers, preparation, softmax warps
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kIssuer) tmem_alloc(&s.tmem, 512);
@@ -236,556 +864,20 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem;
-  PfItem it{};
   // A softmax thread holds a row of 128 scores: with two softmax warpgroups
   // the 168 registers a thread is launched with are moved to them (128 x 88 +
   // 256 x 208 = 384 x 168).
   if (warp >= kLoader) {
     if constexpr (NT == 2) regs_dec<88>();
-    if (warp == kLoader) {
-      // ---------------------------------------------------------------- loader
-      Ring<NS> r;
-      uint32_t nq[NT] = {};
-      long long issued = 0;
-      int blocks = 0;
-      bool live = true;
-      int ids = 0, ids_at = -1;  // 32 table entries, one a lane, from page index ids_at
-      auto load = [&](const CUtensorMap* map, int chunk0, int j, int item_b, int head, int chunks) {
-        const int k0 = it.lo + j * kPfBlock;
-        const int pages = min(kPfBlock, it.hi - k0 + kPfPage - 1) / kPfPage;  // those that hold keys of the item
-        const int p0 = k0 / kPfPage;
-        if (ids_at < 0 || p0 < ids_at || p0 + 4 > ids_at + 32) {
-          ids_at = p0;
-          const int at = p0 + lane;
-          ids = at < a.max_blocks ? a.block_tables[static_cast<long long>(item_b) * a.max_blocks + at] : 0;
-        }
-        int page = __shfl_sync(0xffffffffu, ids, p0 - ids_at + (lane & 3));
-        const bool use = (lane & 3) < pages && lane < 4 * C::kBlocks;
-        const bool bad = use && (page < 0 || page >= a.num_blocks);
-        const bool any_bad = __any_sync(0xffffffffu, bad);
-        if (bad) page = 0;
-        for (int c = 0; c < chunks && live; ++c) {
-          live = wait_phase(&s.empty[r.stage], r.phase ^ 1u, &s.abort_flag, a.status, kStatusEmpty, a.wait_limit);
-          live = __all_sync(0xffffffffu, live);
-          if (!live) break;
-          if (lane == 0) {
-            s.stage_bad[r.stage] = any_bad;
-            mbar_arrive_expect_tx(&s.full[r.stage], pages * C::kBlocks * kPfPage * ROW);
-          }
-          __syncwarp();
-          if (use)
-            tma_load_4d(s.ring[r.stage] + (lane >> 2) * C::kBlockBytes + (lane & 3) * kPfPage * ROW, map, 0,
-                        page * kPfPage, chunk0 + c * C::kBlocks + (lane >> 2), head, &s.full[r.stage]);
-          ++issued;
-          r.next();
-        }
-      };
-      while (live && w.next(a, it)) {
-        if (it.kb1 <= it.kb0) continue;
-        ids_at = -1;
-        for (int t = 0; t < NT && live && !FP8; ++t) {
-          const TileSpan sp = tile_span(a, it, t, tile_toks);
-          if (sp.je <= sp.jb) continue;
-          live = wait_phase(&s.q_empty[t], (nq[t] & 1u) ^ 1u, &s.abort_flag, a.status, kStatusEmpty, a.wait_limit);
-          live = __all_sync(0xffffffffu, live);
-          if (!live) break;
-          ++nq[t];
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&s.q_full[t], tile_toks * a.group * D * 2);
-            for (int c = 0; c < D / 64; ++c)
-              asm volatile(
-                  "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                  " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(s.q[t] + c * 128 * 128)),
-                  "l"(reinterpret_cast<uint64_t>(&tq)), "r"(0), "r"(0), "r"(it.row0 + sp.tok0), "r"(c), "r"(it.head),
-                  "r"(smem_addr(&s.q_full[t]))
-                  : "memory");
-          }
-        }
-        const int vc0 = it.part * (DV / C::kCols);
-        for (int j = it.kb0; j < it.kb1 && live; ++j) {
-          if (static_cast<int>(blockIdx.x) == a.withhold_cta && blocks >= a.withhold_block) {
-            live = false;  // test hook: the issuer's wait for this block runs out
-            break;
-          }
-          ++blocks;
-          if constexpr (NT == 2) {
-            load(&tk, 0, j, it.b, it.head, NKC);
-            if (live) load(&tv, vc0, j, it.b, it.head, NVC);
-          } else {
-            if (j == it.kb0) load(&tk, 0, j, it.b, it.head, NKC);
-            if (live && j + 1 < it.kb1) load(&tk, 0, j + 1, it.b, it.head, NKC);
-            if (live) load(&tv, vc0, j, it.b, it.head, NVC);
-          }
-        }
-      }
-      if (!live) {
-        // let this CTA's copies land before it exits
-        volatile int never = 0;
-        for (long long k = 1; k <= (issued < NS ? issued : NS); ++k) {
-          const long long n = issued - k;
-          if (!wait_phase(&s.full[n % NS], static_cast<uint32_t>((n / NS) & 1), &never, a.status, kStatusDrain,
-                          kDrainLimitCycles))
-            break;
-        }
-        for (int t = 0; t < NT; ++t)
-          if (nq[t])
-            wait_phase(&s.q_full[t], (nq[t] - 1) & 1u, &never, a.status, kStatusDrain, kDrainLimitCycles);
-      }
-    } else if (warp == kIssuer) {
-      // ---------------------------------------------------------------- MMA issuer
-      Ring<NS> r;
-      uint32_t nq[NT] = {}, np[C::kNumS] = {}, no[NT] = {};
-      uint32_t vphase = 0;  // one bit a stage
-      bool live = true;
-      const uint32_t idesc_qk = FP8 ? umma_idesc_e4m3(kPfBlock, false)
-                                    : umma_idesc_f16(true, kPfBlock, false) | (a.neg_scale ? kUmmaNegateA : 0u);
-      const uint32_t idesc_pv = FP8 ? umma_idesc_e4m3(CW, true) : umma_idesc_f16(true, CW, true);
-      auto wait = [&](unsigned long long* bar, uint32_t parity, unsigned code) {
-        if (live) live = wait_phase(bar, parity, &s.abort_flag, a.status, code, a.wait_limit);
-        return live;
-      };
-      // S(buf) (+)= Q_t chunk c x K chunk in the stage
-      auto qk = [&](int t, int buf, int c, int stage) {
-        if (lane != 0) return;
-        const uint32_t qa = smem_addr(s.q[t]), kb = smem_addr(s.ring[stage]);
-        constexpr int kSteps = ROW / 32;  // MMAs of a block's columns
-#pragma unroll
-        for (int term = 0; term < (FP8 ? 2 : 1); ++term)
-#pragma unroll
-          for (int k = 0; k < C::kBlocks * kSteps; ++k) {
-            const uint32_t at = (k / kSteps) * C::kBlockBytes + (k % kSteps) * 32;
-            umma_ss<FP8>(tmem + buf * 128,
-                         umma_desc(qa + term * (128 * D) + c * C::kStageBytes + at, 16, 8 * ROW, C::kSwizzle),
-                         umma_desc(kb + at, 16, 8 * ROW, C::kSwizzle), idesc_qk, c > 0 || term > 0 || k > 0);
-          }
-      };
-      // O_t chunk c (+)= P(buf) x V chunk in the stage, over ksteps of KS keys
-      auto pv = [&](int t, int buf, int c, int stage, int ksteps, bool acc) {
-        if (lane != 0) return;
-        const uint32_t vb = smem_addr(s.ring[stage]);
-        const uint32_t d = tmem + C::kTmemO + t * DV + c * CW, p = tmem + buf * 128;
-        for (int k = 0; k < ksteps; ++k) {
-          const uint64_t v = umma_desc(vb + k * KS * ROW, C::kBlockBytes, 8 * ROW, C::kSwizzle);
-          umma_ts<FP8>(d, p + k * 8, v, idesc_pv, acc || k > 0);
-          if constexpr (FP8) umma_ts<FP8>(d, p + 32 + k * 8, v, idesc_pv, true);  // P's low terms
-        }
-      };
-      while (live && w.next(a, it)) {
-        if (it.kb1 <= it.kb0) continue;
-        TileSpan sp[NT];
-        int flags = 0;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          sp[t] = tile_span(a, it, t, tile_toks);
-          if (sp[t].je > sp[t].jb) {
-            if (!wait(&s.q_full[t], nq[t] & 1u, kStatusFull)) break;
-            ++nq[t];
-          }
-        }
-        auto finish = [&](int t) {  // after the tile's last P V
-          if (lane == 0) {
-            s.flags[t] = flags;
-            umma_commit(&s.o_full[t]);
-            mbar_arrive(&s.o_full[t]);
-          }
-          ++no[t];
-        };
-        auto prep_wait = [&](int stage, int j) {
-          if (!needs_prep(a, it, j)) return;
-          wait(&s.vready[stage], (vphase >> stage) & 1u, kStatusSync);
-          vphase ^= 1u << stage;
-          if (live && s.stage_fix[stage]) flags |= kItemFix;
-        };
-        // Preparation of block j may start: it must not look at a stage's barrier
-        // while an earlier use of the stage is outstanding (a wait tells phases
-        // apart by parity only).
-        auto prep_go = [&](int j) {
-          if (!needs_prep(a, it, j)) return;
-          if (lane == 0) mbar_arrive(&s.prep_go);
-        };
-        auto keys_to = [&](int t, int j) {  // k-steps of block j that tile t's rows need
-          const int n = it.pos0 + sp[t].tok0 + sp[t].ntok - (it.lo + j * kPfBlock);
-          return (min(n, kPfBlock) + KS - 1) / KS;
-        };
-        if constexpr (NT == 2) {
-          Ring<NS> k = r;  // K of block j + 1
-          auto first_qk = [&](int t, int j) {
-            if (j < sp[t].jb || j >= sp[t].je) return;
-            qk(t, t, 0, k.stage);
-            if (lane == 0) {
-              umma_commit(&s.s_full[t]);
-              if (j == sp[t].je - 1) umma_commit(&s.q_empty[t]);
-            }
-          };
-          if (!wait(&s.full[k.stage], k.phase, kStatusFull)) break;
-          tc_fence_after();
-          if (s.stage_bad[k.stage]) flags |= kItemBad;
-          prep_go(it.kb0);
-          for (int t = 0; t < NT; ++t) first_qk(t, it.kb0);
-          if (lane == 0) umma_commit(&s.empty[k.stage]);
-          k.next();
-          for (int j = it.kb0; j < it.kb1 && live; ++j) {
-            const Ring<NS> v = k;  // the ring holds K0 V0 K1 V1 ...
-            k.next();
-            bool have_v = false, have_k = false;
-            for (int t = 0; t < NT && live; ++t) {
-              if (j >= sp[t].jb && j < sp[t].je) {
-                if (!wait(&s.p_ready[t], np[t] & 1u, kStatusSync)) break;
-                ++np[t];
-                if (j == sp[t].jb && !wait(&s.o_free[t], (no[t] & 1u) ^ 1u, kStatusSync)) break;
-                if (!have_v) {
-                  if (!wait(&s.full[v.stage], v.phase, kStatusFull)) break;
-                  prep_wait(v.stage, j);
-                  if (!live) break;
-                  have_v = true;
-                }
-                tc_fence_after();
-                pv(t, t, 0, v.stage, keys_to(t, j), j > sp[t].jb);
-                if (j == sp[t].je - 1) finish(t);
-              }
-              if (j + 1 < it.kb1 && j + 1 >= sp[t].jb && j + 1 < sp[t].je) {
-                if (!have_k) {
-                  if (!wait(&s.full[k.stage], k.phase, kStatusFull)) break;
-                  if (s.stage_bad[k.stage]) flags |= kItemBad;
-                  prep_go(j + 1);
-                  have_k = true;
-                }
-                tc_fence_after();
-                first_qk(t, j + 1);
-              }
-            }
-            if (!live) break;
-            if (lane == 0) umma_commit(&s.empty[v.stage]);
-            if (j + 1 < it.kb1) {
-              if (lane == 0) umma_commit(&s.empty[k.stage]);
-              k.next();
-            }
-          }
-          r = k;
-        } else {
-          auto all_qk = [&](int j) {
-            const int buf = (np[0] + np[1] + (j > it.kb0 ? 1 : 0)) & 1;  // blocks alternate buffers
-            for (int c = 0; c < NKC && live; ++c) {
-              if (!wait(&s.full[r.stage], r.phase, kStatusFull)) break;
-              tc_fence_after();
-              if (s.stage_bad[r.stage]) flags |= kItemBad;
-              qk(0, buf, c, r.stage);
-              if (lane == 0) umma_commit(&s.empty[r.stage]);
-              r.next();
-            }
-            if (live && lane == 0) {
-              umma_commit(&s.s_full[buf]);
-              if (j == it.kb1 - 1) umma_commit(&s.q_empty[0]);
-            }
-          };
-          all_qk(it.kb0);
-          for (int j = it.kb0; j < it.kb1 && live; ++j) {
-            if (j + 1 < it.kb1) all_qk(j + 1);
-            if (live) prep_go(j);  // the ring holds K0 K1 V0 K2 V1 ...: whatever used V's stages before is done
-            const int buf = (np[0] + np[1]) & 1;
-            if (!live || !wait(&s.p_ready[buf], np[buf] & 1u, kStatusSync)) break;
-            ++np[buf];
-            if (j == it.kb0 && !wait(&s.o_free[0], (no[0] & 1u) ^ 1u, kStatusSync)) break;
-            for (int c = 0; c < NVC; ++c) {
-              if (!wait(&s.full[r.stage], r.phase, kStatusFull)) break;
-              prep_wait(r.stage, j);
-              if (!live) break;
-              tc_fence_after();
-              pv(0, buf, c, r.stage, keys_to(0, j), j > it.kb0);
-              if (lane == 0) umma_commit(&s.empty[r.stage]);
-              r.next();
-            }
-            if (!live) break;
-            if (j == it.kb1 - 1) finish(0);
-            if (lane == 0) umma_commit(&s.pv_done);
-          }
-        }
-      }
-      __syncwarp();
-      // every MMA has to be done before tensor memory is given back
-      if (lane == 0) umma_commit(&s.drain);
-      volatile int never = 0;
-      wait_phase(&s.drain, 0, &never, a.status, kStatusDrain, kDrainLimitCycles);
-    } else if (warp == kPrep) {
-      // ---------------------------------------------------------------- V preparation
-      Ring<NS> r;
-      bool live = true;
-      uint32_t ngo = 0;
-      while (live && w.next(a, it)) {
-        if (it.kb1 <= it.kb0) continue;
-        auto skip = [&](int n) {
-          for (int i = 0; i < n; ++i) r.next();
-        };
-        if constexpr (NT == 1) skip(NKC);
-        for (int j = it.kb0; j < it.kb1 && live; ++j) {
-          if (NT == 2 || j + 1 < it.kb1) skip(NKC);
-          if (!needs_prep(a, it, j)) {
-            skip(NVC);
-            continue;
-          }
-          live = wait_phase(&s.prep_go, ngo & 1u, &s.abort_flag, a.status, kStatusSync, a.wait_limit);
-          live = __all_sync(0xffffffffu, live);
-          if (!live) break;
-          ++ngo;
-          const int k0 = it.lo + j * kPfBlock;
-          const int end = min(kPfBlock, (it.hi - k0 + KS - 1) / KS * KS);  // slots the products read
-          for (int c = 0; c < NVC && live; ++c) {
-            live = wait_phase(&s.full[r.stage], r.phase, &s.abort_flag, a.status, kStatusFull, a.wait_limit);
-            live = __all_sync(0xffffffffu, live);
-            if (!live) break;
-            bool fix = false;
-            constexpr int kPieces = ROW / 16;
-            for (int i = lane; i < end * kPieces; i += 32) {  // a 16-byte piece of a slot's row
-              const int slot = i / kPieces, t = k0 + slot;
-              const bool none = t < it.lo_exact || t >= it.hi;
-              const bool all = t <= it.pos0 && (a.window == 0 || t >= it.hi - a.window);
-              if (all && !none) continue;
-              for (int cb = 0; cb < C::kBlocks; ++cb) {
-                uint4* p = reinterpret_cast<uint4*>(s.ring[r.stage] + cb * C::kBlockBytes + i * 16);
-                if (none) {
-                  *p = make_uint4(0, 0, 0, 0);
-                } else {
-                  uint4 x = *p;
-                  const uint32_t m0 = not_finite<FP8>(x.x), m1 = not_finite<FP8>(x.y), m2 = not_finite<FP8>(x.z),
-                                 m3 = not_finite<FP8>(x.w);
-                  if (m0 | m1 | m2 | m3) {
-                    fix = true;
-                    x.x &= ~m0, x.y &= ~m1, x.z &= ~m2, x.w &= ~m3;
-                    *p = x;
-                  }
-                }
-              }
-            }
-            fix = __any_sync(0xffffffffu, fix);
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-              s.stage_fix[r.stage] = fix;
-              mbar_arrive(&s.vready[r.stage]);
-            }
-            r.next();
-          }
-        }
-      }
-    }
+    if (warp == kLoader)
+      tc_loader<C>(tq, tk, tv, a, s, w, lane);
+    else if (warp == kPrep)
+      tc_prepare<C>(a, s, lane);
+    else
+      tc_issuer<C>(a, s, tmem, warp - kIssuer, lane);
   } else {
     if constexpr (NT == 2) regs_inc<208>();
-    // ---------------------------------------------------------------- softmax: one row a thread
-    const int t = NT == 2 ? warp >> 2 : 0;
-    const int row = tid & 127;
-    const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes a warp, lane in bits 16..
-    uint32_t ns[C::kNumS] = {}, no = 0;
-    uint32_t blocks = 0;  // of NT == 1: buffers alternate
-    bool live = true;
-    while (live && w.next(a, it)) {
-      const TileSpan sp = tile_span(a, it, t, tile_toks);
-      const int tok = row / a.group, g = row - tok * a.group;
-      const bool valid = tok < tile_toks && tok < sp.ntok;
-      const int pos = it.pos0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1);
-      float m = -CUDART_INF_F, l = 0.f;
-      float scale = a.scale_log2;  // from a score in tensor memory to the log2 domain
-      if constexpr (FP8) {
-        // This row of Q as two E4M3 terms in the layout TMA gives K.  (The
-        // previous item's last scores are here, so its Q is done with.)
-        if (sp.je > sp.jb) {
-          const float ks = a.k_scale[it.head] * (a.neg_scale ? -1.f : 1.f);
-          const uint4* src = reinterpret_cast<const uint4*>(
-              static_cast<const __nv_bfloat16*>(a.q) +
-              (static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads + it.head * a.group + g) * D);
-          uint32_t most = 0;  // largest magnitude, as bf16 bits
-          if (valid) {
-#pragma unroll 8
-            for (int i = 0; i < D / 8; ++i) {
-              const uint4 x = src[i];
-              most = __vmaxu2(most, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                             __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-            }
-          }
-          most = max(most & 0xffffu, most >> 16);
-          // the largest magnitude goes to [2^7, 2^8); rows below 2^-100 count as zero
-          const int e = min(max(static_cast<int>(most >> 7) - 127, -100), 127);
-          const float up = pow2f(7 - max(e, -119));
-          scale = a.scale_log2 * fabsf(ks) * pow2f(max(e, -119) - 7);
-          if (scale == 0.f) scale = 1e-37f;
-          const float mul = ks < 0.f ? -up : up;
-#pragma unroll 2
-          for (int i = 0; i < D / 16; ++i) {
-            uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-            if (valid) {
-              x0 = src[2 * i];
-              x1 = src[2 * i + 1];
-            }
-            const uint32_t in[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t h0, h1, l0, l1;
-              e4m3x2_terms(bf16_lo_f(in[2 * k]) * mul, bf16_hi_f(in[2 * k]) * mul, h0, l0);
-              e4m3x2_terms(bf16_lo_f(in[2 * k + 1]) * mul, bf16_hi_f(in[2 * k + 1]) * mul, h1, l1);
-              hi[k] = h0 | (h1 << 16);
-              lo[k] = l0 | (l1 << 16);
-            }
-            const int blk = i / (ROW / 16), ch = i % (ROW / 16);
-            const int swz = ROW == 128 ? (ch ^ (row & 7)) : (ch ^ ((row >> 1) & 3));
-            unsigned char* dst = s.q[t] + blk * C::kBlockBytes + row * ROW + swz * 16;
-            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(dst + 128 * D) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-          fence_proxy_async_shared();
-          mbar_arrive(&s.q_full[t]);
-        }
-      }
-      for (int j = sp.jb; j < sp.je; ++j) {
-        const int buf = NT == 2 ? t : static_cast<int>(blocks & 1u);
-        const uint32_t tS = tmem + lane_base + buf * 128;
-        live = wait_phase(&s.s_full[buf], ns[buf] & 1u, &s.abort_flag, a.status, kStatusSync, a.wait_limit);
-        live = __all_sync(0xffffffffu, live);
-        if (!live) break;
-        ++ns[buf];
-        tc_fence_after();
-        float x[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
-        tmem_wait_ld();
-        const int k0 = it.lo + j * kPfBlock;
-        // rows see keys (pos - window, pos]; block columns [from, upto]
-        const bool masked = k0 + kPfBlock > it.pos0 + sp.tok0 + 1 ||
-                            (a.window > 0 && k0 < it.pos0 + sp.tok0 + sp.ntok - a.window);
-        if (masked) {
-          const int upto = pos - k0, from = a.window > 0 ? pos - a.window + 1 - k0 : 0;
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c > upto || c < from) x[c] = -CUDART_INF_F;
-        }
-        float top0 = x[0], top1 = x[1];
-#pragma unroll
-        for (int c = 2; c < 128; c += 2) {
-          top0 = fmaxf(top0, x[c]);
-          top1 = fmaxf(top1, x[c + 1]);
-        }
-        const float top = fmaxf(top0, top1) * scale;
-        if (__any_sync(0xffffffffu, top > m + kLazy)) {
-          const float mn = fmaxf(m, top);
-          const float keep = m == -CUDART_INF_F ? 0.f : ex2(m - mn);
-          if (j > sp.jb) {
-            // the accumulator is still: this tile's earlier products are done
-            if constexpr (NT == 1) {
-              live = wait_phase(&s.pv_done, (blocks & 1u) ^ 1u, &s.abort_flag, a.status, kStatusSync, a.wait_limit);
-              live = __all_sync(0xffffffffu, live);
-              if (!live) break;
-              tc_fence_after();
-            }
-            const uint32_t tO = tmem + lane_base + C::kTmemO + t * DV;
-#pragma unroll 1
-            for (int c = 0; c < DV; c += 32) {
-              float o[32];
-              tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= keep;
-              tmem_st32(tO + c, reinterpret_cast<const uint32_t*>(o));
-            }
-          }
-          l *= keep;
-          m = mn;
-        }
-        const float mb = (m == -CUDART_INF_F ? 0.f : m) - kWeightExp;
-        float sum0 = 0.f, sum1 = 0.f;
-        if constexpr (FP8) {
-          uint32_t hi[32], lo[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float p0 = ex2(fmaf(x[4 * e], scale, -mb)), p1 = ex2(fmaf(x[4 * e + 1], scale, -mb));
-            const float p2 = ex2(fmaf(x[4 * e + 2], scale, -mb)), p3 = ex2(fmaf(x[4 * e + 3], scale, -mb));
-            sum0 += p0 + p2;
-            sum1 += p1 + p3;
-            uint32_t h0, h1, l0, l1;
-            e4m3x2_terms(p0, p1, h0, l0);
-            e4m3x2_terms(p2, p3, h1, l1);
-            hi[e] = h0 | (h1 << 16);
-            lo[e] = l0 | (l1 << 16);
-          }
-          tmem_st32(tS, hi);
-          tmem_st32(tS + 32, lo);
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t p[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float p0 = ex2(fmaf(x[64 * h + 2 * e], scale, -mb));
-              const float p1 = ex2(fmaf(x[64 * h + 2 * e + 1], scale, -mb));
-              sum0 += p0;
-              sum1 += p1;
-              p[e] = pack_bf16(p0, p1);
-            }
-            tmem_st32(tS + 32 * h, p);
-          }
-        }
-        l += sum0 + sum1;
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&s.p_ready[buf]);
-        ++blocks;
-      }
-      if (!live) break;
-
-      const bool any = sp.je > sp.jb;  // O holds sums of this tile
-      int flags = 0;
-      if (any) {
-        live = wait_phase(&s.o_full[t], no & 1u, &s.abort_flag, a.status, kStatusSync, a.wait_limit);
-        live = __all_sync(0xffffffffu, live);
-        if (!live) break;
-        ++no;
-        tc_fence_after();
-        flags = s.flags[t];
-      }
-      const bool split = it.kb0 > 0 || it.pieces > 0;
-      if (it.pieces > 0 && tid == 0)
-        a.splits[blockIdx.x] = PrefillSplit{it.pieces, it.row0, it.ntok, it.head, it.part};
-      const long long rec = (2ll * blockIdx.x + (it.kb0 > 0 ? 1 : 0)) * (NT * 128) + t * 128 + row;
-      const bool bad = it.bad || (flags & kItemBad);
-      const float vs = FP8 ? a.v_scale[it.head] : 1.f;
-      const float inv = bad ? CUDART_NAN_F : vs / l;
-      const uint32_t tO = tmem + lane_base + C::kTmemO + t * DV;
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
-                           (static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads + it.head * a.group + g) *
-                               D + it.part * DV;
-      if (split && valid) a.ml[rec] = make_float2(bad ? CUDART_NAN_F : m, l);
-#pragma unroll 1
-      for (int c = 0; c < DV; c += 32) {
-        float o[32];
-        if (any) {
-          tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
-          tmem_wait_ld();
-          if (flags & kItemFix) {
-            add_taken_values<FP8>(a, it, D, pos, it.part * DV + c, o);
-            __syncwarp();
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
-        }
-        if (valid && split && l != 0.f) {  // (the combine reads no sums of a row without weight)
-          float4* p = reinterpret_cast<float4*>(a.part + rec * DV + c);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = make_float4(o[4 * e] * vs, o[4 * e + 1] * vs, o[4 * e + 2] * vs, o[4 * e + 3] * vs);
-        } else if (valid && !split) {
-          uint4* p = reinterpret_cast<uint4*>(dst + c);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            p[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
-                              pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                              pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                              pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-        }
-        __syncwarp();  // the next load of tensor memory is the whole warp's
-      }
-      if (any) {
-        tc_fence_before();
-        mbar_arrive(&s.o_free[t]);
-      }
-    }
+    tc_softmax<C>(a, s, tmem, tid);
   }
   // every role is done with tensor memory
   tc_fence_before();
@@ -806,7 +898,7 @@ struct TcVariant {
     return cudaGetLastError();
   }
   static PrefillVariant info() {
-    return PrefillVariant{C::kThreads, C::kNT * 128, 128, C::kDV, 1, C::kStages, smem,
+    return PrefillVariant{C::kThreads, C::kNT * 128, 128, C::kDV, 1, C::kStagesK + C::kStagesV, smem,
                           reinterpret_cast<const void*>(&prefill_tc_kernel<C>), &launch};
   }
 };
