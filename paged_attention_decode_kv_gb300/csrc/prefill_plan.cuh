@@ -82,17 +82,20 @@ __device__ __forceinline__ PfSeq pf_seq(const PrefillArgs& a, int b) {
   return s;
 }
 
-// Weight of the first K of the sequence's tiles (one head).
+__device__ __forceinline__ long long pf_mul(int a, int b) { return static_cast<long long>(a) * b; }
+
+// Weight of the first K of the sequence's tiles (one head).  (Products of two
+// 32-bit numbers and one 32-bit division: 64-bit ones are long code.)
 __device__ __forceinline__ long long pf_weight(const PrefillArgs& a, const PfSeq& s, int K) {
-  const long long T = a.tile_tokens, k = K;
+  const int T = a.tile_tokens;
   if (K <= 0) return 0;
-  if (s.bad) return k * kPfItemWeight;
-  long long w = T * k * (k + 1) / 2 + k * (static_cast<long long>(s.p0) + kPfItemWeight);
-  if (K == s.tiles) w -= T * k - s.n;
+  if (s.bad) return pf_mul(K, kPfItemWeight);
+  long long w = ((pf_mul(K, K) + K) >> 1) * T + pf_mul(K, s.p0) + pf_mul(K, kPfItemWeight);
+  if (K == s.tiles) w -= pf_mul(T, K) - s.n;
   if (a.window > 0) {
-    const long long A = static_cast<long long>(s.p0) - a.window + 1;  // window start of the first token
-    const long long f = A >= 0 ? 0 : (-A + T - 1) / T;                // first tile whose start is clipped
-    if (k > f) w -= (k - f) * A + T * ((k * (k - 1) - f * (f - 1)) / 2);
+    const int A = s.p0 - a.window + 1;            // window start of the first token
+    const int f = A >= 0 ? 0 : (-A + T - 1) / T;  // first tile whose start is clipped
+    if (K > f) w -= pf_mul(K - f, A) + ((pf_mul(K, K - 1) - pf_mul(f, f - 1)) >> 1) * T;
   }
   return w;
 }
@@ -118,11 +121,17 @@ struct PfItem {
 struct PfWalk {
   long long x, end;       // weights: next item's part starts at x
   long long item_x;       // weight where the current item starts
-  long long total;
+  long long quot;         // total weight = quot * ctas + rem
+  unsigned rem;
   int ctas;               // CTAs with a share
   int cta;                // this CTA
   PfSeq s;
   int b, vh, tile, heads;
+
+  // Where CTA c's share starts.
+  __device__ __forceinline__ long long share(unsigned c) const {
+    return quot * c + rem * c / static_cast<unsigned>(ctas);
+  }
 
   // kb(r): block boundary nearest to weight r of an item.
   __device__ __forceinline__ static int cut(long long r, long long W, int nkv) {
@@ -134,20 +143,22 @@ struct PfWalk {
   // False when the share is done.  Items without this CTA's blocks are skipped.
   __device__ __forceinline__ bool next(const PrefillArgs& a, PfItem& it) {
     while (x < end) {
-      const long long W = pf_weight(a, s, tile + 1) - pf_weight(a, s, tile);
+      long long W = 0;  // of the item: the difference of two sums (a loop: one copy of the code)
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) W = pf_weight(a, s, tile + i) - W;
       it.b = b;
       it.vh = vh;
       it.tile = tile;
-      it.head = vh / a.v_parts;
-      it.part = vh - it.head * a.v_parts;
+      it.head = vh >> (a.v_parts - 1);  // v_parts is 1 or 2
+      it.part = vh & (a.v_parts - 1);
       it.row0 = s.row0 + tile * a.tile_tokens;
       it.ntok = min(a.tile_tokens, s.n - tile * a.tile_tokens);
       it.pos0 = s.p0 + tile * a.tile_tokens;
       it.L = s.p0 + s.n;
       it.hi = it.pos0 + it.ntok;
       it.lo_exact = a.window > 0 ? max(0, it.pos0 - a.window + 1) : 0;
-      it.lo = it.lo_exact / kPfPage * kPfPage;
-      it.nkv = s.bad ? 0 : (it.hi - it.lo + kPfBlock - 1) / kPfBlock;
+      it.lo = it.lo_exact & ~(kPfPage - 1);
+      it.nkv = s.bad ? 0 : (it.hi - it.lo + kPfBlock - 1) >> 7;
       it.bad = s.bad;
       it.pieces = 0;
       const long long ra = x - item_x, rb = end - item_x;
@@ -157,12 +168,10 @@ struct PfWalk {
       if (it.kb0 == 0 && it.kb1 < it.nkv && it.kb1 > 0) {
         // the head piece of a split item: count the cuts inside it
         it.pieces = 1;
-        long long c = cta;
-        for (;;) {
-          ++c;
-          const long long e = total * c / ctas;
-          const int k = e - item_x >= W ? it.nkv : cut(e - item_x, W, it.nkv);
-          if (k >= it.nkv) break;
+#pragma unroll 1
+        for (unsigned c = cta + 1;; ++c) {
+          const long long e = share(c) - item_x;
+          if ((e >= W ? it.nkv : cut(e, W, it.nkv)) >= it.nkv) break;
           ++it.pieces;
         }
       }
@@ -191,81 +200,96 @@ struct PfWalk {
   }
 };
 
-// The CTA's share: every thread calls it once, with all threads of the CTA;
-// `scan` holds blockDim.x / 32 + 4 values of shared memory.
-__device__ inline void pf_begin(const PrefillArgs& a, long long* scan, PfWalk& w) {
-  const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nth >> 5;
-  const int heads = a.num_kv_heads * a.v_parts;
-  // total weight, in chunks of blockDim.x sequences
-  long long sum = 0;
-  for (int b = tid; b < a.num_seqs; b += nth) {
-    const PfSeq s = pf_seq(a, b);
-    sum += heads * pf_weight(a, s, s.tiles);
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  if (lane == 0) scan[warp] = sum;
-  __syncthreads();
-  long long total = 0;
-  for (int k = 0; k < warps; ++k) total += scan[k];
-  __syncthreads();
-  w.total = total;
-  w.heads = heads;
-  const long long most = total / a.min_weight;
-  w.ctas = static_cast<int>(most < 1 ? 1 : (most < gridDim.x ? most : gridDim.x));
+// The share of this CTA in a total weight; false if it has none.
+__device__ __forceinline__ bool pf_share(const PrefillArgs& a, long long total, PfWalk& w) {
+  w.heads = a.num_kv_heads * a.v_parts;
+  // (weights stay far below 2^38: 2^31 blocks of 128)
+  const unsigned most = static_cast<unsigned>(total >> 7) / static_cast<unsigned>(a.min_weight >> 7);
+  w.ctas = static_cast<int>(most < 1 ? 1 : min(most, gridDim.x));
   w.cta = blockIdx.x;
-  const long long c = blockIdx.x;
-  w.x = w.cta < w.ctas ? total * c / w.ctas : 0;
-  w.end = w.cta < w.ctas ? total * (c + 1) / w.ctas : 0;
-  if (total == 0 || w.x >= w.end) {  // nothing to do
-    w.x = w.end = 0;
-    return;
+  w.x = w.end = 0;
+  if (total == 0 || w.cta >= w.ctas) return false;
+  w.quot = static_cast<unsigned long long>(total) / static_cast<unsigned>(w.ctas);
+  w.rem = static_cast<unsigned>(total - w.quot * w.ctas);
+  w.x = w.share(blockIdx.x);
+  w.end = w.share(blockIdx.x + 1);
+  return w.x < w.end;
+}
+
+// The item that holds weight w.x, in sequence b whose items start at weight `start`.
+__device__ __forceinline__ void pf_locate(const PrefillArgs& a, int b, long long start, PfWalk& w) {
+  w.b = b;
+  w.s = pf_seq(a, b);
+  // first the head, then by bisection the tile: W(lo) <= x - start < W(hi), W(0) = 0
+  int lo = 0, hi = w.s.tiles, at = w.s.tiles;
+  long long at_lo = 0;
+  w.vh = -1;
+#pragma unroll 1
+  for (;;) {
+    const long long m = pf_weight(a, w.s, at);
+    if (w.vh < 0) {
+      for (w.vh = 0; w.x - start >= m; start += m) ++w.vh;
+    } else if (m <= w.x - start) {
+      lo = at;
+      at_lo = m;
+    } else {
+      hi = at;
+    }
+    if (hi - lo <= 1) break;
+    at = (lo + hi) >> 1;
   }
-  // the sequence that holds weight x: inclusive scan over chunks
-  long long before = 0;
+  w.tile = lo;
+  w.item_x = start + at_lo;
+}
+
+__device__ __forceinline__ long long pf_warp_scan(long long x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += o;
+  }
+  return x;
+}
+
+// The CTA's share: every thread calls it once, with all threads of the CTA;
+// `scan` holds blockDim.x / 32 + 4 values of shared memory.  A batch of up to
+// blockDim.x sequences takes one pass; a larger one is summed first.
+__device__ __forceinline__ void pf_begin(const PrefillArgs& a, long long* scan, PfWalk& w) {
+  const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nth >> 5;
+  const int chunks = static_cast<int>((static_cast<unsigned>(a.num_seqs) + nth - 1) / nth);
   if (tid == 0) scan[warps] = -1;
-  for (int b0 = 0; b0 < a.num_seqs; b0 += nth) {
-    const int b = b0 + tid;
+  long long total = 0;
+#pragma unroll 1
+  for (int i = chunks == 1 ? chunks : 0; i < 2 * chunks; ++i) {
+    const bool find = i >= chunks;
+    const int b = (find ? i - chunks : i) * nth + tid;
+    if (i == chunks && chunks > 1) {
+      if (!pf_share(a, total, w)) return;
+      total = 0;  // now the weight before this chunk
+    }
     long long mine = 0;
     if (b < a.num_seqs) {
       const PfSeq s = pf_seq(a, b);
-      mine = heads * pf_weight(a, s, s.tiles);
+      mine = a.num_kv_heads * a.v_parts * pf_weight(a, s, s.tiles);
     }
-    long long inc = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += o;
-    }
+    const long long inc = pf_warp_scan(mine, lane);
     if (lane == 31) scan[warp] = inc;
     __syncthreads();
-    long long base = before, chunk = 0;
+    long long base = total;
+#pragma unroll 1
     for (int k = 0; k < warps; ++k) {
       if (k < warp) base += scan[k];
-      chunk += scan[k];
+      total += scan[k];
     }
-    const long long lo = base + inc - mine;
-    if (mine > 0 && w.x >= lo && w.x < base + inc) {
+    if (chunks == 1 && !pf_share(a, total, w)) return;
+    if (find && mine > 0 && w.x >= base + inc - mine && w.x < base + inc) {
       scan[warps] = b;
-      scan[warps + 1] = lo;
+      scan[warps + 1] = base + inc - mine;
     }
-    before += chunk;
     __syncthreads();
-    if (scan[warps] >= 0) break;
+    if (find && scan[warps] >= 0) break;
   }
-  w.b = static_cast<int>(scan[warps]);
-  long long start = scan[warps + 1];
-  w.s = pf_seq(a, w.b);
-  const long long per_head = pf_weight(a, w.s, w.s.tiles);
-  w.vh = static_cast<int>((w.x - start) / per_head);
-  start += w.vh * per_head;
-  int lo = 0, hi = w.s.tiles;  // pf_weight(lo) <= x - start < pf_weight(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (pf_weight(a, w.s, mid) <= w.x - start) lo = mid; else hi = mid;
-  }
-  w.tile = lo;
-  w.item_x = start + pf_weight(a, w.s, lo);
+  pf_locate(a, static_cast<int>(scan[warps]), scan[warps + 1], w);
 }
 
 }  // namespace vt

@@ -30,6 +30,8 @@
 
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "decode_kernel.cuh"
 #include "prefill_variants.cuh"
 #include "tcgen05.cuh"
@@ -55,7 +57,7 @@ struct TcConfig {
   static constexpr int kKBlockBytes = kPfBlock * kRow, kVBlockBytes = VK * kRow;
   static constexpr int kKBytes = kKBlocks * kKBlockBytes, kVBytes = kVBlocks * kVBlockBytes;
   static constexpr int kQBytes = 128 * D * 2;          // FP8: two E4M3 terms of each element, high terms first
-  static constexpr int kThreads = NT * 128 + 128;
+  static constexpr int kThreads = NT * 128 + 256;      // softmax, epilogue, control
   static constexpr int kTmemO = 256;                   // S of tile (or buffer) i at 128 i
   static constexpr int kNumS = 2;                      // tiles, or buffers of one tile
   static constexpr int kItems = 4;                     // queue of items
@@ -73,16 +75,18 @@ struct TcSmem {
   unsigned long long q_full[C::kNT], q_empty[C::kNT];
   unsigned long long s_full[C::kNumS], s_free[C::kNumS];  // s_free: one tile only
   unsigned long long p_ready[2][C::kNumS];                // weights of the block's first and second 64 keys
+  unsigned long long l_full[C::kNT], l_free[C::kNT];
   unsigned long long o_full[C::kNT], o_free[C::kNT];
   unsigned long long item_full[C::kItems], item_empty[C::kItems];
   unsigned long long drain[2];
-  long long scan[C::kThreads / 32 + 4];
   PfItem items[C::kItems];
+  alignas(8) float2 ml[C::kNT][128];    // rows' (reference maximum, sum) for the epilogue (first: the partition's scan)
   uint32_t tmem;
   volatile int stage_bad[C::kStagesV];  // a page id of this stage was out of range
   volatile int stage_fix[C::kStagesV];  // V preparation took out a value that is not finite
   volatile int flags[C::kNT];           // of the item whose O is full
-  volatile int abort_flag;
+  volatile int abort_flag;              // status bit | thread << 8 of a wait that gave up
+  volatile uint32_t abort_at[2];        // its barrier and parity
 };
 
 // Weights are 2^(score - m + kWeightExp) with m at most kLazy below the largest
@@ -137,36 +141,39 @@ struct Ring {
   }
 };
 
-// Adds the values that preparation took out to the output columns [c0, c0 + 32)
-// of a row at `pos`: they are not finite, so neither is the result.
+// Adds the values that preparation took out to a row's sums, in tensor memory
+// from column 0 of `o` on: they are not finite, so neither is the result.  (All
+// threads of a warp together; rare, so compact.)
 template <bool FP8>
-__device__ __forceinline__ void add_taken_values(const PrefillArgs& a, const PfItem& it, int head_dim, int pos, int c0,
-                                                 float (&o)[32]) {
+__device__ __forceinline__ void add_taken_values(const PrefillArgs& a, const PfItem& it, int head_dim, int pos, int cols,
+                                              uint32_t o) {
   const int first = max(it.lo_exact, it.lo + it.kb0 * kPfBlock);
   const int last = min(it.hi, it.lo + it.kb1 * kPfBlock);
 #pragma unroll 1
-  for (int t = first; t < last; ++t) {
-    const bool all = t <= it.pos0 && (a.window == 0 || t >= it.hi - a.window);
-    if (all) continue;  // seen by every row: was left in place
-    if (t > pos || (a.window > 0 && t <= pos - a.window)) continue;
-    const int page = a.block_tables[static_cast<long long>(it.b) * a.max_blocks + t / kPfPage];
-    if (page < 0 || page >= a.num_blocks) continue;
-    const long long at = ((static_cast<long long>(page) * kPfPage + t % kPfPage) * a.num_kv_heads + it.head) *
-                             head_dim + c0;
-    if constexpr (FP8) {
-      const uint8_t* v = static_cast<const uint8_t*>(a.v_cache) + at;
-#pragma unroll
-      for (int c = 0; c < 32; ++c)
-        if ((v[c] & 0x7f) == 0x7f) o[c] = CUDART_NAN_F;
-    } else {
-      const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v_cache) + at;
-#pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(v + c);
-        if ((w & 0x7f80u) == 0x7f80u) o[c] += bf16_lo_f(w);
-        if ((w & 0x7f800000u) == 0x7f800000u) o[c + 1] += bf16_hi_f(w);
+  for (int c = 0; c < cols; ++c) {
+    float add = 0.f;
+#pragma unroll 1
+    for (int t = first; t < last; ++t) {
+      const bool all = t <= it.pos0 && (a.window == 0 || t >= it.hi - a.window);
+      if (all) continue;  // seen by every row: was left in place
+      if (t > pos || (a.window > 0 && t <= pos - a.window)) continue;
+      const int page = a.block_tables[static_cast<long long>(it.b) * a.max_blocks + t / kPfPage];
+      if (page < 0 || page >= a.num_blocks) continue;
+      const long long at = ((static_cast<long long>(page) * kPfPage + t % kPfPage) * a.num_kv_heads + it.head) *
+                               head_dim + it.part * cols + c;
+      if constexpr (FP8) {
+        if ((static_cast<const uint8_t*>(a.v_cache)[at] & 0x7f) == 0x7f) add = CUDART_NAN_F;
+      } else {
+        const float x = __bfloat162float(static_cast<const __nv_bfloat16*>(a.v_cache)[at]);
+        if (!isfinite(x)) add += x;
       }
     }
+    __syncwarp();
+    uint32_t sum;
+    tmem_ld1(o + c, sum);
+    tmem_wait_ld();
+    tmem_st1(o + c, __float_as_uint(__uint_as_float(sum) + add));
+    tmem_wait_st();
   }
 }
 
@@ -223,6 +230,41 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// In each group of four lanes: lane k's x[r] becomes what lane r held in x[k].
+__device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & d) continue;
+      const bool up = lane & d;
+      uint4 give = up ? x[i] : x[i | d];
+      give.x = __shfl_xor_sync(0xffffffffu, give.x, d);
+      give.y = __shfl_xor_sync(0xffffffffu, give.y, d);
+      give.z = __shfl_xor_sync(0xffffffffu, give.z, d);
+      give.w = __shfl_xor_sync(0xffffffffu, give.w, d);
+      if (up)
+        x[i] = give;
+      else
+        x[i | d] = give;
+    }
+  }
+}
+
+// Up to 64 probes of an mbarrier phase.
+__device__ __forceinline__ bool probe(unsigned long long* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 64;\n\t"
+      "PROBE_%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra MET_%=;\n\t"
+      "sub.u32 n, n, 1;\n\tsetp.ne.u32 p, n, 0;\n\t@p bra PROBE_%=;\n\tsetp.ne.u32 p, n, 0;\n\t"
+      "MET_%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Everything a role needs besides its own state.
 template <typename C>
 struct TcRole {
@@ -231,10 +273,35 @@ struct TcRole {
   int lane;
   bool live = true;  // false once a bounded wait has given up; uniform over a warp
 
+  // Bounded wait on an mbarrier phase.  A wait that passes `limit` clock
+  // cycles raises the CTA's abort flag, with what to report at the end, and
+  // every other wait then gives up too.  (Short code: it is inlined often,
+  // and the roles' loops together have to stay in the instruction cache.)
   __device__ __forceinline__ bool wait(unsigned long long* bar, uint32_t parity, unsigned code) {
-    if (live) live = wait_phase(bar, parity & 1u, &s.abort_flag, a.status, code, a.wait_limit);
+    if (live && !probe(bar, parity & 1u)) {
+      const long long t0 = clock64();
+      do {
+        if (s.abort_flag) live = false;
+        if (live && clock64() - t0 > a.wait_limit) {
+          s.abort_at[0] = smem_addr(bar);
+          s.abort_at[1] = parity & 1u;
+          s.abort_flag = static_cast<int>(code | (threadIdx.x << 8));
+          live = false;
+        }
+      } while (live && !probe(bar, parity & 1u));
+    }
     live = __all_sync(0xffffffffu, live);
     return live;
+  }
+  // For copies and MMAs in flight, whatever the abort flag says.
+  __device__ __forceinline__ void drain(unsigned long long* bar, uint32_t parity) {
+    const long long t0 = clock64();
+    while (!probe(bar, parity & 1u))
+      if (clock64() - t0 > kDrainLimitCycles) {
+        s.abort_flag = static_cast<int>(kStatusDrain | (threadIdx.x << 8));
+        break;
+      }
+    __syncwarp();
   }
   // Item n of the CTA's share; false at the end.
   __device__ __forceinline__ bool item(uint32_t n, PfItem& it) {
@@ -255,7 +322,7 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
   TcRole<C> role{a, s, lane};
   Ring<C::kStagesK> rk;
   Ring<C::kStagesV> rv;
-  uint32_t nq[C::kNT] = {}, items = 0;
+  uint32_t nq = 0, used = 0, items = 0;  // nq: parity of a tile's Q loads in bit 16 t
   long long nk = 0, nv = 0;
   int blocks = 0;
   const int tile_toks = 128 / a.group;
@@ -277,6 +344,7 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
     int page = page_of(k0 / kPfPage, lane & 3);
     const bool use = (lane & 3) < pages && lane < 4 * C::kKBlocks;
     if (page < 0 || page >= a.num_blocks) page = 0;  // (load_v reports it)
+#pragma unroll 1
     for (int c = 0; c < C::kKChunks; ++c) {
       if (!role.wait(&s.k_empty[rk.stage], rk.phase ^ 1u, kStatusEmpty)) return;
       if (lane == 0) mbar_arrive_expect_tx(&s.k_full[rk.stage], pages * C::kKBlocks * kPfPage * C::kRow);
@@ -291,6 +359,7 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
   auto load_v = [&](int j) {
     constexpr int kPages = C::kVK / kPfPage;  // of a stage
     const int stages = v_stages<C>(it, j);
+#pragma unroll 1
     for (int i = 0; i < stages; ++i) {
       const int k0 = it.lo + j * kPfBlock + i * C::kVK;
       const int pages = min(C::kVK, it.hi - k0 + kPfPage - 1) / kPfPage;
@@ -324,11 +393,13 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
     ++items;
     if (!more) break;
     ids_at = -1;
+#pragma unroll 1
     for (int t = 0; t < C::kNT && !C::kFp8; ++t) {
       const TileSpan sp = tile_span(a, it, t, tile_toks);
       if (sp.je <= sp.jb) continue;
-      if (!role.wait(&s.q_empty[t], nq[t] ^ 1u, kStatusEmpty)) break;
-      ++nq[t];
+      if (!role.wait(&s.q_empty[t], (nq >> (16 * t)) ^ 1u, kStatusEmpty)) break;
+      nq ^= 1u << (16 * t);
+      used |= 1u << t;
       if (lane == 0) mbar_arrive_expect_tx(&s.q_full[t], tile_toks * a.group * C::kD * 2);
       __syncwarp();
       if (lane < C::kD / 64)
@@ -339,31 +410,29 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
             "r"(smem_addr(&s.q_full[t]))
             : "memory");
     }
-    for (int j = it.kb0; j < it.kb1 && role.live; ++j) {
-      if (static_cast<int>(blockIdx.x) == a.withhold_cta && blocks >= a.withhold_block) {
-        role.live = false;  // test hook: an issuer's wait for this block runs out
-        break;
+#pragma unroll 1
+    for (int j = it.kb0 - 1; j < it.kb1 && role.live; ++j) {  // K of block j + 1, then V of block j
+      if (j + 1 < it.kb1) {
+        if (static_cast<int>(blockIdx.x) == a.withhold_cta && blocks >= a.withhold_block) {
+          role.live = false;  // test hook: an issuer's wait for this block runs out
+          break;
+        }
+        ++blocks;
+        load_k(j + 1);
       }
-      ++blocks;
-      if (j == it.kb0) load_k(j);
-      if (role.live && j + 1 < it.kb1) load_k(j + 1);
-      if (role.live) load_v(j);
+      if (role.live && j >= it.kb0) load_v(j);
     }
   }
   if (!role.live) {
     // let this CTA's copies land before it exits
-    volatile int never = 0;
-    auto drain = [&](unsigned long long* bars, long long n, int stages) {
-      for (long long k = 1; k <= (n < stages ? n : stages); ++k)
-        if (!wait_phase(&bars[(n - k) % stages], static_cast<uint32_t>(((n - k) / stages) & 1), &never, a.status,
-                        kStatusDrain, kDrainLimitCycles))
-          break;
-    };
-    drain(s.k_full, nk, C::kStagesK);
-    drain(s.v_full, nv, C::kStagesV);
+#pragma unroll 1
+    for (long long k = 1; k <= (nk < C::kStagesK ? nk : C::kStagesK); ++k)
+      role.drain(&s.k_full[(nk - k) % C::kStagesK], static_cast<uint32_t>((nk - k) / C::kStagesK));
+#pragma unroll 1
+    for (long long k = 1; k <= (nv < C::kStagesV ? nv : C::kStagesV); ++k)
+      role.drain(&s.v_full[(nv - k) % C::kStagesV], static_cast<uint32_t>((nv - k) / C::kStagesV));
     for (int t = 0; t < C::kNT; ++t)
-      if (nq[t])
-        wait_phase(&s.q_full[t], (nq[t] - 1) & 1u, &never, a.status, kStatusDrain, kDrainLimitCycles);
+      if (used >> t & 1u) role.drain(&s.q_full[t], (nq >> (16 * t)) ^ 1u);
   }
 }
 
@@ -377,7 +446,6 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
   constexpr int NT = C::kNT, KS = C::kKStep, ROW = C::kRow;
   constexpr bool FP8 = C::kFp8;
   constexpr uint32_t kHi = umma_desc_hi(8 * ROW, C::kSwizzle);
-  constexpr int kHalf = kPfBlock / 2 / KS;  // k-steps of half a block
   TcRole<C> role{a, s, lane};
   Ring<C::kStagesK> rk;
   Ring<C::kStagesV> rv;
@@ -389,105 +457,111 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
   const int tile_toks = 128 / a.group;
   PfItem it{};
 
-  // S(buf) = Q K^T for block j's keys
-  auto qk = [&](int j, int buf, const TileSpan& sp) {
+  // S(buf) = Q K^T for block j's keys: the MMAs of chunk c and what follows them.  One lane.
+  auto qk_issue = [&](int j, int buf, int c, const TileSpan& sp) {
     const bool active = j >= sp.jb && j < sp.je;
-    const int keys = min(kPfBlock, it.hi - (it.lo + j * kPfBlock));
-    const uint32_t idesc = (FP8 ? umma_idesc_e4m3(0, false)
-                                : umma_idesc_f16(true, 0, false) | (a.neg_scale ? kUmmaNegateA : 0u)) |
-                           (static_cast<uint32_t>((keys + 15) / 16 * 2) << 17);
-    for (int c = 0; c < C::kKChunks; ++c) {
-      if (!role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) return;
-      tc_fence_after();
+    if (active) {
+      const int keys = min(kPfBlock, it.hi - (it.lo + j * kPfBlock));
+      const uint32_t idesc = (FP8 ? umma_idesc_e4m3(0, false)
+                                  : umma_idesc_f16(true, 0, false) | (a.neg_scale ? kUmmaNegateA : 0u)) |
+                             (static_cast<uint32_t>((keys + 15) / 16 * 2) << 17);
       const uint32_t qa = umma_desc_lo(smem_addr(s.q[t]) + c * C::kKBytes, 16);
       const uint32_t kb = umma_desc_lo(smem_addr(s.k[rk.stage]), 16);
       const uint32_t d = tmem + buf * 128, more = c > 0;
-      if (elect_one()) {
-        if (active) {
-          constexpr int kSteps = ROW / 32;  // MMAs of a block's columns
+      constexpr int kSteps = ROW / 32;  // MMAs of a block's columns
 #pragma unroll
-          for (int term = 0; term < (FP8 ? 2 : 1); ++term)
+      for (int term = 0; term < (FP8 ? 2 : 1); ++term)
 #pragma unroll
-            for (int k = 0; k < C::kKBlocks * kSteps; ++k) {
-              const uint32_t at = ((k / kSteps) * C::kKBlockBytes + (k % kSteps) * 32) >> 4;
-              umma_ss<FP8>(d, qa + ((term * 128 * C::kD) >> 4) + at, kHi, kb + at, kHi, idesc,
-                           term > 0 || k > 0 ? 1u : more);
-            }
+        for (int k = 0; k < C::kKBlocks * kSteps; ++k) {
+          const uint32_t at = ((k / kSteps) * C::kKBlockBytes + (k % kSteps) * 32) >> 4;
+          umma_ss<FP8>(d, qa + ((term * 128 * C::kD) >> 4) + at, kHi, kb + at, kHi, idesc,
+                       term > 0 || k > 0 ? 1u : more);
         }
-        umma_commit(&s.k_empty[rk.stage]);
-        if (active && c == C::kKChunks - 1) {
-          umma_commit(&s.s_full[buf]);
-          if (j == sp.je - 1) umma_commit(&s.q_empty[t]);
-        }
-      }
+    }
+    umma_commit(&s.k_empty[rk.stage]);
+    if (active && c == C::kKChunks - 1) {
+      umma_commit(&s.s_full[buf]);
+      if (j == sp.je - 1) umma_commit(&s.q_empty[t]);
+    }
+  };
+  auto qk = [&](int j, int buf, const TileSpan& sp) {
+#pragma unroll 1
+    for (int c = 0; c < C::kKChunks; ++c) {
+      if (!role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) return;
+      tc_fence_after();
+      if (elect_one()) qk_issue(j, buf, c, sp);
       __syncwarp();
       rk.next();
     }
   };
-  // O (+)= P(buf) V for block j's keys; adds to `flags`
-  auto pv = [&](int j, int buf, const TileSpan& sp, int& flags) {
-    const bool active = j >= sp.jb && j < sp.je;
-    const bool prepared = needs_prep(a, it, j);
-    const int stages = v_stages<C>(it, j);
-    const int n = it.pos0 + sp.tok0 + sp.ntok - (it.lo + j * kPfBlock);
-    const int steps = active ? (min(n, kPfBlock) + KS - 1) / KS : 0;  // that the tile's rows need
-    const uint32_t idesc = FP8 ? umma_idesc_e4m3(C::kDV, true) : umma_idesc_f16(true, C::kDV, true);
-    const uint32_t d = tmem + C::kTmemO + t * C::kDV, p = tmem + buf * 128;
-    uint32_t acc = j > sp.jb;
+  // The tile's O is whole once its products so far are done.
+  auto finish = [&](int flags) {
+    if (elect_one()) {
+      s.flags[t] = flags;
+      umma_commit(&s.o_full[t]);
+      mbar_arrive(&s.o_full[t]);
+    }
+    __syncwarp();
+    ++no;
+  };
+  // Waits for the V stage at hand (and its preparation, where block j needs it).
+  auto v_here = [&](bool prepared, int& flags) {
+    if (!role.wait(&s.v_full[rv.stage], rv.phase, kStatusFull)) return false;
+    if (prepared) {
+      if (!role.wait(&s.v_ready[rv.stage], vphase >> rv.stage, kStatusSync)) return false;
+      vphase ^= 1u << rv.stage;
+      if (s.stage_fix[rv.stage]) flags |= kItemFix;
+    }
+    if (s.stage_bad[rv.stage]) flags |= kItemBad;
+    return true;
+  };
+  // k-steps of block j that the tile's rows need
+  auto steps_of = [&](int j, const TileSpan& sp) {
+    return (min(it.pos0 + sp.tok0 + sp.ntok - (it.lo + j * kPfBlock), kPfBlock) + KS - 1) / KS;
+  };
+  constexpr int kHalf = kPfBlock / 2 / KS;  // k-steps of half a block
+  const uint32_t idesc_pv = FP8 ? umma_idesc_e4m3(C::kDV, true) : umma_idesc_f16(true, C::kDV, true);
+  const uint32_t d_pv = tmem + C::kTmemO + t * C::kDV;
+  // N k-steps of P V from block k-step `first`; vb: the V stage at that step.  One lane.
+  auto pv_steps = [&](int buf, int first, int n, uint32_t vb, uint32_t acc, auto count) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (active) {
-        if (!role.wait(&s.p_ready[h][buf], np[buf], kStatusSync)) return;
-        if (h == 0 && j == sp.jb && !role.wait(&s.o_free[t], no ^ 1u, kStatusSync)) return;
+    for (int k = 0; k < decltype(count)::value; ++k) {
+      if (k < n) {
+        const uint32_t b = vb + ((k * KS * ROW) >> 4), from = tmem + buf * 128 + (first + k) * 8;
+        umma_ts<FP8>(d_pv, from, b, kHi, idesc_pv, k > 0 ? 1u : acc);
+        if constexpr (FP8) umma_ts<FP8>(d_pv, from + 32, b, kHi, idesc_pv, 1u);  // P's low terms
       }
-      constexpr int kPer = C::kVK == 128 ? 1 : 64 / C::kVK;  // stages of half a block (one stage holds both: 128)
-      constexpr int kSteps = C::kVK == 128 ? kHalf : C::kVK / KS;
-#pragma unroll
+    }
+  };
+  // One tile: O (+)= P(buf) V for block j's keys, V in stages of VK keys.
+  auto pv = [&](int j, int buf, const TileSpan& sp, int& flags) {
+    const bool prepared = needs_prep(a, it, j);
+    const int stages = v_stages<C>(it, j), steps = steps_of(j, sp);
+    constexpr int kSteps = C::kVK < 64 ? C::kVK / KS : kHalf;  // of a stage
+    constexpr int kPer = kHalf / kSteps;                       // stages of half a block
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      if (!role.wait(&s.p_ready[h][buf], np[buf], kStatusSync)) return;
+      if (h == 0 && j == sp.jb && !role.wait(&s.o_free[t], no ^ 1u, kStatusSync)) return;
+#pragma unroll 1
       for (int i = 0; i < kPer; ++i) {
-        const int first = h * kHalf + i * kSteps;  // k-step of the block
-        if (C::kVK == 128 ? h == 0 : h * kPer + i < stages) {
-          if (!role.wait(&s.v_full[rv.stage], rv.phase, kStatusFull)) return;
-          if (prepared) {
-            if (!role.wait(&s.v_ready[rv.stage], vphase >> rv.stage, kStatusSync)) return;
-            vphase ^= 1u << rv.stage;
-            if (s.stage_fix[rv.stage]) flags |= kItemFix;
-          }
-          if (s.stage_bad[rv.stage]) flags |= kItemBad;
-        } else if (C::kVK != 128) {
-          continue;
-        }
+        if (h * kPer + i >= stages) continue;
+        if (!v_here(prepared, flags)) return;
         tc_fence_after();
-        const uint32_t vb = umma_desc_lo(smem_addr(s.v[rv.stage]), C::kVBlockBytes) +
-                            (C::kVK == 128 ? (h * kHalf * KS * ROW) >> 4 : 0);
-        const bool last = C::kVK != 128 || h == 1;  // of the stage
+        const int first = (h * kPer + i) * kSteps;
         if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kSteps; ++k) {
-            if (first + k < steps) {
-              const uint32_t b = vb + ((k * KS * ROW) >> 4);
-              umma_ts<FP8>(d, p + (first + k) * 8, b, kHi, idesc, first + k > 0 ? 1u : acc);
-              if constexpr (FP8) umma_ts<FP8>(d, p + 32 + (first + k) * 8, b, kHi, idesc, 1u);  // P's low terms
-            }
-          }
-          if (last) umma_commit(&s.v_empty[rv.stage]);
+          pv_steps(buf, first, steps - first, umma_desc_lo(smem_addr(s.v[rv.stage]), C::kVBlockBytes),
+                   first > 0 || j > sp.jb, std::integral_constant<int, kSteps>());
+          umma_commit(&s.v_empty[rv.stage]);
         }
         __syncwarp();
-        if (last) rv.next();
+        rv.next();
       }
     }
-    if (active) {
-      ++np[buf];
-      if (elect_one()) {
-        if constexpr (NT == 1) umma_commit(&s.s_free[buf]);
-        if (j == sp.je - 1) {
-          s.flags[t] = flags;
-          umma_commit(&s.o_full[t]);
-          mbar_arrive(&s.o_full[t]);
-        }
-      }
-      __syncwarp();
-      if (j == sp.je - 1) ++no;
-    }
+    ++np[buf];
+    if (elect_one()) umma_commit(&s.s_free[buf]);
+    __syncwarp();
+    if (j == sp.je - 1) finish(flags);
   };
 
   for (; role.item(items, it); ++items) {
@@ -499,10 +573,36 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
         ++nq;
       }
       if constexpr (NT == 2) {
-        qk(it.kb0, t, sp);
-        for (int j = it.kb0; j < it.kb1 && role.live; ++j) {
-          pv(j, t, sp, flags);
-          if (role.live && j + 1 < it.kb1) qk(j + 1, t, sp);
+        static_assert(NT == 1 || (C::kVK == kPfBlock && C::kKChunks == 1), "one stage a block");
+        for (int j = it.kb0 - 1; j < it.kb1 && role.live; ++j) {  // P V of block j, then Q K^T of block j + 1
+          // What can be waited for ahead of the weights is: between them and
+          // the next scores this thread only issues.
+          const bool mine = j >= it.kb0, active = j >= sp.jb && j < sp.je, next = j + 1 < it.kb1;
+          if (mine && !v_here(needs_prep(a, it, j), flags)) break;
+          if (next && !active && !role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) break;
+          const int steps = active ? steps_of(j, sp) : 0;
+          const uint32_t vb = umma_desc_lo(smem_addr(s.v[rv.stage]), C::kVBlockBytes);
+#pragma unroll 1
+          for (int h = 0; h < 2 && active; ++h) {
+            if (h == 0 && j == sp.jb && !role.wait(&s.o_free[t], no ^ 1u, kStatusSync)) break;
+            if (!role.wait(&s.p_ready[h][t], np[0], kStatusSync)) break;
+            tc_fence_after();
+            if (elect_one())
+              pv_steps(t, h * kHalf, steps - h * kHalf, vb + ((h * kHalf * KS * ROW) >> 4), h > 0 || j > sp.jb,
+                       std::integral_constant<int, kHalf>());
+            __syncwarp();
+          }
+          if (active) ++np[0];
+          if (next && active && !role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (mine) umma_commit(&s.v_empty[rv.stage]);
+            if (next) qk_issue(j + 1, t, 0, sp);
+          }
+          __syncwarp();
+          if (mine) rv.next();
+          if (next) rk.next();
+          if (active && j == sp.je - 1) finish(flags);
         }
       } else {
         for (int j = it.kb0; j < it.kb1 && role.live; ++j, ++nblk) {
@@ -522,8 +622,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
   __syncwarp();
   if (elect_one()) umma_commit(&s.drain[who]);
   __syncwarp();
-  volatile int never = 0;
-  wait_phase(&s.drain[who], 0, &never, a.status, kStatusDrain, kDrainLimitCycles);
+  role.drain(&s.drain[who], 0);
 }
 
 // --------------------------------------------------------------------- V preparation
@@ -536,9 +635,11 @@ __device__ __forceinline__ void tc_prepare(const PrefillArgs& a, TcSmem<C>& s, i
   PfItem it{};
   uint32_t items = 0;
   for (; role.item(items, it); ++items) {
+#pragma unroll 1
     for (int j = it.kb0; j < it.kb1 && role.live; ++j) {
       const bool prepare = needs_prep(a, it, j);
       const int stages = v_stages<C>(it, j);
+#pragma unroll 1
       for (int i = 0; i < stages; ++i, rv.next()) {
         // (stages are passed over in order too: a wait tells phases apart by parity only)
         if (!role.wait(&s.v_full[rv.stage], rv.phase, kStatusFull)) break;
@@ -547,11 +648,13 @@ __device__ __forceinline__ void tc_prepare(const PrefillArgs& a, TcSmem<C>& s, i
           const int end = min(C::kVK, (it.hi - k0 + KS - 1) / KS * KS);  // slots the products read
           constexpr int kPieces = C::kRow / 16;
           bool fix = false;
+#pragma unroll 1
           for (int p = lane; p < end * kPieces; p += 32) {  // a 16-byte piece of a slot's row
             const int t = k0 + p / kPieces;
             const bool none = t < it.lo_exact || t >= it.hi;
             const bool all = t <= it.pos0 && (a.window == 0 || t >= it.hi - a.window);
             if (all && !none) continue;
+#pragma unroll 1
             for (int cb = 0; cb < C::kVBlocks; ++cb) {
               uint4* at = reinterpret_cast<uint4*>(s.v[rv.stage] + cb * C::kVBlockBytes + p * 16);
               if (none) {
@@ -595,12 +698,12 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
   const int tile_toks = 128 / a.group;
   const int t = NT == 2 ? warp >> 2 : 0;
   const int row = tid & 127;
-  const int tok = row / a.group, g = row - tok * a.group;
+  const int tok = row / a.group;
   const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes a warp, lane in bits 16..
   const uint32_t tO = tmem + lane_base + C::kTmemO + t * DV;
   TcRole<C> role{a, s, lane};
   PfItem it{};
-  uint32_t items = 0, no = 0;
+  uint32_t items = 0;
   uint32_t blocks = 0;  // of this tile; one tile: the parity is the buffer
   for (; role.item(items, it); ++items) {
     const TileSpan sp = tile_span(a, it, t, tile_toks);
@@ -615,7 +718,8 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
         const float ks = a.k_scale[it.head] * (a.neg_scale ? -1.f : 1.f);
         const uint4* src = reinterpret_cast<const uint4*>(
             static_cast<const __nv_bfloat16*>(a.q) +
-            (static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads + it.head * a.group + g) * D);
+            (static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads + it.head * a.group + row -
+             tok * a.group) * D);
         uint32_t most = 0;  // largest magnitude, as bf16 bits
         if (valid) {
 #pragma unroll 8
@@ -714,98 +818,157 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        // weights of keys 64 h .. 64 h + 63; the issuer starts on the first half at once
-        uint32_t p[32];
+        // weights of keys 64 h .. 64 h + 63, stored by 32; the issuer starts on the first half at once
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float2 w[2];
+        for (int q = 0; q < 2; ++q) {
+          uint32_t p[16];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int c = 64 * h + 4 * e + 2 * i;
-            w[i] = fma2(make_float2(x[c], x[c + 1]), scale2, mb2);
-            w[i].x = ex2(w[i].x);
-            w[i].y = ex2(w[i].y);
-            sum[i] = add2(sum[i], w[i]);
+          for (int e = 0; e < 8; ++e) {
+            float2 w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int c = 64 * h + 32 * q + 4 * e + 2 * i;
+              w[i] = fma2(make_float2(x[c], x[c + 1]), scale2, mb2);
+              w[i].x = ex2(w[i].x);
+              w[i].y = ex2(w[i].y);
+              sum[i] = add2(sum[i], w[i]);
+            }
+            if constexpr (FP8) {
+              uint32_t h0, h1, l0, l1;
+              e4m3x2_terms(w[0].x, w[0].y, h0, l0);
+              e4m3x2_terms(w[1].x, w[1].y, h1, l1);
+              p[e] = h0 | (h1 << 16);
+              p[8 + e] = l0 | (l1 << 16);
+            } else {
+              p[2 * e] = pack_bf16(w[0].x, w[0].y);
+              p[2 * e + 1] = pack_bf16(w[1].x, w[1].y);
+            }
           }
           if constexpr (FP8) {
-            uint32_t h0, h1, l0, l1;
-            e4m3x2_terms(w[0].x, w[0].y, h0, l0);
-            e4m3x2_terms(w[1].x, w[1].y, h1, l1);
-            p[e] = h0 | (h1 << 16);
-            p[16 + e] = l0 | (l1 << 16);
+            tmem_st8(tS + 16 * h + 8 * q, p);
+            tmem_st8(tS + 32 + 16 * h + 8 * q, p + 8);
           } else {
-            p[2 * e] = pack_bf16(w[0].x, w[0].y);
-            p[2 * e + 1] = pack_bf16(w[1].x, w[1].y);
+            tmem_st16(tS + 32 * h + 16 * q, p);
           }
-        }
-        if constexpr (FP8) {
-          tmem_st16(tS + 16 * h, p);
-          tmem_st16(tS + 32 + 16 * h, p + 16);
-        } else {
-          tmem_st32(tS + 32 * h, p);
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&s.p_ready[h][buf]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.p_ready[h][buf]);
       }
       const float2 both = add2(sum[0], sum[1]);
       l += both.x + both.y;
     }
     if (!role.live) break;
 
-    const bool any = sp.je > sp.jb;  // O holds sums of this tile
-    int flags = 0;
-    if (any) {
-      if (!role.wait(&s.o_full[t], no, kStatusSync)) break;
-      ++no;
-      tc_fence_after();
-      flags = s.flags[t];
-    }
-    const bool split = it.kb0 > 0 || it.pieces > 0;
-    if (it.pieces > 0 && tid == 0)
-      a.splits[blockIdx.x] = PrefillSplit{it.pieces, it.row0, it.ntok, it.head, it.part};
-    const long long rec = (2ll * blockIdx.x + (it.kb0 > 0 ? 1 : 0)) * (NT * 128) + t * 128 + row;
-    const bool bad = it.bad || (flags & kItemBad);
-    const float vs = FP8 ? a.v_scale[it.head] : 1.f;
-    const float inv = bad ? CUDART_NAN_F : vs / l;
-    const uint32_t tO = tmem + lane_base + C::kTmemO + t * DV;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
-                         (static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads + it.head * a.group + g) *
-                             D + it.part * DV;
-    if (split && valid) a.ml[rec] = make_float2(bad ? CUDART_NAN_F : m, l);
+    if (!role.wait(&s.l_free[t], items ^ 1u, kStatusSync)) break;
+    s.ml[t][row] = make_float2(m, l);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.l_full[t]);
+    role.item_done(items);
+  }
+}
+
+// --------------------------------------------------------------------- epilogue
+// A warpgroup of its own divides O by the rows' sums and stores it (or, of a
+// split item, the sums as they are), tile by tile, while the softmax threads
+// are at the next item.
+template <typename C>
+__device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, uint32_t tmem, int row) {
+  constexpr int D = C::kD, NT = C::kNT, DV = C::kDV;
+  constexpr bool FP8 = C::kFp8;
+  const int lane = row & 31;
+  const int tile_toks = 128 / a.group;
+  const int tok = row / a.group, g = row - tok * a.group;
+  const uint32_t lane_base = static_cast<uint32_t>(row >> 5) << 21;
+  TcRole<C> role{a, s, lane};
+  PfItem it{};
+  uint32_t items = 0, no = 0;  // no: parity of a tile's accumulators in bit t
+  for (; role.item(items, it); ++items) {
 #pragma unroll 1
-    for (int c = 0; c < DV; c += 32) {
-      float o[32];
+    for (int t = 0; t < NT; ++t) {
+      const uint32_t tO = tmem + lane_base + C::kTmemO + t * DV;
+      const TileSpan sp = tile_span(a, it, t, tile_toks);
+      const bool valid = tok < tile_toks && tok < sp.ntok;
+      const int pos = it.pos0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1);
+      if (!role.wait(&s.l_full[t], items, kStatusSync)) break;
+      const float m = s.ml[t][row].x, l = s.ml[t][row].y;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.l_free[t]);
+      const bool any = sp.je > sp.jb;  // O holds sums of this tile
+      int flags = 0;
       if (any) {
-        tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
-        tmem_wait_ld();
-        if (flags & kItemFix) {
-          add_taken_values<FP8>(a, it, D, pos, it.part * DV + c, o);
-          __syncwarp();
+        if (!role.wait(&s.o_full[t], no >> t, kStatusSync)) break;
+        no ^= 1u << t;
+        tc_fence_after();
+        flags = s.flags[t];
+        if (flags & kItemFix) add_taken_values<FP8>(a, it, D, pos, DV, tO);
+      }
+      const bool split = it.kb0 > 0 || it.pieces > 0;
+      if (it.pieces > 0 && t == 0 && row == 0)
+        a.splits[blockIdx.x] = PrefillSplit{it.pieces, it.row0, it.ntok, it.head, it.part};
+      const long long rec = (2ll * blockIdx.x + (it.kb0 > 0 ? 1 : 0)) * (NT * 128) + t * 128 + row;
+      const bool bad = it.bad || (flags & kItemBad);
+      const float vs = FP8 ? a.v_scale[it.head] : 1.f;
+      const float mul = split ? vs : bad ? CUDART_NAN_F : vs / l;
+      if (split && valid) a.ml[rec] = make_float2(bad ? CUDART_NAN_F : m, l);
+      // Rows go out four lanes to a row: a lane's 16-byte pieces of its own row
+      // are exchanged within groups of four, so that a store touches eight rows
+      // of 64 bytes and not 32 of 16 (which took 7000 cycles an item).
+      const bool put = valid && !(split && l == 0.f);  // (the combine reads no sums of a row without weight)
+      const long long mine = split ? rec * DV
+                                   : (static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads +
+                                      it.head * a.group + g) * D + it.part * DV;
+      long long at[4];  // of the group's rows; -1: not written
+#pragma unroll
+      for (int r = 0; r < 4; ++r) at[r] = __shfl_sync(0xffffffffu, put ? mine : -1ll, (lane & ~3) + r);
+#pragma unroll 1
+      for (int c = 0; c < DV; c += 32) {
+        float o[32];
+        if (any) {
+          tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
-      } else {
+        if (split) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          for (int q = 0; q < 2; ++q) {
+            uint4 x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = make_uint4(__float_as_uint(o[16 * q + 4 * e] * mul), __float_as_uint(o[16 * q + 4 * e + 1] * mul),
+                                __float_as_uint(o[16 * q + 4 * e + 2] * mul),
+                                __float_as_uint(o[16 * q + 4 * e + 3] * mul));
+            transpose4(x, lane);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (at[r] >= 0) *reinterpret_cast<uint4*>(a.part + at[r] + c + 16 * q + 4 * (lane & 3)) = x[r];
+          }
+        } else {
+          uint4 x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[e] = make_uint4(pack_bf16(o[8 * e] * mul, o[8 * e + 1] * mul),
+                              pack_bf16(o[8 * e + 2] * mul, o[8 * e + 3] * mul),
+                              pack_bf16(o[8 * e + 4] * mul, o[8 * e + 5] * mul),
+                              pack_bf16(o[8 * e + 6] * mul, o[8 * e + 7] * mul));
+          transpose4(x, lane);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (at[r] >= 0)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at[r] + c + 8 * (lane & 3)) = x[r];
+        }
+        __syncwarp();  // the next load of tensor memory is the whole warp's
       }
-      if (valid && split && l != 0.f) {  // (the combine reads no sums of a row without weight)
-        float4* p = reinterpret_cast<float4*>(a.part + rec * DV + c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = make_float4(o[4 * e] * vs, o[4 * e + 1] * vs, o[4 * e + 2] * vs, o[4 * e + 3] * vs);
-      } else if (valid && !split) {
-        uint4* p = reinterpret_cast<uint4*>(dst + c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          p[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
-                            pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                            pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                            pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+      if (any) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.o_free[t]);
       }
-      __syncwarp();  // the next load of tensor memory is the whole warp's
     }
-    if (any) {
-      tc_fence_before();
-      mbar_arrive(&s.o_free[t]);
-    }
+    if (!role.live) break;
     role.item_done(items);
   }
 }
@@ -815,11 +978,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ PrefillArgs a) {
   constexpr int NT = C::kNT;
-  extern __shared__ unsigned char raw[];
-  TcSmem<C>& s = *reinterpret_cast<TcSmem<C>*>(
-      raw + ((1024 - (static_cast<uint32_t>(__cvta_generic_to_shared(raw)) & 1023)) & 1023));
+  extern __shared__ __align__(1024) unsigned char raw[];  // whole swizzle atoms
+  TcSmem<C>& s = *reinterpret_cast<TcSmem<C>*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kLoader = NT * 4, kIssuer = kLoader + 1, kPrep = kLoader + 3;
+  constexpr int kEpilogue = NT * 4, kLoader = kEpilogue + 4, kIssuer = kLoader + 1, kPrep = kLoader + 3;
 
   if (tid == 0) {
     a.splits[blockIdx.x].pieces = 0;
@@ -837,18 +999,20 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       mbar_init(&s.q_full[i], C::kFp8 ? 128 : 1);
       mbar_init(&s.q_empty[i], 1);
       mbar_init(&s.o_full[i], 2);        // the commit, and the issuer's flags
-      mbar_init(&s.o_free[i], 128);
+      mbar_init(&s.o_free[i], 4);        // warps of a warpgroup
+      mbar_init(&s.l_full[i], 4);
+      mbar_init(&s.l_free[i], 4);
     }
     for (int i = 0; i < C::kNumS; ++i) {
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.s_free[i], 1);
-      mbar_init(&s.p_ready[0][i], 128);
-      mbar_init(&s.p_ready[1][i], 128);
+      mbar_init(&s.p_ready[0][i], 4);
+      mbar_init(&s.p_ready[1][i], 4);
       mbar_init(&s.drain[i], 1);
     }
     for (int i = 0; i < C::kItems; ++i) {
       mbar_init(&s.item_full[i], 1);
-      mbar_init(&s.item_empty[i], 3 + 4 * NT);  // issuers, preparation, softmax warps
+      mbar_init(&s.item_empty[i], 7 + 4 * NT);  // issuers, preparation, epilogue and softmax warps
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -860,23 +1024,27 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   }
   tc_fence_before();
   PfWalk w;
-  pf_begin(a, s.scan, w);
+  pf_begin(a, reinterpret_cast<long long*>(s.ml), w);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem;
-  // A softmax thread holds a row of 128 scores: with two softmax warpgroups
-  // the 168 registers a thread is launched with are moved to them (128 x 88 +
-  // 256 x 208 = 384 x 168).
+  // A softmax thread holds a row of 128 scores; registers move to it from the
+  // other warpgroups (two tiles: 512 x 128 = 128 x (64 + 80) + 256 x 184; one:
+  // 384 x 168 = 128 x (120 + 144 + 240)).
   if (warp >= kLoader) {
-    if constexpr (NT == 2) regs_dec<88>();
-    if (warp == kLoader)
+    regs_dec<NT == 2 ? 64 : 120>();
+    if (warp == kLoader) {
       tc_loader<C>(tq, tk, tv, a, s, w, lane);
-    else if (warp == kPrep)
+    } else if (warp == kPrep) {
       tc_prepare<C>(a, s, lane);
-    else
+    } else {
       tc_issuer<C>(a, s, tmem, warp - kIssuer, lane);
+    }
+  } else if (warp >= kEpilogue) {
+    regs_dec<NT == 2 ? 80 : 144>();
+    tc_epilogue<C>(a, s, tmem, tid - kEpilogue * 32);
   } else {
-    if constexpr (NT == 2) regs_inc<208>();
+    regs_inc<NT == 2 ? 184 : 240>();
     tc_softmax<C>(a, s, tmem, tid);
   }
   // every role is done with tensor memory
@@ -886,11 +1054,19 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (tid == 0 && s.abort_flag) {
+    atomicOr(a.status, static_cast<unsigned>(s.abort_flag) & 0xffu);
+    if (atomicCAS(a.status + 1, 0u, 1u + blockIdx.x) == 0u) {  // first in the grid: where
+      a.status[2] = static_cast<unsigned>(s.abort_flag);
+      a.status[3] = s.abort_at[0];
+      a.status[4] = s.abort_at[1];
+    }
+  }
 }
 
 template <typename C>
 struct TcVariant {
-  static constexpr size_t smem = sizeof(TcSmem<C>) + 1024;
+  static constexpr size_t smem = sizeof(TcSmem<C>);
   static_assert(smem <= 232448, "does not fit in shared memory");
   static cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PrefillArgs& a,
                             int grid, cudaStream_t stream) {
