@@ -121,17 +121,14 @@ struct PfItem {
 struct PfWalk {
   long long x, end;       // weights: next item's part starts at x
   long long item_x;       // weight where the current item starts
-  long long quot;         // total weight = quot * ctas + rem
-  unsigned rem;
+  long long total, quot;  // total weight, and of one share (the last takes the remainder)
   int ctas;               // CTAs with a share
   int cta;                // this CTA
   PfSeq s;
   int b, vh, tile, heads;
 
   // Where CTA c's share starts.
-  __device__ __forceinline__ long long share(unsigned c) const {
-    return quot * c + rem * c / static_cast<unsigned>(ctas);
-  }
+  __device__ __forceinline__ long long share(unsigned c) const { return c >= static_cast<unsigned>(ctas) ? total : quot * c; }
 
   // kb(r): block boundary nearest to weight r of an item.
   __device__ __forceinline__ static int cut(long long r, long long W, int nkv) {
@@ -209,35 +206,37 @@ __device__ __forceinline__ bool pf_share(const PrefillArgs& a, long long total, 
   w.cta = blockIdx.x;
   w.x = w.end = 0;
   if (total == 0 || w.cta >= w.ctas) return false;
-  w.quot = static_cast<unsigned long long>(total) / static_cast<unsigned>(w.ctas);
-  w.rem = static_cast<unsigned>(total - w.quot * w.ctas);
+  w.total = total;
+  const int shift = total >> 32 ? 16 : 0;  // (a 32-bit division: the shares need not be even to the last token)
+  w.quot = static_cast<long long>(static_cast<unsigned>(total >> shift) / static_cast<unsigned>(w.ctas)) << shift;
   w.x = w.share(blockIdx.x);
   w.end = w.share(blockIdx.x + 1);
   return w.x < w.end;
 }
 
-// The item that holds weight w.x, in sequence b whose items start at weight `start`.
-__device__ __forceinline__ void pf_locate(const PrefillArgs& a, int b, long long start, PfWalk& w) {
+// The item that holds weight w.x, in sequence b whose items start at weight
+// `start`.  By one whole warp: 32 tiles are weighed at a time.
+__device__ __forceinline__ void pf_locate(const PrefillArgs& a, int b, long long start, int lane, PfWalk& w) {
   w.b = b;
   w.s = pf_seq(a, b);
-  // first the head, then by bisection the tile: W(lo) <= x - start < W(hi), W(0) = 0
-  int lo = 0, hi = w.s.tiles, at = w.s.tiles;
+  int lo = 0, hi = w.s.tiles, step = w.s.tiles;  // first the head (weight of all tiles), then the tile: W(0) = 0
   long long at_lo = 0;
   w.vh = -1;
 #pragma unroll 1
-  for (;;) {
-    const long long m = pf_weight(a, w.s, at);
+  do {
+    const int K = min(lo + (lane + 1) * step, hi);
+    const long long m = pf_weight(a, w.s, K);
     if (w.vh < 0) {
       for (w.vh = 0; w.x - start >= m; start += m) ++w.vh;
-    } else if (m <= w.x - start) {
-      lo = at;
-      at_lo = m;
     } else {
-      hi = at;
+      const unsigned below = __ballot_sync(0xffffffffu, K < hi && m <= w.x - start);
+      const int n = __popc(below);  // candidates up to there weigh no more
+      if (n > 0) at_lo = __shfl_sync(0xffffffffu, m, n - 1);
+      hi = min(hi, lo + (n + 1) * step);
+      lo += n * step;
     }
-    if (hi - lo <= 1) break;
-    at = (lo + hi) >> 1;
-  }
+    step = (hi - lo + 31) / 32;
+  } while (hi - lo > 1);
   w.tile = lo;
   w.item_x = start + at_lo;
 }
@@ -252,9 +251,10 @@ __device__ __forceinline__ long long pf_warp_scan(long long x, int lane) {
 }
 
 // The CTA's share: every thread calls it once, with all threads of the CTA;
-// `scan` holds blockDim.x / 32 + 4 values of shared memory.  A batch of up to
+// `scan` holds blockDim.x / 32 + 4 values of shared memory.  The walk is valid
+// in the warps for which `walks` is true.  A batch of up to
 // blockDim.x sequences takes one pass; a larger one is summed first.
-__device__ __forceinline__ void pf_begin(const PrefillArgs& a, long long* scan, PfWalk& w) {
+__device__ __forceinline__ void pf_begin(const PrefillArgs& a, long long* scan, bool walks, PfWalk& w) {
   const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nth >> 5;
   const int chunks = static_cast<int>((static_cast<unsigned>(a.num_seqs) + nth - 1) / nth);
   if (tid == 0) scan[warps] = -1;
@@ -289,7 +289,7 @@ __device__ __forceinline__ void pf_begin(const PrefillArgs& a, long long* scan, 
     __syncthreads();
     if (find && scan[warps] >= 0) break;
   }
-  pf_locate(a, static_cast<int>(scan[warps]), scan[warps + 1], w);
+  if (walks) pf_locate(a, static_cast<int>(scan[warps]), scan[warps + 1], lane, w);
 }
 
 }  // namespace vt

@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kSimtThreads) prefill_simt_kernel(const Prefil
   constexpr int NC = D / 64;
   if (tid == 0) a.splits[blockIdx.x].pieces = 0;
   PfWalk w;
-  pf_begin(a, s.scan, w);
+  pf_begin(a, s.scan, true, w);
   PfItem it;
   const float sign = a.neg_scale ? -1.f : 1.f;
   while (w.next(a, it)) {

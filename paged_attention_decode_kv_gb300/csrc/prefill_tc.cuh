@@ -30,8 +30,6 @@
 
 #include <math_constants.h>
 
-#include <type_traits>
-
 #include "decode_kernel.cuh"
 #include "prefill_variants.cuh"
 #include "tcgen05.cuh"
@@ -78,7 +76,7 @@ struct TcSmem {
   unsigned long long l_full[C::kNT], l_free[C::kNT];
   unsigned long long o_full[C::kNT], o_free[C::kNT];
   unsigned long long item_full[C::kItems], item_empty[C::kItems];
-  unsigned long long drain[2];
+  unsigned long long turn[2], drain[2];
   PfItem items[C::kItems];
   alignas(8) float2 ml[C::kNT][128];    // rows' (reference maximum, sum) for the epilogue (first: the partition's scan)
   uint32_t tmem;
@@ -180,16 +178,13 @@ __device__ __forceinline__ void add_taken_values(const PrefillArgs& a, const PfI
 // All ones in the place of a word's elements that are not finite.
 template <bool FP8>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-  uint32_t m = 0;
   if constexpr (FP8) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 8)
-      if (((w >> i) & 0x7fu) == 0x7fu) m |= 0xffu << i;
-    return m;
+    const uint32_t m = (((w & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;  // 1 for the codes 0x7f and 0xff
+    return m * 0xffu;
+  } else {
+    const uint32_t m = (((w & 0x7f807f80u) + 0x00800080u) >> 15) & 0x00010001u;  // exponents of all ones carry
+    return m * 0xffffu;
   }
-  if ((w & 0x7f80u) == 0x7f80u) m |= 0xffffu;
-  if ((w & 0x7f800000u) == 0x7f800000u) m |= 0xffff0000u;
-  return m;
 }
 
 // Two floats as E4M3 terms, hi + lo: lo is the rest that hi leaves, itself
@@ -275,22 +270,24 @@ struct TcRole {
 
   // Bounded wait on an mbarrier phase.  A wait that passes `limit` clock
   // cycles raises the CTA's abort flag, with what to report at the end, and
-  // every other wait then gives up too.  (Short code: it is inlined often,
-  // and the roles' loops together have to stay in the instruction cache.)
+  // every other wait then gives up too.  (Short code where the wait is met:
+  // it is inlined often, and the roles' loops together have to stay in the
+  // instruction caches.)
   __device__ __forceinline__ bool wait(unsigned long long* bar, uint32_t parity, unsigned code) {
-    if (live && !probe(bar, parity & 1u)) {
+    if (__builtin_expect(!__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u)), 0)) {
       const long long t0 = clock64();
-      do {
-        if (s.abort_flag) live = false;
-        if (live && clock64() - t0 > a.wait_limit) {
+      bool met = false;
+      while (live && !met) {
+        met = __all_sync(0xffffffffu, probe(bar, parity & 1u));
+        if (!met && __any_sync(0xffffffffu, s.abort_flag != 0)) live = false;
+        if (!met && live && __any_sync(0xffffffffu, clock64() - t0 > a.wait_limit)) {
           s.abort_at[0] = smem_addr(bar);
           s.abort_at[1] = parity & 1u;
           s.abort_flag = static_cast<int>(code | (threadIdx.x << 8));
           live = false;
         }
-      } while (live && !probe(bar, parity & 1u));
+      }
     }
-    live = __all_sync(0xffffffffu, live);
     return live;
   }
   // For copies and MMAs in flight, whatever the abort flag says.
@@ -450,7 +447,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
   Ring<C::kStagesK> rk;
   Ring<C::kStagesV> rv;
   uint32_t vphase = 0;  // of v_ready, one bit a stage
-  uint32_t items = 0, nq = 0, no = 0, np[2] = {};
+  uint32_t items = 0, nq = 0, no = 0, np[2] = {}, turns = 0;
   uint32_t nblk = 0;    // one tile: blocks so far, whose parity is the buffer
   const int t = NT == 2 ? who : 0;
   const bool do_qk = NT == 2 || who == 0, do_pv = NT == 2 || who == 1;
@@ -458,7 +455,8 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
   PfItem it{};
 
   // S(buf) = Q K^T for block j's keys: the MMAs of chunk c and what follows them.  One lane.
-  auto qk_issue = [&](int j, int buf, int c, const TileSpan& sp) {
+  // `pass` (or none) is told before the last column block: the other issuer wakes meanwhile.
+  auto qk_issue = [&](int j, int buf, int c, const TileSpan& sp, unsigned long long* pass) {
     const bool active = j >= sp.jb && j < sp.je;
     if (active) {
       const int keys = min(kPfBlock, it.hi - (it.lo + j * kPfBlock));
@@ -468,16 +466,20 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
       const uint32_t qa = umma_desc_lo(smem_addr(s.q[t]) + c * C::kKBytes, 16);
       const uint32_t kb = umma_desc_lo(smem_addr(s.k[rk.stage]), 16);
       const uint32_t d = tmem + buf * 128, more = c > 0;
-      constexpr int kSteps = ROW / 32;  // MMAs of a block's columns
-#pragma unroll
-      for (int term = 0; term < (FP8 ? 2 : 1); ++term)
-#pragma unroll
-        for (int k = 0; k < C::kKBlocks * kSteps; ++k) {
-          const uint32_t at = ((k / kSteps) * C::kKBlockBytes + (k % kSteps) * 32) >> 4;
-          umma_ss<FP8>(d, qa + ((term * 128 * C::kD) >> 4) + at, kHi, kb + at, kHi, idesc,
-                       term > 0 || k > 0 ? 1u : more);
-        }
+      // (rolled loops: an MMA takes 64 cycles, and unrolled code of a warp that
+      // runs once a block is fetched anew each time)
+      uint32_t acc = more;
+#pragma unroll 1
+      for (int b = 0; b < (FP8 ? 2 : 1) * C::kKBlocks; ++b) {
+        if (b == (FP8 ? 2 : 1) * C::kKBlocks - 1 && pass) mbar_arrive(pass);
+        const int blk = FP8 ? b % C::kKBlocks : b;  // FP8: the high terms of Q, then the low ones
+        uint32_t qx = qa + ((blk * C::kKBlockBytes + (FP8 ? b / C::kKBlocks * 128 * C::kD : 0)) >> 4);
+        uint32_t kx = kb + ((blk * C::kKBlockBytes) >> 4);
+#pragma unroll 1
+        for (int k = 0; k < ROW / 32; ++k, qx += 2, kx += 2, acc = 1u) umma_ss<FP8>(d, qx, kHi, kx, kHi, idesc, acc);
+      }
     }
+    if (!active && pass) mbar_arrive(pass);
     umma_commit(&s.k_empty[rk.stage]);
     if (active && c == C::kKChunks - 1) {
       umma_commit(&s.s_full[buf]);
@@ -489,7 +491,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
     for (int c = 0; c < C::kKChunks; ++c) {
       if (!role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) return;
       tc_fence_after();
-      if (elect_one()) qk_issue(j, buf, c, sp);
+      if (elect_one()) qk_issue(j, buf, c, sp, nullptr);
       __syncwarp();
       rk.next();
     }
@@ -522,15 +524,13 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
   constexpr int kHalf = kPfBlock / 2 / KS;  // k-steps of half a block
   const uint32_t idesc_pv = FP8 ? umma_idesc_e4m3(C::kDV, true) : umma_idesc_f16(true, C::kDV, true);
   const uint32_t d_pv = tmem + C::kTmemO + t * C::kDV;
-  // N k-steps of P V from block k-step `first`; vb: the V stage at that step.  One lane.
-  auto pv_steps = [&](int buf, int first, int n, uint32_t vb, uint32_t acc, auto count) {
-#pragma unroll
-    for (int k = 0; k < decltype(count)::value; ++k) {
-      if (k < n) {
-        const uint32_t b = vb + ((k * KS * ROW) >> 4), from = tmem + buf * 128 + (first + k) * 8;
-        umma_ts<FP8>(d_pv, from, b, kHi, idesc_pv, k > 0 ? 1u : acc);
-        if constexpr (FP8) umma_ts<FP8>(d_pv, from + 32, b, kHi, idesc_pv, 1u);  // P's low terms
-      }
+  // k-steps [first, last) of P V; vb: the V stage at step `first`.  One lane.
+  auto pv_steps = [&](int buf, int first, int last, uint32_t vb, uint32_t acc) {
+    uint32_t from = tmem + buf * 128 + first * 8;
+#pragma unroll 1
+    for (int k = first; k < last; ++k, from += 8, vb += (KS * ROW) >> 4, acc = 1u) {
+      umma_ts<FP8>(d_pv, from, vb, kHi, idesc_pv, acc);
+      if constexpr (FP8) umma_ts<FP8>(d_pv, from + 32, vb, kHi, idesc_pv, 1u);  // P's low terms
     }
   };
   // One tile: O (+)= P(buf) V for block j's keys, V in stages of VK keys.
@@ -550,8 +550,8 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
         tc_fence_after();
         const int first = (h * kPer + i) * kSteps;
         if (elect_one()) {
-          pv_steps(buf, first, steps - first, umma_desc_lo(smem_addr(s.v[rv.stage]), C::kVBlockBytes),
-                   first > 0 || j > sp.jb, std::integral_constant<int, kSteps>());
+          pv_steps(buf, first, min(steps, first + kSteps), umma_desc_lo(smem_addr(s.v[rv.stage]), C::kVBlockBytes),
+                   first > 0 || j > sp.jb);
           umma_commit(&s.v_empty[rv.stage]);
         }
         __syncwarp();
@@ -574,30 +574,39 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
       }
       if constexpr (NT == 2) {
         static_assert(NT == 1 || (C::kVK == kPfBlock && C::kKChunks == 1), "one stage a block");
+        // The tiles take turns: all of one's P V and next Q K^T, then the
+        // other's.  Left to themselves the two issuers' MMAs interleave, both
+        // tiles wait for twice the products and then both wait for the
+        // softmax, in step (3500 cycles a block; the products take 2048).
+        const bool both = it.ntok > tile_toks;
         for (int j = it.kb0 - 1; j < it.kb1 && role.live; ++j) {  // P V of block j, then Q K^T of block j + 1
-          // What can be waited for ahead of the weights is: between them and
-          // the next scores this thread only issues.
+          // What can be waited for ahead of the weights is: after them this
+          // thread only issues.
           const bool mine = j >= it.kb0, active = j >= sp.jb && j < sp.je, next = j + 1 < it.kb1;
           if (mine && !v_here(needs_prep(a, it, j), flags)) break;
-          if (next && !active && !role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) break;
+          if (next && !role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) break;
+          if (active && j == sp.jb && !role.wait(&s.o_free[t], no ^ 1u, kStatusSync)) break;
           const int steps = active ? steps_of(j, sp) : 0;
           const uint32_t vb = umma_desc_lo(smem_addr(s.v[rv.stage]), C::kVBlockBytes);
-#pragma unroll 1
-          for (int h = 0; h < 2 && active; ++h) {
-            if (h == 0 && j == sp.jb && !role.wait(&s.o_free[t], no ^ 1u, kStatusSync)) break;
-            if (!role.wait(&s.p_ready[h][t], np[0], kStatusSync)) break;
+          if (active && !role.wait(&s.p_ready[0][t], np[0], kStatusSync)) break;
+          if (active && !both) {  // nothing else to run meanwhile: the first half's products at once
             tc_fence_after();
-            if (elect_one())
-              pv_steps(t, h * kHalf, steps - h * kHalf, vb + ((h * kHalf * KS * ROW) >> 4), h > 0 || j > sp.jb,
-                       std::integral_constant<int, kHalf>());
+            if (elect_one()) pv_steps(t, 0, min(steps, kHalf), vb, j > sp.jb);
             __syncwarp();
           }
-          if (active) ++np[0];
-          if (next && active && !role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) break;
+          if (active && !role.wait(&s.p_ready[1][t], np[0]++, kStatusSync)) break;
+          if (both && !role.wait(&s.turn[t], turns++ ^ (t ^ 1u), kStatusSync)) break;
           tc_fence_after();
           if (elect_one()) {
+            if (active) {
+              const int from = both ? 0 : kHalf;
+              pv_steps(t, from, steps, vb + ((from * KS * ROW) >> 4), from > 0 || j > sp.jb);
+            }
             if (mine) umma_commit(&s.v_empty[rv.stage]);
-            if (next) qk_issue(j + 1, t, 0, sp);
+            if (next)
+              qk_issue(j + 1, t, 0, sp, both ? &s.turn[t ^ 1] : nullptr);
+            else if (both)
+              mbar_arrive(&s.turn[t ^ 1]);
           }
           __syncwarp();
           if (mine) rv.next();
@@ -645,29 +654,35 @@ __device__ __forceinline__ void tc_prepare(const PrefillArgs& a, TcSmem<C>& s, i
         if (!role.wait(&s.v_full[rv.stage], rv.phase, kStatusFull)) break;
         if (prepare) {
           const int k0 = it.lo + j * kPfBlock + i * C::kVK;
+          constexpr int kPieces = C::kRow / 16;  // 16-byte pieces of a slot's row
+          constexpr int kLines = 32 / kPieces;   // slots a warp takes at a time
           const int end = min(C::kVK, (it.hi - k0 + KS - 1) / KS * KS);  // slots the products read
-          constexpr int kPieces = C::kRow / 16;
+          const int lo = min(end, max(0, it.lo_exact - k0)), hi = min(end, max(lo, it.hi - k0));  // item's keys
+          const int early = a.window == 0 ? 0 : min(hi, max(lo, it.hi - a.window - k0));  // before it some rows' windows
+          const int late = min(hi, max(early, it.pos0 + 1 - k0));                         // from it on later tokens
           bool fix = false;
+          // [0, lo) and [hi, end) zeroed; [lo, early) and [late, hi) looked at
 #pragma unroll 1
-          for (int p = lane; p < end * kPieces; p += 32) {  // a 16-byte piece of a slot's row
-            const int t = k0 + p / kPieces;
-            const bool none = t < it.lo_exact || t >= it.hi;
-            const bool all = t <= it.pos0 && (a.window == 0 || t >= it.hi - a.window);
-            if (all && !none) continue;
+          for (int cb = 0; cb < C::kVBlocks; ++cb) {
+            unsigned char* rows = s.v[rv.stage] + cb * C::kVBlockBytes + lane * 16;
 #pragma unroll 1
-            for (int cb = 0; cb < C::kVBlocks; ++cb) {
-              uint4* at = reinterpret_cast<uint4*>(s.v[rv.stage] + cb * C::kVBlockBytes + p * 16);
-              if (none) {
+            for (int slot = lane / kPieces; slot < end; slot += kLines) {
+              uint4* at = reinterpret_cast<uint4*>(rows + (slot - lane / kPieces) * C::kRow);
+              if (slot >= early && slot < late) {
+                // every row sees these: skip to the later ones
+                slot += (late - slot - 1) / kLines * kLines;
+                continue;
+              }
+              if (slot < lo || slot >= hi) {
                 *at = make_uint4(0, 0, 0, 0);
-              } else {
-                uint4 x = *at;
-                const uint32_t m0 = not_finite<FP8>(x.x), m1 = not_finite<FP8>(x.y), m2 = not_finite<FP8>(x.z),
-                               m3 = not_finite<FP8>(x.w);
-                if (m0 | m1 | m2 | m3) {
-                  fix = true;
-                  x.x &= ~m0, x.y &= ~m1, x.z &= ~m2, x.w &= ~m3;
-                  *at = x;
-                }
+                continue;
+              }
+              uint4 x = *at;
+              const uint32_t m0 = not_finite<FP8>(x.x), m1 = not_finite<FP8>(x.y), m2 = not_finite<FP8>(x.z),
+                             m3 = not_finite<FP8>(x.w);
+              if (m0 | m1 | m2 | m3) {
+                fix = true;
+                *at = make_uint4(x.x & ~m0, x.y & ~m1, x.z & ~m2, x.w & ~m3);
               }
             }
           }
@@ -1008,6 +1023,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       mbar_init(&s.s_free[i], 1);
       mbar_init(&s.p_ready[0][i], 4);
       mbar_init(&s.p_ready[1][i], 4);
+      mbar_init(&s.turn[i], 1);
       mbar_init(&s.drain[i], 1);
     }
     for (int i = 0; i < C::kItems; ++i) {
@@ -1024,7 +1040,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   }
   tc_fence_before();
   PfWalk w;
-  pf_begin(a, reinterpret_cast<long long*>(s.ml), w);
+  pf_begin(a, reinterpret_cast<long long*>(s.ml), warp == kLoader, w);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem;
