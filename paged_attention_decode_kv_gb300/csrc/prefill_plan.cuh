@@ -250,46 +250,36 @@ __device__ __forceinline__ long long pf_warp_scan(long long x, int lane) {
   return x;
 }
 
-// The CTA's share: every thread calls it once, with all threads of the CTA;
-// `scan` holds blockDim.x / 32 + 4 values of shared memory.  The walk is valid
-// in the warps for which `walks` is true.  A batch of up to
-// blockDim.x sequences takes one pass; a larger one is summed first.
-__device__ __forceinline__ void pf_begin(const PrefillArgs& a, long long* scan, bool walks, PfWalk& w) {
-  const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nth >> 5;
-  const int chunks = static_cast<int>((static_cast<unsigned>(a.num_seqs) + nth - 1) / nth);
-  if (tid == 0) scan[warps] = -1;
-  long long total = 0;
+// The CTA's share, by one whole warp: each lane sums the weights of a run of
+// consecutive sequences, a scan over lanes gives the total and the run that
+// holds the share's start, and the warp looks through that run.
+__device__ __forceinline__ void pf_begin(const PrefillArgs& a, int lane, PfWalk& w) {
+  const int heads = a.num_kv_heads * a.v_parts;
+  const int run = static_cast<int>((static_cast<unsigned>(a.num_seqs) + 31u) >> 5);
+  int from = lane * run, to = min(from + run, a.num_seqs);
+  long long before = 0;
+  // round 0: runs of `run` sequences; round 1: the one run, in runs of its own
 #pragma unroll 1
-  for (int i = chunks == 1 ? chunks : 0; i < 2 * chunks; ++i) {
-    const bool find = i >= chunks;
-    const int b = (find ? i - chunks : i) * nth + tid;
-    if (i == chunks && chunks > 1) {
-      if (!pf_share(a, total, w)) return;
-      total = 0;  // now the weight before this chunk
-    }
+  for (int round = 0;; ++round) {
     long long mine = 0;
-    if (b < a.num_seqs) {
-      const PfSeq s = pf_seq(a, b);
-      mine = a.num_kv_heads * a.v_parts * pf_weight(a, s, s.tiles);
-    }
-    const long long inc = pf_warp_scan(mine, lane);
-    if (lane == 31) scan[warp] = inc;
-    __syncthreads();
-    long long base = total;
 #pragma unroll 1
-    for (int k = 0; k < warps; ++k) {
-      if (k < warp) base += scan[k];
-      total += scan[k];
+    for (int b = from; b < to; ++b) {
+      const PfSeq s = pf_seq(a, b);
+      mine += heads * pf_weight(a, s, s.tiles);
     }
-    if (chunks == 1 && !pf_share(a, total, w)) return;
-    if (find && mine > 0 && w.x >= base + inc - mine && w.x < base + inc) {
-      scan[warps] = b;
-      scan[warps + 1] = base + inc - mine;
+    const long long inc = before + pf_warp_scan(mine, lane);
+    if (round == 0 && !pf_share(a, __shfl_sync(0xffffffffu, inc, 31), w)) return;
+    const int hit = __ffs(__ballot_sync(0xffffffffu, w.x < inc)) - 1;
+    before = __shfl_sync(0xffffffffu, inc - mine, hit);
+    const int first = __shfl_sync(0xffffffffu, from, hit), last = __shfl_sync(0xffffffffu, to, hit);
+    if (last - first <= 1) {
+      pf_locate(a, first, before, lane, w);
+      return;
     }
-    __syncthreads();
-    if (find && scan[warps] >= 0) break;
+    const int step = (last - first + 31) >> 5;
+    from = min(first + lane * step, last);
+    to = min(from + step, last);
   }
-  if (walks) pf_locate(a, static_cast<int>(scan[warps]), scan[warps + 1], lane, w);
 }
 
 }  // namespace vt

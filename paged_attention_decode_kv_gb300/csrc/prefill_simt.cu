@@ -26,7 +26,6 @@ struct SimtSmem {
   float k[kPfPage][D + 4];
   float v[kPfPage][D];
   float p[kSimtRows][kPfPage + 4];
-  long long scan[kSimtThreads / 32 + 4];
   int bad;
 };
 
@@ -43,7 +42,7 @@ __global__ void __launch_bounds__(kSimtThreads) prefill_simt_kernel(const Prefil
   constexpr int NC = D / 64;
   if (tid == 0) a.splits[blockIdx.x].pieces = 0;
   PfWalk w;
-  pf_begin(a, s.scan, true, w);
+  pf_begin(a, tid & 31, w);  // each warp for itself
   PfItem it;
   const float sign = a.neg_scale ? -1.f : 1.f;
   while (w.next(a, it)) {

@@ -78,7 +78,7 @@ struct TcSmem {
   unsigned long long item_full[C::kItems], item_empty[C::kItems];
   unsigned long long turn[2], drain[2];
   PfItem items[C::kItems];
-  alignas(8) float2 ml[C::kNT][128];    // rows' (reference maximum, sum) for the epilogue (first: the partition's scan)
+  float2 ml[C::kNT][128];               // rows' (reference maximum, sum) for the epilogue
   uint32_t tmem;
   volatile int stage_bad[C::kStagesV];  // a page id of this stage was out of range
   volatile int stage_fix[C::kStagesV];  // V preparation took out a value that is not finite
@@ -175,16 +175,18 @@ __device__ __forceinline__ void add_taken_values(const PrefillArgs& a, const PfI
   }
 }
 
-// All ones in the place of a word's elements that are not finite.
+// A word whose elements that are not finite (exponents of all ones; the E4M3
+// codes 0x7f and 0xff) carry into the bits of kCarry, and all ones in their place.
+template <bool FP8>
+constexpr uint32_t kCarry = FP8 ? 0x80808080u : 0x80008000u;
+template <bool FP8>
+__device__ __forceinline__ uint32_t carries(uint32_t w) {
+  return FP8 ? (w & 0x7f7f7f7fu) + 0x01010101u : (w & 0x7f807f80u) + 0x00800080u;
+}
 template <bool FP8>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-  if constexpr (FP8) {
-    const uint32_t m = (((w & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;  // 1 for the codes 0x7f and 0xff
-    return m * 0xffu;
-  } else {
-    const uint32_t m = (((w & 0x7f807f80u) + 0x00800080u) >> 15) & 0x00010001u;  // exponents of all ones carry
-    return m * 0xffffu;
-  }
+  const uint32_t m = carries<FP8>(w) & kCarry<FP8>;
+  return FP8 ? (m >> 7) * 0xffu : (m >> 15) * 0xffffu;
 }
 
 // Two floats as E4M3 terms, hi + lo: lo is the rest that hi leaves, itself
@@ -390,6 +392,7 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
     ++items;
     if (!more) break;
     ids_at = -1;
+    if (it.kb1 > it.kb0) page_of((it.lo + it.kb0 * kPfBlock) / kPfPage, 0);  // table entries on their way
 #pragma unroll 1
     for (int t = 0; t < C::kNT && !C::kFp8; ++t) {
       const TileSpan sp = tile_span(a, it, t, tile_toks);
@@ -660,33 +663,50 @@ __device__ __forceinline__ void tc_prepare(const PrefillArgs& a, TcSmem<C>& s, i
           const int lo = min(end, max(0, it.lo_exact - k0)), hi = min(end, max(lo, it.hi - k0));  // item's keys
           const int early = a.window == 0 ? 0 : min(hi, max(lo, it.hi - a.window - k0));  // before it some rows' windows
           const int late = min(hi, max(early, it.pos0 + 1 - k0));                         // from it on later tokens
-          bool fix = false;
           // [0, lo) and [hi, end) zeroed; [lo, early) and [late, hi) looked at
+          unsigned char* piece = s.v[rv.stage] + lane * 16;
+          const int line = lane / kPieces;
+          auto zero = [&](int first, int last) {
 #pragma unroll 1
-          for (int cb = 0; cb < C::kVBlocks; ++cb) {
-            unsigned char* rows = s.v[rv.stage] + cb * C::kVBlockBytes + lane * 16;
+            for (int slot = first; slot + line < last; slot += kLines)
+#pragma unroll
+              for (int cb = 0; cb < C::kVBlocks; ++cb)
+                *reinterpret_cast<uint4*>(piece + cb * C::kVBlockBytes + slot * C::kRow) = make_uint4(0, 0, 0, 0);
+          };
+          bool fix = false;
+          auto look = [&](int first, int last) {
+            uint32_t seen = 0;
 #pragma unroll 1
-            for (int slot = lane / kPieces; slot < end; slot += kLines) {
-              uint4* at = reinterpret_cast<uint4*>(rows + (slot - lane / kPieces) * C::kRow);
-              if (slot >= early && slot < late) {
-                // every row sees these: skip to the later ones
-                slot += (late - slot - 1) / kLines * kLines;
-                continue;
-              }
-              if (slot < lo || slot >= hi) {
-                *at = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              uint4 x = *at;
-              const uint32_t m0 = not_finite<FP8>(x.x), m1 = not_finite<FP8>(x.y), m2 = not_finite<FP8>(x.z),
-                             m3 = not_finite<FP8>(x.w);
-              if (m0 | m1 | m2 | m3) {
-                fix = true;
-                *at = make_uint4(x.x & ~m0, x.y & ~m1, x.z & ~m2, x.w & ~m3);
+            for (int slot = first; slot < last; slot += 4 * kLines) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int at = min(slot + u * kLines, last - 1 - line);  // (a piece may be looked at twice)
+                if (at < 0) continue;
+#pragma unroll
+                for (int cb = 0; cb < C::kVBlocks; ++cb) {
+                  const uint4 x = *reinterpret_cast<const uint4*>(piece + cb * C::kVBlockBytes + at * C::kRow);
+                  seen |= carries<FP8>(x.x) | carries<FP8>(x.y) | carries<FP8>(x.z) | carries<FP8>(x.w);
+                }
               }
             }
+            if (!__any_sync(0xffffffffu, seen & kCarry<FP8>)) return;
+#pragma unroll 1
+            for (int slot = first; slot + line < last; slot += kLines)
+#pragma unroll 1
+              for (int cb = 0; cb < C::kVBlocks; ++cb) {
+                uint4* at = reinterpret_cast<uint4*>(piece + cb * C::kVBlockBytes + slot * C::kRow);
+                uint4 x = *at;
+                x.x &= ~not_finite<FP8>(x.x), x.y &= ~not_finite<FP8>(x.y);
+                x.z &= ~not_finite<FP8>(x.z), x.w &= ~not_finite<FP8>(x.w);
+                *at = x;
+              }
+            fix = true;
+          };
+#pragma unroll 1
+          for (int side = 0; side < 2; ++side) {
+            zero(side ? hi : 0, side ? end : lo);
+            look(side ? late : lo, side ? hi : early);
           }
-          fix = __any_sync(0xffffffffu, fix);
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) {
@@ -783,28 +803,41 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
       const uint32_t tS = tmem + lane_base + buf * 128;
       if (!role.wait(&s.s_full[buf], NT == 2 ? blocks : blocks >> 1, kStatusSync)) break;
       tc_fence_after();
-      float x[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
-      tmem_wait_ld();
       const int k0 = it.lo + j * kPfBlock;
       // rows see keys (pos - window, pos]; block columns [from, upto]
-      const bool masked = k0 + kPfBlock > it.pos0 + sp.tok0 + 1 ||
-                          (a.window > 0 && k0 < it.pos0 + sp.tok0 + sp.ntok - a.window);
-      if (masked) {
+      if (k0 + kPfBlock > it.pos0 + sp.tok0 + 1 ||
+          (a.window > 0 && k0 < it.pos0 + sp.tok0 + sp.ntok - a.window)) {
         const int upto = pos - k0, from = a.window > 0 ? pos - a.window + 1 - k0 : 0;
+#pragma unroll 1
+        for (int q = 0; q < kPfBlock; q += 32) {
+          float x[32];
+          tmem_ld32(tS + q, reinterpret_cast<uint32_t*>(x));
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c > upto || c < from) x[c] = -CUDART_INF_F;
+          for (int c = 0; c < 32; ++c)
+            if (c > upto - q || c < from - q) x[c] = -CUDART_INF_F;
+          tmem_st32(tS + q, reinterpret_cast<const uint32_t*>(x));
+        }
+        tmem_wait_st();
       }
-      float top[4] = {x[0], x[1], x[2], x[3]};  // independent chains
+      // The scores are read twice, for their maximum and for the weights: a
+      // read of tensor memory takes 25 cycles, and the loop over halves keeps
+      // the code of a block short enough for the instruction caches.
+      float most = -CUDART_INF_F;
+      {
+        float x[128];
 #pragma unroll
-      for (int c = 4; c < 124; c += 8)
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
+        tmem_wait_ld();
+        float top[4] = {x[0], x[1], x[2], x[3]};  // independent chains
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top[e] = max3(top[e], x[c + 2 * e], x[c + 2 * e + 1]);
+        for (int c = 4; c < 124; c += 8)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], x[124 + e]);
-      const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+          for (int e = 0; e < 4; ++e) top[e] = max3(top[e], x[c + 2 * e], x[c + 2 * e + 1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], x[124 + e]);
+        most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+      }
       if (__any_sync(0xffffffffu, most > m + kLazy)) {
         const float mn = fmaxf(m, most);
         const float keep = m == -CUDART_INF_F ? 0.f : ex2(m - mn);
@@ -831,9 +864,13 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
       const float mb = kWeightExp - (m == -CUDART_INF_F ? 0.f : m);
       const float2 scale2 = make_float2(scale, scale), mb2 = make_float2(mb, mb);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        // weights of keys 64 h .. 64 h + 63, stored by 32; the issuer starts on the first half at once
+        // weights of keys 64 h .. 64 h + 63; the issuer may start on the first half at once
+        float x[64];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) tmem_ld32(tS + 64 * h + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
+        tmem_wait_ld();
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t p[16];
@@ -842,7 +879,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
             float2 w[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const int c = 64 * h + 32 * q + 4 * e + 2 * i;
+              const int c = 32 * q + 4 * e + 2 * i;
               w[i] = fma2(make_float2(x[c], x[c + 1]), scale2, mb2);
               w[i].x = ex2(w[i].x);
               w[i].y = ex2(w[i].y);
@@ -859,6 +896,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
               p[2 * e + 1] = pack_bf16(w[1].x, w[1].y);
             }
           }
+          // (P lies over scores that have been read: columns up to 32 h + 31, or 32 + 16 h + 15)
           if constexpr (FP8) {
             tmem_st8(tS + 16 * h + 8 * q, p);
             tmem_st8(tS + 32 + 16 * h + 8 * q, p + 8);
@@ -1040,15 +1078,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   }
   tc_fence_before();
   PfWalk w;
-  pf_begin(a, reinterpret_cast<long long*>(s.ml), warp == kLoader, w);
+  if (warp == kLoader) pf_begin(a, lane, w);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem;
-  // A softmax thread holds a row of 128 scores; registers move to it from the
-  // other warpgroups (two tiles: 512 x 128 = 128 x (64 + 80) + 256 x 184; one:
-  // 384 x 168 = 128 x (120 + 144 + 240)).
+  // A softmax thread holds a row of 128 scores; with two tiles registers move
+  // to it from the other warpgroups (512 x 128 = 128 x (96 + 96) + 256 x 160).
   if (warp >= kLoader) {
-    regs_dec<NT == 2 ? 64 : 120>();
+    if constexpr (NT == 2) regs_dec<96>();
     if (warp == kLoader) {
       tc_loader<C>(tq, tk, tv, a, s, w, lane);
     } else if (warp == kPrep) {
@@ -1057,10 +1094,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       tc_issuer<C>(a, s, tmem, warp - kIssuer, lane);
     }
   } else if (warp >= kEpilogue) {
-    regs_dec<NT == 2 ? 80 : 144>();
+    if constexpr (NT == 2) regs_dec<96>();
     tc_epilogue<C>(a, s, tmem, tid - kEpilogue * 32);
   } else {
-    regs_inc<NT == 2 ? 184 : 240>();
+    if constexpr (NT == 2) regs_inc<160>();
     tc_softmax<C>(a, s, tmem, tid);
   }
   // every role is done with tensor memory
