@@ -491,81 +491,103 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, kind: int = VT_ROPE_PL
     return torch.tensor(inv, dtype=torch.float64, device=device), amplitude
 
 
-def _rows(name, t, heads=None, head_dim=None, dtype=None, like=None):
+_torch = None
+
+
+def _t():
+    """torch, imported at the first call that takes tensors."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+# The checks below run on every call of operators that take a few microseconds
+# on the GPU: plain comparisons, no helper objects.
+def _row_stride(name, t, T, H, D, dtype, device):
     """Checks packed rows [T][H][D] whose heads are contiguous; the token
     stride in elements."""
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (head_dim is not None and t.shape[2] != head_dim):
-        raise ValueError(f"{name} must be [tokens][heads][head_dim]")
-    _cuda(name, t, like, contiguous=False)
-    if dtype is not None and t.dtype != dtype:
+    if t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    T, H, D = t.shape
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+    if t.shape != (T, H, D):
+        raise ValueError(f"{name} must be [{T}][{H}][{D}], got {tuple(t.shape)}")
+    row, head, one = t.stride()
+    if (one != 1 and D > 1) or (head != D and H > 1):
         raise ValueError(f"{name} must have contiguous heads (only the token stride is free)")
-    return t.stride(0) if T > 1 else max(H * D, t.stride(0))
+    return row if T > 1 else max(row, H * D)
 
 
-def _cuda(name, t, like=None, contiguous=True):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}")
-    if contiguous and not t.is_contiguous():
+def _check_plain(name, t, dtype, device):
+    if t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _ragged(q_starts, block_tables, context_lens, like):
-    import torch
-    for name, t in (("q_starts", q_starts), ("block_tables", block_tables), ("context_lens", context_lens)):
-        _cuda(name, t, like)
-        if t.dtype != torch.int32:
-            raise TypeError("q_starts, block_tables and context_lens must be int32")
+def _check_ragged(torch, q_starts, block_tables, context_lens, device):
+    """(num_seqs, max_blocks) of a ragged batch."""
+    int32 = torch.int32
+    _check_plain("q_starts", q_starts, int32, device)
+    _check_plain("block_tables", block_tables, int32, device)
+    _check_plain("context_lens", context_lens, int32, device)
     B = context_lens.numel()
     if q_starts.numel() != B + 1 or block_tables.dim() != 2 or block_tables.shape[0] != B:
         raise ValueError("q_starts must be [num_seqs + 1] and block_tables [num_seqs][max_blocks]")
-    return B
+    return B, block_tables.shape[1]
 
 
-def _frequencies(inv_freq, like):
-    import torch
-    if inv_freq is None or inv_freq.numel() == 0:
-        return None, 0
-    _cuda("inv_freq", inv_freq, like)
-    if inv_freq.dtype != torch.float64:
-        raise TypeError("inv_freq must be float64")
-    return inv_freq.data_ptr(), 2 * inv_freq.numel()
+def _check_scales(torch, k_scale, v_scale, heads, device):
+    _check_plain("k_scale", k_scale, torch.float32, device)
+    _check_plain("v_scale", v_scale, torch.float32, device)
+    if k_scale.numel() != heads or v_scale.numel() != heads:
+        raise TypeError("k_scale and v_scale must be float32 [num_kv_heads]")
 
 
-def _codes(t):
-    import torch
-    t = t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t
+def _codes(torch, t):
+    if t.dtype == torch.float8_e4m3fn:
+        t = t.view(torch.uint8)
     if t.dtype != torch.uint8:
         raise TypeError("the caches must be uint8 or float8_e4m3fn E4M3 codes")
     return t
 
 
-def _scales(k_scale, v_scale, heads, like):
-    import torch
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _cuda(name, t, like)
-        if t.dtype != torch.float32 or t.numel() != heads:
-            raise TypeError("k_scale and v_scale must be float32 [num_kv_heads]")
+def _check_freq(torch, inv_freq, device):
+    """(pointer, rot_dim) of a frequency table, or of none."""
+    if inv_freq is None:
+        return None, 0
+    _check_plain("inv_freq", inv_freq, torch.float64, device)
+    n = inv_freq.numel()
+    return (inv_freq.data_ptr(), 2 * n) if n else (None, 0)
 
 
-def _on(t, stream):
-    """The tensors' device made current, and the stream handle on it."""
-    import torch
+def _cuda_device(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
 
-    class _Guard:
-        def __enter__(self):
-            self.guard = torch.cuda.device(t.device)
-            self.guard.__enter__()
-            return _stream_handle(stream)
 
-        def __exit__(self, *exc):
-            return self.guard.__exit__(*exc)
+def _launch(torch, device, stream, where, call, before, after):
+    """call(*before, stream handle, *after) with the tensors' device current;
+    raises VtError."""
+    index = device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            status = call(*before, _stream_on(torch, index, stream), *after)
+    else:
+        status = call(*before, _stream_on(torch, index, stream), *after)
+    if status != VT_OK:
+        _check(status, where)
 
-    return _Guard()
+
+def _stream_on(torch, index, stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def rope(x, positions, inv_freq, interleaved: bool = False, amplitude: float = 1.0, out=None, stream=None):
@@ -576,72 +598,68 @@ def rope(x, positions, inv_freq, interleaved: bool = False, amplitude: float = 1
     ``rope_frequencies``).  Returns out [T][H][D] (allocated unless given; x
     itself rotates in place).  A negative position turns back, so the gradient
     of ``rope(x, p)`` is ``rope(grad, -p)``.  Asynchronous on ``stream``."""
-    import torch
-    x_stride = _rows("x", x)
-    T, H, D = x.shape
+    torch = _t()
+    device = _cuda_device("x", x)
     code = dtype_code(x)
-    _cuda("positions", positions, x)
-    if positions.dtype != torch.int32 or positions.numel() != T:
-        raise TypeError("positions must be int32 [tokens]")
-    freq, rot = _frequencies(inv_freq, x)
+    T, H, D = x.shape
+    x_stride = _row_stride("x", x, T, H, D, x.dtype, device)
+    _check_plain("positions", positions, torch.int32, device)
+    if positions.numel() != T:
+        raise ValueError("positions must be [tokens]")
+    freq, rot = _check_freq(torch, inv_freq, device)
     if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    out_stride = _rows("out", out, H, D, x.dtype, x)
-    if out.shape[0] != T:
-        raise ValueError("out must have x's shape")
-    with _on(x, stream) as handle:
-        st = vt_rope(out.data_ptr(), x.data_ptr(), positions.data_ptr(), freq, T, H, D, rot, interleaved, amplitude,
-                     x_stride, out_stride, handle, code)
-        _check(st, "vt_rope")
+        out = torch.empty((T, H, D), dtype=x.dtype, device=device)
+    out_stride = _row_stride("out", out, T, H, D, x.dtype, device)
+    _launch(torch, device, stream, "vt_rope", library().vt_rope,
+            (out.data_ptr(), x.data_ptr(), positions.data_ptr(), freq, T, H, D, rot, 1 if interleaved else 0, amplitude,
+             x_stride, out_stride), (code,))
     return out
 
 
-def _append(k, v, k_cache, v_cache, scales, q_starts, block_tables, context_lens, q, q_out, positions, inv_freq,
-            interleaved, amplitude, stream):
-    import torch
+def _append(torch, k, v, k_cache, v_cache, scales, q_starts, block_tables, context_lens, q, q_out, positions,
+            inv_freq, interleaved, amplitude, stream):
+    device = _cuda_device("k", k)
     T, Hkv, D = k.shape
-    io = torch.bfloat16 if scales is not None else k_cache.dtype
-    code = VT_E4M3 if scales is not None else dtype_code(k_cache)
-    ks = _rows("k", k, dtype=io)
-    vs = _rows("v", v, Hkv, D, io, k)
-    if v.shape[0] != T:
-        raise ValueError("k and v must have the same rows")
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _cuda(name, t, k)
-        if t.dim() != 4 or tuple(t.shape[2:]) != (Hkv, D) or t.shape != k_cache.shape or t.dtype != k_cache.dtype:
-            raise ValueError("k_cache/v_cache must be [num_blocks][32][Hkv][head_dim] matching k")
-    nb, P = k_cache.shape[:2]
-    B = _ragged(q_starts, block_tables, context_lens, k)
-    freq, rot = _frequencies(inv_freq, k)
+    fp8 = scales is not None
+    io = torch.bfloat16 if fp8 else k_cache.dtype
+    code = 0 if fp8 else dtype_code(k_cache)
+    ks = _row_stride("k", k, T, Hkv, D, io, device)
+    vs = _row_stride("v", v, T, Hkv, D, io, device)
+    _check_plain("k_cache", k_cache, k_cache.dtype, device)
+    _check_plain("v_cache", v_cache, k_cache.dtype, device)
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[2] != Hkv or shape[3] != D or v_cache.shape != shape:
+        raise ValueError("k_cache/v_cache must be [num_blocks][32][Hkv][head_dim] matching k")
+    B, max_blocks = _check_ragged(torch, q_starts, block_tables, context_lens, device)
+    freq, rot = _check_freq(torch, inv_freq, device)
     Hq = qs = 0
+    q_ptr = out_ptr = pos_ptr = None
     if q is not None:
-        Hq = q.shape[1] if q.dim() == 3 else 0
-        qs = _rows("q", q, Hq, D, io, k)
-        if q.shape[0] != T:
-            raise ValueError("q must have k's rows")
+        Hq = q.shape[1]
+        qs = _row_stride("q", q, T, Hq, D, io, device)
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=io, device=k.device)
-        _cuda("q_out", q_out, k)
-        if q_out.shape != q.shape or q_out.dtype != io:
-            raise ValueError("q_out must be a contiguous tensor shaped and typed like q")
+            q_out = torch.empty((T, Hq, D), dtype=io, device=device)
+        _check_plain("q_out", q_out, io, device)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must be shaped like q")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if positions is not None:
-        _cuda("positions", positions, k)
-        if positions.dtype != torch.int32 or positions.numel() != T:
-            raise TypeError("positions must be int32 [tokens]")
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    head = (k_cache.data_ptr(), v_cache.data_ptr(), ptr(q_out), k.data_ptr(), v.data_ptr(), ptr(q))
-    mid = (q_starts.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), ptr(positions), freq, B, T, Hq, Hkv,
-           D, P, rot, interleaved, amplitude, qs, ks, vs)
-    with _on(k, stream) as handle:
-        tail = (handle, block_tables.shape[1], nb)
-        if scales is not None:
-            st = vt_paged_kv_append_fp8(*head, scales[0].data_ptr(), scales[1].data_ptr(), *mid, *tail)
-            _check(st, "vt_paged_kv_append_fp8")
-        else:
-            st = vt_paged_kv_append(*head, *mid, *tail, code)
-            _check(st, "vt_paged_kv_append")
+        _check_plain("positions", positions, torch.int32, device)
+        if positions.numel() != T:
+            raise ValueError("positions must be [tokens]")
+        pos_ptr = positions.data_ptr()
+    head = (k_cache.data_ptr(), v_cache.data_ptr(), out_ptr, k.data_ptr(), v.data_ptr(), q_ptr)
+    rest = (q_starts.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), pos_ptr, freq, B, T, Hq, Hkv, D,
+            shape[1], rot, 1 if interleaved else 0, amplitude, qs, ks, vs)
+    if fp8:
+        _check_scales(torch, *scales, Hkv, device)
+        _launch(torch, device, stream, "vt_paged_kv_append_fp8", library().vt_paged_kv_append_fp8,
+                head + (scales[0].data_ptr(), scales[1].data_ptr()) + rest, (max_blocks, shape[0]))
+    else:
+        _launch(torch, device, stream, "vt_paged_kv_append", library().vt_paged_kv_append, head + rest,
+                (max_blocks, shape[0], code))
     return q_out
 
 
@@ -656,53 +674,53 @@ def append(k, v, k_cache, v_cache, q_starts, block_tables, context_lens, q=None,
     token's place in its context, or at positions [T]; without inv_freq it
     rotates nothing.  Returns the rotated queries [T][Hq][D] (q_out, allocated
     unless given; None without q).  Asynchronous on ``stream``."""
-    return _append(k, v, k_cache, v_cache, None, q_starts, block_tables, context_lens, q, q_out, positions, inv_freq,
-                   interleaved, amplitude, stream)
+    return _append(_t(), k, v, k_cache, v_cache, None, q_starts, block_tables, context_lens, q, q_out, positions,
+                   inv_freq, interleaved, amplitude, stream)
 
 
 def append_fp8(k, v, k_codes, v_codes, k_scale, v_scale, q_starts, block_tables, context_lens, q=None, q_out=None,
                positions=None, inv_freq=None, interleaved: bool = False, amplitude: float = 1.0, stream=None):
     """``append`` into an FP8 (E4M3) cache of codes with a scale per kv head
     (rows bf16; codes uint8 or torch.float8_e4m3fn)."""
-    _scales(k_scale, v_scale, k.shape[1], k)
-    return _append(k, v, _codes(k_codes), _codes(v_codes), (k_scale, v_scale), q_starts, block_tables, context_lens,
-                   q, q_out, positions, inv_freq, interleaved, amplitude, stream)
+    torch = _t()
+    return _append(torch, k, v, _codes(torch, k_codes), _codes(torch, v_codes), (k_scale, v_scale), q_starts,
+                   block_tables, context_lens, q, q_out, positions, inv_freq, interleaved, amplitude, stream)
 
 
-def _prefill(q, k_cache, v_cache, scales, q_starts, block_tables, context_lens, scale, window, out, stream):
-    import torch
+def _prefill(torch, q, k_cache, v_cache, scales, q_starts, block_tables, context_lens, scale, window, out, stream):
+    device = _cuda_device("q", q)
     if q.dim() != 3:
         raise ValueError("q must be [tokens][heads][head_dim]")
     T, Hq, D = q.shape
-    _cuda("q", q)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _cuda(name, t, q)
-        if t.dim() != 4 or t.shape[3] != D or t.shape != k_cache.shape:
-            raise ValueError("k_cache/v_cache must be [num_blocks][32][Hkv][head_dim] matching q")
-    nb, P, Hkv, _ = k_cache.shape
-    if scales is None and (k_cache.dtype != q.dtype or v_cache.dtype != q.dtype):
-        raise TypeError("q, k_cache and v_cache must share one dtype")
-    if scales is not None:
-        if q.dtype != torch.bfloat16:
-            raise TypeError("q must be bfloat16")
-        _scales(*scales, Hkv, q)
-    B = _ragged(q_starts, block_tables, context_lens, q)
+    fp8 = scales is not None
+    io = torch.bfloat16 if fp8 else q.dtype
+    code = 0 if fp8 else dtype_code(q)
+    _check_plain("q", q, io, device)
+    kv = k_cache.dtype if fp8 else io
+    _check_plain("k_cache", k_cache, kv, device)
+    _check_plain("v_cache", v_cache, kv, device)
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[3] != D or v_cache.shape != shape:
+        raise ValueError("k_cache/v_cache must be [num_blocks][32][Hkv][head_dim] matching q")
+    B, max_blocks = _check_ragged(torch, q_starts, block_tables, context_lens, device)
     if out is None:
         out = torch.empty_like(q)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != q.device:
-        raise ValueError("out must be a contiguous CUDA tensor shaped and typed like q")
+    else:
+        _check_plain("out", out, io, device)
+        if out.shape != q.shape:
+            raise ValueError("out must be shaped like q")
     if scale is None:
         scale = D ** -0.5
-    mid = (q_starts.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), B, T, Hq, Hkv, D, P, scale, window)
-    with _on(q, stream) as handle:
-        tail = (handle, block_tables.shape[1], nb)
-        head = (out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr())
-        if scales is not None:
-            st = vt_paged_attn_prefill_fp8(*head, scales[0].data_ptr(), scales[1].data_ptr(), *mid, *tail)
-            _check(st, "vt_paged_attn_prefill_fp8")
-        else:
-            st = vt_paged_attn_prefill(*head, *mid, *tail, dtype_code(q))
-            _check(st, "vt_paged_attn_prefill")
+    head = (out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr())
+    rest = (q_starts.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), B, T, Hq, shape[2], D, shape[1],
+            scale, window)
+    if fp8:
+        _check_scales(torch, *scales, shape[2], device)
+        _launch(torch, device, stream, "vt_paged_attn_prefill_fp8", library().vt_paged_attn_prefill_fp8,
+                head + (scales[0].data_ptr(), scales[1].data_ptr()) + rest, (max_blocks, shape[0]))
+    else:
+        _launch(torch, device, stream, "vt_paged_attn_prefill", library().vt_paged_attn_prefill, head + rest,
+                (max_blocks, shape[0], code))
     return out
 
 
@@ -716,12 +734,13 @@ def prefill(q, k_cache, v_cache, q_starts, block_tables, context_lens, scale=Non
     rest as for ``decode``.  Returns out [T][Hq][D] (allocated unless given;
     rows behind the last sequence are not written).  Asynchronous on
     ``stream``."""
-    return _prefill(q, k_cache, v_cache, None, q_starts, block_tables, context_lens, scale, window, out, stream)
+    return _prefill(_t(), q, k_cache, v_cache, None, q_starts, block_tables, context_lens, scale, window, out, stream)
 
 
 def prefill_fp8(q, k_codes, v_codes, k_scale, v_scale, q_starts, block_tables, context_lens, scale=None,
                 window: int = 0, out=None, stream=None):
     """``prefill`` over an FP8 (E4M3) cache (q and out bf16; codes uint8 or
     torch.float8_e4m3fn with a float32 scale per kv head)."""
-    return _prefill(q, _codes(k_codes), _codes(v_codes), (k_scale, v_scale), q_starts, block_tables, context_lens,
-                    scale, window, out, stream)
+    torch = _t()
+    return _prefill(torch, q, _codes(torch, k_codes), _codes(torch, v_codes), (k_scale, v_scale), q_starts,
+                    block_tables, context_lens, scale, window, out, stream)
