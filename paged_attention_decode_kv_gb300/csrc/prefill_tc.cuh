@@ -329,12 +329,15 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
   PfItem it{};
   // This lane's box of a stage whose first page is the item's page p0: page
   // p0 + box % pages, column block box / pages.
-  auto page_of = [&](int p0, int i) {
+  auto read_ids = [&](int p0) {
     if (ids_at < 0 || p0 < ids_at || p0 + 4 > ids_at + 32) {
       ids_at = max(0, p0 - 4);  // K runs a block ahead of V
       const int at = ids_at + lane;
       ids = at < a.max_blocks ? a.block_tables[static_cast<long long>(it.b) * a.max_blocks + at] : 0;
     }
+  };
+  auto page_of = [&](int p0, int i) {
+    read_ids(p0);
     return __shfl_sync(0xffffffffu, ids, p0 - ids_at + i);
   };
   auto load_k = [&](int j) {
@@ -392,7 +395,7 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
     ++items;
     if (!more) break;
     ids_at = -1;
-    if (it.kb1 > it.kb0) page_of((it.lo + it.kb0 * kPfBlock) / kPfPage, 0);  // table entries on their way
+    if (it.kb1 > it.kb0) read_ids((it.lo + it.kb0 * kPfBlock) / kPfPage);  // on their way while Q is asked for
 #pragma unroll 1
     for (int t = 0; t < C::kNT && !C::kFp8; ++t) {
       const TileSpan sp = tile_span(a, it, t, tile_toks);
@@ -458,8 +461,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
   PfItem it{};
 
   // S(buf) = Q K^T for block j's keys: the MMAs of chunk c and what follows them.  One lane.
-  // `pass` (or none) is told before the last column block: the other issuer wakes meanwhile.
-  auto qk_issue = [&](int j, int buf, int c, const TileSpan& sp, unsigned long long* pass) {
+  auto qk_issue = [&](int j, int buf, int c, const TileSpan& sp) {
     const bool active = j >= sp.jb && j < sp.je;
     if (active) {
       const int keys = min(kPfBlock, it.hi - (it.lo + j * kPfBlock));
@@ -474,7 +476,6 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
       uint32_t acc = more;
 #pragma unroll 1
       for (int b = 0; b < (FP8 ? 2 : 1) * C::kKBlocks; ++b) {
-        if (b == (FP8 ? 2 : 1) * C::kKBlocks - 1 && pass) mbar_arrive(pass);
         const int blk = FP8 ? b % C::kKBlocks : b;  // FP8: the high terms of Q, then the low ones
         uint32_t qx = qa + ((blk * C::kKBlockBytes + (FP8 ? b / C::kKBlocks * 128 * C::kD : 0)) >> 4);
         uint32_t kx = kb + ((blk * C::kKBlockBytes) >> 4);
@@ -482,7 +483,6 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
         for (int k = 0; k < ROW / 32; ++k, qx += 2, kx += 2, acc = 1u) umma_ss<FP8>(d, qx, kHi, kx, kHi, idesc, acc);
       }
     }
-    if (!active && pass) mbar_arrive(pass);
     umma_commit(&s.k_empty[rk.stage]);
     if (active && c == C::kKChunks - 1) {
       umma_commit(&s.s_full[buf]);
@@ -494,7 +494,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
     for (int c = 0; c < C::kKChunks; ++c) {
       if (!role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) return;
       tc_fence_after();
-      if (elect_one()) qk_issue(j, buf, c, sp, nullptr);
+      if (elect_one()) qk_issue(j, buf, c, sp);
       __syncwarp();
       rk.next();
     }
@@ -580,7 +580,9 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
         // The tiles take turns: all of one's P V and next Q K^T, then the
         // other's.  Left to themselves the two issuers' MMAs interleave, both
         // tiles wait for twice the products and then both wait for the
-        // softmax, in step (3500 cycles a block; the products take 2048).
+        // softmax, in step (3500 cycles a block; the products take 2048).  The
+        // turn passes when all is issued: passed a few MMAs earlier, the two
+        // tiles' products mix again (8192-token prompt 412 us, 419 then).
         const bool both = it.ntok > tile_toks;
         for (int j = it.kb0 - 1; j < it.kb1 && role.live; ++j) {  // P V of block j, then Q K^T of block j + 1
           // What can be waited for ahead of the weights is: after them this
@@ -606,10 +608,8 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
               pv_steps(t, from, steps, vb + ((from * KS * ROW) >> 4), from > 0 || j > sp.jb);
             }
             if (mine) umma_commit(&s.v_empty[rv.stage]);
-            if (next)
-              qk_issue(j + 1, t, 0, sp, both ? &s.turn[t ^ 1] : nullptr);
-            else if (both)
-              mbar_arrive(&s.turn[t ^ 1]);
+            if (next) qk_issue(j + 1, t, 0, sp);
+            if (both) mbar_arrive(&s.turn[t ^ 1]);
           }
           __syncwarp();
           if (mine) rv.next();
@@ -810,6 +810,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
         const int upto = pos - k0, from = a.window > 0 ? pos - a.window + 1 - k0 : 0;
 #pragma unroll 1
         for (int q = 0; q < kPfBlock; q += 32) {
+          if (__all_sync(0xffffffffu, upto - q >= 31 && from - q <= 0)) continue;  // all seen
           float x[32];
           tmem_ld32(tS + q, reinterpret_cast<uint32_t*>(x));
           tmem_wait_ld();
