@@ -36,7 +36,7 @@
 
 namespace vt {
 
-template <bool FP8, int D, int NT, int DV, int KCW, int NSK, int VK, int NSV>
+template <bool FP8, int D, int NT, int DV, int KCW, int NSK, int VK, int NSV, int NSW = 1>
 struct TcConfig {
   static constexpr bool kFp8 = FP8;                    // E4M3 codes in the cache, else bf16
   static constexpr int kD = D, kNT = NT, kDV = DV;
@@ -46,7 +46,6 @@ struct TcConfig {
   static constexpr int kCols = FP8 ? (D < 128 ? D : 128) : 64;
   static constexpr int kRow = kCols * kElem;
   static constexpr uint32_t kSwizzle = kRow == 128 ? 2 : 4;
-  static constexpr int kKStep = 32 / kElem;            // k extent of an MMA
   // A K stage: 128 keys x KCW columns.  A V stage: VK keys x all DV columns,
   // so that an MMA of P V is as wide as O (one MMA, not several narrow ones).
   static constexpr int kStagesK = NSK, kStagesV = NSV, kVK = VK;
@@ -55,7 +54,11 @@ struct TcConfig {
   static constexpr int kKBlockBytes = kPfBlock * kRow, kVBlockBytes = VK * kRow;
   static constexpr int kKBytes = kKBlocks * kKBlockBytes, kVBytes = kVBlocks * kVBlockBytes;
   static constexpr int kQBytes = 128 * D * 2;          // FP8: two E4M3 terms of each element, high terms first
-  static constexpr int kThreads = NT * 128 + 256;      // softmax, epilogue, control
+  // What P V reads: V's stages (bf16), or for codes stages of their f16 values
+  // in the same layout (64-column blocks of 128-byte rows).
+  static constexpr int kStagesP = FP8 ? NSW : NSV;
+  static constexpr int kPBlockBytes = VK * 128, kPBytes = DV / 64 * kPBlockBytes;
+  static constexpr int kThreads = NT * 128 + 256 + (FP8 ? 128 : 0);  // softmax, epilogue, control; widening
   static constexpr int kTmemO = 256;                   // S of tile (or buffer) i at 128 i
   static constexpr int kNumS = 2;                      // tiles, or buffers of one tile
   static constexpr int kItems = 4;                     // queue of items
@@ -63,13 +66,23 @@ struct TcConfig {
   static_assert(4 * kKBlocks <= 32 && VK / kPfPage * kVBlocks <= 32, "a lane for each box of a stage");
 };
 
+// Widened stages of V, for codes.
+template <typename C, bool FP8>
+struct TcWide {};
+template <typename C>
+struct TcWide<C, true> {
+  alignas(1024) unsigned char w[C::kStagesP][C::kPBytes];
+};
+
 template <typename C>
 struct TcSmem {
   alignas(1024) unsigned char q[C::kNT][C::kQBytes];
   alignas(1024) unsigned char k[C::kStagesK][C::kKBytes];
   alignas(1024) unsigned char v[C::kStagesV][C::kVBytes];
+  TcWide<C, C::kFp8> wide;
   alignas(8) unsigned long long k_full[C::kStagesK], k_empty[C::kStagesK];
   unsigned long long v_full[C::kStagesV], v_empty[C::kStagesV], v_ready[C::kStagesV];
+  unsigned long long w_full[C::kStagesP], w_empty[C::kStagesP];  // FP8
   unsigned long long q_full[C::kNT], q_empty[C::kNT];
   unsigned long long s_full[C::kNumS], s_free[C::kNumS];  // s_free: one tile only
   unsigned long long p_ready[2][C::kNumS];                // weights of the block's first and second 64 keys
@@ -83,17 +96,13 @@ struct TcSmem {
   volatile int stage_bad[C::kStagesV];  // a page id of this stage was out of range
   volatile int stage_fix[C::kStagesV];  // V preparation took out a value that is not finite
   volatile int flags[C::kNT];           // of the item whose O is full
+  alignas(4) volatile unsigned char w_flags[C::kStagesP][4];  // FP8: of the four widening warps
   volatile int abort_flag;              // status bit | thread << 8 of a wait that gave up
   volatile uint32_t abort_at[2];        // its barrier and parity
 };
 
-// Weights are 2^(score - m + kWeightExp) with m at most kLazy below the largest
-// score: at most 2^8 in bf16, 2^8.5 as E4M3 terms (largest 448), whose
-// absolute step of 2^-10 is then 2^-17 of a row's largest weight.
-template <bool FP8>
-constexpr float lazy_bound() { return FP8 ? 1.5f : 8.f; }
-template <bool FP8>
-constexpr float weight_exp() { return FP8 ? 7.f : 0.f; }
+// Weights are 2^(score - m) with m at most kLazy below the largest score.
+constexpr float kLazy = 8.f;
 
 enum : int { kItemBad = 1, kItemFix = 2 };
 
@@ -446,12 +455,12 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
 // issuer 1 runs P V; s_free hands the buffers back.
 template <typename C>
 __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, uint32_t tmem, int who, int lane) {
-  constexpr int NT = C::kNT, KS = C::kKStep, ROW = C::kRow;
+  constexpr int NT = C::kNT, KS = 16, ROW = C::kRow;  // KS: keys of an MMA of P V
   constexpr bool FP8 = C::kFp8;
-  constexpr uint32_t kHi = umma_desc_hi(8 * ROW, C::kSwizzle);
+  constexpr uint32_t kHi = umma_desc_hi(8 * ROW, C::kSwizzle), kHiP = umma_desc_hi(1024, 2);
   TcRole<C> role{a, s, lane};
   Ring<C::kStagesK> rk;
-  Ring<C::kStagesV> rv;
+  Ring<C::kStagesP> rv;
   uint32_t vphase = 0;  // of v_ready, one bit a stage
   uint32_t items = 0, nq = 0, no = 0, np[2] = {}, turns = 0;
   uint32_t nblk = 0;    // one tile: blocks so far, whose parity is the buffer
@@ -511,30 +520,46 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
   };
   // Waits for the V stage at hand (and its preparation, where block j needs it).
   auto v_here = [&](bool prepared, int& flags) {
-    if (!role.wait(&s.v_full[rv.stage], rv.phase, kStatusFull)) return false;
-    if (prepared) {
-      if (!role.wait(&s.v_ready[rv.stage], vphase >> rv.stage, kStatusSync)) return false;
-      vphase ^= 1u << rv.stage;
-      if (s.stage_fix[rv.stage]) flags |= kItemFix;
+    if constexpr (FP8) {
+      if (!role.wait(&s.w_full[rv.stage], rv.phase, kStatusFull)) return false;
+      const uint32_t f = *reinterpret_cast<volatile uint32_t*>(const_cast<unsigned char*>(s.w_flags[rv.stage]));
+      if (f) flags |= (f | f >> 8 | f >> 16 | f >> 24) & 0xffu;
+    } else {
+      if (!role.wait(&s.v_full[rv.stage], rv.phase, kStatusFull)) return false;
+      if (prepared) {
+        if (!role.wait(&s.v_ready[rv.stage], vphase >> rv.stage, kStatusSync)) return false;
+        vphase ^= 1u << rv.stage;
+        if (s.stage_fix[rv.stage]) flags |= kItemFix;
+      }
+      if (s.stage_bad[rv.stage]) flags |= kItemBad;
     }
-    if (s.stage_bad[rv.stage]) flags |= kItemBad;
     return true;
+  };
+  auto v_addr = [&] {
+    if constexpr (FP8)
+      return smem_addr(s.wide.w[rv.stage]);
+    else
+      return smem_addr(s.v[rv.stage]);
+  };
+  auto v_free = [&] {
+    if constexpr (FP8)
+      return &s.w_empty[rv.stage];
+    else
+      return &s.v_empty[rv.stage];
   };
   // k-steps of block j that the tile's rows need
   auto steps_of = [&](int j, const TileSpan& sp) {
     return (min(it.pos0 + sp.tok0 + sp.ntok - (it.lo + j * kPfBlock), kPfBlock) + KS - 1) / KS;
   };
   constexpr int kHalf = kPfBlock / 2 / KS;  // k-steps of half a block
-  const uint32_t idesc_pv = FP8 ? umma_idesc_e4m3(C::kDV, true) : umma_idesc_f16(true, C::kDV, true);
+  const uint32_t idesc_pv = umma_idesc_f16(!FP8, C::kDV, true);
   const uint32_t d_pv = tmem + C::kTmemO + t * C::kDV;
   // k-steps [first, last) of P V; vb: the V stage at step `first`.  One lane.
   auto pv_steps = [&](int buf, int first, int last, uint32_t vb, uint32_t acc) {
     uint32_t from = tmem + buf * 128 + first * 8;
 #pragma unroll 1
-    for (int k = first; k < last; ++k, from += 8, vb += (KS * ROW) >> 4, acc = 1u) {
-      umma_ts<FP8>(d_pv, from, vb, kHi, idesc_pv, acc);
-      if constexpr (FP8) umma_ts<FP8>(d_pv, from + 32, vb, kHi, idesc_pv, 1u);  // P's low terms
-    }
+    for (int k = first; k < last; ++k, from += 8, vb += (KS * 128) >> 4, acc = 1u)
+      umma_ts<false>(d_pv, from, vb, kHiP, idesc_pv, acc);
   };
   // One tile: O (+)= P(buf) V for block j's keys, V in stages of VK keys.
   auto pv = [&](int j, int buf, const TileSpan& sp, int& flags) {
@@ -553,9 +578,9 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
         tc_fence_after();
         const int first = (h * kPer + i) * kSteps;
         if (elect_one()) {
-          pv_steps(buf, first, min(steps, first + kSteps), umma_desc_lo(smem_addr(s.v[rv.stage]), C::kVBlockBytes),
+          pv_steps(buf, first, min(steps, first + kSteps), umma_desc_lo(v_addr(), C::kPBlockBytes),
                    first > 0 || j > sp.jb);
-          umma_commit(&s.v_empty[rv.stage]);
+          umma_commit(v_free());
         }
         __syncwarp();
         rv.next();
@@ -592,7 +617,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
           if (next && !role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) break;
           if (active && j == sp.jb && !role.wait(&s.o_free[t], no ^ 1u, kStatusSync)) break;
           const int steps = active ? steps_of(j, sp) : 0;
-          const uint32_t vb = umma_desc_lo(smem_addr(s.v[rv.stage]), C::kVBlockBytes);
+          const uint32_t vb = umma_desc_lo(v_addr(), C::kPBlockBytes);
           if (active && !role.wait(&s.p_ready[0][t], np[0], kStatusSync)) break;
           if (active && !both) {  // nothing else to run meanwhile: the first half's products at once
             tc_fence_after();
@@ -605,9 +630,9 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
           if (elect_one()) {
             if (active) {
               const int from = both ? 0 : kHalf;
-              pv_steps(t, from, steps, vb + ((from * KS * ROW) >> 4), from > 0 || j > sp.jb);
+              pv_steps(t, from, steps, vb + ((from * KS * 128) >> 4), from > 0 || j > sp.jb);
             }
-            if (mine) umma_commit(&s.v_empty[rv.stage]);
+            if (mine) umma_commit(v_free());
             if (next) qk_issue(j + 1, t, 0, sp);
             if (both) mbar_arrive(&s.turn[t ^ 1]);
           }
@@ -640,8 +665,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
 // --------------------------------------------------------------------- V preparation
 template <typename C>
 __device__ __forceinline__ void tc_prepare(const PrefillArgs& a, TcSmem<C>& s, int lane) {
-  constexpr bool FP8 = C::kFp8;
-  constexpr int KS = C::kKStep;
+  constexpr int KS = 16;
   TcRole<C> role{a, s, lane};
   Ring<C::kStagesV> rv;
   PfItem it{};
@@ -685,19 +709,19 @@ __device__ __forceinline__ void tc_prepare(const PrefillArgs& a, TcSmem<C>& s, i
 #pragma unroll
                 for (int cb = 0; cb < C::kVBlocks; ++cb) {
                   const uint4 x = *reinterpret_cast<const uint4*>(piece + cb * C::kVBlockBytes + at * C::kRow);
-                  seen |= carries<FP8>(x.x) | carries<FP8>(x.y) | carries<FP8>(x.z) | carries<FP8>(x.w);
+                  seen |= carries<false>(x.x) | carries<false>(x.y) | carries<false>(x.z) | carries<false>(x.w);
                 }
               }
             }
-            if (!__any_sync(0xffffffffu, seen & kCarry<FP8>)) return;
+            if (!__any_sync(0xffffffffu, seen & kCarry<false>)) return;
 #pragma unroll 1
             for (int slot = first; slot + line < last; slot += kLines)
 #pragma unroll 1
               for (int cb = 0; cb < C::kVBlocks; ++cb) {
                 uint4* at = reinterpret_cast<uint4*>(piece + cb * C::kVBlockBytes + slot * C::kRow);
                 uint4 x = *at;
-                x.x &= ~not_finite<FP8>(x.x), x.y &= ~not_finite<FP8>(x.y);
-                x.z &= ~not_finite<FP8>(x.z), x.w &= ~not_finite<FP8>(x.w);
+                x.x &= ~not_finite<false>(x.x), x.y &= ~not_finite<false>(x.y);
+                x.z &= ~not_finite<false>(x.z), x.w &= ~not_finite<false>(x.w);
                 *at = x;
               }
             fix = true;
@@ -723,12 +747,90 @@ __device__ __forceinline__ void tc_prepare(const PrefillArgs& a, TcSmem<C>& s, i
   }
 }
 
+// --------------------------------------------------------------------- widening
+// FP8: four warps turn V's codes into f16, exactly, in the layout bf16 pages
+// have; a code is widened once for the item's 256 rows.  (As E4M3 MMA operands
+// codes would need P as two E4M3 terms: 12 more cycles of conversions for two
+// weights in the softmax, which then took 2300 cycles a block and the chunks'
+// case 435 us.)  Preparation is part of it.
+template <typename C>
+__device__ __forceinline__ void tc_widen(const PrefillArgs& a, TcSmem<C>& s, int tid) {
+  constexpr int KS = 16;
+  const int lane = tid & 31, warp = tid >> 5;
+  TcRole<C> role{a, s, lane};
+  Ring<C::kStagesV> rv;
+  Ring<C::kStagesP> rw;
+  PfItem it{};
+  uint32_t items = 0;
+  for (; role.item(items, it); ++items) {
+#pragma unroll 1
+    for (int j = it.kb0; j < it.kb1 && role.live; ++j) {
+      const bool prepare = needs_prep(a, it, j);
+      const int stages = v_stages<C>(it, j);
+#pragma unroll 1
+      for (int i = 0; i < stages; ++i, rv.next(), rw.next()) {
+        if (!role.wait(&s.w_empty[rw.stage], rw.phase ^ 1u, kStatusEmpty)) break;
+        if (!role.wait(&s.v_full[rv.stage], rv.phase, kStatusFull)) break;
+        const int k0 = it.lo + j * kPfBlock + i * C::kVK;
+        const int end = min(C::kVK, (it.hi - k0 + KS - 1) / KS * KS);  // slots the products read
+        const unsigned char* src = s.v[rv.stage];
+        unsigned char* dst = s.wide.w[rw.stage];
+        bool fix = false;
+        constexpr int kRowPieces = C::kDV / 16;  // 16 codes each
+        constexpr int kPieces = C::kRow / 16;    // of a swizzled block's row
+#pragma unroll 2
+        for (int p = tid; p < end * kRowPieces; p += 128) {
+          const int slot = p / kRowPieces, piece = p % kRowPieces;
+          const int cb = piece / kPieces, ch = piece % kPieces;
+          const int swz = C::kRow == 128 ? ch ^ (slot & 7) : ch ^ ((slot >> 1) & 3);
+          uint4 x = *reinterpret_cast<const uint4*>(src + cb * C::kVBlockBytes + slot * C::kRow + swz * 16);
+          if (prepare) {
+            const int t = k0 + slot;
+            if (t < it.lo_exact || t >= it.hi) {
+              x = make_uint4(0, 0, 0, 0);
+            } else if (t > it.pos0 || (a.window > 0 && t < it.hi - a.window)) {
+              const uint32_t m = (carries<true>(x.x) | carries<true>(x.y) | carries<true>(x.z) | carries<true>(x.w)) &
+                                 kCarry<true>;
+              if (m) {
+                fix = true;
+                x.x &= ~not_finite<true>(x.x), x.y &= ~not_finite<true>(x.y);
+                x.z &= ~not_finite<true>(x.z), x.w &= ~not_finite<true>(x.w);
+              }
+            }
+          }
+          uint4 y[2];
+          e4m3x4_to_f16(x.x, y[0].x, y[0].y);
+          e4m3x4_to_f16(x.y, y[0].z, y[0].w);
+          e4m3x4_to_f16(x.z, y[1].x, y[1].y);
+          e4m3x4_to_f16(x.w, y[1].z, y[1].w);
+          // two 16-byte pieces of a 128-byte row of 64 columns; the lanes of
+          // every other block store them the other way round (no bank conflicts)
+          unsigned char* row = dst + (piece >> 2) * C::kPBlockBytes + slot * 128;
+          const int at = (piece & 3) * 2, odd = (piece >> 2) & 1;
+          *reinterpret_cast<uint4*>(row + (((at + odd) ^ (slot & 7)) << 4)) = odd ? y[1] : y[0];
+          *reinterpret_cast<uint4*>(row + (((at + (odd ^ 1)) ^ (slot & 7)) << 4)) = odd ? y[0] : y[1];
+        }
+        fix = __any_sync(0xffffffffu, fix);
+        const bool bad = s.stage_bad[rv.stage] != 0;
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          s.w_flags[rw.stage][warp] = static_cast<unsigned char>((bad ? kItemBad : 0) | (fix ? kItemFix : 0));
+          mbar_arrive(&s.w_full[rw.stage]);
+          mbar_arrive(&s.v_empty[rv.stage]);
+        }
+      }
+    }
+    if (!role.live) break;
+    role.item_done(items);
+  }
+}
+
 // --------------------------------------------------------------------- softmax: one row a thread
 template <typename C>
 __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, uint32_t tmem, int tid) {
   constexpr int D = C::kD, NT = C::kNT, DV = C::kDV, ROW = C::kRow;
   constexpr bool FP8 = C::kFp8;
-  constexpr float kLazy = lazy_bound<FP8>(), kWeightExp = weight_exp<FP8>();
   const int warp = tid >> 5, lane = tid & 31;
   const int tile_toks = 128 / a.group;
   const int t = NT == 2 ? warp >> 2 : 0;
@@ -862,7 +964,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
         l *= keep;
         m = mn;
       }
-      const float mb = kWeightExp - (m == -CUDART_INF_F ? 0.f : m);
+      const float mb = m == -CUDART_INF_F ? 0.f : -m;
       const float2 scale2 = make_float2(scale, scale), mb2 = make_float2(mb, mb);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
@@ -887,23 +989,14 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
               sum[i] = add2(sum[i], w[i]);
             }
             if constexpr (FP8) {
-              uint32_t h0, h1, l0, l1;
-              e4m3x2_terms(w[0].x, w[0].y, h0, l0);
-              e4m3x2_terms(w[1].x, w[1].y, h1, l1);
-              p[e] = h0 | (h1 << 16);
-              p[8 + e] = l0 | (l1 << 16);
+              p[2 * e] = pack_f16(w[0].x, w[0].y);
+              p[2 * e + 1] = pack_f16(w[1].x, w[1].y);
             } else {
               p[2 * e] = pack_bf16(w[0].x, w[0].y);
               p[2 * e + 1] = pack_bf16(w[1].x, w[1].y);
             }
           }
-          // (P lies over scores that have been read: columns up to 32 h + 31, or 32 + 16 h + 15)
-          if constexpr (FP8) {
-            tmem_st8(tS + 16 * h + 8 * q, p);
-            tmem_st8(tS + 32 + 16 * h + 8 * q, p + 8);
-          } else {
-            tmem_st16(tS + 32 * h + 16 * q, p);
-          }
+          tmem_st16(tS + 32 * h + 16 * q, p);  // (P lies over scores that have been read)
         }
         tmem_wait_st();
         tc_fence_before();
@@ -1035,7 +1128,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   extern __shared__ __align__(1024) unsigned char raw[];  // whole swizzle atoms
   TcSmem<C>& s = *reinterpret_cast<TcSmem<C>*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kEpilogue = NT * 4, kLoader = kEpilogue + 4, kIssuer = kLoader + 1, kPrep = kLoader + 3;
+  constexpr int kEpilogue = NT * 4, kLoader = kEpilogue + 4, kWiden = kLoader + 4, kIssuer = kLoader + 1, kPrep = kLoader + 3;
 
   if (tid == 0) {
     a.splits[blockIdx.x].pieces = 0;
@@ -1046,9 +1139,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     for (int i = 0; i < C::kStagesV; ++i) {
       mbar_init(&s.v_full[i], 1);
-      mbar_init(&s.v_empty[i], NT + 1);  // the issuers of P V, and preparation
+      mbar_init(&s.v_empty[i], C::kFp8 ? 4 : NT + 1);  // widening; or the issuers of P V, and preparation
       mbar_init(&s.v_ready[i], 1);
     }
+    if constexpr (C::kFp8)
+      for (int i = 0; i < C::kStagesP; ++i) {
+        mbar_init(&s.w_full[i], 4);
+        mbar_init(&s.w_empty[i], NT);
+      }
     for (int i = 0; i < NT; ++i) {
       mbar_init(&s.q_full[i], C::kFp8 ? 128 : 1);
       mbar_init(&s.q_empty[i], 1);
@@ -1067,7 +1165,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     for (int i = 0; i < C::kItems; ++i) {
       mbar_init(&s.item_full[i], 1);
-      mbar_init(&s.item_empty[i], 7 + 4 * NT);  // issuers, preparation, epilogue and softmax warps
+      mbar_init(&s.item_empty[i], (C::kFp8 ? 10 : 7) + 4 * NT);  // every warp but the loader
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1084,21 +1182,27 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s.tmem;
   // A softmax thread holds a row of 128 scores; with two tiles registers move
-  // to it from the other warpgroups (512 x 128 = 128 x (96 + 96) + 256 x 160).
-  if (warp >= kLoader) {
-    if constexpr (NT == 2) regs_dec<96>();
+  // to it from the other warpgroups (512 x 128 = 128 x (96 + 96) + 256 x 160;
+  // with widening 640 x 96 >= 128 x 3 x 72 + 256 x 128).
+  constexpr bool kMove = NT == 2;
+  constexpr int kFew = C::kFp8 ? 72 : 96, kMany = C::kFp8 ? 128 : 160;
+  if (warp >= kWiden) {
+    if constexpr (kMove) regs_dec<kFew>();
+    if constexpr (C::kFp8) tc_widen<C>(a, s, tid - kWiden * 32);
+  } else if (warp >= kLoader) {
+    if constexpr (kMove) regs_dec<kFew>();
     if (warp == kLoader) {
       tc_loader<C>(tq, tk, tv, a, s, w, lane);
     } else if (warp == kPrep) {
-      tc_prepare<C>(a, s, lane);
+      if constexpr (!C::kFp8) tc_prepare<C>(a, s, lane);
     } else {
       tc_issuer<C>(a, s, tmem, warp - kIssuer, lane);
     }
   } else if (warp >= kEpilogue) {
-    if constexpr (NT == 2) regs_dec<96>();
+    if constexpr (kMove) regs_dec<kFew>();
     tc_epilogue<C>(a, s, tmem, tid - kEpilogue * 32);
   } else {
-    if constexpr (NT == 2) regs_inc<160>();
+    if constexpr (kMove) regs_inc<kMany>();
     tc_softmax<C>(a, s, tmem, tid);
   }
   // every role is done with tensor memory
