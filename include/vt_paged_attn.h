@@ -307,7 +307,7 @@ VT_API vt_status vt_rope(void* out, const void* x, const int32_t* positions, con
  *
  *   k_cache, v_cache  as for vt_paged_attn_decode, written; no other slot is touched.
  *   q_out, q    [num_tokens][num_q_heads][head_dim], q_out contiguous, q rows q_stride elements apart; both NULL
- *               to append alone.  q_out == q with q_stride == num_q_heads * head_dim rotates in place.
+ *               to append alone (num_q_heads is then not looked at).  q_out == q with q_stride == num_q_heads * head_dim rotates in place.
  *   k, v        [num_tokens] rows of [num_kv_heads][head_dim], k_stride and v_stride elements apart.
  *   q_starts    [num_seqs + 1] int32, q_starts[0] = 0, not decreasing, last entry <= num_tokens.  Rows behind the
  *               last sequence (a padded batch) are left as they were.
@@ -355,7 +355,8 @@ VT_API vt_status vt_paged_kv_append_fp8(void* k_cache, void* v_cache, void* q_ou
  * which is the operation of vt_paged_attn_decode_multi with a chunk length of
  * its own for each sequence and no bound on it.
  *
- *   out, q      [num_tokens][num_q_heads][head_dim]; out rows behind the last sequence are left as they were.
+ *   out, q      [num_tokens][num_q_heads][head_dim], not overlapping; out rows behind the last sequence are left as
+ *               they were.
  *   q_starts, num_seqs, num_tokens  as for vt_paged_kv_append.
  *   num_q_heads / num_kv_heads at most 128, fp32 64 (else VT_ERR_UNSUPPORTED); the other arguments, layouts and
  *   limits as for vt_paged_attn_decode.
@@ -383,6 +384,11 @@ VT_API vt_status vt_paged_attn_prefill(void* out, const void* q, const void* k_c
  * vt_paged_attn_prefill_fp8 -- the same over an FP8 (E4M3) cache (bf16 q and
  * out; codes times per-kv-head scales, as for vt_paged_attn_decode_fp8);
  * head_dim 64, 128 or 256.
+ * Arithmetic: each query row is scaled by a power of two that puts its largest
+ * magnitude in [2^7, 2^8) and split into two E4M3 terms, which hold a bf16
+ * value exactly down to 2^-9 of that largest and to 2^-17 of it absolutely
+ * below; key codes enter the products as they are.  Value codes are widened
+ * exactly to f16 and the weights rounded to f16.  Sums are fp32.
  */
 VT_API vt_status vt_paged_attn_prefill_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
                                            const float* k_scale, const float* v_scale, const int32_t* q_starts,

@@ -88,6 +88,7 @@ vt_status validate(const PrefillCall& c) {
   if (c.num_seqs < 0 || c.num_tokens < 0) return VT_ERR_INVALID_ARG;
   if (!c.out || !c.q || !c.k_cache || !c.v_cache || !c.q_starts || !c.block_tables || !c.context_lens)
     return VT_ERR_INVALID_ARG;
+  if (c.out == c.q) return VT_ERR_INVALID_ARG;  // rows are read again after others' results are written
   if (c.dtype != VT_BF16 && c.dtype != VT_F32 && c.dtype != VT_E4M3) return VT_ERR_INVALID_ARG;
   if (c.dtype == VT_E4M3 && (!c.k_scale || !c.v_scale || !aligned(c.k_scale, 4) || !aligned(c.v_scale, 4)))
     return VT_ERR_INVALID_ARG;
@@ -225,7 +226,8 @@ vt_status prefill(const PrefillCall& c) {
   a.group = c.num_q_heads / c.num_kv_heads;
   a.max_blocks = c.max_blocks;
   a.num_blocks = c.num_blocks;
-  a.window = c.window > 0 ? c.window : 0;
+  // (a window no context can fill is none, and no sum with it overflows)
+  a.window = c.window > 0 && c.window < c.max_blocks * kPfPage ? c.window : 0;
   // (a hidden score is -inf, which a scale of 0 would turn into NaN: 1e-37 leaves any finite score at 0)
   a.scale_log2 = c.scale == 0.f ? 1e-37f : std::fabs(c.scale) * 1.4426950408889634f;
   a.neg_scale = c.scale < 0.f;

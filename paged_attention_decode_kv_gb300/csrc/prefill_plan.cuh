@@ -94,7 +94,8 @@ __device__ __forceinline__ long long pf_weight(const PrefillArgs& a, const PfSeq
   if (K == s.tiles) w -= pf_mul(T, K) - s.n;
   if (a.window > 0) {
     const int A = s.p0 - a.window + 1;            // window start of the first token
-    const int f = A >= 0 ? 0 : (-A + T - 1) / T;  // first tile whose start is clipped
+    // first tile whose start is not clipped
+    const int f = A >= 0 ? 0 : static_cast<int>((static_cast<unsigned>(-A) + T - 1) / static_cast<unsigned>(T));
     if (K > f) w -= pf_mul(K - f, A) + ((pf_mul(K, K - 1) - pf_mul(f, f - 1)) >> 1) * T;
   }
   return w;

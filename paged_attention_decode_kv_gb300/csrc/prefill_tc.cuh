@@ -856,6 +856,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
         const float up = pow2f(7 - max(e, -119));
         scale = a.scale_log2 * fabsf(ks) * pow2f(max(e, -119) - 7);
         if (scale == 0.f) scale = 1e-37f;
+        if (most >= 0x7f80u) scale = CUDART_NAN_F;  // a query that is not finite, which codes cannot hold
         const float mul = ks < 0.f ? -up : up;
 #pragma unroll 2
         for (int i = 0; i < D / 16; ++i) {

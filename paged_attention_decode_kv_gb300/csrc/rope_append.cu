@@ -594,6 +594,7 @@ vt_status append(const RopeArgs& a, int block_size, int interleaved, cudaStream_
   if (!a.k_cache || !a.v_cache || !a.k || !a.v || !a.q_starts || !a.block_tables || !a.context_lens)
     return VT_ERR_INVALID_ARG;
   if ((a.q == nullptr) != (a.q_out == nullptr)) return VT_ERR_INVALID_ARG;
+  if (a.q && a.q == a.q_out && a.q_stride != a.q_out_stride) return VT_ERR_INVALID_ARG;
   if (dtype == VT_E4M3 && (!a.k_scale || !a.v_scale || !aligned(a.k_scale, 4) || !aligned(a.v_scale, 4)))
     return VT_ERR_INVALID_ARG;
   if (a.kv_heads <= 0 || (a.q && a.q_heads <= 0) || a.max_blocks <= 0 || a.num_blocks <= 0 || block_size <= 0 ||

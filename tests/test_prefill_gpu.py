@@ -2,16 +2,14 @@
 
 Tolerances, from the kernel's arithmetic, with w = sum_t p_t |v_t| of an
 output element: the softmax weights are rounded to bf16 (2^-8 of each, so at
-most 2^-8 w), or for codes to two E4M3 terms; the output to bf16 (2^-8 of
-it); scores, their exponentials and sums are fp32, whose errors over D
-products and a few thousand keys stay below 2^-12 w at these magnitudes.
-Two E4M3 terms: the first leaves at most 2^-4 of a weight, the second 2^-4 of
-that, 2^-8 together, but never less than half the smallest step, 2^-10, where
-a row's largest weight is held as 2^7 at least (the reference maximum is at
-most the largest score): an absolute 2^-17 of the largest weight for every
-key, which moves an output by up to 2^-17 max p sum |v|.  fp32 storage: a score
-sums D products of magnitude up to sum |q k| with 2^-24 each, the output up
-to n of them.
+most 2^-8 w), or for codes to f16 (2^-11, and 2^-25 of the largest), the
+output to bf16 (2^-8 of it); scores, their exponentials and sums are fp32,
+whose errors over D products and a few thousand keys stay below 2^-12 w at
+these magnitudes.  Codes: a query is two E4M3 terms, off by at most 2^-17 of
+the row's largest magnitude an element, so a score by up to
+e = 2^-17 max|q| sum_d |k_d| scale, twice that in weights that are
+quotients, 2 e w.  fp32 storage: a score sums D products of magnitude up to
+sum |q k| with 2^-24 each, the output up to n of them.
 """
 from __future__ import annotations
 
@@ -73,7 +71,10 @@ def check(batch, got, scale=None, window=0):
     else:
         tol = (2.0 ** -8 + 2.0 ** -12) * reach + 2.0 ** -8 * ref.abs() + 1e-30
         if batch.dtype == "e4m3":
-            tol = tol + 2.0 ** -17 * even
+            most = batch.q[:live].double().abs().amax(-1, keepdim=True)
+            keys = max(float(k.abs().sum(-1).max()) for k in batch.dense("k") if k.numel())
+            e = 2.0 ** -17 * most * keys * abs(D ** -0.5 if scale is None else scale)
+            tol = (2.0 ** -11 + 2.0 ** -12 + 2 * e) * reach + 2.0 ** -8 * ref.abs() + 2.0 ** -25 * even
     assert (err <= tol).all(), (float((err - tol).max()), float(err.max()))
     if live:
         nmse = float((err ** 2).sum() / (ref ** 2).sum())
@@ -211,6 +212,77 @@ def test_values_that_are_not_finite_in_masked_places(dev, dtype, D):
     assert not torch.isfinite(out[30:, :, 3]).any() and not torch.isfinite(out[30:, :, D - 1]).any()
     clean = [c for c in range(D) if c not in (3, D - 1)]
     assert (out[30:][..., clean].double() - ref[30:][..., clean]).abs().max() < 0.02
+
+
+def test_queries_that_are_not_finite(dev):
+    """A row whose query is not finite is NaN, the others are as ever."""
+    for dtype, D in (("bf16", 128), ("e4m3", 128), ("e4m3", 256), ("f32", 64)):
+        batch = make_batch([40], [150], 2, 1, D, dtype)
+        ref, _ = attention(batch, D ** -0.5)
+        batch.q[7, 1, 5] = float("inf")
+        batch.q[20, 0, 0] = float("nan")
+        out = run(batch)
+        assert torch.isnan(out[7, 1]).all() and torch.isnan(out[20, 0]).all()
+        keep = torch.ones(out.shape[:2], dtype=torch.bool, device=dev)
+        keep[7, 1] = keep[20, 0] = False
+        assert (out[keep].double() - ref[keep]).abs().max() < 0.02
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_bounded_wait_gives_up_and_reports(dev, dtype, D):
+    """A withheld block: the waits for it run out, the kernel returns, the status says so, and the next call is
+    exact.  (fp32 has no waits: it is not concerned.)"""
+    if dtype == "f32":
+        return
+    batch = make_batch([100, 30], [900, 2000], 8, 2, D, dtype)
+    run(batch)
+    torch.cuda.synchronize()
+    vt.vt_paged_attn_set_test_wait(4_000_000, 0, 1)
+    run(batch)
+    vt.vt_paged_attn_set_test_wait(0, -1, -1)
+    torch.cuda.synchronize()
+    words = vt.vt_paged_attn_device_status_detail()
+    assert words[0] != 0 and words[1] == 1
+    assert vt.vt_paged_attn_device_status() != 0
+    assert vt.vt_paged_attn_device_status() == 0
+    check(batch, run(batch))
+
+
+def test_capture_before_the_first_call_is_refused(dev):
+    """The scratch is allocated outside captures only; a refused call leaves the capture usable."""
+    batch = make_batch([10], [50], 2, 1, 64, "bf16")
+    out = torch.zeros_like(batch.q)
+    torch.cuda.synchronize()
+    vt.vt_paged_attn_release()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out.add_(1)
+        with pytest.raises(vt.VtError) as e:
+            run(batch, out=out)
+    assert e.value.status == vt.VT_ERR_SCRATCH_LIMIT
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (out == 1).all()
+    check(batch, run(batch, out=out))
+
+
+def test_larger_scratch_leaves_a_captured_graph_alone(dev):
+    """A call that needs a larger scratch does not take away the one a graph names."""
+    batch = make_batch([100, 30], [900, 2000], 8, 2, 64, "bf16")
+    out = torch.zeros_like(batch.q)
+    torch.cuda.synchronize()
+    vt.vt_paged_attn_release()
+    run(batch, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(batch, out=out)
+    wide = make_batch([100, 30], [900, 2000], 8, 2, 256, "bf16")
+    run(wide)
+    other = run(wide, grid=400)
+    out.zero_()
+    graph.replay()
+    check(batch, out)
+    check(wide, other)
 
 
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f32", 64)])

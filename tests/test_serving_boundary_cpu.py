@@ -71,6 +71,7 @@ COMMON_APPEND = [
     (dict(v_stride=258), vt.VT_ERR_INVALID_ARG),
     (dict(q_stride=8), vt.VT_ERR_INVALID_ARG),
     (dict(rot_dim=0), vt.VT_ERR_INVALID_ARG),           # a table without a rotated part
+    (dict(q_out=0x6000, q_stride=2048), vt.VT_ERR_INVALID_ARG),  # in place, but with other strides
     (dict(inv_freq=None), vt.VT_ERR_INVALID_ARG),
     (dict(rot_dim=7), vt.VT_ERR_INVALID_ARG),
     (dict(amplitude=float("inf")), vt.VT_ERR_INVALID_ARG),
@@ -110,6 +111,7 @@ COMMON_PREFILL = [
     (dict(q_starts=None), vt.VT_ERR_INVALID_ARG),
     (dict(context_lens=0x7002), vt.VT_ERR_INVALID_ARG),
     (dict(q=0x2004), vt.VT_ERR_INVALID_ARG),
+    (dict(q=0x1000), vt.VT_ERR_INVALID_ARG),            # in place
     (dict(num_q_heads=7), vt.VT_ERR_INVALID_ARG),
     (dict(scale=float("nan")), vt.VT_ERR_INVALID_ARG),
     (dict(num_blocks=0), vt.VT_ERR_INVALID_ARG),
@@ -213,3 +215,29 @@ def test_frequencies_need_their_arrays(lib):
     assert lib.vt_rope_frequencies(None, ctypes.byref(amp), 64, 1e4, None) == vt.VT_ERR_INVALID_ARG
     inv = (ctypes.c_double * 32)()
     assert lib.vt_rope_frequencies(inv, None, 64, 1e4, None) == vt.VT_ERR_INVALID_ARG
+
+
+# ---- the torch wrappers' own checks ----------------------------------------------
+def test_wrappers_refuse_host_tensors():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
+    kv = torch.zeros((2, 2, 64), dtype=torch.bfloat16)
+    cache = torch.zeros((3, 32, 2, 64), dtype=torch.bfloat16)
+    i32 = torch.zeros((2,), dtype=torch.int32)
+    table = torch.zeros((1, 2), dtype=torch.int32)
+    inv, amp = vt.rope_frequencies(64, device="cpu")
+    assert inv.dtype == torch.float64 and inv.shape == (32,) and amp == 1.0
+    with pytest.raises(ValueError, match="CUDA"):
+        vt.rope(x, i32, inv)
+    with pytest.raises(ValueError, match="CUDA"):
+        vt.append(kv, kv, cache, cache.clone(), i32, table, i32[:1], q=x, inv_freq=inv)
+    with pytest.raises(ValueError, match="CUDA"):
+        vt.prefill(x, cache, cache.clone(), i32, table, i32[:1])
+    codes = cache.to(torch.float8_e4m3fn)
+    ones = torch.ones((2,))
+    with pytest.raises(ValueError, match="CUDA"):
+        vt.prefill_fp8(x, codes, codes.clone(), ones, ones, i32, table, i32[:1])
+    with pytest.raises(TypeError):
+        vt.append_fp8(kv, kv, cache, cache.clone(), ones, ones, i32, table, i32[:1])  # not codes
+    with pytest.raises(vt.VtError):
+        vt.rope_frequencies(63, device="cpu")
