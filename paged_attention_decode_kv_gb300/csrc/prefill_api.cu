@@ -1,4 +1,5 @@
 // C entry points of the ragged prefill: checks, scratch, tensor maps, launch.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -232,6 +233,11 @@ vt_status prefill(const PrefillCall& c) {
   a.scale_log2 = c.scale == 0.f ? 1e-37f : std::fabs(c.scale) * 1.4426950408889634f;
   a.neg_scale = c.scale < 0.f;
   a.tile_tokens = v.rows / v.tile_rows * (v.tile_rows / a.group);
+  // Division by T = tile_tokens: with s = ceil(log2 T), 2^(31 + s) < mul T <= 2^(31 + s) + 2^s.
+  unsigned log2_up = 0;
+  while ((1u << log2_up) < static_cast<unsigned>(a.tile_tokens)) ++log2_up;
+  a.tile_shift = 31 + log2_up;
+  a.tile_mul = static_cast<unsigned>((1ull << a.tile_shift) / static_cast<unsigned>(a.tile_tokens) + 1);
   a.v_parts = c.head_dim / v.cols;
   const int min_blocks = g_override_min_units > 0 ? g_override_min_units : kDefaultMinBlocks;
   a.min_weight = kPfBlock * (min_blocks < 2 ? 2 : min_blocks);
@@ -239,7 +245,8 @@ vt_status prefill(const PrefillCall& c) {
   a.splits = reinterpret_cast<PrefillSplit*>(base);
   a.ml = reinterpret_cast<float2*>(base + splits_bytes(grid));
   a.part = reinterpret_cast<float*>(base + splits_bytes(grid) + ml_bytes(v, grid));
-  a.wait_limit = g_test_wait_limit > 0 ? g_test_wait_limit : kWaitLimitCycles;
+  a.wait_limit = static_cast<unsigned>(
+      g_test_wait_limit > 0 ? std::min(g_test_wait_limit, kWaitLimitCycles) : kWaitLimitCycles);
   a.withhold_cta = g_test_withhold_tile >= 0 ? g_test_withhold_cta : -1;
   a.withhold_block = g_test_withhold_tile;
 

@@ -44,6 +44,7 @@ struct PrefillArgs {
   float scale_log2;  // |scale| * log2(e); the sign is applied where the product is formed
   int neg_scale;
   int tile_tokens;   // new tokens of an item
+  unsigned tile_mul, tile_shift;  // x / tile_tokens = x * tile_mul >> tile_shift for 0 <= x < 2^31
   int v_parts;       // items that share a (kv head, tile), each with a part of V's columns
   int min_weight;    // least share of a CTA, at least 2 * kPfBlock
   // Partials: record s (2 for each CTA: 2c an item's head piece, 2c + 1 a later piece) holds `rows` rows of
@@ -52,7 +53,7 @@ struct PrefillArgs {
   float2* ml;
   struct PrefillSplit* splits;  // [grid] the item whose head piece CTA c has, if it is split
   unsigned* status;
-  long long wait_limit;
+  unsigned wait_limit;   // clock cycles
   int withhold_cta, withhold_block;  // test hook: this CTA stops loading before its withhold_block-th key block
 };
 
@@ -70,6 +71,11 @@ struct PfSeq {
   int tiles;
 };
 
+// x / tile_tokens, 0 <= x < 2^31 (a division's code is long).
+__device__ __forceinline__ int pf_tiles_in(const PrefillArgs& a, int x) {
+  return static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(x)) * a.tile_mul >> a.tile_shift);
+}
+
 __device__ __forceinline__ PfSeq pf_seq(const PrefillArgs& a, int b) {
   PfSeq s;
   const int r0 = a.q_starts[b], r1 = a.q_starts[b + 1];
@@ -78,7 +84,7 @@ __device__ __forceinline__ PfSeq pf_seq(const PrefillArgs& a, int b) {
   s.n = (r0 >= 0 && r1 > r0 && r1 <= a.num_tokens) ? r1 - r0 : 0;
   s.bad = L < s.n || static_cast<long long>(L) > static_cast<long long>(a.max_blocks) * kPfPage;
   s.p0 = s.bad ? 0 : L - s.n;
-  s.tiles = (s.n + a.tile_tokens - 1) / a.tile_tokens;
+  s.tiles = s.n > 0 ? pf_tiles_in(a, s.n - 1) + 1 : 0;
   return s;
 }
 
@@ -95,7 +101,7 @@ __device__ __forceinline__ long long pf_weight(const PrefillArgs& a, const PfSeq
   if (a.window > 0) {
     const int A = s.p0 - a.window + 1;            // window start of the first token
     // first tile whose start is not clipped
-    const int f = A >= 0 ? 0 : static_cast<int>((static_cast<unsigned>(-A) + T - 1) / static_cast<unsigned>(T));
+    const int f = A >= 0 ? 0 : pf_tiles_in(a, -A - 1) + 1;
     if (K > f) w -= pf_mul(K - f, A) + ((pf_mul(K, K - 1) - pf_mul(f, f - 1)) >> 1) * T;
   }
   return w;

@@ -4,7 +4,9 @@
 // heads of one kv head), against 128 keys (four pages) at a time:
 //   S = Q K^T   tcgen05.mma, Q and K in shared memory, S in tensor memory;
 //   P = 2^(scale S - m), rows masked and summed in registers, one row to a
-//       thread, rounded to bf16 and written over S in tensor memory;
+//       thread, rounded to bf16 (f16 against codes, whose V is f16: at most
+//       2^-8 or 2^-11 of a weight, like the rounding of a bf16 result)
+//       and written over S in tensor memory;
 //   O += P V    tcgen05.mma, P from tensor memory, V as it lies in its pages
 //       (token-major, i.e. the N-major right operand), O in tensor memory.
 // A row's reference maximum m moves only when a score passes it by more than
@@ -13,14 +15,18 @@
 //
 // Roles: one warp loads (walks the CTA's share, passes its items on through a
 // queue, and fetches Q tiles and K and V pages by TMA into two rings of
-// stages), two issue MMAs, one prepares V (below); one warpgroup of softmax
-// threads a tile.  With two tiles (head_dim 64 and 128) each has an issuer of
-// its own, and one tile's products run while the other's softmax does: an
-// issuing thread needs 50 to 70 cycles for an MMA of 64, so one thread for
-// both left the tensor cores idle half of the time (8192-token prompt, 32 q /
-// 8 kv heads, head_dim 128: 758 us with one issuer).  With one tile (head_dim
-// 256 and 512, whose O takes half of tensor memory) S is double-buffered, one
-// warp issues Q K^T, a block ahead, and the other P V.
+// stages), two issue MMAs, one prepares V (below; for codes four warps, which
+// widen them too); a warpgroup of softmax threads a tile; one warpgroup writes
+// results.  With two tiles (head_dim 64 and 128) each has an issuer of its
+// own, and one tile's products run while the other's softmax does.  With one
+// tile (head_dim 256 and 512, whose O takes half of tensor memory) S is
+// double-buffered, one warp issues Q K^T, a block ahead, and the other P V.
+//
+// What bounds it: a block of 128 keys is 2048 cycles of products a tile pair
+// (32 MMAs of 64 cycles), and 128 x 128 exponentials at 4 a cycle and
+// scheduler, 1024 cycles a tile, with twice that of other softmax
+// instructions on the same schedulers: 8192 tokens, 32 q / 8 kv heads,
+// head_dim 128 take 400 us, 1376 TFLOP/s, 0.74 of the measured 1863.
 //
 // V preparation: in blocks that some row of the item may see only in part,
 // slots outside the item's keys are zeroed (0 * NaN is NaN, whatever P is),
@@ -92,14 +98,15 @@ struct TcSmem {
   unsigned long long item_full[C::kItems], item_empty[C::kItems];
   unsigned long long turn[2], drain[2];
   PfItem items[C::kItems];
+  alignas(16) int4 spans[C::kItems][C::kNT];  // of the items' tiles
   float2 ml[C::kNT][128];               // rows' (reference maximum, sum) for the epilogue
   uint32_t tmem;
   volatile int stage_bad[C::kStagesV];  // a page id of this stage was out of range
   volatile int stage_fix[C::kStagesV];  // V preparation took out a value that is not finite
   volatile int flags[C::kNT];           // of the item whose O is full
   alignas(4) volatile unsigned char w_flags[C::kStagesP][4];  // FP8: of the four widening warps
-  volatile int abort_flag;              // status bit | thread << 8 of a wait that gave up
-  volatile uint32_t abort_at[2];        // its barrier and parity
+  // A wait that gave up: status bit | thread << 8 (0: none), its barrier, its parity.
+  alignas(16) volatile uint32_t abort_at[4];
 };
 
 // Weights are 2^(score - m) with m at most kLazy below the largest score.
@@ -241,18 +248,23 @@ __device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
   }
 }
 
-// Up to 64 probes of an mbarrier phase.
-__device__ __forceinline__ bool probe(unsigned long long* bar, uint32_t parity) {
-  uint32_t done;
+// Probes an mbarrier phase until it is met (1), or another wait has given up or
+// this one takes more than `limit` clock cycles and says so in `abort_at` (0).
+__device__ __forceinline__ uint32_t wait_or_abort(unsigned long long* bar, uint32_t parity, volatile uint32_t* abort_at,
+                                                  uint32_t limit, uint32_t code) {
+  uint32_t met;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 64;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 t0, t;\n\tmov.u32 t0, %%clock;\n\t"
       "PROBE_%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra MET_%=;\n\t"
-      "sub.u32 n, n, 1;\n\tsetp.ne.u32 p, n, 0;\n\t@p bra PROBE_%=;\n\tsetp.ne.u32 p, n, 0;\n\t"
+      "ld.volatile.shared.u32 t, [%3];\n\tsetp.ne.u32 q, t, 0;\n\t@q bra MET_%=;\n\t"
+      "mov.u32 t, %%clock;\n\tsub.u32 t, t, t0;\n\tsetp.le.u32 q, t, %4;\n\t@q bra PROBE_%=;\n\t"
+      "mov.u32 t, %%tid.x;\n\tshl.b32 t, t, 8;\n\tor.b32 t, t, %5;\n\t"
+      "st.volatile.shared.v4.u32 [%3], {t, %1, %2, %5};\n\t"
       "MET_%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
+      : "=r"(met)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(smem_addr(const_cast<uint32_t*>(abort_at))), "r"(limit), "r"(code)
       : "memory");
-  return done != 0;
+  return met;
 }
 
 // Everything a role needs besides its own state.
@@ -263,34 +275,22 @@ struct TcRole {
   int lane;
   bool live = true;  // false once a bounded wait has given up; uniform over a warp
 
-  // Bounded wait on an mbarrier phase.  A wait that passes `limit` clock
-  // cycles raises the CTA's abort flag, with what to report at the end, and
-  // every other wait then gives up too.  (Short code where the wait is met:
-  // it is inlined often, and the roles' loops together have to stay in the
-  // instruction caches.)
+  // Bounded wait on an mbarrier phase.  A wait that passes the limit (clock
+  // cycles) raises the CTA's abort flag, with what to report at the end, and
+  // every other wait then gives up too.  (Few instructions: it is inlined
+  // often, and the roles' loops together have to stay in the instruction
+  // caches.)
   __device__ __forceinline__ bool wait(unsigned long long* bar, uint32_t parity, unsigned code) {
-    if (__builtin_expect(!__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u)), 0)) {
-      const long long t0 = clock64();
-      bool met = false;
-      while (live && !met) {
-        met = __all_sync(0xffffffffu, probe(bar, parity & 1u));
-        if (!met && __any_sync(0xffffffffu, s.abort_flag != 0)) live = false;
-        if (!met && live && __any_sync(0xffffffffu, clock64() - t0 > a.wait_limit)) {
-          s.abort_at[0] = smem_addr(bar);
-          s.abort_at[1] = parity & 1u;
-          s.abort_flag = static_cast<int>(code | (threadIdx.x << 8));
-          live = false;
-        }
-      }
-    }
+    const uint32_t met = wait_or_abort(bar, parity & 1u, s.abort_at, a.wait_limit, code);
+    if (__builtin_expect(!__all_sync(0xffffffffu, met), 0)) live = false;
     return live;
   }
   // For copies and MMAs in flight, whatever the abort flag says.
   __device__ __forceinline__ void drain(unsigned long long* bar, uint32_t parity) {
     const long long t0 = clock64();
-    while (!probe(bar, parity & 1u))
+    while (!mbar_try_wait(bar, parity & 1u))
       if (clock64() - t0 > kDrainLimitCycles) {
-        s.abort_flag = static_cast<int>(kStatusDrain | (threadIdx.x << 8));
+        s.abort_at[0] = kStatusDrain | (threadIdx.x << 8);
         break;
       }
     __syncwarp();
@@ -300,6 +300,11 @@ struct TcRole {
     if (!wait(&s.item_full[n % C::kItems], n / C::kItems, kStatusSync)) return false;
     it = s.items[n % C::kItems];
     return it.b >= 0;
+  }
+  // The blocks and tokens of its tile t.
+  __device__ __forceinline__ TileSpan span(uint32_t n, int t) {
+    const int4 x = s.spans[n % C::kItems][t];
+    return TileSpan{x.x, x.y, x.z, x.w};
   }
   __device__ __forceinline__ void item_done(uint32_t n) {
     __syncwarp();
@@ -317,7 +322,7 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
   uint32_t nq = 0, used = 0, items = 0;  // nq: parity of a tile's Q loads in bit 16 t
   long long nk = 0, nv = 0;
   int blocks = 0;
-  const int tile_toks = 128 / a.group;
+  const int tile_toks = a.tile_tokens / C::kNT;
   int ids = 0, ids_at = -1;  // 32 table entries, one a lane, from page index ids_at
   PfItem it{};
   // This lane's box of a stage whose first page is the item's page p0: page
@@ -380,18 +385,19 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
     const bool more = w.next(a, it);
     if (!role.wait(&s.item_empty[items % C::kItems], (items / C::kItems) ^ 1u, kStatusEmpty)) break;
     if (!more) it.b = -1;
-    if (lane == 0) {
-      s.items[items % C::kItems] = it;
-      mbar_arrive(&s.item_full[items % C::kItems]);
+    if (lane < C::kNT) {
+      const TileSpan sp = tile_span(a, it, lane, tile_toks);
+      s.spans[items % C::kItems][lane] = make_int4(sp.jb, sp.je, sp.tok0, sp.ntok);
+      if (lane == 0) s.items[items % C::kItems] = it;
     }
     __syncwarp();
-    ++items;
+    if (lane == 0) mbar_arrive(&s.item_full[items % C::kItems]);
     if (!more) break;
     ids_at = -1;
     if (it.kb1 > it.kb0) read_ids((it.lo + it.kb0 * kPfBlock) / kPfPage);  // on their way while Q is asked for
 #pragma unroll 1
     for (int t = 0; t < C::kNT && !C::kFp8; ++t) {
-      const TileSpan sp = tile_span(a, it, t, tile_toks);
+      const TileSpan sp = role.span(items, t);
       if (sp.je <= sp.jb) continue;
       if (!role.wait(&s.q_empty[t], (nq >> (16 * t)) ^ 1u, kStatusEmpty)) break;
       nq ^= 1u << (16 * t);
@@ -418,6 +424,7 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
       }
       if (role.live && j >= it.kb0) load_v(j);
     }
+    ++items;
   }
   if (!role.live) {
     // let this CTA's copies land before it exits
@@ -450,7 +457,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
   uint32_t nblk = 0;    // one tile: blocks so far, whose parity is the buffer
   const int t = NT == 2 ? who : 0;
   const bool do_qk = NT == 2 || who == 0, do_pv = NT == 2 || who == 1;
-  const int tile_toks = 128 / a.group;
+  const int tile_toks = a.tile_tokens / C::kNT;
   PfItem it{};
 
   // S(buf) = Q K^T for block j's keys: the MMAs of chunk c and what follows them.  One lane.
@@ -458,7 +465,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
     const bool active = j >= sp.jb && j < sp.je;
     if (active) {
       const int keys = min(kPfBlock, it.hi - (it.lo + j * kPfBlock));
-      const uint32_t idesc = (FP8 ? umma_idesc_e4m3(0, false)
+      const uint32_t idesc = (FP8 ? umma_idesc_e4m3(0)
                                   : umma_idesc_f16(true, 0, false) | (a.neg_scale ? kUmmaNegateA : 0u)) |
                              (static_cast<uint32_t>((keys + 15) / 16 * 2) << 17);
       const uint32_t qa = umma_desc_lo(smem_addr(s.q[t]) + c * C::kKBytes, 16);
@@ -543,7 +550,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
     uint32_t from = tmem + buf * 128 + first * 8;
 #pragma unroll 1
     for (int k = first; k < last; ++k, from += 8, vb += (KS * 128) >> 4, acc = 1u)
-      umma_ts<false>(d_pv, from, vb, kHiP, idesc_pv, acc);
+      umma_ts(d_pv, from, vb, kHiP, idesc_pv, acc);
   };
   // One tile: O (+)= P(buf) V for block j's keys, V in stages of VK keys.
   auto pv = [&](int j, int buf, const TileSpan& sp, int& flags) {
@@ -578,7 +585,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
 
   for (; role.item(items, it); ++items) {
     if (it.kb1 > it.kb0) {
-      const TileSpan sp = tile_span(a, it, t, tile_toks);
+      const TileSpan sp = role.span(items, t);
       int flags = 0;
       if (do_qk && sp.je > sp.jb) {
         if (!role.wait(&s.q_full[t], nq, kStatusFull)) break;
@@ -589,9 +596,9 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
         // The tiles take turns: all of one's P V and next Q K^T, then the
         // other's.  Left to themselves the two issuers' MMAs interleave, both
         // tiles wait for twice the products and then both wait for the
-        // softmax, in step (3500 cycles a block; the products take 2048).  The
-        // turn passes when all is issued: passed a few MMAs earlier, the two
-        // tiles' products mix again (8192-token prompt 412 us, 419 then).
+        // softmax, in step.  The turn passes when all is issued: passed a few
+        // MMAs earlier, the two tiles' products mix again (8192-token prompt
+        // 2 % slower).
         const bool both = it.ntok > tile_toks;
         for (int j = it.kb0 - 1; j < it.kb1 && role.live; ++j) {  // P V of block j, then Q K^T of block j + 1
           // What can be waited for ahead of the weights is: after them this
@@ -816,7 +823,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
   constexpr int D = C::kD, NT = C::kNT, DV = C::kDV, ROW = C::kRow;
   constexpr bool FP8 = C::kFp8;
   const int warp = tid >> 5, lane = tid & 31;
-  const int tile_toks = 128 / a.group;
+  const int tile_toks = a.tile_tokens / C::kNT;
   const int t = NT == 2 ? warp >> 2 : 0;
   const int row = tid & 127;
   const int tok = row / a.group;
@@ -827,7 +834,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
   uint32_t items = 0;
   uint32_t blocks = 0;  // of this tile; one tile: the parity is the buffer
   for (; role.item(items, it); ++items) {
-    const TileSpan sp = tile_span(a, it, t, tile_toks);
+    const TileSpan sp = role.span(items, t);
     const bool valid = tok < tile_toks && tok < sp.ntok;
     const int pos = it.pos0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1);
     float m = -CUDART_INF_F, l = 0.f;
@@ -898,12 +905,15 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
 #pragma unroll 1
         for (int q = 0; q < kPfBlock; q += 32) {
           if (__all_sync(0xffffffffu, upto - q >= 31 && from - q <= 0)) continue;  // all seen
+          const int last = upto - q, first = from - q;
+          const uint32_t seen = (last < 0 ? 0u : last >= 31 ? ~0u : (2u << last) - 1u) &
+                                (first <= 0 ? ~0u : first > 31 ? 0u : ~0u << first);
           float x[32];
           tmem_ld32(tS + q, reinterpret_cast<uint32_t*>(x));
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < 32; ++c)
-            if (c > upto - q || c < from - q) x[c] = -CUDART_INF_F;
+            if (!(seen & (1u << c))) x[c] = -CUDART_INF_F;
           tmem_st32(tS + q, reinterpret_cast<const uint32_t*>(x));
         }
         tmem_wait_st();
@@ -1010,7 +1020,7 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
   constexpr int D = C::kD, NT = C::kNT, DV = C::kDV;
   constexpr bool FP8 = C::kFp8;
   const int lane = row & 31;
-  const int tile_toks = 128 / a.group;
+  const int tile_toks = a.tile_tokens / C::kNT;
   const int tok = row / a.group, g = row - tok * a.group;
   const uint32_t lane_base = static_cast<uint32_t>(row >> 5) << 21;
   TcRole<C> role{a, s, lane};
@@ -1020,7 +1030,7 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
 #pragma unroll 1
     for (int t = 0; t < NT; ++t) {
       const uint32_t tO = tmem + lane_base + C::kTmemO + t * DV;
-      const TileSpan sp = tile_span(a, it, t, tile_toks);
+      const TileSpan sp = role.span(items, t);
       const bool valid = tok < tile_toks && tok < sp.ntok;
       const int pos = it.pos0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1);
       if (!role.wait(&s.l_full[t], items, kStatusSync)) break;
@@ -1048,50 +1058,45 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
       // are exchanged within groups of four, so that a store touches eight rows
       // of 64 bytes and not 32 of 16 (which took 7000 cycles an item).
       const bool put = valid && !(split && l == 0.f);  // (the combine reads no sums of a row without weight)
-      const long long mine = split ? rec * DV
-                                   : (static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads +
-                                      it.head * a.group + g) * D + it.part * DV;
-      long long at[4];  // of the group's rows; -1: not written
+      char* const to = split ? reinterpret_cast<char*>(a.part) : static_cast<char*>(a.out);
+      const long long mine = split ? rec * DV * 4
+                                   : ((static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads +
+                                       it.head * a.group + g) * D + it.part * DV) * 2;
+      long long at[4];  // byte offsets of the group's rows; -1: not written
 #pragma unroll
       for (int r = 0; r < 4; ++r) at[r] = __shfl_sync(0xffffffffu, put ? mine : -1ll, (lane & ~3) + r);
+      // 64 bytes of a row at a time: 32 bf16 or 16 fp32 columns, from 32 columns read
 #pragma unroll 1
-      for (int c = 0; c < DV; c += 32) {
+      for (int c = 0; c < DV; c += split ? 16 : 32) {
         float o[32];
+        uint4 x[4];
         if (any) {
-          tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
+          tmem_ld32(tO + (c & ~31), reinterpret_cast<uint32_t*>(o));
           tmem_wait_ld();
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] *= mul;
         if (split) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint4 x[4];
+          for (int e = 0; e < 4; ++e) {
+            float f[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[e] = make_uint4(__float_as_uint(o[16 * q + 4 * e] * mul), __float_as_uint(o[16 * q + 4 * e + 1] * mul),
-                                __float_as_uint(o[16 * q + 4 * e + 2] * mul),
-                                __float_as_uint(o[16 * q + 4 * e + 3] * mul));
-            transpose4(x, lane);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (at[r] >= 0) *reinterpret_cast<uint4*>(a.part + at[r] + c + 16 * q + 4 * (lane & 3)) = x[r];
+            for (int i = 0; i < 4; ++i) f[i] = c & 16 ? o[16 + 4 * e + i] : o[4 * e + i];
+            x[e] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
           }
         } else {
-          uint4 x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            x[e] = make_uint4(pack_bf16(o[8 * e] * mul, o[8 * e + 1] * mul),
-                              pack_bf16(o[8 * e + 2] * mul, o[8 * e + 3] * mul),
-                              pack_bf16(o[8 * e + 4] * mul, o[8 * e + 5] * mul),
-                              pack_bf16(o[8 * e + 6] * mul, o[8 * e + 7] * mul));
-          transpose4(x, lane);
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (at[r] >= 0)
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at[r] + c + 8 * (lane & 3)) = x[r];
+            x[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                              pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
         }
+        transpose4(x, lane);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (at[r] >= 0) *reinterpret_cast<uint4*>(to + at[r] + c * (split ? 4 : 2) + 16 * (lane & 3)) = x[r];
         __syncwarp();  // the next load of tensor memory is the whole warp's
       }
       if (any) {
@@ -1117,7 +1122,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 
   if (tid == 0) {
     a.splits[blockIdx.x].pieces = 0;
-    s.abort_flag = 0;
+    s.abort_at[0] = 0;
     for (int i = 0; i < C::kStagesK; ++i) {
       mbar_init(&s.k_full[i], 1);
       mbar_init(&s.k_empty[i], NT);      // the issuers of Q K^T
@@ -1197,12 +1202,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (tid == 0 && s.abort_flag) {
-    atomicOr(a.status, static_cast<unsigned>(s.abort_flag) & 0xffu);
+  if (tid == 0 && s.abort_at[0]) {
+    atomicOr(a.status, s.abort_at[0] & 0xffu);
     if (atomicCAS(a.status + 1, 0u, 1u + blockIdx.x) == 0u) {  // first in the grid: where
-      a.status[2] = static_cast<unsigned>(s.abort_flag);
-      a.status[3] = s.abort_at[0];
-      a.status[4] = s.abort_at[1];
+      a.status[2] = s.abort_at[0];
+      a.status[3] = s.abort_at[1];
+      a.status[4] = s.abort_at[2];
     }
   }
 }

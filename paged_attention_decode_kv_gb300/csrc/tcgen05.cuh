@@ -1,8 +1,9 @@
 // tcgen05 (5th-generation tensor core) and tensor-memory helpers, sm_103a.
 //
 // Operand conventions used here: A and B tiles in shared memory as written by
-// TMA with the 128-byte swizzle (8-row atoms of 1024 bytes); accumulators and
-// the left operand P in tensor memory, one query row per lane.
+// TMA with the 128-byte swizzle (8-row atoms of 1024 bytes; 64-byte for codes of
+// head_dim 64); accumulators and the left operand P in tensor memory, one query
+// row per lane.
 #pragma once
 
 #include <stdint.h>
@@ -15,9 +16,7 @@ constexpr uint32_t umma_idesc_f16(bool bf16, int n, bool b_n_major) {
          (static_cast<uint32_t>(n / 8) << 17) | (8u << 24);
 }
 // The same for kind::f8f6f4 with E4M3 operands.
-constexpr uint32_t umma_idesc_e4m3(int n, bool b_n_major) {
-  return (1u << 4) | ((b_n_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(n / 8) << 17) | (8u << 24);
-}
+constexpr uint32_t umma_idesc_e4m3(int n) { return (1u << 4) | (static_cast<uint32_t>(n / 8) << 17) | (8u << 24); }
 constexpr uint32_t kUmmaNegateA = 1u << 13;
 
 // Shared-memory matrix descriptor: the address (in 16-byte units) in the low
@@ -66,22 +65,14 @@ __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi
         "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
         : "memory");
 }
-// The same with A in tensor memory.
-template <bool FP8>
+// The same with A in tensor memory, kind::f16.
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
                                         uint32_t acc) {
-  if constexpr (FP8)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
+      : "memory");
 }
 // Arrives on the barrier once every MMA this thread issued before has completed.
 __device__ __forceinline__ void umma_commit(unsigned long long* bar) {
@@ -123,11 +114,6 @@ __device__ __forceinline__ void tmem_ld1(uint32_t addr, uint32_t& r) {
 }
 __device__ __forceinline__ void tmem_st1(uint32_t addr, uint32_t r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%1], {%0};" ::"r"(r), "r"(addr) : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(addr)
-               : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
