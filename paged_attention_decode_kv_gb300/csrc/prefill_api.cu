@@ -2,6 +2,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <limits>
 #include <new>
 
 #include "../../include/vt_paged_attn.h"
@@ -14,7 +15,14 @@ namespace {
 
 using namespace vt::host;
 
-constexpr int kDefaultMinBlocks = 4;  // least 128-key blocks (and item weights) of a CTA
+// A CTA's least share is one 128-key block (or one item's fixed weight): calls
+// too small for the GPU are over soonest when every block and item has a CTA of
+// its own (8 new tokens, 16 q / 4 kv heads of 128: 10 us; 4 blocks 19 us).  But
+// each piece of an item costs the combine 0.3 us, so where (sequence, head)
+// pairs weigh more than 16 blocks on average it is two blocks (1 token over
+// 4000: 18 us, 23 with one block, 19 with four).  On CUDA cores a block takes
+// longer than that, and one block is always best.
+constexpr long long kLongWeight = 16 * kPfBlock;
 
 struct PrefillCall {
   void* out;
@@ -238,9 +246,12 @@ vt_status prefill(const PrefillCall& c) {
   while ((1u << log2_up) < static_cast<unsigned>(a.tile_tokens)) ++log2_up;
   a.tile_shift = 31 + log2_up;
   a.tile_mul = static_cast<unsigned>((1ull << a.tile_shift) / static_cast<unsigned>(a.tile_tokens) + 1);
+  a.group_mul = (65535 + a.group) / a.group;  // (128 rows x an excess below 128 stay below 2^16)
   a.v_parts = c.head_dim / v.cols;
-  const int min_blocks = g_override_min_units > 0 ? g_override_min_units : kDefaultMinBlocks;
-  a.min_weight = kPfBlock * (min_blocks < 2 ? 2 : min_blocks);
+  const bool set = g_override_min_units > 0;
+  a.min_weight = kPfBlock * (set ? std::min(g_override_min_units, 1 << 20) : 1);
+  a.long_total = set || !v.tensor_cores ? std::numeric_limits<long long>::max()
+                                        : kLongWeight * c.num_seqs * c.num_kv_heads * a.v_parts;
   a.status = reinterpret_cast<unsigned*>(status);
   a.splits = reinterpret_cast<PrefillSplit*>(base);
   a.ml = reinterpret_cast<float2*>(base + splits_bytes(grid));

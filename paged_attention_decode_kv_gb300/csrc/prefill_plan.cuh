@@ -45,8 +45,10 @@ struct PrefillArgs {
   int neg_scale;
   int tile_tokens;   // new tokens of an item
   unsigned tile_mul, tile_shift;  // x / tile_tokens = x * tile_mul >> tile_shift for 0 <= x < 2^31
+  int group_mul;     // r / group = r * group_mul >> 16 for 0 <= r <= 128
   int v_parts;       // items that share a (kv head, tile), each with a part of V's columns
-  int min_weight;    // least share of a CTA, at least 2 * kPfBlock
+  int min_weight;    // least share of a CTA, whole kPfBlocks (every cut of an item then takes a block)
+  long long long_total;  // total weight above which it doubles
   // Partials: record s (2 for each CTA: 2c an item's head piece, 2c + 1 a later piece) holds `rows` rows of
   // `cols` unnormalised fp32 sums; ml the rows' (running maximum, sum) in the log2 domain.
   float* part;
@@ -75,6 +77,9 @@ struct PfSeq {
 __device__ __forceinline__ int pf_tiles_in(const PrefillArgs& a, int x) {
   return static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(x)) * a.tile_mul >> a.tile_shift);
 }
+
+// Token of a tile's row r.
+__device__ __forceinline__ int pf_token_of(const PrefillArgs& a, int r) { return r * a.group_mul >> 16; }
 
 __device__ __forceinline__ PfSeq pf_seq(const PrefillArgs& a, int b) {
   PfSeq s;
@@ -208,7 +213,8 @@ struct PfWalk {
 __device__ __forceinline__ bool pf_share(const PrefillArgs& a, long long total, PfWalk& w) {
   w.heads = a.num_kv_heads * a.v_parts;
   // (weights stay far below 2^38: 2^31 blocks of 128)
-  const unsigned most = static_cast<unsigned>(total >> 7) / static_cast<unsigned>(a.min_weight >> 7);
+  const unsigned most =
+      static_cast<unsigned>(total >> 7) / static_cast<unsigned>(a.min_weight >> (total > a.long_total ? 6 : 7));
   w.ctas = static_cast<int>(most < 1 ? 1 : min(most, gridDim.x));
   w.cta = blockIdx.x;
   w.x = w.end = 0;

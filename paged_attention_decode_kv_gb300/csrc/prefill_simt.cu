@@ -5,9 +5,12 @@
 // 16-byte load takes the SM four cycles whatever its lanes share, so what
 // counts is how many FMAs a loaded value feeds.  Each of 128 threads holds 8
 // rows x 4 keys of S and 8 rows x D / 16 columns of O: 12 loads for 64 f32x2
-// FMAs of Q K^T and 24 for 128 of P V at head_dim 128.  (4 x 2 and 4 rows, with
-// 256 threads, took 227 us where this takes 204: 1263 tokens over contexts of
-// up to 972, 16 q / 8 kv heads of 128.)  P lies over K's tile.
+// FMAs of Q K^T and 16 for 128 of P V at head_dim 128.  (4 x 2 and 4 rows, with
+// 256 threads, took 227 us where 8 x 4 took 204: 1263 tokens over contexts of
+// up to 972, 16 q / 8 kv heads of 128.)  Q, K and V come by asynchronous copies;
+// at head_dim 128 P lies over K's tile.  Values are looked at only in tiles that
+// some row sees in part, and only if one is not finite do weights of 0 branch
+// around it: 185 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -24,14 +27,17 @@ constexpr int kSimtThreads = 128;
 constexpr int kSimtRows = 64;
 constexpr int kSimtKeys = 64;
 
+// Where it fits beside them (at head_dim 128 two CTAs an SM would no longer),
+// P has a place of its own, and the next K is fetched behind the softmax and P V.
+template <int D>
+constexpr bool kOwnP = D != 128;
+
 template <int D>
 struct SimtSmem {
   float q[kSimtRows][D + 4];
-  union {
-    float k[kSimtKeys][D + 4];
-    float p[kSimtRows][kSimtKeys + 4];
-  };
+  float k[kSimtKeys][D + 4];  // and P, where that has no place of its own
   float v[kSimtKeys][D];
+  float p[kOwnP<D> ? kSimtRows : 1][kSimtKeys + 4];
   int bad;
 };
 
@@ -57,21 +63,19 @@ __global__ void __launch_bounds__(kSimtThreads) prefill_simt_kernel(const Prefil
   PfWalk w;
   pf_begin(a, tid & 31, w);  // each warp for itself
   PfItem it;
-  const float sign = a.neg_scale ? -1.f : 1.f;
+  const float scale = a.neg_scale ? -a.scale_log2 : a.scale_log2;
+  float(*const ps)[kSimtKeys + 4] = reinterpret_cast<float(*)[kSimtKeys + 4]>(kOwnP<D> ? &s.p[0][0] : &s.k[0][0]);
+  constexpr int kLanes = D / 4, kLines = kSimtThreads / kLanes;  // lanes of a row, rows at a time
+  const int line = tid / kLanes, col = tid % kLanes * 4;
   while (w.next(a, it)) {
     __syncthreads();  // the previous item's tiles are done with
     if (tid == 0) s.bad = it.bad;
     const int rows = it.ntok * a.group;
-    for (int i = tid; i < kSimtRows * (D / 4); i += kSimtThreads) {
-      const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < rows) {
-        const int t = r / a.group, g = r - t * a.group;
-        x = load4(static_cast<const float*>(a.q) +
-                  (static_cast<long long>(it.row0 + t) * a.num_q_heads + it.head * a.group + g) * D + c);
-        x.x *= sign, x.y *= sign, x.z *= sign, x.w *= sign;
-      }
-      *reinterpret_cast<float4*>(&s.q[r][c]) = x;
+#pragma unroll 2
+    for (int r = line; r < kSimtRows; r += kLines) {
+      const int t = pf_token_of(a, r), g = r - t * a.group;
+      const long long at = (static_cast<long long>(it.row0 + (r < rows ? t : 0)) * a.num_q_heads + it.head * a.group + g) * D;
+      copy_async(&s.q[r][col], static_cast<const float*>(a.q) + at + col, r < rows);
     }
     float m[NR], l[NR];
     float2 o[NR][NC][2];  // columns 4 tx + 64 c, +1 and +2, +3
@@ -80,7 +84,7 @@ __global__ void __launch_bounds__(kSimtThreads) prefill_simt_kernel(const Prefil
     for (int i = 0; i < NR; ++i) {
       m[i] = -CUDART_INF_F;
       l[i] = 0.f;
-      pos[i] = it.pos0 + min((ty * NR + i) / a.group, it.ntok - 1);
+      pos[i] = it.pos0 + min(pf_token_of(a, ty * NR + i), it.ntok - 1);
 #pragma unroll
       for (int c = 0; c < NC; ++c) o[i][c][0] = o[i][c][1] = make_float2(0.f, 0.f);
     }
@@ -88,30 +92,35 @@ __global__ void __launch_bounds__(kSimtThreads) prefill_simt_kernel(const Prefil
     const int last = min(it.hi, it.lo + it.kb1 * kPfBlock);
     // K or V of 64 keys: slots outside [lo_exact, last) hold nothing a row may
     // use and are zeros
-    auto fetch = [&](const void* cache, int t0, float* to, int stride) {
-      const int* row = a.block_tables + static_cast<long long>(it.b) * a.max_blocks;
-      int page[2];
-#pragma unroll
+    auto fetch = [&](bool of_v, int t0) {
+#pragma unroll 1
       for (int i = 0; i < 2; ++i) {
-        const int at = t0 / kPfPage + i;
-        page[i] = t0 + i * kPfPage < last ? row[at] : 0;
-        if (page[i] < 0 || page[i] >= a.num_blocks) {
+        const int t = t0 + i * kPfPage;
+        int page = t < last ? a.block_tables[static_cast<long long>(it.b) * a.max_blocks + t / kPfPage] : 0;
+        if (page < 0 || page >= a.num_blocks) {
           if (tid == 0) s.bad = 1;
-          page[i] = 0;
+          page = 0;
         }
-      }
-      for (int i = tid; i < kSimtKeys * (D / 4); i += kSimtThreads) {
-        const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
-        const bool valid = t0 + r >= it.lo_exact && t0 + r < last;
-        const long long at =
-            ((static_cast<long long>(page[r / kPfPage]) * kPfPage + r % kPfPage) * a.num_kv_heads + it.head) * D + c;
-        copy_async(to + r * stride + c, static_cast<const float*>(cache) + at, valid);
+        const long long step = static_cast<long long>(a.num_kv_heads) * D;
+        const float* from = static_cast<const float*>(of_v ? a.v_cache : a.k_cache) +
+                            (static_cast<long long>(page) * kPfPage + line) * step + it.head * D + col;
+        float* to = of_v ? &s.v[i * kPfPage + line][col] : &s.k[i * kPfPage + line][col];
+        const int stride = kLines * (of_v ? D : D + 4);
+#pragma unroll 2
+        for (int r = t + line; r < t + kPfPage; r += kLines) {
+          copy_async(to, from, r >= it.lo_exact && r < last);
+          from += kLines * step;
+          to += stride;
+        }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    if (first < last) {
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) fetch(i, first);  // (with Q)
+    }
     for (int t0 = first; t0 < last; t0 += kSimtKeys) {
-      fetch(a.k_cache, t0, &s.k[0][0], D + 4);
-      fetch(a.v_cache, t0, &s.v[0][0], D);
+      const int next = t0 + kSimtKeys;
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncthreads();
       float2 y[NR][NK];  // sums over even and odd columns
@@ -134,28 +143,30 @@ __global__ void __launch_bounds__(kSimtThreads) prefill_simt_kernel(const Prefil
           }
         }
       }
-      __syncthreads();  // P goes over K
+      __syncthreads();  // K is done with
+      if (kOwnP<D> && next < last) fetch(false, next);
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
         float x[NK], top = -CUDART_INF_F;
+        const int at = t0 + tx, upto = min(pos[i], last - 1) - at;
+        const int from = a.window > 0 ? pos[i] - a.window + 1 - at : 0;
 #pragma unroll
         for (int e = 0; e < NK; ++e) {
-          const int t = t0 + tx + 16 * e;
-          const bool seen = t <= pos[i] && t < last && (a.window == 0 || t > pos[i] - a.window);
-          x[e] = seen ? (y[i][e].x + y[i][e].y) * a.scale_log2 : -CUDART_INF_F;
+          const bool seen = 16 * e <= upto && 16 * e >= from;
+          x[e] = seen ? (y[i][e].x + y[i][e].y) * scale : -CUDART_INF_F;
           top = fmaxf(top, x[e]);
         }
 #pragma unroll
         for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float mn = fmaxf(m[i], top);
         const float mb = mn == -CUDART_INF_F ? 0.f : mn;
-        const float keep = exp2f(m[i] - mb);
+        const float keep = ex2(m[i] - mb);
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < NK; ++e) {
-          const float p = exp2f(x[e] - mb);
+          const float p = ex2(x[e] - mb);
           sum += p;
-          s.p[ty * NR + i][tx + 16 * e] = p;
+          ps[ty * NR + i][tx + 16 * e] = p;
         }
 #pragma unroll
         for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -169,18 +180,31 @@ __global__ void __launch_bounds__(kSimtThreads) prefill_simt_kernel(const Prefil
             o[i][c][x2].y *= keep;
           }
       }
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (kOwnP<D> && next < last)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncthreads();
-      // Where some row sees only part of the keys, weights of 0 take no part:
-      // 0 times a value that is not finite would be NaN.
-      const bool partial = t0 + kSimtKeys > it.pos0 + 1 || (a.window > 0 && t0 < it.hi - a.window);
+      // Where some row sees only part of the keys, and a value is not finite,
+      // weights of 0 take no part: 0 times such a value would be NaN.
       const int keys = min(kSimtKeys, last - t0);
-      if (partial) {
+      bool apart = false;
+      if (t0 + kSimtKeys > it.pos0 + 1 || (a.window > 0 && t0 < it.hi - a.window)) {
+        unsigned seen = 0;
+#pragma unroll 1
+        for (int i = tid; i < keys * (D / 4); i += kSimtThreads) {
+          const uint4 x = reinterpret_cast<const uint4*>(&s.v[0][0])[i];
+          seen |= ((x.x & 0x7f800000u) + 0x00800000u) | ((x.y & 0x7f800000u) + 0x00800000u) |
+                  ((x.z & 0x7f800000u) + 0x00800000u) | ((x.w & 0x7f800000u) + 0x00800000u);
+        }
+        apart = __syncthreads_or(static_cast<int>(seen >> 31));
+      }
+      if (apart) {
 #pragma unroll 1
         for (int t = 0; t < keys; ++t) {
           float pe[NR];
 #pragma unroll
-          for (int i = 0; i < NR; ++i) pe[i] = s.p[ty * NR + i][t];
+          for (int i = 0; i < NR; ++i) pe[i] = ps[ty * NR + i][t];
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             const float4 v = load4(&s.v[t][4 * tx + 64 * c]);
@@ -195,10 +219,10 @@ __global__ void __launch_bounds__(kSimtThreads) prefill_simt_kernel(const Prefil
         }
       } else {
 #pragma unroll 1
-        for (int t = 0; t < kSimtKeys; t += 4) {
+        for (int t = 0; t < keys; t += 4) {
           float4 p[NR];
 #pragma unroll
-          for (int i = 0; i < NR; ++i) p[i] = load4(&s.p[ty * NR + i][t]);
+          for (int i = 0; i < NR; ++i) p[i] = load4(&ps[ty * NR + i][t]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
 #pragma unroll
@@ -215,6 +239,10 @@ __global__ void __launch_bounds__(kSimtThreads) prefill_simt_kernel(const Prefil
         }
       }
       __syncthreads();  // before the tiles are filled again
+      if (next < last) {
+#pragma unroll 1
+        for (int i = kOwnP<D> ? 1 : 0; i < 2; ++i) fetch(i, next);
+      }
     }
     __syncthreads();
     const bool bad = s.bad != 0;
@@ -232,7 +260,7 @@ __global__ void __launch_bounds__(kSimtThreads) prefill_simt_kernel(const Prefil
         dst = a.part + (slot * kSimtRows + r) * D;
         if (tx == 0) a.ml[slot * kSimtRows + r] = make_float2(bad ? CUDART_NAN_F : m[i], l[i]);
       } else {
-        const int t = r / a.group, g = r - t * a.group;
+        const int t = pf_token_of(a, r), g = r - t * a.group;
         dst = static_cast<float*>(a.out) +
               (static_cast<long long>(it.row0 + t) * a.num_q_heads + it.head * a.group + g) * D;
         mul = bad ? CUDART_NAN_F : 1.f / l[i];
@@ -280,12 +308,13 @@ __global__ void __launch_bounds__(kCombineThreads)
   const int r = blockIdx.y * kCombineRows + (threadIdx.x >> 3);
   const int tile_toks = tile_rows / a.group;
   const int tile = r / tile_rows, rr = r - tile * tile_rows;
-  const int g = rr % a.group;
-  const int tok = tile * tile_toks + rr / a.group;
+  const int g = rr - pf_token_of(a, rr) * a.group;
+  const int tok = tile * tile_toks + pf_token_of(a, rr);
   if (r >= rows || rr >= tile_toks * a.group || tok >= sp.ntok) return;
   auto record = [&](int p) { return (p == 0 ? 2ll * c : 2ll * (c + p) + 1) * rows + r; };
   float m = -CUDART_INF_F;
   bool bad = false;
+#pragma unroll 4
   for (int p = 0; p < sp.pieces; ++p) {
     const float mk = a.ml[record(p)].x;
     bad |= isnan(mk);
@@ -297,19 +326,33 @@ __global__ void __launch_bounds__(kCombineThreads)
   float4 o[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = 0; p < sp.pieces; ++p) {
-    const float2 ml = a.ml[record(p)];
-    const float f = exp2f(ml.x - mb);
-    if (f == 0.f) continue;  // nothing attended there
-    l += f * ml.y;
-    const float* src = a.part + record(p) * COLS + 4 * lane;
+  constexpr int U = COLS >= 256 ? 1 : 256 / COLS;  // pieces whose loads are in flight together
+#pragma unroll 1
+  for (int p0 = 0; p0 < sp.pieces; p0 += U) {
+    float f[U];
+    float4 x[U][N];
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float4 x = load4(src + 32 * e);
-      o[e].x += f * x.x;
-      o[e].y += f * x.y;
-      o[e].z += f * x.z;
-      o[e].w += f * x.w;
+    for (int u = 0; u < U; ++u) {
+      f[u] = 0.f;
+      if (p0 + u < sp.pieces) {
+        const float2 ml = a.ml[record(p0 + u)];
+        f[u] = ex2(ml.x - mb);
+        l += f[u] * ml.y;
+        const float* src = a.part + record(p0 + u) * COLS + 4 * lane;
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[u][e] = load4(src + 32 * e);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (f[u] == 0.f) continue;  // nothing attended there, nothing written
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        o[e].x += f[u] * x[u][e].x;
+        o[e].y += f[u] * x[u][e].y;
+        o[e].z += f[u] * x[u][e].z;
+        o[e].w += f[u] * x[u][e].w;
+      }
     }
   }
   const float inv = bad ? CUDART_NAN_F : 1.f / l;

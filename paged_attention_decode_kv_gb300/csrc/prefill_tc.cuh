@@ -826,7 +826,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
   const int tile_toks = a.tile_tokens / C::kNT;
   const int t = NT == 2 ? warp >> 2 : 0;
   const int row = tid & 127;
-  const int tok = row / a.group;
+  const int tok = pf_token_of(a, row);
   const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes a warp, lane in bits 16..
   const uint32_t tO = tmem + lane_base + C::kTmemO + t * DV;
   TcRole<C> role{a, s, lane};
@@ -1021,7 +1021,7 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
   constexpr bool FP8 = C::kFp8;
   const int lane = row & 31;
   const int tile_toks = a.tile_tokens / C::kNT;
-  const int tok = row / a.group, g = row - tok * a.group;
+  const int tok = pf_token_of(a, row), g = row - tok * a.group;
   const uint32_t lane_base = static_cast<uint32_t>(row >> 5) << 21;
   TcRole<C> role{a, s, lane};
   PfItem it{};
