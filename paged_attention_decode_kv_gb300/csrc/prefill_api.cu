@@ -15,14 +15,13 @@ namespace {
 
 using namespace vt::host;
 
-// A CTA's least share is one 128-key block (or one item's fixed weight): calls
-// too small for the GPU are over soonest when every block and item has a CTA of
-// its own (8 new tokens, 16 q / 4 kv heads of 128: 10 us; 4 blocks 19 us).  But
-// each piece of an item costs the combine 0.3 us, so where (sequence, head)
-// pairs weigh more than 16 blocks on average it is two blocks (1 token over
-// 4000: 18 us, 23 with one block, 19 with four).  On CUDA cores a block takes
-// longer than that, and one block is always best.
-constexpr long long kLongWeight = 16 * kPfBlock;
+// A CTA's least share is one 128-key block: calls too small for the GPU are over
+// soonest when every block and item has a CTA of its own (8 new tokens, 16 q /
+// 4 kv heads of 128: 10 us; with 4 blocks 19 us).  But each piece of an item
+// costs the combine 0.3 us, so where items have more than 8 blocks on average
+// it is two blocks (1 token over 4000: 18 us; with one block 23 us, with four
+// 19).  On CUDA cores a block takes longer than that, and one is always best.
+constexpr long long kLongItem = 8 * kPfBlock;
 
 struct PrefillCall {
   void* out;
@@ -248,10 +247,11 @@ vt_status prefill(const PrefillCall& c) {
   a.tile_mul = static_cast<unsigned>((1ull << a.tile_shift) / static_cast<unsigned>(a.tile_tokens) + 1);
   a.group_mul = (65535 + a.group) / a.group;  // (128 rows x an excess below 128 stay below 2^16)
   a.v_parts = c.head_dim / v.cols;
+  a.item_weight = v.item_weight;
   const bool set = g_override_min_units > 0;
   a.min_weight = kPfBlock * (set ? std::min(g_override_min_units, 1 << 20) : 1);
-  a.long_total = set || !v.tensor_cores ? std::numeric_limits<long long>::max()
-                                        : kLongWeight * c.num_seqs * c.num_kv_heads * a.v_parts;
+  const long long items = (static_cast<long long>(c.num_tokens) / a.tile_tokens + c.num_seqs) * c.num_kv_heads * a.v_parts;
+  a.long_total = set || !v.tensor_cores ? std::numeric_limits<long long>::max() : items * (v.item_weight + kLongItem);
   a.status = reinterpret_cast<unsigned*>(status);
   a.splits = reinterpret_cast<PrefillSplit*>(base);
   a.ml = reinterpret_cast<float2*>(base + splits_bytes(grid));

@@ -4,7 +4,7 @@
 // rows of tile_tokens consecutive new tokens for the query heads of one kv
 // head, over the keys any of them attends to.  Items are ordered sequence,
 // head, tile; item weights are lengths in tokens,
-//   W = hi - lo + kItemWeight,
+//   W = hi - lo + item_weight,
 // the attended span plus a fixed part for the query load and the epilogue.
 // The total weight is cut into even shares, one for each CTA, wherever the
 // cuts fall: a share's items inside it are done whole, an item that a cut
@@ -26,7 +26,6 @@ namespace vt {
 
 constexpr int kPfPage = 32;         // tokens per KV page
 constexpr int kPfBlock = 128;       // keys per step
-constexpr int kPfItemWeight = 128;  // an item's fixed cost in tokens
 
 struct PrefillArgs {
   void* out;
@@ -47,6 +46,7 @@ struct PrefillArgs {
   unsigned tile_mul, tile_shift;  // x / tile_tokens = x * tile_mul >> tile_shift for 0 <= x < 2^31
   int group_mul;     // r / group = r * group_mul >> 16 for 0 <= r <= 128
   int v_parts;       // items that share a (kv head, tile), each with a part of V's columns
+  int item_weight;   // an item's fixed cost in tokens
   int min_weight;    // least share of a CTA, whole kPfBlocks (every cut of an item then takes a block)
   long long long_total;  // total weight above which it doubles
   // Partials: record s (2 for each CTA: 2c an item's head piece, 2c + 1 a later piece) holds `rows` rows of
@@ -100,8 +100,8 @@ __device__ __forceinline__ long long pf_mul(int a, int b) { return static_cast<l
 __device__ __forceinline__ long long pf_weight(const PrefillArgs& a, const PfSeq& s, int K) {
   const int T = a.tile_tokens;
   if (K <= 0) return 0;
-  if (s.bad) return pf_mul(K, kPfItemWeight);
-  long long w = ((pf_mul(K, K) + K) >> 1) * T + pf_mul(K, s.p0) + pf_mul(K, kPfItemWeight);
+  if (s.bad) return pf_mul(K, a.item_weight);
+  long long w = ((pf_mul(K, K) + K) >> 1) * T + pf_mul(K, s.p0) + pf_mul(K, a.item_weight);
   if (K == s.tiles) w -= pf_mul(T, K) - s.n;
   if (a.window > 0) {
     const int A = s.p0 - a.window + 1;            // window start of the first token
@@ -143,9 +143,9 @@ struct PfWalk {
   __device__ __forceinline__ long long share(unsigned c) const { return c >= static_cast<unsigned>(ctas) ? total : quot * c; }
 
   // kb(r): block boundary nearest to weight r of an item.
-  __device__ __forceinline__ static int cut(long long r, long long W, int nkv) {
+  __device__ __forceinline__ static int cut(const PrefillArgs& a, long long r, long long W, int nkv) {
     if (r >= W) return nkv;
-    const long long k = (r - kPfItemWeight + kPfBlock / 2) >> 7;
+    const long long k = (r - a.item_weight + kPfBlock / 2) >> 7;
     return k < 0 ? 0 : (k > nkv ? nkv : static_cast<int>(k));
   }
 
@@ -172,15 +172,15 @@ struct PfWalk {
       it.pieces = 0;
       const long long ra = x - item_x, rb = end - item_x;
       const bool whole_end = rb >= W;
-      it.kb0 = ra <= 0 ? 0 : cut(ra, W, it.nkv);
-      it.kb1 = whole_end ? it.nkv : cut(rb, W, it.nkv);
+      it.kb0 = ra <= 0 ? 0 : cut(a, ra, W, it.nkv);
+      it.kb1 = whole_end ? it.nkv : cut(a, rb, W, it.nkv);
       if (it.kb0 == 0 && it.kb1 < it.nkv && it.kb1 > 0) {
         // the head piece of a split item: count the cuts inside it
         it.pieces = 1;
 #pragma unroll 1
         for (unsigned c = cta + 1;; ++c) {
           const long long e = share(c) - item_x;
-          if ((e >= W ? it.nkv : cut(e, W, it.nkv)) >= it.nkv) break;
+          if ((e >= W ? it.nkv : cut(a, e, W, it.nkv)) >= it.nkv) break;
           ++it.pieces;
         }
       }

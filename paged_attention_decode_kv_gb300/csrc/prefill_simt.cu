@@ -281,7 +281,7 @@ struct SimtVariant {
     return cudaGetLastError();
   }
   static PrefillVariant info() {
-    return PrefillVariant{kSimtThreads, kSimtRows, kSimtRows, D, 0, 1, sizeof(SimtSmem<D>),
+    return PrefillVariant{kSimtThreads, kSimtRows, kSimtRows, D, 0, 1, 128, sizeof(SimtSmem<D>),
                           reinterpret_cast<const void*>(&prefill_simt_kernel<D>), &launch};
   }
 };

@@ -26,7 +26,7 @@
 // (32 MMAs of 64 cycles), and 128 x 128 exponentials at 4 a cycle and
 // scheduler, 1024 cycles a tile, with twice that of other softmax
 // instructions on the same schedulers: 8192 tokens, 32 q / 8 kv heads,
-// head_dim 128 take 400 us, 1376 TFLOP/s, 0.74 of the measured 1863.
+// head_dim 128 take 383 us, 1435 TFLOP/s, 0.77 of the measured 1863.
 //
 // V preparation: in blocks that some row of the item may see only in part,
 // slots outside the item's keys are zeroed (0 * NaN is NaN, whatever P is),
@@ -108,6 +108,14 @@ struct TcSmem {
   // A wait that gave up: status bit | thread << 8 (0: none), its barrier, its parity.
   alignas(16) volatile uint32_t abort_at[4];
 };
+
+// An item's start and end cost as much as 1.5 blocks of keys; with codes the
+// softmax threads write Q's terms first, and it is three.  What the shares
+// assume is what balances them: a 4096-token prompt (32 q / 8 kv heads of 128)
+// takes 140 us over codes with 384, 169 with 128, 145 with 768; an 8192-token
+// one over bf16 383 us with 192, 389 with 128, 387 with 256.
+template <bool FP8>
+constexpr int kItemWeight = FP8 ? 384 : 192;
 
 // Weights are 2^(score - m) with m at most kLazy below the largest score.
 constexpr float kLazy = 8.f;
@@ -742,8 +750,8 @@ __device__ __forceinline__ void tc_prepare(const PrefillArgs& a, TcSmem<C>& s, i
 // FP8: four warps turn V's codes into f16, exactly, in the layout bf16 pages
 // have; a code is widened once for the item's 256 rows.  (As E4M3 MMA operands
 // codes would need P as two E4M3 terms: 12 more cycles of conversions for two
-// weights in the softmax, which then took 2300 cycles a block and the chunks'
-// case 435 us.)  Preparation is part of it.
+// weights in the softmax: four chunks of 500 to 2000 tokens took 436 us where
+// f16 weights took 381.)  Preparation is part of it.
 template <typename C>
 __device__ __forceinline__ void tc_widen(const PrefillArgs& a, TcSmem<C>& s, int tid) {
   constexpr int KS = 16;
@@ -835,59 +843,81 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
   uint32_t blocks = 0;  // of this tile; one tile: the parity is the buffer
   for (; role.item(items, it); ++items) {
     const TileSpan sp = role.span(items, t);
-    const bool valid = tok < tile_toks && tok < sp.ntok;
     const int pos = it.pos0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1);
     float m = -CUDART_INF_F, l = 0.f;
     float scale = a.scale_log2;  // from a score in tensor memory to the log2 domain
     if constexpr (FP8) {
-      // This row of Q as two E4M3 terms in the layout TMA gives K.  (The
-      // previous item's last scores are here, so its Q is done with.)
+      // Q as two E4M3 terms in the layout TMA gives K.  (The previous item's last
+      // scores are here, so its Q is done with.)  A warp takes its 32 rows a few
+      // at a time, 16 elements a lane, the next loads under way while it
+      // converts (a row a thread, read twice, took that prompt 203 us where
+      // this takes 169).
       if (sp.je > sp.jb) {
         const float ks = a.k_scale[it.head] * (a.neg_scale ? -1.f : 1.f);
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(a.q) +
-            (static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads + it.head * a.group + row -
-             tok * a.group) * D);
-        uint32_t most = 0;  // largest magnitude, as bf16 bits
-        if (valid) {
-#pragma unroll 8
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 x = src[i];
-            most = __vmaxu2(most, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                           __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+        constexpr int kLanes = D / 16, kRows = 32 / kLanes, kSteps = kLanes;  // lanes of a row, rows of a step
+        constexpr int kAhead = 2;                                             // steps of a batch of loads
+        const int piece = lane % kLanes;
+        const int blk = piece / (ROW / 16), ch = piece % (ROW / 16);
+        uint4 in[kAhead][2], next[kAhead][2];
+        auto load = [&](int step) {
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            const int r = (row & ~31) + (step + u) * kRows + lane / kLanes;
+            const int rt = pf_token_of(a, r);
+            next[u][0] = next[u][1] = make_uint4(0, 0, 0, 0);
+            if (step < kSteps && rt < min(tile_toks, sp.ntok)) {
+              const uint4* src = reinterpret_cast<const uint4*>(
+                  static_cast<const __nv_bfloat16*>(a.q) +
+                  (static_cast<long long>(it.row0 + sp.tok0 + rt) * a.num_q_heads + it.head * a.group + r -
+                   rt * a.group) * D);
+              next[u][0] = src[2 * piece];
+              next[u][1] = src[2 * piece + 1];
+            }
+          }
+        };
+        uint32_t own = 0;  // largest magnitude of this thread's row, as bf16 bits
+        load(0);
+#pragma unroll 1
+        for (int step = 0; step < kSteps; step += kAhead) {
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) in[u][0] = next[u][0], in[u][1] = next[u][1];
+          load(step + kAhead);
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            const uint32_t x[8] = {in[u][0].x, in[u][0].y, in[u][0].z, in[u][0].w,
+                                   in[u][1].x, in[u][1].y, in[u][1].z, in[u][1].w};
+            uint32_t most = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) most = __vmaxu2(most, x[k] & 0x7fff7fffu);
+            most = max(most & 0xffffu, most >> 16);
+#pragma unroll
+            for (int d = 1; d < kLanes; d <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+            const uint32_t given = __shfl_sync(0xffffffffu, most, lane % kRows * kLanes);
+            if (lane / kRows == step + u) own = given;
+            // the largest magnitude goes to [2^7, 2^8); rows below 2^-100 count as zero
+            const int e = min(max(static_cast<int>(most >> 7) - 127, -100), 127);
+            const float up = pow2f(7 - max(e, -119));
+            const float mul = ks < 0.f ? -up : up;
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t h0, h1, l0, l1;
+              e4m3x2_terms(bf16_lo_f(x[2 * k]) * mul, bf16_hi_f(x[2 * k]) * mul, h0, l0);
+              e4m3x2_terms(bf16_lo_f(x[2 * k + 1]) * mul, bf16_hi_f(x[2 * k + 1]) * mul, h1, l1);
+              hi[k] = h0 | (h1 << 16);
+              lo[k] = l0 | (l1 << 16);
+            }
+            const int r = (row & ~31) + (step + u) * kRows + lane / kLanes;
+            const int swz = ROW == 128 ? (ch ^ (r & 7)) : (ch ^ ((r >> 1) & 3));
+            unsigned char* dst = s.q[t] + blk * C::kKBlockBytes + r * ROW + swz * 16;
+            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(dst + 128 * D) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
-        most = max(most & 0xffffu, most >> 16);
-        // the largest magnitude goes to [2^7, 2^8); rows below 2^-100 count as zero
-        const int e = min(max(static_cast<int>(most >> 7) - 127, -100), 127);
-        const float up = pow2f(7 - max(e, -119));
+        const int e = min(max(static_cast<int>(own >> 7) - 127, -100), 127);
         scale = a.scale_log2 * fabsf(ks) * pow2f(max(e, -119) - 7);
         if (scale == 0.f) scale = 1e-37f;
-        if (most >= 0x7f80u) scale = CUDART_NAN_F;  // a query that is not finite, which codes cannot hold
-        const float mul = ks < 0.f ? -up : up;
-#pragma unroll 2
-        for (int i = 0; i < D / 16; ++i) {
-          uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-          if (valid) {
-            x0 = src[2 * i];
-            x1 = src[2 * i + 1];
-          }
-          const uint32_t in[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t h0, h1, l0, l1;
-            e4m3x2_terms(bf16_lo_f(in[2 * k]) * mul, bf16_hi_f(in[2 * k]) * mul, h0, l0);
-            e4m3x2_terms(bf16_lo_f(in[2 * k + 1]) * mul, bf16_hi_f(in[2 * k + 1]) * mul, h1, l1);
-            hi[k] = h0 | (h1 << 16);
-            lo[k] = l0 | (l1 << 16);
-          }
-          const int blk = i / (ROW / 16), ch = i % (ROW / 16);
-          const int swz = ROW == 128 ? (ch ^ (row & 7)) : (ch ^ ((row >> 1) & 3));
-          unsigned char* dst = s.q[t] + blk * C::kKBlockBytes + row * ROW + swz * 16;
-          *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(dst + 128 * D) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
+        if (own >= 0x7f80u) scale = CUDART_NAN_F;  // a query that is not finite, which codes cannot hold
         fence_proxy_async_shared();
         mbar_arrive(&s.q_full[t]);
       }
@@ -1222,7 +1252,7 @@ struct TcVariant {
     return cudaGetLastError();
   }
   static PrefillVariant info() {
-    return PrefillVariant{C::kThreads, C::kNT * 128, 128, C::kDV, 1, C::kStagesK + C::kStagesV, smem,
+    return PrefillVariant{C::kThreads, C::kNT * 128, 128, C::kDV, 1, C::kStagesK + C::kStagesV, kItemWeight<C::kFp8>, smem,
                           reinterpret_cast<const void*>(&prefill_tc_kernel<C>), &launch};
   }
 };

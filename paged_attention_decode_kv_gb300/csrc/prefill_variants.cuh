@@ -15,6 +15,7 @@ struct PrefillVariant {
   int cols;         // V columns of an item
   int tensor_cores;
   int stages;
+  int item_weight;  // an item's fixed cost in tokens (PrefillArgs)
   size_t smem_bytes;
   const void* func;
   cudaError_t (*launch)(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PrefillArgs& a,

@@ -231,21 +231,21 @@ def test_queries_that_are_not_finite(dev):
 @pytest.mark.parametrize("dtype,D", KINDS)
 def test_bounded_wait_gives_up_and_reports(dev, dtype, D):
     """A withheld block: the waits for it run out, the kernel returns, the status says so, and the next call is
-    exact.  (fp32 has no waits: it is not concerned.  CTA 0 has a second block to withhold if shares are of 4.)"""
+    exact.  (fp32 has no waits: it is not concerned.  CTA 0 has a second block to withhold if shares are of 8.)"""
     if dtype == "f32":
         return
     batch = make_batch([100, 30], [900, 2000], 8, 2, D, dtype)
     run(batch)
     torch.cuda.synchronize()
     vt.vt_paged_attn_set_test_wait(4_000_000, 0, 1)
-    run(batch, blocks=4)
+    run(batch, blocks=8)
     vt.vt_paged_attn_set_test_wait(0, -1, -1)
     torch.cuda.synchronize()
     words = vt.vt_paged_attn_device_status_detail()
     assert words[0] != 0 and words[1] == 1
     assert vt.vt_paged_attn_device_status() != 0
     assert vt.vt_paged_attn_device_status() == 0
-    check(batch, run(batch, blocks=4))
+    check(batch, run(batch, blocks=8))
     check(batch, run(batch))
 
 
