@@ -617,20 +617,21 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
           if (active && j == sp.jb && !role.wait(&s.o_free[t], no ^ 1u, kStatusSync)) break;
           const int steps = active ? steps_of(j, sp) : 0;
           const uint32_t vb = umma_desc_lo(v_addr(), C::kPBlockBytes);
-          if (active && !role.wait(&s.p_ready[0][t], np[0], kStatusSync)) break;
+          int from = 0;
           if (active && !both) {  // nothing else to run meanwhile: the first half's products at once
+            if (!role.wait(&s.p_ready[0][t], np[0], kStatusSync)) break;
             tc_fence_after();
+            from = kHalf;
             if (elect_one()) pv_steps(t, 0, min(steps, kHalf), vb, j > sp.jb);
             __syncwarp();
           }
-          if (active && !role.wait(&s.p_ready[1][t], np[0]++, kStatusSync)) break;
+          // (the turn before the weights, which are there last: a wait costs
+          // 250 cycles even if it is over when it begins)
           if (both && !role.wait(&s.turn[t], turns++ ^ (t ^ 1u), kStatusSync)) break;
+          if (active && !role.wait(&s.p_ready[1][t], np[0]++, kStatusSync)) break;
           tc_fence_after();
           if (elect_one()) {
-            if (active) {
-              const int from = both ? 0 : kHalf;
-              pv_steps(t, from, steps, vb + ((from * KS * 128) >> 4), from > 0 || j > sp.jb);
-            }
+            if (active) pv_steps(t, from, steps, vb + ((from * KS * 128) >> 4), from > 0 || j > sp.jb);
             if (mine) umma_commit(v_free());
             if (next) qk_issue(j + 1, t, 0, sp);
             if (both) mbar_arrive(&s.turn[t ^ 1]);
