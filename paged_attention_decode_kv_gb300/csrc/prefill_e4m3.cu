@@ -10,7 +10,7 @@ const PrefillVariant* prefill_e4m3_variant(int head_dim) {
   static const PrefillVariant table[] = {
       TcVariant<TcConfig<true, 64, 2, 64, 64, 4, 128, 3, 3>>::info(),
       TcVariant<TcConfig<true, 128, 2, 128, 128, 3, 128, 3, 2>>::info(),
-      TcVariant<TcConfig<true, 256, 1, 256, 128, 4, 64, 2, 2>>::info(),
+      TcVariant<TcConfig<true, 256, 1, 256, 256, 2, 64, 2, 2>>::info(),
   };
   return head_dim == 64 ? &table[0] : head_dim == 128 ? &table[1] : head_dim == 256 ? &table[2] : nullptr;
 }

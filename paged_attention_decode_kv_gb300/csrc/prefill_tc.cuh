@@ -289,6 +289,9 @@ struct TcRole {
   // often, and the roles' loops together have to stay in the instruction
   // caches.)
   __device__ __forceinline__ bool wait(unsigned long long* bar, uint32_t parity, unsigned code) {
+    // (most waits end in the first probe, which sleeps a while: with the clock
+    // read before it an 8192-token prompt took 366 us where this takes 352)
+    if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u)), 1)) return live;
     const uint32_t met = wait_or_abort(bar, parity & 1u, s.abort_at, a.wait_limit, code);
     if (__builtin_expect(!__all_sync(0xffffffffu, met), 0)) live = false;
     return live;
