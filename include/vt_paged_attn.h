@@ -1,6 +1,9 @@
 /*
  * vt_paged_attn -- single-token decode attention over a paged KV cache,
- * hand-written for NVIDIA GB300 (sm_103a).
+ * hand-written for NVIDIA GB300 (sm_103a), and what a serving step runs around
+ * it: rotary positions (vt_rope), the append of new keys and values to their
+ * pages (vt_paged_kv_append), the attention of ragged batches of prompts and
+ * chunks (vt_paged_attn_prefill).
  *
  * The operation (issue "ROCm gfx1200: PagedAttnOnline is 8.1x slower per call
  * than vLLM's paged-attention kernel", section "Where to look"; PR
@@ -372,7 +375,8 @@ VT_API vt_status vt_paged_kv_append_fp8(void* k_cache, void* v_cache, void* q_ou
  * sized by the head_dim and the device, not by the batch, and a call that would have to allocate it inside a stream
  * capture returns VT_ERR_SCRATCH_LIMIT (make one call before capturing).  With vt_paged_attn_set_workspace the
  * caller's area is used instead and must hold vt_paged_attn_prefill_workspace_bytes() beyond the decodes' counters.
- * vt_paged_attn_set_override and vt_paged_attn_set_test_wait apply; vt_paged_attn_device_status reports.
+ * vt_paged_attn_set_override (min_units_per_cta in blocks of 128 keys) and vt_paged_attn_set_test_wait (withhold_tile
+ * the key block of the CTA, fp32 has no waits) apply; vt_paged_attn_device_status reports.
  */
 VT_API vt_status vt_paged_attn_prefill(void* out, const void* q, const void* k_cache, const void* v_cache,
                                        const int32_t* q_starts, const int32_t* block_tables,

@@ -23,9 +23,14 @@
 namespace vt {
 namespace {
 
-constexpr int kSimtThreads = 128;
 constexpr int kSimtRows = 64;
 constexpr int kSimtKeys = 64;
+
+// 8 rows x 4 keys and 8 rows x D / 16 columns a thread; at head_dim 256 there is
+// room for one CTA an SM and not for that in a thread's registers: 4 rows, and
+// twice the threads.
+template <int D>
+constexpr int kSimtThreads = D == 256 ? 256 : 128;
 
 // Where it fits beside them (at head_dim 128 two CTAs an SM would no longer),
 // P has a place of its own, and the next K is fetched behind the softmax and P V.
@@ -53,30 +58,24 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, bool vali
 }
 
 template <int D>
-__global__ void __launch_bounds__(kSimtThreads) prefill_simt_kernel(const PrefillArgs a) {
+__global__ void __launch_bounds__(kSimtThreads<D>) prefill_simt_kernel(const PrefillArgs a) {
   extern __shared__ char raw[];
   SimtSmem<D>& s = *reinterpret_cast<SimtSmem<D>*>(raw);
   const int tid = threadIdx.x;
-  const int ty = tid >> 4, tx = tid & 15;  // rows 8 ty..+7; keys tx + 16 e; columns 4 tx + 64 c
-  constexpr int NC = D / 64, NR = 8, NK = 4;
+  const int ty = tid >> 4, tx = tid & 15;  // rows NR ty ...; keys tx + 16 e; columns 4 tx + 64 c
+  constexpr int NC = D / 64, NR = 1024 / kSimtThreads<D>, NK = 4;
   if (tid == 0) a.splits[blockIdx.x].pieces = 0;
   PfWalk w;
   pf_begin(a, tid & 31, w);  // each warp for itself
   PfItem it;
   const float scale = a.neg_scale ? -a.scale_log2 : a.scale_log2;
   float(*const ps)[kSimtKeys + 4] = reinterpret_cast<float(*)[kSimtKeys + 4]>(kOwnP<D> ? &s.p[0][0] : &s.k[0][0]);
-  constexpr int kLanes = D / 4, kLines = kSimtThreads / kLanes;  // lanes of a row, rows at a time
+  constexpr int kLanes = D / 4, kLines = kSimtThreads<D> / kLanes;  // lanes of a row, rows at a time
   const int line = tid / kLanes, col = tid % kLanes * 4;
   while (w.next(a, it)) {
     __syncthreads();  // the previous item's tiles are done with
     if (tid == 0) s.bad = it.bad;
     const int rows = it.ntok * a.group;
-#pragma unroll 2
-    for (int r = line; r < kSimtRows; r += kLines) {
-      const int t = pf_token_of(a, r), g = r - t * a.group;
-      const long long at = (static_cast<long long>(it.row0 + (r < rows ? t : 0)) * a.num_q_heads + it.head * a.group + g) * D;
-      copy_async(&s.q[r][col], static_cast<const float*>(a.q) + at + col, r < rows);
-    }
     float m[NR], l[NR];
     float2 o[NR][NC][2];  // columns 4 tx + 64 c, +1 and +2, +3
     int pos[NR];
@@ -116,8 +115,14 @@ __global__ void __launch_bounds__(kSimtThreads) prefill_simt_kernel(const Prefil
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if (first < last) {
+#pragma unroll 2
+      for (int r = line; r < kSimtRows; r += kLines) {
+        const int t = pf_token_of(a, r), g = r - t * a.group;
+        const long long at = (static_cast<long long>(it.row0 + (r < rows ? t : 0)) * a.num_q_heads + it.head * a.group + g) * D;
+        copy_async(&s.q[r][col], static_cast<const float*>(a.q) + at + col, r < rows);
+      }
 #pragma unroll 1
-      for (int i = 0; i < 2; ++i) fetch(i, first);  // (with Q)
+      for (int i = 0; i < 2; ++i) fetch(i, first);  // (Q comes with K)
     }
     for (int t0 = first; t0 < last; t0 += kSimtKeys) {
       const int next = t0 + kSimtKeys;
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(kSimtThreads) prefill_simt_kernel(const Prefil
       if (t0 + kSimtKeys > it.pos0 + 1 || (a.window > 0 && t0 < it.hi - a.window)) {
         unsigned seen = 0;
 #pragma unroll 1
-        for (int i = tid; i < keys * (D / 4); i += kSimtThreads) {
+        for (int i = tid; i < keys * (D / 4); i += kSimtThreads<D>) {
           const uint4 x = reinterpret_cast<const uint4*>(&s.v[0][0])[i];
           seen |= ((x.x & 0x7f800000u) + 0x00800000u) | ((x.y & 0x7f800000u) + 0x00800000u) |
                   ((x.z & 0x7f800000u) + 0x00800000u) | ((x.w & 0x7f800000u) + 0x00800000u);
@@ -277,11 +282,11 @@ template <int D>
 struct SimtVariant {
   static cudaError_t launch(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const PrefillArgs& a, int grid,
                             cudaStream_t stream) {
-    prefill_simt_kernel<D><<<grid, kSimtThreads, sizeof(SimtSmem<D>), stream>>>(a);
+    prefill_simt_kernel<D><<<grid, kSimtThreads<D>, sizeof(SimtSmem<D>), stream>>>(a);
     return cudaGetLastError();
   }
   static PrefillVariant info() {
-    return PrefillVariant{kSimtThreads, kSimtRows, kSimtRows, D, 0, 1, 128, sizeof(SimtSmem<D>),
+    return PrefillVariant{kSimtThreads<D>, kSimtRows, kSimtRows, D, 0, 1, 128, sizeof(SimtSmem<D>),
                           reinterpret_cast<const void*>(&prefill_simt_kernel<D>), &launch};
   }
 };
