@@ -505,12 +505,12 @@ def _t():
 
 # The checks below run on every call of operators that take a few microseconds
 # on the GPU: plain comparisons, no helper objects.
-def _row_stride(name, t, T, H, D, dtype, device):
+def _row_stride(name, t, T, H, D, dtype, index):
     """Checks packed rows [T][H][D] whose heads are contiguous; the token
     stride in elements."""
-    if t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != dtype:
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.shape != (T, H, D):
         raise ValueError(f"{name} must be [{T}][{H}][{D}], got {tuple(t.shape)}")
@@ -520,30 +520,41 @@ def _row_stride(name, t, T, H, D, dtype, device):
     return row if T > 1 else max(row, H * D)
 
 
-def _check_plain(name, t, dtype, device):
-    if t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != dtype:
+def _check_plain(name, t, dtype, index):
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _check_ragged(torch, q_starts, block_tables, context_lens, device):
-    """(num_seqs, max_blocks) of a ragged batch."""
+def _check_ragged(torch, k_cache, v_cache, kv, q_starts, block_tables, context_lens, index):
+    """(num_seqs, max_blocks) of a ragged batch over caches of type kv."""
     int32 = torch.int32
-    _check_plain("q_starts", q_starts, int32, device)
-    _check_plain("block_tables", block_tables, int32, device)
-    _check_plain("context_lens", context_lens, int32, device)
+    # (in line what _check_plain says of each: five calls cost a microsecond)
+    if not (k_cache.get_device() == v_cache.get_device() == q_starts.get_device() == block_tables.get_device()
+            == context_lens.get_device() == index and k_cache.dtype is kv and v_cache.dtype is kv
+            and q_starts.dtype is int32 and block_tables.dtype is int32 and context_lens.dtype is int32
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and q_starts.is_contiguous()
+            and block_tables.is_contiguous() and context_lens.is_contiguous()):
+        _check_plain("k_cache", k_cache, kv, index)
+        _check_plain("v_cache", v_cache, kv, index)
+        _check_plain("q_starts", q_starts, int32, index)
+        _check_plain("block_tables", block_tables, int32, index)
+        _check_plain("context_lens", context_lens, int32, index)
     B = context_lens.numel()
-    if q_starts.numel() != B + 1 or block_tables.dim() != 2 or block_tables.shape[0] != B:
+    if q_starts.numel() != B + 1 or block_tables.dim() != 2:
         raise ValueError("q_starts must be [num_seqs + 1] and block_tables [num_seqs][max_blocks]")
-    return B, block_tables.shape[1]
+    rows, max_blocks = block_tables.shape
+    if rows != B:
+        raise ValueError("q_starts must be [num_seqs + 1] and block_tables [num_seqs][max_blocks]")
+    return B, max_blocks
 
 
-def _check_scales(torch, k_scale, v_scale, heads, device):
-    _check_plain("k_scale", k_scale, torch.float32, device)
-    _check_plain("v_scale", v_scale, torch.float32, device)
+def _check_scales(torch, k_scale, v_scale, heads, index):
+    _check_plain("k_scale", k_scale, torch.float32, index)
+    _check_plain("v_scale", v_scale, torch.float32, index)
     if k_scale.numel() != heads or v_scale.numel() != heads:
         raise TypeError("k_scale and v_scale must be float32 [num_kv_heads]")
 
@@ -556,26 +567,34 @@ def _codes(torch, t):
     return t
 
 
-def _check_freq(torch, inv_freq, device):
+def _check_freq(torch, inv_freq, index):
     """(pointer, rot_dim) of a frequency table, or of none."""
     if inv_freq is None:
         return None, 0
-    _check_plain("inv_freq", inv_freq, torch.float64, device)
+    _check_plain("inv_freq", inv_freq, torch.float64, index)
     n = inv_freq.numel()
     return (inv_freq.data_ptr(), 2 * n) if n else (None, 0)
 
 
-def _cuda_device(name, t):
-    if not t.is_cuda:
+def _cuda_index(name, t):
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return index
 
 
-def _launch(torch, device, stream, where, call, before, after):
+def _io_code(torch, dtype):
+    if dtype is torch.bfloat16:
+        return VT_BF16
+    if dtype is torch.float32:
+        return VT_F32
+    raise TypeError(f"storage dtype must be bfloat16 or float32, got {dtype}")
+
+
+def _launch(torch, index, stream, where, call, before, after):
     """call(*before, stream handle, *after) with the tensors' device current;
     raises VtError."""
-    index = device.index
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             status = call(*before, _stream_on(torch, index, stream), *after)
     else:
@@ -599,18 +618,19 @@ def rope(x, positions, inv_freq, interleaved: bool = False, amplitude: float = 1
     itself rotates in place).  A negative position turns back, so the gradient
     of ``rope(x, p)`` is ``rope(grad, -p)``.  Asynchronous on ``stream``."""
     torch = _t()
-    device = _cuda_device("x", x)
-    code = dtype_code(x)
+    index = _cuda_index("x", x)
+    io = x.dtype
+    code = _io_code(torch, io)
     T, H, D = x.shape
-    x_stride = _row_stride("x", x, T, H, D, x.dtype, device)
-    _check_plain("positions", positions, torch.int32, device)
+    x_stride = _row_stride("x", x, T, H, D, io, index)
+    _check_plain("positions", positions, torch.int32, index)
     if positions.numel() != T:
         raise ValueError("positions must be [tokens]")
-    freq, rot = _check_freq(torch, inv_freq, device)
+    freq, rot = _check_freq(torch, inv_freq, index)
     if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=device)
-    out_stride = _row_stride("out", out, T, H, D, x.dtype, device)
-    _launch(torch, device, stream, "vt_rope", library().vt_rope,
+        out = torch.empty((T, H, D), dtype=io, device=x.device)
+    out_stride = _row_stride("out", out, T, H, D, io, index)
+    _launch(torch, index, stream, "vt_rope", library().vt_rope,
             (out.data_ptr(), x.data_ptr(), positions.data_ptr(), freq, T, H, D, rot, 1 if interleaved else 0, amplitude,
              x_stride, out_stride), (code,))
     return out
@@ -618,35 +638,33 @@ def rope(x, positions, inv_freq, interleaved: bool = False, amplitude: float = 1
 
 def _append(torch, k, v, k_cache, v_cache, scales, q_starts, block_tables, context_lens, q, q_out, positions,
             inv_freq, interleaved, amplitude, stream):
-    device = _cuda_device("k", k)
+    index = _cuda_index("k", k)
     T, Hkv, D = k.shape
     fp8 = scales is not None
     io = torch.bfloat16 if fp8 else k_cache.dtype
-    code = 0 if fp8 else dtype_code(k_cache)
-    ks = _row_stride("k", k, T, Hkv, D, io, device)
-    vs = _row_stride("v", v, T, Hkv, D, io, device)
-    _check_plain("k_cache", k_cache, k_cache.dtype, device)
-    _check_plain("v_cache", v_cache, k_cache.dtype, device)
+    code = 0 if fp8 else _io_code(torch, io)
+    ks = _row_stride("k", k, T, Hkv, D, io, index)
+    vs = _row_stride("v", v, T, Hkv, D, io, index)
+    B, max_blocks = _check_ragged(torch, k_cache, v_cache, k_cache.dtype, q_starts, block_tables, context_lens, index)
     shape = k_cache.shape
     if len(shape) != 4 or shape[2] != Hkv or shape[3] != D or v_cache.shape != shape:
         raise ValueError("k_cache/v_cache must be [num_blocks][32][Hkv][head_dim] matching k")
-    B, max_blocks = _check_ragged(torch, q_starts, block_tables, context_lens, device)
-    freq, rot = _check_freq(torch, inv_freq, device)
+    freq, rot = _check_freq(torch, inv_freq, index)
     Hq = qs = 0
     q_ptr = out_ptr = pos_ptr = None
     if q is not None:
         Hq = q.shape[1]
-        qs = _row_stride("q", q, T, Hq, D, io, device)
+        qs = _row_stride("q", q, T, Hq, D, io, index)
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=io, device=device)
-        _check_plain("q_out", q_out, io, device)
+            q_out = torch.empty((T, Hq, D), dtype=io, device=q.device)
+        _check_plain("q_out", q_out, io, index)
         if q_out.shape != q.shape:
             raise ValueError("q_out must be shaped like q")
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if positions is not None:
-        _check_plain("positions", positions, torch.int32, device)
+        _check_plain("positions", positions, torch.int32, index)
         if positions.numel() != T:
             raise ValueError("positions must be [tokens]")
         pos_ptr = positions.data_ptr()
@@ -654,11 +672,11 @@ def _append(torch, k, v, k_cache, v_cache, scales, q_starts, block_tables, conte
     rest = (q_starts.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), pos_ptr, freq, B, T, Hq, Hkv, D,
             shape[1], rot, 1 if interleaved else 0, amplitude, qs, ks, vs)
     if fp8:
-        _check_scales(torch, *scales, Hkv, device)
-        _launch(torch, device, stream, "vt_paged_kv_append_fp8", library().vt_paged_kv_append_fp8,
+        _check_scales(torch, *scales, Hkv, index)
+        _launch(torch, index, stream, "vt_paged_kv_append_fp8", library().vt_paged_kv_append_fp8,
                 head + (scales[0].data_ptr(), scales[1].data_ptr()) + rest, (max_blocks, shape[0]))
     else:
-        _launch(torch, device, stream, "vt_paged_kv_append", library().vt_paged_kv_append, head + rest,
+        _launch(torch, index, stream, "vt_paged_kv_append", library().vt_paged_kv_append, head + rest,
                 (max_blocks, shape[0], code))
     return q_out
 
@@ -688,25 +706,23 @@ def append_fp8(k, v, k_codes, v_codes, k_scale, v_scale, q_starts, block_tables,
 
 
 def _prefill(torch, q, k_cache, v_cache, scales, q_starts, block_tables, context_lens, scale, window, out, stream):
-    device = _cuda_device("q", q)
+    index = _cuda_index("q", q)
     if q.dim() != 3:
         raise ValueError("q must be [tokens][heads][head_dim]")
     T, Hq, D = q.shape
     fp8 = scales is not None
     io = torch.bfloat16 if fp8 else q.dtype
-    code = 0 if fp8 else dtype_code(q)
-    _check_plain("q", q, io, device)
-    kv = k_cache.dtype if fp8 else io
-    _check_plain("k_cache", k_cache, kv, device)
-    _check_plain("v_cache", v_cache, kv, device)
+    code = 0 if fp8 else _io_code(torch, io)
+    _check_plain("q", q, io, index)
+    B, max_blocks = _check_ragged(torch, k_cache, v_cache, k_cache.dtype if fp8 else io, q_starts, block_tables,
+                                  context_lens, index)
     shape = k_cache.shape
     if len(shape) != 4 or shape[3] != D or v_cache.shape != shape:
         raise ValueError("k_cache/v_cache must be [num_blocks][32][Hkv][head_dim] matching q")
-    B, max_blocks = _check_ragged(torch, q_starts, block_tables, context_lens, device)
     if out is None:
         out = torch.empty_like(q)
     else:
-        _check_plain("out", out, io, device)
+        _check_plain("out", out, io, index)
         if out.shape != q.shape:
             raise ValueError("out must be shaped like q")
     if scale is None:
@@ -715,11 +731,11 @@ def _prefill(torch, q, k_cache, v_cache, scales, q_starts, block_tables, context
     rest = (q_starts.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), B, T, Hq, shape[2], D, shape[1],
             scale, window)
     if fp8:
-        _check_scales(torch, *scales, shape[2], device)
-        _launch(torch, device, stream, "vt_paged_attn_prefill_fp8", library().vt_paged_attn_prefill_fp8,
+        _check_scales(torch, *scales, shape[2], index)
+        _launch(torch, index, stream, "vt_paged_attn_prefill_fp8", library().vt_paged_attn_prefill_fp8,
                 head + (scales[0].data_ptr(), scales[1].data_ptr()) + rest, (max_blocks, shape[0]))
     else:
-        _launch(torch, device, stream, "vt_paged_attn_prefill", library().vt_paged_attn_prefill, head + rest,
+        _launch(torch, index, stream, "vt_paged_attn_prefill", library().vt_paged_attn_prefill, head + rest,
                 (max_blocks, shape[0], code))
     return out
 
