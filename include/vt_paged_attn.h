@@ -288,7 +288,8 @@ VT_API vt_status vt_rope_frequencies(double* inv_freq, float* amplitude, int rot
  *               allowed.
  *   positions   [num_tokens] int32.
  *   inv_freq    [rot_dim / 2] device fp64, finite, 8-byte aligned.
- *   num_tokens >= 0 (0 is a no-op), head_dim a multiple of 8 and at most 1024 (else VT_ERR_UNSUPPORTED), rot_dim
+ *   num_tokens >= 0 (0 is a no-op) and below 2^31 - 2^20, head_dim a multiple of 8 and at most 1024 (else
+ *   VT_ERR_UNSUPPORTED), rot_dim
  *   even, 0 < rot_dim <= head_dim; interleaved 0 or 1; amplitude finite; dtype VT_BF16 or VT_F32.
  * Needs no workspace.
  */
@@ -334,7 +335,8 @@ VT_API vt_status vt_paged_kv_append(void* k_cache, void* v_cache, void* q_out, c
 /*
  * vt_paged_kv_append_fp8 -- the append into an FP8 (E4M3) cache: q, k, v and
  * q_out bf16, a cached code is the E4M3 value nearest to row / k_scale[h]
- * (v_scale[h]), ties to even, magnitudes past 448 held at 448, NaN kept.
+ * (v_scale[h]; the quotient as fp32, two roundings at most), ties to even,
+ * magnitudes past 448 held at 448, NaN kept.
  * head_dim 64, 128 or 256; k_scale, v_scale device float32 [num_kv_heads].
  */
 VT_API vt_status vt_paged_kv_append_fp8(void* k_cache, void* v_cache, void* q_out, const void* k, const void* v,

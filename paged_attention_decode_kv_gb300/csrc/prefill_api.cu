@@ -148,7 +148,10 @@ vt_status prepare(DeviceState& ds, const PrefillVariant& v, int* per_sm) {
   return VT_OK;
 }
 
-// The call's scratch: [status 256 B | counters of decodes, caller's area only | splits | ml | part].
+// The call's scratch: [status 256 B | splits | ml | part], or in the caller's
+// area [status | counters of decodes ... | splits | ml | part], at its end: a
+// captured prefill then stays off the counters, which larger decodes extend
+// and which keep their contents between calls.
 // Caller holds g_mutex.
 vt_status scratch(DeviceState& ds, size_t need, cudaStream_t stream, char** status, char** base, int* source) {
   if (ds.user.base) {
@@ -159,7 +162,7 @@ vt_status scratch(DeviceState& ds, size_t need, cudaStream_t stream, char** stat
       return VT_ERR_SCRATCH_LIMIT;
     }
     *status = ds.user.base;
-    *base = ds.user.base + at;
+    *base = ds.user.base + (ds.user.bytes - need) / 256 * 256;
     *source = 1;
     return VT_OK;
   }

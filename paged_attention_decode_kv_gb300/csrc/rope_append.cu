@@ -38,6 +38,8 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kPage = 32;
+// (a warp's tokens, at most 2^20, past the last row stay below 2^31)
+constexpr int kMaxTokens = 0x7fffffff - (1 << 20);
 constexpr int kMaxTokensPerBlock = 4;
 
 struct RopeArgs {
@@ -143,6 +145,21 @@ __device__ __forceinline__ int find_sequence(const int* starts, int num_seqs, in
     lo = min(nlo, hi - 1);
   }
   return lo;
+}
+
+// The fraction of a turn a position is worth, as a 64-bit fixed-point number.
+__device__ __forceinline__ unsigned long long turn_fraction(double inv_freq) {
+  const double turns = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
+  return __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+}
+// (cos, sin) of position p's angle, times the amplitude.
+__device__ __forceinline__ float2 cos_sin(unsigned long long fraction, int p, float amplitude) {
+  const unsigned long long w = fraction * static_cast<unsigned long long>(static_cast<long long>(p));
+  // the top 32 bits, rounded, as a signed fraction of a turn; sincospi takes half turns
+  const int top = static_cast<int>(static_cast<unsigned>((w + 0x80000000ull) >> 32));
+  float s, c;
+  sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+  return make_float2(c * amplitude, s * amplitude);
 }
 
 // What a block knows of each of its tokens.
@@ -251,16 +268,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
   }
   for (int r = tid; r < nt * half; r += kRopeThreads) {
     const int t = r / half, j = r - t * half;
-    const double turns = a.inv_freq[j] * 0.15915494309189533577;  // 1 / (2 pi)
-    // the fraction of a turn as a 64-bit fixed-point number
-    const unsigned long long u64 = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
-    const int p = APPEND ? tok[t].position : a.positions[t0 + t];
-    const unsigned long long w = u64 * static_cast<unsigned long long>(static_cast<long long>(p));
-    // the top 32 bits, rounded, as a signed fraction of a turn; sincospi takes half turns
-    const int top = static_cast<int>(static_cast<unsigned>((w + 0x80000000ull) >> 32));
-    float s, c;
-    sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-    table[r] = make_float2(c * a.amplitude, s * a.amplitude);
+    table[r] = cos_sin(turn_fraction(a.inv_freq[j]), APPEND ? tok[t].position : a.positions[t0 + t], a.amplitude);
   }
   __syncthreads();
 
@@ -333,20 +341,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
       }
     }
   }
-}
-
-__device__ __forceinline__ unsigned long long turn_fraction(double inv_freq) {
-  const double turns = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-  return __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
-}
-// (cos, sin) of position p's angle, times the amplitude.
-__device__ __forceinline__ float2 cos_sin(unsigned long long fraction, int p, float amplitude) {
-  const unsigned long long w = fraction * static_cast<unsigned long long>(static_cast<long long>(p));
-  // the top 32 bits, rounded, as a signed fraction of a turn; sincospi takes half turns
-  const int top = static_cast<int>(static_cast<unsigned>((w + 0x80000000ull) >> 32));
-  float s, c;
-  sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-  return make_float2(c * amplitude, s * amplitude);
 }
 
 // What is known of packed row t: found by a whole warp.  `b` is where the last
@@ -605,6 +599,7 @@ vt_status append(const RopeArgs& a, int block_size, int interleaved, cudaStream_
       !aligned(a.context_lens, 4) || !aligned(a.positions, 4))
     return VT_ERR_INVALID_ARG;
   if (!rotation_ok(a.inv_freq, a.rot_dim, a.head_dim, interleaved, a.amplitude, true)) return VT_ERR_INVALID_ARG;
+  if (a.num_tokens > kMaxTokens) return VT_ERR_UNSUPPORTED;
   if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256 && a.head_dim != 512) return VT_ERR_UNSUPPORTED;
   if (a.head_dim == 512 && dtype != VT_BF16) return VT_ERR_UNSUPPORTED;
   if (block_size != kPage) return VT_ERR_UNSUPPORTED;
@@ -728,7 +723,7 @@ vt_status vt_rope(void* out, const void* x, const int32_t* positions, const doub
   if (!stride_ok(x_stride, num_heads, head_dim, es) || !stride_ok(out_stride, num_heads, head_dim, es))
     return VT_ERR_INVALID_ARG;
   if (out == x && x_stride != out_stride) return VT_ERR_INVALID_ARG;
-  if (head_dim % 8 != 0 || head_dim > 1024) return VT_ERR_UNSUPPORTED;
+  if (num_tokens > kMaxTokens || head_dim % 8 != 0 || head_dim > 1024) return VT_ERR_UNSUPPORTED;
   if (static_cast<long long>(num_heads) * head_dim * kMaxTokensPerBlock > 0x3fffffffLL) return VT_ERR_UNSUPPORTED;
   int sms = 0;
   const vt_status st = current_sms(&sms);

@@ -301,6 +301,30 @@ def test_workspace_of_the_caller(dev, dtype, D):
     assert e.value.status == vt.VT_ERR_SCRATCH_LIMIT
 
 
+def test_captured_prefill_stays_off_the_decodes_counters(dev):
+    """In the caller's area a decode of more sequences extends the counters, which have to stay zero between decodes:
+    replays of a prefill captured before it do not write there."""
+    batch = make_batch([100, 30], [900, 2000], 8, 2, 64, "bf16")
+    area = torch.empty(vt.vt_paged_attn_prefill_workspace_bytes(64, vt.VT_BF16) + (64 << 20), dtype=torch.uint8,
+                       device=dev)
+    vt.vt_paged_attn_set_workspace(area.data_ptr(), area.numel())
+    out = torch.zeros_like(batch.q)
+    run(batch, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(batch, out=out)
+    seqs = 200000
+    table = batch.block_tables[1:2, :4].expand(seqs, 4).contiguous()
+    lens = torch.full((seqs,), 100, dtype=torch.int32, device=dev)
+    q = torch.randn((seqs, 2, 64), device=dev).to(torch.bfloat16)
+    first = vt.decode(q, batch.k_cache, batch.v_cache, table, lens)
+    out.zero_()
+    graph.replay()
+    again = vt.decode(q, batch.k_cache, batch.v_cache, table, lens)
+    assert torch.equal(first, again)
+    check(batch, out)
+
+
 def test_captured_and_replayed_with_other_lengths(dev):
     """The plan is made on the device: a replay follows the lengths as they then are."""
     batch = make_batch([100, 30], [900, 2000], 8, 2, 128, "bf16")

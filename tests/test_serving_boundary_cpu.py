@@ -49,6 +49,7 @@ SCALES = dict(k_scale=0xb000, v_scale=0xc000)
     (dict(out=0x2000, out_stride=1024), vt.VT_ERR_INVALID_ARG),
     (dict(dtype=vt.VT_E4M3), vt.VT_ERR_INVALID_ARG),
     (dict(num_heads=0), vt.VT_ERR_INVALID_ARG),
+    (dict(num_tokens=0x7fffffff), vt.VT_ERR_UNSUPPORTED),
     (dict(head_dim=100, rot_dim=100), vt.VT_ERR_UNSUPPORTED),
     (dict(head_dim=1032, x_stride=8256, out_stride=8256), vt.VT_ERR_UNSUPPORTED),
 ])
@@ -77,6 +78,7 @@ COMMON_APPEND = [
     (dict(amplitude=float("inf")), vt.VT_ERR_INVALID_ARG),
     (dict(num_kv_heads=0), vt.VT_ERR_INVALID_ARG),
     (dict(max_blocks_per_seq=0), vt.VT_ERR_INVALID_ARG),
+    (dict(num_tokens=0x7ff00000), vt.VT_ERR_UNSUPPORTED),
     (dict(head_dim=96, rot_dim=96), vt.VT_ERR_UNSUPPORTED),
     (dict(block_size=16), vt.VT_ERR_UNSUPPORTED),
     (dict(num_blocks=1 << 27), vt.VT_ERR_UNSUPPORTED),
