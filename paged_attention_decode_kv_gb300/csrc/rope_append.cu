@@ -10,8 +10,8 @@
 // angle of 10^5 radians would be off by 4e-3.)
 //
 // What bounds it: every element is read and written once, so HBM for long
-// batches and the launch for short ones.  A warp takes a token (or a slice of
-// its heads, where tokens are few).  A lane has a fixed place in a head's row,
+// batches and the launch for short ones.  A warp takes tokens one by one (or a
+// part of one's heads at either end of its share).  A lane has a fixed place in a head's row,
 // 16 elements with 16-byte accesses, and walks over the token's heads four
 // rounds at a time; the first rounds' loads are issued before the token is
 // looked up (a warp-wide search of the row starts, then the block table).
@@ -20,7 +20,7 @@
 // and no block-wide wait, and a warp's next token reuses its frequencies.
 // Measured (bf16, head_dim 128): 16803 tokens of 32 + 8 + 8 heads appended in
 // 74 to 77 us, 5.5 TB/s of reads and writes; 5173 tokens of 64 + 8 + 8 into
-// E4M3 pages 45 us; a block-wide kernel with a table in shared memory took 86
+// E4M3 pages 43 us; a block-wide kernel with a table in shared memory took 86
 // and 54.  That one remains for rows the lanes do not divide (rot_dim or
 // head_dim not a multiple of 16, head_dim 80 or 1024, say).
 #include <cuda_bf16.h>
@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kPage = 32;
-// (a warp's tokens, at most 2^20, past the last row stay below 2^31)
+// (row numbers past the last one stay in 32 bits)
 constexpr int kMaxTokens = 0x7fffffff - (1 << 20);
 constexpr int kMaxTokensPerBlock = 4;
 
@@ -365,20 +365,22 @@ __device__ __forceinline__ Token look_up(const RopeArgs& a, int t, int lane, int
 }
 
 // U lanes to a head's row of 16 U elements (U = 4 to 32, a power of two), 16 |
-// rot_dim.  Grid: warps of (token group, slice of the heads).
+// rot_dim.  The work is units of `unit` rounds of R heads, nb of them a token;
+// a warp takes consecutive ones, `per` or (the first `extra` warps) per + 1.
 template <typename T, typename KV, bool APPEND, bool INTER, int U>
-__global__ void __launch_bounds__(kRopeThreads) rope_warp_kernel(const RopeArgs a, int slices, int per_slice) {
+__global__ void __launch_bounds__(kRopeThreads) rope_warp_kernel(const RopeArgs a, int nb, int unit, int warps, long long per, int extra) {
   constexpr int R = 32 / U;                // heads of a round
   constexpr int NP = U >= 4 ? U / 4 : 1;   // pairs a lane forms: pairs NP lane ..
   constexpr int P = sizeof(T) == 2 ? 4 : 2;  // rounds in flight
   constexpr int D = 16 * U;
   const int lane = threadIdx.x & 31;
   const int warp = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
-  const int group = warp / slices, slice = warp - group * slices;
-  const int t0 = group * a.tokens_per_block, t1 = min(t0 + a.tokens_per_block, a.num_tokens);
-  if (t0 >= t1) return;
+  if (warp >= warps) return;
+  long long todo = per + (warp < extra ? 1 : 0);
+  const long long from = warp * per + min(warp, extra);
+  int t = static_cast<int>(from / nb);
+  int part = static_cast<int>(from - static_cast<long long>(t) * nb);  // the token's first unit to do
   const int heads = a.q_heads + (APPEND ? 2 * a.kv_heads : 0);
-  const int first = slice * per_slice, last = min(first + per_slice, heads);
   const int u = lane & (U - 1), r = lane / U;
   const int half = a.rot_dim >> 1;
   const bool turns = u < (a.rot_dim >> 4);  // else this lane's elements are copied
@@ -401,6 +403,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_warp_kernel(const RopeArgs 
       p = static_cast<const T*>(a.v) + t * a.v_stride + static_cast<long long>(head - a.q_heads - a.kv_heads) * D;
     return p;
   };
+  int last = 0;  // heads of the token at hand up to here
   auto fetch = [&](int t, int h0) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -418,7 +421,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_warp_kernel(const RopeArgs 
   };
   int b = -1;
 #pragma unroll 1
-  for (int t = t0; t < t1; ++t) {
+  for (int parts; todo > 0; todo -= parts, ++t, part = 0) {
+    parts = todo < nb - part ? static_cast<int>(todo) : nb - part;
+    const int first = part * unit * R;
+    last = min((part + parts) * unit * R, heads);
     fetch(t, first);
     Token k{0, 1, -1};
     if constexpr (APPEND)
@@ -489,33 +495,28 @@ __global__ void __launch_bounds__(kRopeThreads) rope_warp_kernel(const RopeArgs 
   }
 }
 
-template <typename T, typename KV, bool APPEND, bool INTER, int U>
-void launch_warps(const RopeArgs& a, int slices, int per_slice, cudaStream_t stream) {
-  const long long groups = (a.num_tokens + a.tokens_per_block - 1) / a.tokens_per_block;
-  const long long blocks = (groups * slices + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  rope_warp_kernel<T, KV, APPEND, INTER, U><<<static_cast<unsigned>(blocks), kRopeThreads, 0, stream>>>(a, slices,
-                                                                                                        per_slice);
-}
-
 // The warp kernel where a head's row is 4, 8, 16 or 32 lanes of 16 elements
 // and the rotated part whole units; false: not taken.
 template <typename T, typename KV, bool APPEND>
-bool launch_rope_warps(RopeArgs a, int interleaved, int num_sms, cudaStream_t stream) {
+bool launch_rope_warps(const RopeArgs& a, int interleaved, int num_sms, cudaStream_t stream) {
   const int U = a.head_dim / 16;
   if (a.rot_dim % 16 != 0 || a.head_dim % 16 != 0 || (U != 4 && U != 8 && U != 16 && U != 32)) return false;
-  const int heads = a.q_heads + (APPEND ? 2 * a.kv_heads : 0), round = 32 / U;
-  // One wave of 16 warps an SM: a warp takes as many tokens as that asks for
-  // (its frequencies, which need fp64, are formed once); where tokens are
-  // fewer, their heads are cut into slices of whole rounds instead.
+  const int heads = a.q_heads + (APPEND ? 2 * a.kv_heads : 0), R = 32 / U;
+  // One wave of 16 warps an SM, all with the same share of the heads' rounds
+  // (with whole tokens a warp a quarter of them idled, and 5173 tokens into
+  // E4M3 pages took 46 us, 43 so), in units of as many rounds as a warp has in flight,
+  // and single rounds where there are few.
+  constexpr int kFlight = sizeof(T) == 2 ? 4 : 2;
   const long long want = 16ll * num_sms;
-  a.tokens_per_block = static_cast<int>((a.num_tokens + want - 1) / want);
-  const long long rounds = (heads + round - 1) / round;
-  long long slices = a.tokens_per_block > 1 ? 1 : want / a.num_tokens;
-  slices = slices < 1 ? 1 : slices > rounds ? rounds : slices;
-  const int per = static_cast<int>((rounds + slices - 1) / slices) * round;
-  const int n = (heads + per - 1) / per;
+  const long long rounds = (heads + R - 1) / R;
+  const int unit = a.num_tokens * rounds >= 2 * kFlight * want ? kFlight : 1;
+  const long long nb = (rounds + unit - 1) / unit, total = a.num_tokens * nb;
+  const long long warps = total < want ? total : want;
+  const unsigned blocks = static_cast<unsigned>((warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32));
   auto go = [&](auto inter, auto units) {
-    launch_warps<T, KV, APPEND, decltype(inter)::value, decltype(units)::value>(a, n, per, stream);
+    rope_warp_kernel<T, KV, APPEND, decltype(inter)::value, decltype(units)::value>
+        <<<blocks, kRopeThreads, 0, stream>>>(a, static_cast<int>(nb), unit, static_cast<int>(warps), total / warps,
+                                              static_cast<int>(total % warps));
   };
   auto with = [&](auto inter) {
     if (U == 4) go(inter, std::integral_constant<int, 4>());
