@@ -11,13 +11,14 @@
 //
 // What bounds it: every element is read and written once, so HBM for long
 // batches and the launch for short ones.  A warp takes tokens one by one (or a
-// part of one's heads at either end of its share).  A lane has a fixed place in a head's row,
-// 16 elements with 16-byte accesses, and walks over the token's heads four
-// rounds at a time; the first rounds' loads are issued before the token is
-// looked up (a warp-wide search of the row starts, then the block table).
-// Each angle is formed once for all heads: the lanes share out a token's pairs
-// and hand (cos, sin) round by shuffles, so there is no table in shared memory
-// and no block-wide wait, and a warp's next token reuses its frequencies.
+// part of one's heads at either end of its share).  A lane has a fixed place in
+// a head's row, 16 elements with 16-byte accesses, and walks over the token's
+// heads four rounds at a time; the first rounds' loads are issued before the
+// token is looked up (a warp-wide search of the row starts, then the block
+// table).  Each angle is formed once for all heads: the lanes share out a
+// token's pairs and hand (cos, sin) round by shuffles, so there is no table in
+// shared memory and no block-wide wait, and a warp's next token reuses its
+// frequencies.
 // Measured (bf16, head_dim 128): 16803 tokens of 32 + 8 + 8 heads appended in
 // 74 to 77 us, 5.5 TB/s of reads and writes; 5173 tokens of 64 + 8 + 8 into
 // E4M3 pages 43 us; a block-wide kernel with a table in shared memory took 86

@@ -49,7 +49,8 @@ def check_rotated(got, x, positions, inv, interleaved, amplitude):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,H,D,rot", [(1, 1, 64, 64), (7, 3, 128, 128), (33, 5, 128, 64), (5, 2, 256, 34),
                                        (130, 1, 80, 48), (3, 4, 512, 512), (2, 2, 1024, 1024), (9, 1, 8, 2),
-                                       (2500, 2, 64, 32)])
+                                       (2500, 2, 64, 32),
+                                       (2999, 20, 128, 128), (4001, 31, 64, 64), (3001, 9, 256, 128)])
 def test_rope(dev, T, H, D, rot, dtype, interleaved):
     inv, _ = vt.rope_frequencies(rot, 10000.0)
     g = torch.Generator().manual_seed(T + D)
@@ -213,6 +214,13 @@ def test_append_many_sequences(dev):
     ctx = [n + int(x) for n, x in zip(new, torch.randint(0, 60, (1500,), generator=g))]
     batch = make_batch(new, ctx, 2, 1, 64, "bf16", pad=5)
     check_append(batch, *run_append(batch, 1, 64, dev, 2, 64))
+
+
+@pytest.mark.parametrize("dtype,heads", [("bf16", 20), ("e4m3", 20), ("f32", 28)])
+def test_append_where_shares_cut_tokens(dev, dtype, heads):
+    """Enough tokens and heads for warps' shares to begin and end inside tokens, at sequences' ends too."""
+    batch = make_batch([1511, 0, 1607, 3], [2000, 10, 1607, 77], heads, 4, 128, dtype, pad=6)
+    check_append(batch, *run_append(batch, 4, 128, dev, heads, 128))
 
 
 def test_append_one_long_prompt(dev):
