@@ -271,9 +271,9 @@ __device__ __forceinline__ void pf_begin(const PrefillArgs& a, int lane, PfWalk&
   const int run = static_cast<int>((static_cast<unsigned>(a.num_seqs) + 31u) >> 5);
   int from = lane * run, to = min(from + run, a.num_seqs);
   long long before = 0;
-  // round 0: runs of `run` sequences; round 1: the one run, in runs of its own
+  // first runs of `run` sequences, then the one run, in runs of its own
 #pragma unroll 1
-  for (int round = 0;; ++round) {
+  for (int depth = 0;; ++depth) {
     long long mine = 0;
 #pragma unroll 1
     for (int b = from; b < to; ++b) {
@@ -281,7 +281,7 @@ __device__ __forceinline__ void pf_begin(const PrefillArgs& a, int lane, PfWalk&
       mine += heads * pf_weight(a, s, s.tiles);
     }
     const long long inc = before + pf_warp_scan(mine, lane);
-    if (round == 0 && !pf_share(a, __shfl_sync(0xffffffffu, inc, 31), w)) return;
+    if (depth == 0 && !pf_share(a, __shfl_sync(0xffffffffu, inc, 31), w)) return;
     const int hit = __ffs(__ballot_sync(0xffffffffu, w.x < inc)) - 1;
     before = __shfl_sync(0xffffffffu, inc - mine, hit);
     const int first = __shfl_sync(0xffffffffu, from, hit), last = __shfl_sync(0xffffffffu, to, hit);

@@ -16,7 +16,7 @@
 #include <math_constants.h>
 #include <stdint.h>
 
-#include "decode_kernel.cuh"  // e4m3x4_to_f16, ex2, packs
+#include "decode_kernel.cuh"  // ex2, smem_addr
 #include "packed.cuh"
 #include "prefill_variants.cuh"
 

@@ -22,11 +22,12 @@
 // tile (head_dim 256 and 512, whose O takes half of tensor memory) S is
 // double-buffered, one warp issues Q K^T, a block ahead, and the other P V.
 //
-// What bounds it: a block of 128 keys is 2048 cycles of products a tile pair
-// (32 MMAs of 64 cycles), and 128 x 128 exponentials at 4 a cycle and
-// scheduler, 1024 cycles a tile, with twice that of other softmax
-// instructions on the same schedulers: 8192 tokens, 32 q / 8 kv heads,
-// head_dim 128 take 383 us, 1435 TFLOP/s, 0.77 of the measured 1863.
+// What bounds it: a tile's softmax (1300 cycles a block of 128 keys, 512 of them
+// exponentials) and its products (16 MMAs of 64 cycles) follow one another, and
+// two tiles take 2900 to 3000 cycles where the products alone take 2048: 8192
+// tokens, 32 q / 8 kv heads, head_dim 128 in 350 us, 1570 TFLOP/s, 0.84 of the
+// measured 1863.  Short items are bound by instruction fetch, so what is inlined
+// often or runs once an item is kept short.
 //
 // V preparation: in blocks that some row of the item may see only in part,
 // slots outside the item's keys are zeroed (0 * NaN is NaN, whatever P is),
@@ -952,22 +953,31 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
         }
         tmem_wait_st();
       }
-      // The scores are read twice, for their maximum and for the weights: a
-      // read of tensor memory takes 25 cycles, and the loop over halves keeps
-      // the code of a block short enough for the instruction caches.
+      // The second half of the scores is read twice, for the maximum and for the
+      // weights: a row of 128 has no room beside them, and the loop over halves
+      // keeps the code of a block short enough for the instruction caches.
       float most = -CUDART_INF_F;
+      float x[64];  // the first half's stay
       {
-        float x[128];
+        float z[64];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
+        for (int c = 0; c < 2; ++c) tmem_ld32(tS + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) tmem_ld32(tS + 64 + 32 * c, reinterpret_cast<uint32_t*>(z) + 32 * c);
         tmem_wait_ld();
         float top[4] = {x[0], x[1], x[2], x[3]};  // independent chains
 #pragma unroll
-        for (int c = 4; c < 124; c += 8)
+        for (int c = 4; c < 60; c += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e) top[e] = max3(top[e], x[c + 2 * e], x[c + 2 * e + 1]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], x[124 + e]);
+        for (int e = 0; e < 4; ++e) top[e] = max3(top[e], x[60 + e], z[e]);
+#pragma unroll
+        for (int c = 4; c < 60; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top[e] = max3(top[e], z[c + 2 * e], z[c + 2 * e + 1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], z[60 + e]);
         most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
       }
       if (__any_sync(0xffffffffu, most > m + kLazy)) {
@@ -999,10 +1009,11 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         // weights of keys 64 h .. 64 h + 63; the issuer may start on the first half at once
-        float x[64];
+        if (h == 1) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32(tS + 64 * h + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
-        tmem_wait_ld();
+          for (int c = 0; c < 2; ++c) tmem_ld32(tS + 64 + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
+          tmem_wait_ld();
+        }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t p[16];
