@@ -166,33 +166,47 @@ struct Ring {
 };
 
 // Adds the values that preparation took out to a row's sums, in tensor memory
-// from column 0 of `o` on: they are not finite, so neither is the result.  (All
-// threads of a warp together; rare, so compact.)
+// from column 0 of `o` on: they are not finite, so neither is the result.  They
+// lie among the keys that only some rows see, as many at either end as the item
+// has tokens and whatever the context is (a walk over a whole context of 30000
+// keys took longer than a bounded wait of 8 million cycles).  A warp looks at 32
+// of them at a time.  (All threads of a warp together; rare, so compact.)
 template <bool FP8>
 __device__ __forceinline__ void add_taken_values(const PrefillArgs& a, const PfItem& it, int head_dim, int pos, int cols,
                                               uint32_t o) {
+  const int lane = threadIdx.x & 31;
   const int first = max(it.lo_exact, it.lo + it.kb0 * kPfBlock);
   const int last = min(it.hi, it.lo + it.kb1 * kPfBlock);
+  // before `early` some rows' windows have not begun, from `late` on are some rows' later tokens
+  const int early = a.window > 0 ? min(last, max(first, it.hi - a.window)) : first;
+  const int late = min(last, max(early, it.pos0 + 1));
 #pragma unroll 1
   for (int c = 0; c < cols; ++c) {
     float add = 0.f;
 #pragma unroll 1
-    for (int t = first; t < last; ++t) {
-      const bool all = t <= it.pos0 && (a.window == 0 || t >= it.hi - a.window);
-      if (all) continue;  // seen by every row: was left in place
-      if (t > pos || (a.window > 0 && t <= pos - a.window)) continue;
-      const int page = a.block_tables[static_cast<long long>(it.b) * a.max_blocks + t / kPfPage];
-      if (page < 0 || page >= a.num_blocks) continue;
-      const long long at = ((static_cast<long long>(page) * kPfPage + t % kPfPage) * a.num_kv_heads + it.head) *
-                               head_dim + it.part * cols + c;
-      if constexpr (FP8) {
-        if ((static_cast<const uint8_t*>(a.v_cache)[at] & 0x7f) == 0x7f) add = CUDART_NAN_F;
-      } else {
-        const float x = __bfloat162float(static_cast<const __nv_bfloat16*>(a.v_cache)[at]);
-        if (!isfinite(x)) add += x;
+    for (int t0 = first; t0 < last; t0 += 32) {
+      if (t0 >= early && t0 < late) t0 = late;
+      const int t = t0 + lane;
+      float x = 0.f;
+      if (t < last && (t < early || t >= late)) {
+        const int page = a.block_tables[static_cast<long long>(it.b) * a.max_blocks + t / kPfPage];
+        if (page >= 0 && page < a.num_blocks) {
+          const long long at = ((static_cast<long long>(page) * kPfPage + t % kPfPage) * a.num_kv_heads + it.head) *
+                                   head_dim + it.part * cols + c;
+          if constexpr (FP8)
+            x = (static_cast<const uint8_t*>(a.v_cache)[at] & 0x7f) == 0x7f ? CUDART_NAN_F : 0.f;
+          else
+            x = __bfloat162float(static_cast<const __nv_bfloat16*>(a.v_cache)[at]);
+        }
+      }
+      unsigned taken = __ballot_sync(0xffffffffu, !isfinite(x));
+#pragma unroll 1
+      for (; taken; taken &= taken - 1) {
+        const int i = __ffs(taken) - 1, key = t0 + i;
+        const float y = __shfl_sync(0xffffffffu, x, i);
+        if (key <= pos && (a.window == 0 || key > pos - a.window)) add += y;
       }
     }
-    __syncwarp();
     uint32_t sum;
     tmem_ld1(o + c, sum);
     tmem_wait_ld();

@@ -423,3 +423,38 @@ def test_serving_steps(dev, dtype):
         vt.decode(q, step.k_cache, step.v_cache, step.block_tables, lens)
     _, reach = attention(step, D ** -0.5)
     assert ((got.double() - dec.double()).abs() <= 2.0 ** -5 * reach + 1e-6).all()
+
+
+@pytest.mark.parametrize("window", [0, 20000])
+@pytest.mark.parametrize("dtype,D", [k for k in KINDS if k[0] != "f32"])
+def test_values_that_are_not_finite_over_a_long_context(dev, dtype, D, window):
+    """What such a value costs is a matter of the keys that only some rows see, not of the context: two items of one
+    CTA over 30000 keys are done within 8 million cycles a wait (128 columns times 30000 keys, a few cycles each,
+    are more)."""
+    L, n = 30000, 40
+    batch = make_batch([n], [L], 4, 2, D, dtype, seed=D)
+    spots = [(L - n + 17, 3, "nan"), (L - n + 30, D - 1, "inf")]
+    if window:
+        spots.append((L - n - window + 12, 5, "nan"))  # at the first rows' window's far end
+    rows = torch.arange(L - n, L, device=dev)
+    hit = torch.zeros((n, D), dtype=torch.bool, device=dev)
+    for t, col, what in spots:
+        seen = (rows >= t) & (rows < t + window if window else rows >= t)
+        assert 0 < int(seen.sum()) < n
+        hit[seen, col] = True
+    ref, _ = attention(batch, D ** -0.5, window)
+    for t, col, what in spots:
+        page = batch.block_tables[0, t // 32].long()
+        batch.v_cache[page, t % 32, :, col] = 0x7F if dtype == "e4m3" else float(what)
+    vt.vt_paged_attn_set_test_wait(8_000_000, -1, -1)
+    out = run(batch, window=window, grid=1)
+    vt.vt_paged_attn_set_test_wait(0, -1, -1)
+    torch.cuda.synchronize()
+    assert vt.vt_paged_attn_device_status() == 0
+    bad = hit[:, None, :].expand_as(out)
+    assert not torch.isfinite(out[bad]).any()
+    assert (out[~bad].double() - ref[~bad]).abs().max() < 0.02
+    check_split = run(batch, window=window)  # the same, in pieces
+    torch.cuda.synchronize()
+    assert not torch.isfinite(check_split[bad]).any()
+    assert (check_split[~bad].double() - ref[~bad]).abs().max() < 0.02
