@@ -503,6 +503,8 @@ std::vector<std::pair<char*, size_t>> status_areas(DeviceState& ds) {
   if (ds.user.base) areas.emplace_back(ds.user.base, kStatusBytes + ds.user.counters_cap);
   if (ds.noalloc) areas.emplace_back(ds.noalloc, kStatusBytes);  // its calls clear their counters themselves
   if (ds.prefill.base) areas.emplace_back(ds.prefill.base, kStatusBytes);  // no counters
+  // replays of graphs that name an outgrown prefill scratch report there
+  for (char* p : ds.prefill_retired) areas.emplace_back(p, kStatusBytes);
   return areas;
 }
 

@@ -458,3 +458,28 @@ def test_values_that_are_not_finite_over_a_long_context(dev, dtype, D, window):
     torch.cuda.synchronize()
     assert not torch.isfinite(check_split[bad]).any()
     assert (check_split[~bad].double() - ref[~bad]).abs().max() < 0.02
+
+
+def test_give_up_in_a_scratch_that_a_graph_still_names(dev):
+    """A replay whose waits run out reports it although a larger call has meanwhile taken a larger scratch."""
+    batch = make_batch([100, 30], [900, 2000], 8, 2, 64, "bf16")
+    out = torch.zeros_like(batch.q)
+    torch.cuda.synchronize()
+    vt.vt_paged_attn_release()
+    run(batch, out=out)
+    graph = torch.cuda.CUDAGraph()
+    vt.vt_paged_attn_set_test_wait(4_000_000, 0, 1)
+    with torch.cuda.graph(graph):
+        run(batch, out=out, blocks=8)
+    vt.vt_paged_attn_set_test_wait(0, -1, -1)
+    wide = make_batch([100, 30], [900, 2000], 8, 2, 256, "bf16")
+    run(wide)
+    run(wide, grid=400)                    # larger again: two buffers are kept for graphs
+    assert vt.vt_paged_attn_device_status() == 0
+    graph.replay()
+    torch.cuda.synchronize()
+    words = vt.vt_paged_attn_device_status_detail()
+    assert words[0] != 0 and words[1] == 1
+    assert vt.vt_paged_attn_device_status() == words[0]
+    assert vt.vt_paged_attn_device_status() == 0
+    check(wide, run(wide))
