@@ -376,7 +376,9 @@ VT_API vt_status vt_paged_kv_append_fp8(void* k_cache, void* v_cache, void* q_ou
  * Workspace: as for vt_paged_attn_decode, but the library's own prefill scratch is apart from the decode's; it is
  * sized by the head_dim and the device, not by the batch, and a call that would have to allocate it inside a stream
  * capture returns VT_ERR_SCRATCH_LIMIT (make one call before capturing).  With vt_paged_attn_set_workspace the
- * caller's area is used instead and must hold vt_paged_attn_prefill_workspace_bytes() beyond the decodes' counters.
+ * caller's area is used instead, from its end, and must hold vt_paged_attn_prefill_workspace_bytes() beyond the
+ * decodes' counters; once a prefill on it has been captured, a decode whose counters would reach what that prefill
+ * uses returns VT_ERR_SCRATCH_LIMIT.
  * vt_paged_attn_set_override (min_units_per_cta in blocks of 128 keys) and vt_paged_attn_set_test_wait (withhold_tile
  * the key block of the CTA, fp32 has no waits) apply; vt_paged_attn_device_status reports.
  */
@@ -525,7 +527,8 @@ VT_API vt_status vt_paged_attn_device_status_detail(vt_stream_t stream, unsigned
  *   stream   the first 256 bytes (status words) are zeroed on it; later
  *            calls zero newly used counter space on their own streams.
  * A decode that needs more than `bytes` returns VT_ERR_SCRATCH_LIMIT before
- * launching anything.  Calls that share the workspace must be ordered on
+ * launching anything, and so does one whose counters would reach what a
+ * captured vt_paged_attn_prefill uses at the area's end.  Calls that share the workspace must be ordered on
  * the GPU.  vt_paged_attn_device_status reads its status words.
  * Returns VT_ERR_INVALID_ARG for a misaligned pointer or a too-small size.
  */

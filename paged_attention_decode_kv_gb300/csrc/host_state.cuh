@@ -24,6 +24,7 @@ struct Scratch {
   char* base = nullptr;
   size_t bytes = 0;
   size_t counters_cap = 0;  // bytes after the status words that hold zeroed counters
+  size_t captured_tail = 0;  // caller-owned: bytes at the end that captured prefills name, where no counter may go
 };
 
 struct DeviceState {

@@ -149,11 +149,18 @@ vt_status prepare(DeviceState& ds, const PrefillVariant& v, int* per_sm) {
 }
 
 // The call's scratch: [status 256 B | splits | ml | part], or in the caller's
-// area [status | counters of decodes ... | splits | ml | part], at its end: a
-// captured prefill then stays off the counters, which larger decodes extend
-// and which keep their contents between calls.
+// area [status | counters of decodes ... | splits | ml | part], at its end: the
+// counters, which larger decodes extend and which keep their contents between
+// calls, stay off what a captured prefill names there (captured_tail).
 // Caller holds g_mutex.
 vt_status scratch(DeviceState& ds, size_t need, cudaStream_t stream, char** status, char** base, int* source) {
+  auto capturing = [&](bool* yes) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing(stream, &cap);
+    *yes = cap != cudaStreamCaptureStatusNone;
+    return e == cudaSuccess ? VT_OK : cuda_fail(e, "cudaStreamIsCapturing");
+  };
+  bool in_capture = false;
   if (ds.user.base) {
     const size_t at = kStatusBytes + align_up(ds.user.counters_cap, 256);
     if (at + need > ds.user.bytes) {
@@ -161,23 +168,26 @@ vt_status scratch(DeviceState& ds, size_t need, cudaStream_t stream, char** stat
                           " bytes of workspace; the caller's workspace holds " + std::to_string(ds.user.bytes);
       return VT_ERR_SCRATCH_LIMIT;
     }
+    const vt_status st = capturing(&in_capture);
+    if (st != VT_OK) return st;
+    const size_t from = (ds.user.bytes - need) / 256 * 256;
+    if (in_capture) ds.user.captured_tail = std::max(ds.user.captured_tail, ds.user.bytes - from);
     *status = ds.user.base;
-    *base = ds.user.base + (ds.user.bytes - need) / 256 * 256;
+    *base = ds.user.base + from;
     *source = 1;
     return VT_OK;
   }
   if (ds.prefill.bytes < kStatusBytes + need) {
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    cudaError_t e = cudaStreamIsCapturing(stream, &cap);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
-    if (cap != cudaStreamCaptureStatusNone) {
+    const vt_status st = capturing(&in_capture);
+    if (st != VT_OK) return st;
+    if (in_capture) {
       g_last_cuda_error = "vt_paged_attn_prefill: the first call with this head_dim allocates scratch; make it "
                           "outside stream capture";
       return VT_ERR_SCRATCH_LIMIT;
     }
     void* p = nullptr;
     const size_t bytes = kStatusBytes + need;
-    e = cudaMalloc(&p, bytes);
+    cudaError_t e = cudaMalloc(&p, bytes);
     if (e != cudaSuccess) {
       cudaGetLastError();
       g_last_cuda_error = std::string("cudaMalloc: ") + cudaGetErrorString(e);

@@ -207,7 +207,8 @@ vt_status ensure_library_scratch(Scratch& w, const WsNeed& n, cudaStream_t strea
 
 // Caller-owned scratch of fixed size: the counter region grows in place (its
 // new part zeroed on `stream`, ahead of the kernel) as long as the buffer
-// holds it and the call's partials after it.
+// holds it and the call's partials after it, and it stays off the end that
+// captured prefills name (partials may lie there: none outlives its call).
 vt_status fit_user_scratch(Scratch& w, const WsNeed& n, cudaStream_t stream) {
   const size_t counters = align_up(n.counters_bytes, 256);
   const size_t cap = counters > w.counters_cap ? counters : w.counters_cap;
@@ -215,6 +216,12 @@ vt_status fit_user_scratch(Scratch& w, const WsNeed& n, cudaStream_t stream) {
   if (total > w.bytes) {
     g_last_cuda_error = "vt_paged_attn_decode: this call needs " + std::to_string(total) +
                         " bytes of workspace; the caller's workspace holds " + std::to_string(w.bytes);
+    return VT_ERR_SCRATCH_LIMIT;
+  }
+  if (cap > w.counters_cap && kStatusBytes + cap > w.bytes - w.captured_tail) {
+    g_last_cuda_error = "vt_paged_attn_decode: this call's " + std::to_string(cap) +
+                        " bytes of counters reach the last " + std::to_string(w.captured_tail) +
+                        " bytes of the caller's workspace, which a captured prefill names";
     return VT_ERR_SCRATCH_LIMIT;
   }
   if (cap > w.counters_cap) {
@@ -595,7 +602,7 @@ vt_status vt_paged_attn_set_workspace(void* dev_ptr, size_t bytes, vt_stream_t s
   }
   e = cudaMemsetAsync(dev_ptr, 0, kStatusBytes, reinterpret_cast<cudaStream_t>(stream_handle));
   if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
-  ds.user = Scratch{static_cast<char*>(dev_ptr), bytes, 0};
+  ds.user = Scratch{static_cast<char*>(dev_ptr), bytes, 0, 0};
   return VT_OK;
 }
 

@@ -483,3 +483,40 @@ def test_give_up_in_a_scratch_that_a_graph_still_names(dev):
     assert vt.vt_paged_attn_device_status() == words[0]
     assert vt.vt_paged_attn_device_status() == 0
     check(wide, run(wide))
+
+
+def test_decode_counters_stay_off_a_captured_prefill(dev):
+    """In a caller's area without room for both, a decode whose counters would reach a captured prefill's scratch is
+    refused; what fits runs, and replays leave its counters alone."""
+    batch = make_batch([100, 30], [900, 2000], 8, 2, 64, "bf16")
+    need = vt.vt_paged_attn_prefill_workspace_bytes(64, vt.VT_BF16)
+    room = 4096                            # of counters, beside the prefill: 1024 rows of heads
+    area = torch.empty(need + room, dtype=torch.uint8, device=dev)
+
+    def decode(seqs):
+        table = batch.block_tables[1:2, :4].expand(seqs, 4).contiguous()
+        lens = torch.full((seqs,), 100, dtype=torch.int32, device=dev)
+        q = torch.randn((seqs, 2, 64), generator=torch.Generator().manual_seed(seqs)).to(torch.bfloat16).to(dev)
+        return vt.decode(q, batch.k_cache, batch.v_cache, table, lens)
+
+    free = decode(500)
+    vt.vt_paged_attn_set_workspace(area.data_ptr(), area.numel())
+    assert area.numel() > vt.vt_paged_attn_workspace_bytes(1000, 2, 2, 64, vt.VT_BF16)
+    out = torch.zeros_like(batch.q)
+    run(batch, out=out)
+    decode(600)                            # 1200 counters, past the prefill's start: nothing names it yet
+    vt.vt_paged_attn_set_workspace(area.data_ptr(), area.numel())
+    run(batch, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(batch, out=out)
+    with pytest.raises(vt.VtError) as e:
+        decode(1000)                       # 2000 counters: 8000 bytes
+    assert e.value.status == vt.VT_ERR_SCRATCH_LIMIT
+    first = decode(500)
+    out.zero_()
+    graph.replay()
+    assert torch.equal(first, decode(500)) and torch.equal(first, free)
+    check(batch, out)
+    vt.vt_paged_attn_set_workspace(area.data_ptr(), area.numel())
+    decode(1000)                           # the caller's area handed over anew: no graph of before counts
