@@ -321,8 +321,9 @@ VT_API vt_status vt_rope(void* out, const void* x, const int32_t* positions, con
  * All pointers 16-byte aligned (int32 arrays 4, inv_freq 8), strides multiples of 16 bytes.
  *
  * Invalid device data never faults: a sequence with a context outside [n_b, max_blocks_per_seq * 32] writes nothing
- * to the cache and gets NaN q_out rows; a token whose page id is outside [0, num_blocks) is not written.  Two rows
- * of one call that name the same slot leave one of the two there.  Needs no workspace.
+ * to the cache and gets NaN q_out rows; a token whose page id is outside [0, num_blocks) is not written; a sequence
+ * whose q_starts are below 0, decrease or pass num_tokens has no rows (where they decrease, rows of the sequences
+ * around them may be left as they were).  Two rows of one call that name the same slot leave one of the two there.  Needs no workspace.
  */
 VT_API vt_status vt_paged_kv_append(void* k_cache, void* v_cache, void* q_out, const void* k, const void* v,
                                     const void* q, const int32_t* q_starts, const int32_t* block_tables,
@@ -371,7 +372,7 @@ VT_API vt_status vt_paged_kv_append_fp8(void* k_cache, void* v_cache, void* q_ou
  * The values of slots outside [0, context_lens[b]) of a sequence's pages are never used, whatever they hold.
  * Invalid device data never faults: rows of a sequence with a context outside [n_b, max_blocks_per_seq * 32] are
  * NaN, and so are rows that attend to a page whose id is outside [0, num_blocks) (other rows of that sequence may be
- * too).  q_starts that decrease or pass num_tokens are read as sequences without rows.
+ * too).  q_starts below 0, that decrease or pass num_tokens are read as sequences without rows.
  *
  * Workspace: as for vt_paged_attn_decode, but the library's own prefill scratch is apart from the decode's; it is
  * sized by the head_dim and the device, not by the batch, and a call that would have to allocate it inside a stream

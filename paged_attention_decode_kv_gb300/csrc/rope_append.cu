@@ -170,6 +170,27 @@ struct Token {
   long long slot;   // cache row (page * 32 + slot); -1: not written
 };
 
+// What is known of packed row t if sequence b owns it.  Starts that are no
+// array of rows (below 0, past num_tokens) own none: whatever they hold,
+// 0 <= p < L, and no difference leaves 32 bits.
+__device__ __forceinline__ Token token_of(const RopeArgs& a, int t, int b) {
+  const int s = a.q_starts[b], e = a.q_starts[b + 1], L = a.context_lens[b];
+  Token k{0, 0, -1};
+  if (s >= 0 && t >= s && t < e && e <= a.num_tokens) {
+    const int n = e - s;
+    if (L < n || L > static_cast<long long>(a.max_blocks) * kPage) {
+      k.live = 2;
+    } else {
+      const int p = L - n + (t - s);
+      k.live = 1;
+      k.position = a.positions ? a.positions[t] : p;
+      const int page = a.block_tables[static_cast<long long>(b) * a.max_blocks + p / kPage];
+      if (page >= 0 && page < a.num_blocks) k.slot = static_cast<long long>(page) * kPage + p % kPage;
+    }
+  }
+  return k;
+}
+
 // Any head_dim and rot_dim: a block takes a few tokens, fills a (cos, sin) table
 // of tokens x pairs in shared memory, then walks units of the tokens' heads.
 // APPEND: keys and values go to the cache as KV elements; otherwise only
@@ -245,25 +266,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     if (warp < nt) {
       const int t = t0 + warp;
       const int b = find_sequence(a.q_starts, a.num_seqs, t, lane);
-      if (lane == 0) {
-        const int s = a.q_starts[b], e = a.q_starts[b + 1];
-        const int L = a.context_lens[b];
-        Token k{0, 0, -1};
-        if (t >= s && t < e) {
-          const int n = e - s;
-          const long long cap = static_cast<long long>(a.max_blocks) * kPage;
-          if (L < n || L > cap) {
-            k.live = 2;
-          } else {
-            const int p = L - n + (t - s);
-            k.live = 1;
-            k.position = a.positions ? a.positions[t] : p;
-            const int page = a.block_tables[static_cast<long long>(b) * a.max_blocks + p / kPage];
-            if (page >= 0 && page < a.num_blocks) k.slot = static_cast<long long>(page) * kPage + p % kPage;
-          }
-        }
-        tok[warp] = k;
-      }
+      if (lane == 0) tok[warp] = token_of(a, t, b);
     }
     __syncthreads();
   }
@@ -344,25 +347,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
   }
 }
 
-// What is known of packed row t: found by a whole warp.  `b` is where the last
-// one was found (rows are looked up in order), or -1.
+// The same, the sequence found by a whole warp.  `b` is where the last one was
+// found (rows are looked up in order), or -1.
 __device__ __forceinline__ Token look_up(const RopeArgs& a, int t, int lane, int& b) {
   if (b < 0 || t >= a.q_starts[b + 1]) b = find_sequence(a.q_starts, a.num_seqs, t, lane);
-  const int s = a.q_starts[b], e = a.q_starts[b + 1], L = a.context_lens[b];
-  Token k{0, 0, -1};
-  if (t >= s && t < e) {
-    const int n = e - s;
-    if (L < n || L > static_cast<long long>(a.max_blocks) * kPage) {
-      k.live = 2;
-    } else {
-      const int p = L - n + (t - s);
-      k.live = 1;
-      k.position = a.positions ? a.positions[t] : p;
-      const int page = a.block_tables[static_cast<long long>(b) * a.max_blocks + p / kPage];
-      if (page >= 0 && page < a.num_blocks) k.slot = static_cast<long long>(page) * kPage + p % kPage;
-    }
-  }
-  return k;
+  return token_of(a, t, b);
 }
 
 // U lanes to a head's row of 16 U elements (U = 4 to 32, a power of two), 16 |

@@ -268,3 +268,38 @@ def test_append_captured(dev):
     torch.cuda.synchronize()
     batch.ctx = [4, 32]
     check_append(batch, q, k, v, inv, kc2, vc2, out2)
+
+
+@pytest.mark.parametrize("rot", [64, 36])          # both kernels
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "e4m3"])
+@pytest.mark.parametrize("starts,must", [
+    ([-2 ** 31, 100, 100, 100], []), ([-2 ** 31, -2 ** 31, 4, 8], [2]), ([-5, 4, 8, 12], [1, 2]),
+    ([0, 4, 400, 12], [0]), ([0, 4, 2 ** 31 - 1, 2 ** 31 - 1], [0]), ([0, 8, 4, 12], []),
+    ([2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, -2 ** 31], []),
+])
+def test_append_bad_row_starts(dev, dtype, rot, starts, must):
+    """Starts below 0, that decrease or pass the rows: those sequences have no rows; nothing is written for them and
+    nothing is read outside the tables, whatever the contexts.  (Where starts decrease, rows of two sequences overlap,
+    and some may be left.)"""
+    for lens in ([60, 61, 62], [0, 0, 0], [1, 2 ** 31 - 1, -2 ** 31]):
+        batch = make_batch([4, 4, 4], [60, 61, 62], 2, 1, 64, dtype)
+        batch.q_starts.copy_(torch.tensor(starts, dtype=torch.int32))
+        batch.context_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        q, k, v, inv, kc, vc, out = run_append(batch, 1, 64, dev, 2, rot)
+        torch.cuda.synchronize()
+        rows = torch.zeros(12, dtype=torch.bool, device=dev)
+        slots = torch.zeros(kc.shape[:2], dtype=torch.bool, device=dev)
+        for b in range(3):
+            n = starts[b + 1] - starts[b]
+            if starts[b] < 0 or n <= 0 or starts[b + 1] > 12:
+                assert b not in must
+                continue
+            rows[starts[b]:starts[b + 1]] = True
+            for p in range(lens[b] - n, lens[b]) if n <= lens[b] <= 64 else ():
+                slots[batch.block_tables[b, p // 32].long(), p % 32] = True
+        bits = {1: torch.uint8, 2: torch.int16, 4: torch.int32}[kc.element_size()]
+        for new, old in ((kc, batch.k_cache), (vc, batch.v_cache)):
+            assert torch.equal(new[~slots].view(bits), old[~slots].view(bits))
+        assert (out[~rows] == 7).all()
+        for b in must:
+            assert not (out[starts[b]:starts[b + 1]] == 7).all(-1).any()
