@@ -209,13 +209,20 @@ struct PfWalk {
   }
 };
 
+// CTAs that get a share of a total weight: shares of min_weight (twice that
+// above long_total) at least, in blocks.  (A 32-bit division: 2^32 blocks and
+// more count as 2^32 - 1, which is more than there are CTAs.)
+__host__ __device__ __forceinline__ unsigned pf_share_count(long long total, int min_weight, long long long_total,
+                                                            unsigned grid) {
+  const unsigned blocks = total >> 39 ? 0xffffffffu : static_cast<unsigned>(total >> 7);
+  const unsigned most = blocks / static_cast<unsigned>(min_weight >> (total > long_total ? 6 : 7));
+  return most < 1 ? 1u : most < grid ? most : grid;
+}
+
 // The share of this CTA in a total weight; false if it has none.
 __device__ __forceinline__ bool pf_share(const PrefillArgs& a, long long total, PfWalk& w) {
   w.heads = a.num_kv_heads * a.v_parts;
-  // (weights stay far below 2^38: 2^31 blocks of 128)
-  const unsigned most =
-      static_cast<unsigned>(total >> 7) / static_cast<unsigned>(a.min_weight >> (total > a.long_total ? 6 : 7));
-  w.ctas = static_cast<int>(most < 1 ? 1 : min(most, gridDim.x));
+  w.ctas = static_cast<int>(pf_share_count(total, a.min_weight, a.long_total, gridDim.x));
   w.cta = blockIdx.x;
   w.x = w.end = 0;
   if (total == 0 || w.cta >= w.ctas) return false;
