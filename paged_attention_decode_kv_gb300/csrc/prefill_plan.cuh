@@ -219,6 +219,15 @@ __host__ __device__ __forceinline__ unsigned pf_share_count(long long total, int
   return most < 1 ? 1u : most < grid ? most : grid;
 }
 
+// What one of `ctas` shares weighs; the last also takes the remainder.  (A 32-bit
+// division of the total's leading 32 bits: of 152 shares the last is at most
+// 152 * 152 / 2^31 of a share larger.)
+__host__ __device__ __forceinline__ long long pf_share_weight(long long total, unsigned ctas) {
+  int shift = 0;
+  while (total >> shift >> 32) ++shift;
+  return static_cast<long long>(static_cast<unsigned>(total >> shift) / ctas) << shift;
+}
+
 // The share of this CTA in a total weight; false if it has none.
 __device__ __forceinline__ bool pf_share(const PrefillArgs& a, long long total, PfWalk& w) {
   w.heads = a.num_kv_heads * a.v_parts;
@@ -227,8 +236,7 @@ __device__ __forceinline__ bool pf_share(const PrefillArgs& a, long long total, 
   w.x = w.end = 0;
   if (total == 0 || w.cta >= w.ctas) return false;
   w.total = total;
-  const int shift = total >> 32 ? 16 : 0;  // (a 32-bit division: the shares need not be even to the last token)
-  w.quot = static_cast<long long>(static_cast<unsigned>(total >> shift) / static_cast<unsigned>(w.ctas)) << shift;
+  w.quot = pf_share_weight(total, w.ctas);
   w.x = w.share(blockIdx.x);
   w.end = w.share(blockIdx.x + 1);
   return w.x < w.end;

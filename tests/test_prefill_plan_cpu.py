@@ -35,3 +35,14 @@ def test_number_of_shares(shares):
     assert [r[0] for r in shares(rows)] == [1, 1, 10, 5, 1]
     large = [(2 ** b + d, 128, long, 152) for b in range(20, 47) for d in (-1, 0, 1, 129) for long in (1000, NEVER)]
     assert all(r[0] == 152 for r in shares(large))
+
+
+@pytest.mark.parametrize("grid", [1, 7, 152, 400])
+def test_shares_are_even(shares, grid):
+    """No share is more than 1 % larger than the others once they are a few hundred tokens, at any total up to 2^46;
+    they add up."""
+    totals = [int(2 ** (b + f)) + d for b in range(18, 46) for f in (0, 0.3, 0.585, 0.99) for d in (-1, 0, 1)]
+    for total, (ctas, weight) in zip(totals, shares([(t, 128, NEVER, grid) for t in totals])):
+        last = total - (ctas - 1) * weight
+        assert ctas == grid and weight >= 128
+        assert weight <= last <= weight + max(grid, 0.01 * weight), total
