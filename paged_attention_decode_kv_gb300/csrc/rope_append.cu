@@ -29,6 +29,7 @@
 #include <stdint.h>
 
 #include <cmath>
+#include <new>
 #include <type_traits>
 
 #include "../../include/vt_paged_attn.h"
@@ -572,6 +573,16 @@ bool rotation_ok(const double* inv_freq, int rot_dim, int head_dim, int interlea
   return inv_freq && aligned(inv_freq, 8) && rot_dim > 0 && rot_dim % 2 == 0 && rot_dim <= head_dim;
 }
 
+// No exception leaves a C entry point (the host state allocates).
+template <typename F>
+vt_status guarded(F f) {
+  try {
+    return f();
+  } catch (const std::bad_alloc&) {
+    return VT_ERR_OOM;
+  }
+}
+
 vt_status append(const RopeArgs& a, int block_size, int interleaved, cudaStream_t stream, vt_dtype dtype) {
   if (a.num_seqs < 0 || a.num_tokens < 0) return VT_ERR_INVALID_ARG;
   if (a.num_seqs == 0 || a.num_tokens == 0) return VT_OK;
@@ -716,9 +727,6 @@ vt_status vt_rope(void* out, const void* x, const int32_t* positions, const doub
   if (out == x && x_stride != out_stride) return VT_ERR_INVALID_ARG;
   if (num_tokens > kMaxTokens || head_dim % 8 != 0 || head_dim > 1024) return VT_ERR_UNSUPPORTED;
   if (static_cast<long long>(num_heads) * head_dim * kMaxTokensPerBlock > 0x3fffffffLL) return VT_ERR_UNSUPPORTED;
-  int sms = 0;
-  const vt_status st = current_sms(&sms);
-  if (st != VT_OK) return st;
   RopeArgs a{};
   a.q = x;
   a.q_out = out;
@@ -732,9 +740,14 @@ vt_status vt_rope(void* out, const void* x, const int32_t* positions, const doub
   a.rot_dim = rot_dim;
   a.amplitude = amplitude;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == VT_BF16 ? launch_rope<__nv_bfloat16, __nv_bfloat16, false>(a, interleaved, sms, s)
-                                         : launch_rope<float, float, false>(a, interleaved, sms, s);
-  return e == cudaSuccess ? VT_OK : cuda_fail(e, "rope launch");
+  return guarded([&] {
+    int sms = 0;
+    const vt_status st = current_sms(&sms);
+    if (st != VT_OK) return st;
+    const cudaError_t e = dtype == VT_BF16 ? launch_rope<__nv_bfloat16, __nv_bfloat16, false>(a, interleaved, sms, s)
+                                           : launch_rope<float, float, false>(a, interleaved, sms, s);
+    return e == cudaSuccess ? VT_OK : cuda_fail(e, "rope launch");
+  });
 }
 
 vt_status vt_paged_kv_append(void* k_cache, void* v_cache, void* q_out, const void* k, const void* v, const void* q,
@@ -745,11 +758,13 @@ vt_status vt_paged_kv_append(void* k_cache, void* v_cache, void* q_out, const vo
                              long long v_stride, vt_stream_t stream, int max_blocks_per_seq, int num_blocks,
                              vt_dtype dtype) {
   if (dtype == VT_E4M3) return VT_ERR_INVALID_ARG;
-  return vt::append(vt::append_args(k_cache, v_cache, q_out, k, v, q, nullptr, nullptr, q_starts, block_tables,
-                                    context_lens, positions, inv_freq, num_seqs, num_tokens, num_q_heads,
-                                    num_kv_heads, head_dim, rot_dim, amplitude, q_stride, k_stride, v_stride,
-                                    max_blocks_per_seq, num_blocks),
-                    block_size, interleaved, reinterpret_cast<cudaStream_t>(stream), dtype);
+  return vt::guarded([&] {
+    return vt::append(vt::append_args(k_cache, v_cache, q_out, k, v, q, nullptr, nullptr, q_starts, block_tables,
+                                      context_lens, positions, inv_freq, num_seqs, num_tokens, num_q_heads,
+                                      num_kv_heads, head_dim, rot_dim, amplitude, q_stride, k_stride, v_stride,
+                                      max_blocks_per_seq, num_blocks),
+                      block_size, interleaved, reinterpret_cast<cudaStream_t>(stream), dtype);
+  });
 }
 
 vt_status vt_paged_kv_append_fp8(void* k_cache, void* v_cache, void* q_out, const void* k, const void* v,
@@ -759,11 +774,13 @@ vt_status vt_paged_kv_append_fp8(void* k_cache, void* v_cache, void* q_out, cons
                                  int num_kv_heads, int head_dim, int block_size, int rot_dim, int interleaved,
                                  float amplitude, long long q_stride, long long k_stride, long long v_stride,
                                  vt_stream_t stream, int max_blocks_per_seq, int num_blocks) {
-  return vt::append(vt::append_args(k_cache, v_cache, q_out, k, v, q, k_scale, v_scale, q_starts, block_tables,
-                                    context_lens, positions, inv_freq, num_seqs, num_tokens, num_q_heads,
-                                    num_kv_heads, head_dim, rot_dim, amplitude, q_stride, k_stride, v_stride,
-                                    max_blocks_per_seq, num_blocks),
-                    block_size, interleaved, reinterpret_cast<cudaStream_t>(stream), VT_E4M3);
+  return vt::guarded([&] {
+    return vt::append(vt::append_args(k_cache, v_cache, q_out, k, v, q, k_scale, v_scale, q_starts, block_tables,
+                                      context_lens, positions, inv_freq, num_seqs, num_tokens, num_q_heads,
+                                      num_kv_heads, head_dim, rot_dim, amplitude, q_stride, k_stride, v_stride,
+                                      max_blocks_per_seq, num_blocks),
+                      block_size, interleaved, reinterpret_cast<cudaStream_t>(stream), VT_E4M3);
+  });
 }
 
 }  // extern "C"
