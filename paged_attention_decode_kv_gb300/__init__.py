@@ -517,7 +517,7 @@ def _row_stride(name, t, T, H, D, dtype, index):
     row, head, one = t.stride()
     if (one != 1 and D > 1) or (head != D and H > 1):
         raise ValueError(f"{name} must have contiguous heads (only the token stride is free)")
-    return row if T > 1 else max(row, H * D)
+    return row if T > 1 else H * D
 
 
 def _check_plain(name, t, dtype, index):

@@ -303,3 +303,23 @@ def test_append_bad_row_starts(dev, dtype, rot, starts, must):
         assert (out[~rows] == 7).all()
         for b in must:
             assert not (out[starts[b]:starts[b + 1]] == 7).all(-1).any()
+
+
+def test_one_token_has_no_stride(dev):
+    """Of one row the distance to the next means nothing: a fused projection's only row is rotated in place by the
+    append, and an odd distance is no fault."""
+    batch = make_batch([1], [40], 4, 2, 64, "bf16")
+    qkv = rows(1, 8, 64, torch.bfloat16, dev)
+    q, k, v = qkv[:, :4], qkv[:, 4:6], qkv[:, 6:]
+    inv, _ = vt.rope_frequencies(64)
+    args = (batch.q_starts, batch.block_tables, batch.context_lens)
+    caches = [(batch.k_cache.clone(), batch.v_cache.clone()) for _ in range(2)]
+    want = vt.append(k, v, *caches[0], *args, q=q, inv_freq=inv)
+    assert vt.append(k, v, *caches[1], *args, q=q, q_out=q, inv_freq=inv) is q
+    assert torch.equal(q, want)
+    for a, b in zip(*caches):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    x = torch.empty_strided((1, 4, 64), (257, 64, 1), dtype=torch.bfloat16, device=dev)
+    x.copy_(rows(1, 4, 64, torch.bfloat16, dev, seed=3))
+    pos = torch.tensor([77], dtype=torch.int32, device=dev)
+    check_rotated(vt.rope(x, pos, inv), x, pos, inv, False, 1.0)
