@@ -316,7 +316,8 @@ VT_API vt_status vt_rope(void* out, const void* x, const int32_t* positions, con
  *   q_starts    [num_seqs + 1] int32, q_starts[0] = 0, not decreasing, last entry <= num_tokens.  Rows behind the
  *               last sequence (a padded batch) are left as they were.
  *   inv_freq, rot_dim, interleaved, amplitude  as for vt_rope; rot_dim 0 (inv_freq NULL) rotates nothing.
- *   num_tokens  rows that q, k, v and q_out hold; num_seqs or num_tokens 0 is a no-op.
+ *   num_tokens  rows that q, k, v and q_out hold; num_seqs or num_tokens 0 is a no-op, 2^31 - 2^20 of either
+ *               VT_ERR_UNSUPPORTED.
  *   head_dim    64, 128, 256 or 512 (fp32: up to 256).
  * All pointers 16-byte aligned (int32 arrays 4, inv_freq 8), strides multiples of 16 bytes.
  *

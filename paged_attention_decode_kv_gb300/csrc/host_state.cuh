@@ -19,6 +19,9 @@ namespace vt {
 namespace host {
 
 constexpr size_t kStatusBytes = 256;
+// Packed rows, and sequences, of a ragged batch: numbers a little past the last
+// one (of a search's probes, of a tile's end) stay in 32 bits.
+constexpr int kMaxTokens = 0x7fffffff - (1 << 20);
 
 struct Scratch {
   char* base = nullptr;

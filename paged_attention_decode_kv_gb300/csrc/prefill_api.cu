@@ -108,6 +108,7 @@ vt_status validate(const PrefillCall& c) {
     return VT_ERR_INVALID_ARG;
   if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256 && c.head_dim != 512) return VT_ERR_UNSUPPORTED;
   if (c.block_size != kPfPage) return VT_ERR_UNSUPPORTED;
+  if (c.num_tokens > kMaxTokens || c.num_seqs > kMaxTokens) return VT_ERR_UNSUPPORTED;
   if (static_cast<long long>(c.num_blocks) * kPfPage > 0x7fffffffLL ||
       static_cast<long long>(c.max_blocks) * kPfPage > 0x7fffffffLL)
     return VT_ERR_UNSUPPORTED;

@@ -40,8 +40,6 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kPage = 32;
-// (row numbers past the last one stay in 32 bits)
-constexpr int kMaxTokens = 0x7fffffff - (1 << 20);
 constexpr int kMaxTokensPerBlock = 4;
 
 struct RopeArgs {
@@ -601,7 +599,7 @@ vt_status append(const RopeArgs& a, int block_size, int interleaved, cudaStream_
       !aligned(a.context_lens, 4) || !aligned(a.positions, 4))
     return VT_ERR_INVALID_ARG;
   if (!rotation_ok(a.inv_freq, a.rot_dim, a.head_dim, interleaved, a.amplitude, true)) return VT_ERR_INVALID_ARG;
-  if (a.num_tokens > kMaxTokens) return VT_ERR_UNSUPPORTED;
+  if (a.num_tokens > kMaxTokens || a.num_seqs > kMaxTokens) return VT_ERR_UNSUPPORTED;
   if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256 && a.head_dim != 512) return VT_ERR_UNSUPPORTED;
   if (a.head_dim == 512 && dtype != VT_BF16) return VT_ERR_UNSUPPORTED;
   if (block_size != kPage) return VT_ERR_UNSUPPORTED;

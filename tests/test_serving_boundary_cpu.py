@@ -243,3 +243,11 @@ def test_wrappers_refuse_host_tensors():
         vt.append_fp8(kv, kv, cache, cache.clone(), ones, ones, i32, table, i32[:1])  # not codes
     with pytest.raises(vt.VtError):
         vt.rope_frequencies(63, device="cpu")
+
+
+@pytest.mark.parametrize("over", [dict(num_seqs=0x7fffffff), dict(num_seqs=0x7ff00000), dict(num_tokens=0x7fffffff),
+                                  dict(num_tokens=0x7ff00000)])
+def test_batches_whose_numbers_would_leave_32_bits(over):
+    """The search for a row's sequence probes past the last one; so many of them are refused."""
+    for call, args in ((vt.vt_paged_kv_append, APPEND), (vt.vt_paged_attn_prefill, PREFILL)):
+        assert call(**dict(args, **over)) == vt.VT_ERR_UNSUPPORTED
