@@ -520,3 +520,72 @@ def test_decode_counters_stay_off_a_captured_prefill(dev):
     check(batch, out)
     vt.vt_paged_attn_set_workspace(area.data_ptr(), area.numel())
     decode(1000)                           # the caller's area handed over anew: no graph of before counts
+
+
+#: groups of which a tile holds one token, with rows that nothing fills
+@pytest.mark.parametrize("q_heads,kv_heads", [(65, 1), (100, 1), (127, 1), (256, 2)])
+@pytest.mark.parametrize("dtype,D", [k for k in KINDS if k[0] != "f32"])
+def test_one_token_a_tile(dev, dtype, D, q_heads, kv_heads):
+    batch = make_batch([70, 0, 3, 131], [200, 5, 3, 131], q_heads, kv_heads, D, dtype, seed=q_heads, pad=2)
+    out = torch.full_like(batch.q, 3.0)
+    check(batch, run(batch, out=out))
+    assert (out[204:] == 3).all()
+    check(batch, run(batch, window=50, grid=11, blocks=2), window=50)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_growing_scores_of_codes(dev, D):
+    """Keys that grow along the context, by codes that grow: every few blocks' scores pass the maximum so far by more
+    than a weight may hold, and the sums are rescaled."""
+    batch = make_batch([64, 10], [1000, 800], 4, 2, D, "e4m3", seed=4)
+    for b, L in enumerate(batch.ctx):
+        for i in range((L + 31) // 32):
+            page = batch.block_tables[b, i].long()
+            k = batch.k_cache[page].view(torch.float8_e4m3fn).float()  # (NaN where nobody owns the slot stays)
+            batch.k_cache[page] = (k * 2.0 ** (i // 8 - 3)).to(torch.float8_e4m3fn).view(torch.uint8)
+    batch.k_scale = batch.k_scale * 8
+    scale = 2 * D ** -0.5
+    # the last page's scores spread by 2 * 8 standard deviations of 1, those of the first pages by 2
+    grow = [(batch.q[:64, 0].double() @ k[0].T * scale).amax(0) for k in batch.dense("k")[:1]][0]
+    assert grow[960:1000].max() - grow[:256].max() > 12
+    check(batch, run(batch, scale=scale), scale=scale)
+    check(batch, run(batch, scale=scale, grid=7, blocks=2), scale=scale)
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_prefill_beside_the_decode_within_their_roundings(dev, dtype, D):
+    """The same rows by the two entry points.  Each is off from the exact value by no more than its own arithmetic
+    allows: prefill by the bounds above; the decode by its weights (two bf16 terms, or f16) and its result's
+    rounding, with what is summed in fp32 below 2^-12 w."""
+    batch = make_batch([6] * 5, [100, 37, 500, 6, 64], 8, 2, D, dtype, seed=5)
+    got = run(batch).double()
+    q = batch.q.view(5, 6, 8, D)
+    args = (batch.block_tables, batch.context_lens)
+    if dtype == "e4m3":
+        dec = vt.decode_fp8(q, batch.k_cache, batch.v_cache, batch.k_scale, batch.v_scale, *args)
+    else:
+        dec = vt.decode_multi(q, batch.k_cache, batch.v_cache, *args)
+    dec = dec.view_as(got).double()
+    ref, reach, even = attention(batch, D ** -0.5, flat=True)
+    if dtype == "f32":
+        span = float(batch.q.double().norm(dim=-1).max()) * 1.5
+        tol = 2 * ((2 * D * span + 500 + 16) * 2.0 ** -24) * reach
+    else:
+        own = 2.0 ** -8                    # prefill's weights
+        if dtype == "e4m3":
+            most = batch.q.double().abs().amax(-1, keepdim=True)
+            keys = max(float(k.abs().sum(-1).max()) for k in batch.dense("k"))
+            own = 2.0 ** -11 + 2 * 2.0 ** -17 * most * keys * D ** -0.5
+        tol = (own + 2.0 ** -11 + 2 * 2.0 ** -12) * reach + 2 * 2.0 ** -8 * ref.abs() + 2 * 2.0 ** -25 * even
+    assert ((got - dec).abs() <= tol).all(), float(((got - dec).abs() - tol).max())
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_no_rows_at_all(dev, dtype, D):
+    """Sequences without new tokens and padding rows only: nothing is written."""
+    batch = make_batch([0, 0, 0], [5, 0, 300], 4, 2, D, dtype, pad=9)
+    out = torch.full_like(batch.q, 3.0)
+    run(batch, out=out)
+    run(batch, out=out, window=7)
+    torch.cuda.synchronize()
+    assert vt.vt_paged_attn_device_status() == 0 and (out == 3).all()
