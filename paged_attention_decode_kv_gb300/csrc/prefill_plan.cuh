@@ -129,7 +129,7 @@ struct PfItem {
   int bad;
 };
 
-// Walks a CTA's share.  Uniform over the threads that use it together.
+// Walks a CTA's share.  Uniform over the threads that use it together, whole warps.
 struct PfWalk {
   long long x, end;       // weights: next item's part starts at x
   long long item_x;       // weight where the current item starts
@@ -147,6 +147,20 @@ struct PfWalk {
     if (r >= W) return nkv;
     const long long k = (r - a.item_weight + kPfBlock / 2) >> 7;
     return k < 0 ? 0 : (k > nkv ? nkv : static_cast<int>(k));
+  }
+
+  // The next sequence with rows.  In a padded batch many may have none, and
+  // one after the other would cost a memory latency each: 32 at a time.
+  __device__ __forceinline__ void next_sequence(const PrefillArgs& a) {
+    if (++b < a.num_seqs) s = pf_seq(a, b);
+#pragma unroll 1
+    while (b < a.num_seqs && s.tiles == 0) {
+      const int at = b + 1 + static_cast<int>(threadIdx.x & 31);
+      const unsigned with_rows = __ballot_sync(0xffffffffu, at < a.num_seqs && pf_seq(a, at).tiles > 0);
+      b += with_rows ? __ffs(with_rows) : 32;
+      if (with_rows) s = pf_seq(a, b);
+    }
+    if (b >= a.num_seqs) x = end;
   }
 
   // False when the share is done.  Items without this CTA's blocks are skipped.
@@ -187,17 +201,11 @@ struct PfWalk {
       const bool mine = it.nkv == 0 ? ra <= 0 : it.kb1 > it.kb0;
       if (whole_end) {
         x = item_x = item_x + W;
-        if (++tile == s.tiles) {
+        if (++tile == s.tiles && x < end) {  // (else the share is over, whatever follows)
           tile = 0;
           if (++vh == heads) {
             vh = 0;
-            do {
-              if (++b >= a.num_seqs) {
-                x = end;
-                break;
-              }
-              s = pf_seq(a, b);
-            } while (s.tiles == 0);
+            next_sequence(a);
           }
         }
       } else {

@@ -589,3 +589,47 @@ def test_no_rows_at_all(dev, dtype, D):
     run(batch, out=out, window=7)
     torch.cuda.synchronize()
     assert vt.vt_paged_attn_device_status() == 0 and (out == 3).all()
+
+
+def spread(batch, gaps):
+    """(run arguments' q_starts, block_tables, context_lens) of the batch with gaps[i] sequences without rows in front
+    of sequence i, and gaps[-1] behind the last."""
+    starts, lens, rows = [0], [], []
+    for b in range(len(batch.new) + 1):
+        starts += [starts[-1]] * gaps[b]
+        lens += [0] * gaps[b]
+        rows += [0] * gaps[b]
+        if b < len(batch.new):
+            starts.append(starts[-1] + batch.new[b])
+            lens.append(batch.ctx[b])
+            rows.append(b)
+    i32 = dict(dtype=torch.int32, device=batch.q.device)
+    return (torch.tensor(starts, **i32), batch.block_tables[torch.tensor(rows, device=batch.q.device)].contiguous(),
+            torch.tensor(lens, **i32))
+
+
+@pytest.mark.parametrize("gaps", [(0, 1, 31, 32), (33, 0, 64, 700), (5, 100, 1000, 0)])
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_sequences_without_rows_among_others(dev, dtype, D, gaps):
+    """A padded batch: sequences without rows in front, between and behind, over any cut."""
+    batch = make_batch([40, 1, 150], [500, 300, 150], 4, 2, D, dtype, seed=9)
+    q_starts, table, lens = batch.q_starts, batch.block_tables, batch.context_lens
+    for grid in (0, 1, 3, 17):
+        batch.q_starts, batch.block_tables, batch.context_lens = spread(batch, gaps)
+        out = run(batch, grid=grid, blocks=2 if grid else 0)
+        batch.q_starts, batch.block_tables, batch.context_lens = q_starts, table, lens
+        check(batch, out)
+
+
+@pytest.mark.parametrize("dtype,D", [k for k in KINDS if k[0] != "f32"])
+def test_many_sequences_without_rows(dev, dtype, D):
+    """65536 of them between two with rows, and as many behind, keep nobody waiting for 5 million cycles (one after
+    the other, at a memory latency each, they would)."""
+    batch = make_batch([40, 30], [200, 150], 4, 2, D, dtype, seed=9)
+    q_starts, table, lens = batch.q_starts, batch.block_tables, batch.context_lens
+    batch.q_starts, batch.block_tables, batch.context_lens = spread(batch, (0, 65536, 65536))
+    vt.vt_paged_attn_set_test_wait(5_000_000, -1, -1)
+    out = run(batch, grid=1)
+    vt.vt_paged_attn_set_test_wait(0, -1, -1)
+    batch.q_starts, batch.block_tables, batch.context_lens = q_starts, table, lens
+    check(batch, out)
