@@ -368,7 +368,8 @@ VT_API vt_status vt_paged_kv_append_fp8(void* k_cache, void* v_cache, void* q_ou
  *   num_q_heads / num_kv_heads at most 128, fp32 64 (else VT_ERR_UNSUPPORTED); the other arguments, layouts and
  *   limits as for vt_paged_attn_decode.
  * bf16 runs on the tensor cores: scores and sums in fp32, softmax weights rounded to bf16 before the product with
- * V.  fp32 runs on CUDA cores.
+ * V (8 bits of each; vt_paged_attn_decode and vt_paged_attn_decode_multi keep 16, so the same rows are closer to the
+ * exact value there).  fp32 runs on CUDA cores.
  *
  * The values of slots outside [0, context_lens[b]) of a sequence's pages are never used, whatever they hold.
  * Invalid device data never faults: rows of a sequence with a context outside [n_b, max_blocks_per_seq * 32] are
@@ -397,8 +398,9 @@ VT_API vt_status vt_paged_attn_prefill(void* out, const void* q, const void* k_c
  * Arithmetic: each query row is scaled by a power of two that puts its largest
  * magnitude in [2^7, 2^8) and split into two E4M3 terms, which hold a bf16
  * value exactly down to 2^-9 of that largest and to 2^-17 of it absolutely
- * below; key codes enter the products as they are.  Value codes are widened
- * exactly to f16 and the weights rounded to f16.  Sums are fp32.
+ * below (vt_paged_attn_decode_fp8's queries keep 2^-28); key codes enter the
+ * products as they are.  Value codes are widened exactly to f16 and the weights
+ * rounded to f16, as there.  Sums are fp32.
  */
 VT_API vt_status vt_paged_attn_prefill_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
                                            const float* k_scale, const float* v_scale, const int32_t* q_starts,
@@ -528,6 +530,8 @@ VT_API vt_status vt_paged_attn_device_status_detail(vt_stream_t stream, unsigned
  *            the sum of their largest needs is.
  *   stream   the first 256 bytes (status words) are zeroed on it; later
  *            calls zero newly used counter space on their own streams.
+ * The call begins anew, with the same area too: graphs captured on it before
+ * are not replayed after it.
  * A decode that needs more than `bytes` returns VT_ERR_SCRATCH_LIMIT before
  * launching anything, and so does one whose counters would reach what a
  * captured vt_paged_attn_prefill uses at the area's end.  Calls that share the workspace must be ordered on

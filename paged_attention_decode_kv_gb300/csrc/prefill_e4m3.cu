@@ -2,6 +2,8 @@
 // of Q K^T as they are (kind::f8f6f4, twice the bf16 rate) and Q, which carries
 // more bits, is the sum of two E4M3 terms, so they cost the tensor cores what
 // bf16 ones do.  V's codes are widened to f16 in shared memory for P V.
+// The two-tile variants have 640 threads of 96 registers each at launch and spill
+// 52 bytes a thread.
 #include "prefill_tc.cuh"
 
 namespace vt {

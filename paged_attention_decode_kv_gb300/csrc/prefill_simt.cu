@@ -1,16 +1,18 @@
 // Ragged prefill on CUDA cores (fp32 storage), and the combine of split items.
 //
 // Per item: S = Q K^T, online softmax, O += P V with everything in fp32, 64
-// query rows against 64 keys (two pages) at a time.  Bound by shared memory: a
-// 16-byte load takes the SM four cycles whatever its lanes share, so what
-// counts is how many FMAs a loaded value feeds.  Each of 128 threads holds 8
-// rows x 4 keys of S and 8 rows x D / 16 columns of O: 12 loads for 64 f32x2
-// FMAs of Q K^T and 16 for 128 of P V at head_dim 128.  (4 x 2 and 4 rows, with
-// 256 threads, took 227 us where 8 x 4 took 204: 1263 tokens over contexts of
-// up to 972, 16 q / 8 kv heads of 128.)  Q, K and V come by asynchronous copies;
-// at head_dim 128 P lies over K's tile.  Values are looked at only in tiles that
-// some row sees in part, and only if one is not finite do weights of 0 branch
-// around it: 185 us.
+// query rows against 64 keys (two pages) at a time.  A 16-byte load from shared
+// memory takes the SM four cycles whatever its lanes share, so what counts is
+// how many FMAs a loaded value feeds.  Each of 128 threads holds 8 rows x 4 keys
+// of S and 8 rows x D / 16 columns of O: 12 loads for 64 f32x2 FMAs of Q K^T and
+// 16 for 128 of P V at head_dim 128.  (4 x 2 and 4 rows, with 256 threads, took
+// 227 us where 8 x 4 took 204: 1263 tokens over contexts of up to 972, 16 q / 8
+// kv heads of 128.)  At that tile the bound is dependent latency, not the loads:
+// two warps a scheduler, the FMA pipe 57 % busy, the load pipe 22 %, and `wait`
+// the first stall; at head_dim 128 its 255 registers spill 76 bytes.  Q, K and V
+// come by asynchronous copies; at head_dim 128 P lies over K's tile.  Values are
+// looked at only in tiles that some row sees in part, and only if one is not
+// finite do weights of 0 branch around it: 182 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -385,7 +387,8 @@ const PrefillVariant* prefill_simt_variant(int head_dim) {
 
 cudaError_t launch_prefill_combine(const PrefillArgs& a, int grid, int rows, int tile_rows, int cols, int head_dim,
                                    int dtype_out, cudaStream_t stream) {
-  // a programmatic dependent: its blocks are resident by the time the pieces are written
+  // a programmatic dependent: the launch itself is prepared while the prefill runs (its blocks start when the last
+  // CTA has ended, since none releases them before)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, (rows + kCombineRows - 1) / kCombineRows);
   cfg.blockDim = dim3(kCombineThreads);

@@ -5,13 +5,19 @@
 //   S = Q K^T   tcgen05.mma, Q and K in shared memory, S in tensor memory;
 //   P = 2^(scale S - m), rows masked and summed in registers, one row to a
 //       thread, rounded to bf16 (f16 against codes, whose V is f16: at most
-//       2^-8 or 2^-11 of a weight, like the rounding of a bf16 result)
-//       and written over S in tensor memory;
+//       2^-8 or 2^-11 of a weight) and written over S in tensor memory;
 //   O += P V    tcgen05.mma, P from tensor memory, V as it lies in its pages
 //       (token-major, i.e. the N-major right operand), O in tensor memory.
 // A row's reference maximum m moves only when a score passes it by more than
 // 2^8 (weights then stay below 2^8, sums below 2^8 n, and the quotient is
 // the same), so O is rescaled a few times an item and not once a block.
+//
+// One bf16 term a weight is a choice of speed: results are off by 0.0020 to
+// 0.0023 of their rms, where the rounding of a result alone makes 0.0017.  With
+// two terms, as the decode has them, that is what is left, but P V is twice the
+// products: an 8192-token prompt (below) takes 485 us where one term takes 350,
+// GQA-8 chunks 215 where 160, a few new tokens over long contexts 213 where 198.
+// f16 weights against codes add nothing that shows.
 //
 // Roles: one warp loads (walks the CTA's share, passes its items on through a
 // queue, and fetches Q tiles and K and V pages by TMA into two rings of
@@ -25,9 +31,13 @@
 // What bounds it: a tile's softmax (1300 cycles a block of 128 keys, 512 of them
 // exponentials) and its products (16 MMAs of 64 cycles) follow one another, and
 // two tiles take 2900 to 3000 cycles where the products alone take 2048: 8192
-// tokens, 32 q / 8 kv heads, head_dim 128 in 350 us, 1570 TFLOP/s, 0.84 of the
-// measured 1863.  Short items are bound by instruction fetch, so what is inlined
-// often or runs once an item is kept short.
+// tokens, 32 q / 8 kv heads, head_dim 128 in 350 us a call of calls in a row,
+// 1570 TFLOP/s, 0.84 of the measured 1863 (a call at a time, with its scratch and
+// inputs out of L2, 365 to 376).  Short items keep the tensor pipe 15 % busy
+// (48 prompts of 1 to 401, head_dim 64): waits are two fifths of their stalls, Q
+// and O having one buffer a tile; instruction fetch, which bound them while the
+// code was 100 KB, is a tenth, so what is inlined often or runs once an item is
+// kept short.
 //
 // V preparation: in blocks that some row of the item may see only in part,
 // slots outside the item's keys are zeroed (0 * NaN is NaN, whatever P is),
