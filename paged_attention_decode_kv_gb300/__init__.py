@@ -603,6 +603,15 @@ def _launch(torch, index, stream, where, call, before, after):
         _check(status, where)
 
 
+def _empty_on(torch, shape, dtype, index, stream):
+    """Memory of the stream that will write it: a block that the current
+    stream has given back may still be read there."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=index) if stream else torch.cuda.default_stream(index)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=index)
+
+
 def _stream_on(torch, index, stream):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index)
@@ -616,7 +625,8 @@ def rope(x, positions, inv_freq, interleaved: bool = False, amplitude: float = 1
     projection); positions [T] int32; inv_freq float64 [rot_dim / 2] (see
     ``rope_frequencies``).  Returns out [T][H][D] (allocated unless given; x
     itself rotates in place).  A negative position turns back, so the gradient
-    of ``rope(x, p)`` is ``rope(grad, -p)``.  Asynchronous on ``stream``."""
+    of ``rope(x, p)`` is ``rope(grad, -p)``.  Asynchronous on ``stream``, whose
+    memory an allocated result is."""
     torch = _t()
     index = _cuda_index("x", x)
     io = x.dtype
@@ -628,7 +638,8 @@ def rope(x, positions, inv_freq, interleaved: bool = False, amplitude: float = 1
         raise ValueError("positions must be [tokens]")
     freq, rot = _check_freq(torch, inv_freq, index)
     if out is None:
-        out = torch.empty((T, H, D), dtype=io, device=x.device)
+        out = torch.empty((T, H, D), dtype=io, device=x.device) if stream is None else \
+            _empty_on(torch, (T, H, D), io, index, stream)
     out_stride = _row_stride("out", out, T, H, D, io, index)
     _launch(torch, index, stream, "vt_rope", library().vt_rope,
             (out.data_ptr(), x.data_ptr(), positions.data_ptr(), freq, T, H, D, rot, 1 if interleaved else 0, amplitude,
@@ -656,7 +667,8 @@ def _append(torch, k, v, k_cache, v_cache, scales, q_starts, block_tables, conte
         Hq = q.shape[1]
         qs = _row_stride("q", q, T, Hq, D, io, index)
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=io, device=q.device)
+            q_out = torch.empty((T, Hq, D), dtype=io, device=q.device) if stream is None else \
+                _empty_on(torch, (T, Hq, D), io, index, stream)
         _check_plain("q_out", q_out, io, index)
         if q_out.shape != q.shape:
             raise ValueError("q_out must be shaped like q")
@@ -691,7 +703,8 @@ def append(k, v, k_cache, v_cache, q_starts, block_tables, context_lens, q=None,
     caches [num_blocks][32][Hkv][D] of the rows' type.  Rotates at each
     token's place in its context, or at positions [T]; without inv_freq it
     rotates nothing.  Returns the rotated queries [T][Hq][D] (q_out, allocated
-    unless given; None without q).  Asynchronous on ``stream``."""
+    unless given; None without q).  Asynchronous on ``stream``, whose memory
+    an allocated result is."""
     return _append(_t(), k, v, k_cache, v_cache, None, q_starts, block_tables, context_lens, q, q_out, positions,
                    inv_freq, interleaved, amplitude, stream)
 
@@ -720,7 +733,7 @@ def _prefill(torch, q, k_cache, v_cache, scales, q_starts, block_tables, context
     if len(shape) != 4 or shape[3] != D or v_cache.shape != shape:
         raise ValueError("k_cache/v_cache must be [num_blocks][32][Hkv][head_dim] matching q")
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty_like(q) if stream is None else _empty_on(torch, (T, Hq, D), io, index, stream)
     else:
         _check_plain("out", out, io, index)
         if out.shape != q.shape:
@@ -749,7 +762,7 @@ def prefill(q, k_cache, v_cache, q_starts, block_tables, context_lens, scale=Non
     its context_lens[b] tokens, attending causally; q_starts [B + 1] int32, the
     rest as for ``decode``.  Returns out [T][Hq][D] (allocated unless given;
     rows behind the last sequence are not written).  Asynchronous on
-    ``stream``."""
+    ``stream``, whose memory an allocated result is."""
     return _prefill(_t(), q, k_cache, v_cache, None, q_starts, block_tables, context_lens, scale, window, out, stream)
 
 

@@ -633,3 +633,31 @@ def test_many_sequences_without_rows(dev, dtype, D):
     vt.vt_paged_attn_set_test_wait(0, -1, -1)
     batch.q_starts, batch.block_tables, batch.context_lens = q_starts, table, lens
     check(batch, out)
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_results_for_another_stream_are_its_own(dev, as_handle):
+    """A result that the call allocates for another stream is that stream's memory: not what the current stream has
+    given back and may still be reading."""
+    batch = make_batch([256], [256], 8, 2, 64, "bf16")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    stream = s.cuda_stream if as_handle else s
+    inv, _ = vt.rope_frequencies(64)
+    pos = torch.arange(256, dtype=torch.int32, device=dev)
+    kv = batch.q[:, :2].contiguous()
+    args = (batch.q_starts, batch.block_tables, batch.context_lens)
+    calls = (lambda: vt.prefill(batch.q, batch.k_cache, batch.v_cache, *args, stream=stream),
+             lambda: vt.rope(batch.q, pos, inv, stream=stream),
+             lambda: vt.append(kv, kv, batch.k_cache.clone(), batch.v_cache.clone(), *args, q=batch.q, inv_freq=inv,
+                               stream=stream))
+    for call in calls:
+        call()
+        torch.cuda.synchronize()
+        spare = [torch.empty_like(batch.q) for _ in range(64)]  # more than a call allocates
+        given_back = {t.data_ptr() for t in spare}
+        del spare
+        out = call()
+        s.synchronize()
+        assert out.data_ptr() not in given_back
+    torch.cuda.synchronize()
