@@ -661,3 +661,56 @@ def test_results_for_another_stream_are_its_own(dev, as_handle):
         s.synchronize()
         assert out.data_ptr() not in given_back
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "e4m3"])
+def test_pages_past_two_billion_elements(dev, dtype):
+    """Pages whose offset in the pool passes 32 bits: append and prefill give the bits that they give in a small pool."""
+    D, Hq, Hkv, far = 128, 8, 8, 66000     # 66000 x 32 x 8 x 128 = 2.16e9 elements
+    batch = make_batch([70, 1, 33], [200, 300, 33], Hq, Hkv, D, dtype, seed=6)
+    qkv = torch.randn((104, Hq + 2 * Hkv, D), generator=torch.Generator().manual_seed(1)).to(batch.q.dtype).to(dev)
+    inv, _ = vt.rope_frequencies(D)
+    scales = (batch.k_scale, batch.v_scale) if dtype == "e4m3" else ()
+    small = batch.k_cache.shape[0]
+    results = []
+    for base in (0, far):
+        pools = [torch.empty((base + small, *c.shape[1:]), dtype=c.dtype, device=dev)
+                 for c in (batch.k_cache, batch.v_cache)]
+        for pool, c in zip(pools, (batch.k_cache, batch.v_cache)):
+            pool[base:] = c
+        table = batch.block_tables + base
+        args = (batch.q_starts, table, batch.context_lens)
+        append, prefill = (vt.append_fp8, vt.prefill_fp8) if dtype == "e4m3" else (vt.append, vt.prefill)
+        q = append(qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], *pools, *scales, *args, q=qkv[:, :Hq], inv_freq=inv)
+        out = prefill(q, *pools, *scales, *args)
+        results.append((q, out, pools[0][base:].clone(), pools[1][base:].clone()))
+        del pools
+    torch.cuda.synchronize()
+    assert vt.vt_paged_attn_device_status() == 0
+    for a, b in zip(*results):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert torch.isfinite(results[0][1]).all()
+
+
+def test_rows_past_two_billion_elements(dev):
+    """Half a million single tokens of 32 heads of 128: the last rows lie past 2^31 elements.  A context of one token
+    gives its value, a rotation by position 0 its query."""
+    T, Hq, Hkv, D = 530000, 32, 8, 128
+    cache = torch.randn((2, 2, 32, Hkv, D), device=dev).to(torch.bfloat16)
+    k = torch.randn((T, Hkv, D), device=dev).to(torch.bfloat16)
+    q = torch.randn((T, Hq, D), device=dev).to(torch.bfloat16)
+    starts = torch.arange(T + 1, dtype=torch.int32, device=dev)
+    table = torch.randint(0, 2, (T, 1), dtype=torch.int32, device=dev)
+    lens = torch.ones(T, dtype=torch.int32, device=dev)
+    out = vt.prefill(q, cache[0], cache[1], starts, table, lens)
+    torch.cuda.synchronize()
+    assert vt.vt_paged_attn_device_status() == 0
+    first = cache[1, :, 0].repeat_interleave(Hq // Hkv, dim=1)   # [pages][Hq][D]
+    for at in range(0, T, 53000):
+        assert torch.equal(out[at:at + 53000], first[table[at:at + 53000, 0].long()])
+    inv, _ = vt.rope_frequencies(D)
+    turned = vt.rope(q, torch.zeros(T, dtype=torch.int32, device=dev), inv)
+    assert torch.equal(turned, q)
+    out.zero_()
+    vt.append(k, k, cache[0], cache[1], starts, table, lens, q=q, q_out=out, inv_freq=inv)
+    assert torch.equal(out, q)
