@@ -412,6 +412,173 @@ VT_API vt_status vt_paged_attn_prefill_fp8(void* out, const void* q, const void*
 /* Bytes of workspace a prefill call with this head_dim and cache type uses on the current device (0: not taken). */
 VT_API size_t vt_paged_attn_prefill_workspace_bytes(int head_dim, vt_dtype dtype);
 
+/*
+ * The operators below serve a step of speculative decoding on the paged cache:
+ * page tables, the masks of trees of drafted tokens, the norm of query and key
+ * heads in the append's pass, the trees' attention, and the accepted branch
+ * moved to consecutive slots.
+ */
+
+/*
+ * vt_paged_step_tables -- block tables, row starts, positions and slots of the
+ * next step, on the device, from request lengths and a stack of free pages.
+ *
+ * A sequence of L = context_lens[b] tokens keeps k = keep_lens[b] of them (all
+ * where keep_lens is NULL) and gets n = new_lens[b] new ones.  With
+ * pg(x) = ceil(x / 32), in this order:
+ *   pages pg(k) .. pg(L) - 1 of its block-table row go to the stack of free pages (of all sequences, before any
+ *   page is taken);
+ *   pages pg(k) .. pg(k + n) - 1 of its row are taken from it;
+ *   context_lens[b] = k + n, and its n rows of the packed batch, from q_starts[b] on, get the positions k + j and the
+ *   slots page * 32 + position % 32 (-1 where a page's id is outside [0, num_blocks)).
+ * Pages are given back and taken in the order of the sequences and of their rows, and the first given back lies on
+ * top: sequences that take as many pages as they give back keep theirs.  A finished sequence keeps 0 and gets 0.
+ *
+ * A sequence does not grow where k + n > max_blocks_per_seq * 32, and from the first other one on whose pages the
+ * stack or whose rows num_tokens does not hold, none does: such sequences are left with k tokens and no rows.  One
+ * whose lengths are none (L or k negative, k > L, L > max_blocks_per_seq * 32, n < 0) is left as it is, without rows.
+ *
+ *   block_tables  [num_seqs][max_blocks_per_seq] int32, in and out; entries behind a context are left as they were.
+ *   context_lens  [num_seqs] int32, in and out.
+ *   free_pages    [num_blocks] int32, in and out: a stack with room for every page of the pool, entry 0 at the bottom.
+ *   counters      [2] int32: pages on the stack, in and out; sequences that asked for something they did not get, out.
+ *   q_starts      [num_seqs + 1] int32, out.
+ *   positions, slots  [num_tokens] int32, out, either may be NULL; entries behind the last row are left as they were.
+ *   keep_lens, new_lens  [num_seqs] int32.
+ *   num_seqs      0 to 16384 (else VT_ERR_UNSUPPORTED); num_tokens, num_blocks, max_blocks_per_seq as for
+ *                 vt_paged_kv_append.
+ * keep_lens may be context_lens; no other arrays may overlap.  All are 4-byte aligned.  One launch, no workspace.
+ */
+VT_API vt_status vt_paged_step_tables(int32_t* block_tables, int32_t* context_lens, int32_t* free_pages,
+                                      int32_t* counters, int32_t* q_starts, int32_t* positions, int32_t* slots,
+                                      const int32_t* keep_lens, const int32_t* new_lens, int num_seqs, int num_tokens,
+                                      int block_size, vt_stream_t stream, int max_blocks_per_seq, int num_blocks);
+
+/*
+ * vt_tree_masks -- masks and positions of trees of drafted tokens.
+ *
+ * The rows of a sequence (packed as for vt_paged_kv_append, already counted in
+ * context_lens) are a tree: parents[row] is the place within the sequence's
+ * rows of the token that a row follows, less than its own, or -1 where it
+ * follows the context (any other value is read as -1).  Bit i % 32 of word
+ * i / 32 of a row's mask says that the row sees its sequence's i-th new token:
+ * itself and those it follows.
+ *
+ *   masks      [num_tokens][mask_words] int32, out.
+ *   positions  [num_tokens] int32, out, may be NULL: context_lens[b] - n_b + the number of tokens the row follows.
+ *   parents    [num_tokens] int32, not overlapping the outputs.
+ *   mask_words 1 to 32 (else VT_ERR_UNSUPPORTED).
+ * Rows of a sequence with more than 32 * mask_words rows, or with fewer context tokens than rows, and those behind
+ * the last sequence are left as they were.  num_seqs or num_tokens 0 is a no-op.  Needs no workspace.
+ */
+VT_API vt_status vt_tree_masks(int32_t* masks, int32_t* positions, const int32_t* parents, const int32_t* q_starts,
+                               const int32_t* context_lens, int num_seqs, int num_tokens, int mask_words,
+                               vt_stream_t stream);
+
+/*
+ * vt_norm_rope -- the RMS norm of each head's row, then vt_rope's rotation:
+ *   y = x / sqrt(mean(x^2) + eps) * weight,   out = y turned,
+ * in fp32, rounded once.
+ *
+ *   weight      device fp32, 16-byte aligned: [head_dim], shared by the heads (weight_stride 0), or a row for each
+ *               head, weight_stride elements apart (>= head_dim, a multiple of 4).
+ *   rot_dim     0 (inv_freq NULL, positions not looked at) rotates nothing.
+ *   eps         finite, >= 0.
+ * The other arguments and limits as for vt_rope.
+ */
+VT_API vt_status vt_norm_rope(void* out, const void* x, const float* weight, const int32_t* positions,
+                              const double* inv_freq, int num_tokens, int num_heads, int head_dim, int rot_dim,
+                              int interleaved, float amplitude, float eps, long long x_stride, long long out_stride,
+                              long long weight_stride, vt_stream_t stream, vt_dtype dtype);
+
+/*
+ * vt_paged_kv_norm_append, vt_paged_kv_norm_append_fp8 -- vt_paged_kv_append
+ * and vt_paged_kv_append_fp8 of queries and keys that are normed first, as
+ * vt_norm_rope norms them (values are not).  k_weight for the kv heads,
+ * q_weight for the query heads (not looked at without q).
+ */
+VT_API vt_status vt_paged_kv_norm_append(void* k_cache, void* v_cache, void* q_out, const void* k, const void* v,
+                                         const void* q, const float* k_weight, const float* q_weight,
+                                         const int32_t* q_starts, const int32_t* block_tables,
+                                         const int32_t* context_lens, const int32_t* positions,
+                                         const double* inv_freq, int num_seqs, int num_tokens, int num_q_heads,
+                                         int num_kv_heads, int head_dim, int block_size, int rot_dim,
+                                         int interleaved, float amplitude, float eps, long long q_stride,
+                                         long long k_stride, long long v_stride, long long q_weight_stride,
+                                         long long k_weight_stride, vt_stream_t stream, int max_blocks_per_seq,
+                                         int num_blocks, vt_dtype dtype);
+VT_API vt_status vt_paged_kv_norm_append_fp8(void* k_cache, void* v_cache, void* q_out, const void* k,
+                                             const void* v, const void* q, const float* k_weight,
+                                             const float* q_weight, const float* k_scale, const float* v_scale,
+                                             const int32_t* q_starts, const int32_t* block_tables,
+                                             const int32_t* context_lens, const int32_t* positions,
+                                             const double* inv_freq, int num_seqs, int num_tokens, int num_q_heads,
+                                             int num_kv_heads, int head_dim, int block_size, int rot_dim,
+                                             int interleaved, float amplitude, float eps, long long q_stride,
+                                             long long k_stride, long long v_stride, long long q_weight_stride,
+                                             long long k_weight_stride, vt_stream_t stream, int max_blocks_per_seq,
+                                             int num_blocks);
+
+/*
+ * vt_paged_attn_prefill_tree, vt_paged_attn_prefill_tree_fp8 -- attention of
+ * trees of drafted tokens over the paged cache, which already holds their keys
+ * and values (vt_paged_attn_prefill's rows with masks of their own).
+ *
+ * A row of sequence b sees every token t < context_lens[b] - n_b, and new
+ * token i where bit i % 32 of word i / 32 of its mask is set (bits from n_b on
+ * are not looked at); with window > 0 the last `window` of those, in the
+ * order of their slots.  So a chain of tokens with vt_tree_masks' masks is
+ * vt_paged_attn_prefill.  Any masks are taken, not only trees'; a row that
+ * sees nothing is 0.
+ *
+ *   masks       [num_tokens][mask_words] int32, 1 <= mask_words <= 32 (else VT_ERR_UNSUPPORTED).
+ * Rows of a sequence with more than 32 * mask_words rows are NaN.  The other arguments, limits, arithmetic, invalid
+ * device data and workspace (vt_paged_attn_prefill_workspace_bytes) as for vt_paged_attn_prefill and
+ * vt_paged_attn_prefill_fp8.
+ */
+VT_API vt_status vt_paged_attn_prefill_tree(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                            const int32_t* masks, const int32_t* q_starts,
+                                            const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+                                            int num_tokens, int mask_words, int num_q_heads, int num_kv_heads,
+                                            int head_dim, int block_size, float scale, int window,
+                                            vt_stream_t stream, int max_blocks_per_seq, int num_blocks,
+                                            vt_dtype dtype);
+VT_API vt_status vt_paged_attn_prefill_tree_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                                const float* k_scale, const float* v_scale, const int32_t* masks,
+                                                const int32_t* q_starts, const int32_t* block_tables,
+                                                const int32_t* context_lens, int num_seqs, int num_tokens,
+                                                int mask_words, int num_q_heads, int num_kv_heads, int head_dim,
+                                                int block_size, float scale, int window, vt_stream_t stream,
+                                                int max_blocks_per_seq, int num_blocks);
+
+/*
+ * vt_paged_kv_keep_path -- the accepted branch of each sequence's tree moved to
+ * consecutive slots, in all layers.
+ *
+ * accepted[b] is the place within sequence b's rows of its last accepted token,
+ * -1 for none (so is any other value outside its rows).  With i_0 < i_1 < ... the tokens that this row's mask names
+ * (itself and those it follows), the keys and values of token
+ * context_lens[b] - n_b + i_r go to the slot of token context_lens[b] - n_b + r, and
+ *   kept_lens[b] = context_lens[b] - n_b + the number of those tokens.
+ * No other slot is touched.  Positions are a matter of the rows: a branch's tokens have the positions of their new
+ * places already.
+ *
+ *   k_cache, v_cache  [num_layers] pools as for vt_paged_attn_decode, k_layer_stride and v_layer_stride elements
+ *               apart (>= a pool, multiples of 16 bytes; not looked at for one layer); 16-byte aligned, a slot's row
+ *               a multiple of 16 bytes.
+ *   kept_lens   [num_seqs] int32, out, none of the inputs.
+ *   masks       [num_tokens][mask_words] int32, 1 <= mask_words <= 32.
+ * A sequence with no rows, more than 32 * mask_words rows, or a context outside [n_b, max_blocks_per_seq * 32] keeps
+ * its context_lens[b], and nothing of it moves; nor does a token from or to a page whose id is outside
+ * [0, num_blocks).  num_seqs 0 is a no-op.  Needs no workspace.
+ */
+VT_API vt_status vt_paged_kv_keep_path(void* k_cache, void* v_cache, int32_t* kept_lens, const int32_t* accepted,
+                                       const int32_t* masks, const int32_t* q_starts, const int32_t* block_tables,
+                                       const int32_t* context_lens, int num_seqs, int num_tokens, int mask_words,
+                                       int num_layers, int num_kv_heads, int head_dim, int block_size,
+                                       long long k_layer_stride, long long v_layer_stride, vt_stream_t stream,
+                                       int max_blocks_per_seq, int num_blocks, vt_dtype dtype);
+
 /* What the last successful decode or prefill call on this host thread
  * launched (a prefill: group_tile is the query rows of a work item, subgroups
  * 1, min_units_per_cta in 128-key blocks, q_len 0). */

@@ -24,6 +24,9 @@ EXPORTED = ("vt_paged_attn_decode", "vt_paged_attn_decode_noalloc", "vt_paged_at
             "vt_paged_attn_decode_multi", "vt_paged_attn_decode_multi_fp8",
             "vt_rope_frequencies", "vt_rope", "vt_paged_kv_append", "vt_paged_kv_append_fp8",
             "vt_paged_attn_prefill", "vt_paged_attn_prefill_fp8", "vt_paged_attn_prefill_workspace_bytes",
+            "vt_paged_step_tables", "vt_tree_masks", "vt_norm_rope", "vt_paged_kv_norm_append",
+            "vt_paged_kv_norm_append_fp8", "vt_paged_attn_prefill_tree", "vt_paged_attn_prefill_tree_fp8",
+            "vt_paged_kv_keep_path",
             "vt_paged_attn_last_plan",
             "vt_paged_attn_set_override", "vt_paged_attn_set_overlap", "vt_paged_attn_set_segment_cost",
             "vt_paged_attn_set_workspace", "vt_paged_attn_set_test_wait",
@@ -109,6 +112,24 @@ def library() -> ctypes.CDLL:
             lib.vt_paged_attn_prefill_fp8.restype = c_int
             lib.vt_paged_attn_prefill_workspace_bytes.argtypes = [c_int, c_int]
             lib.vt_paged_attn_prefill_workspace_bytes.restype = c_size
+            lib.vt_paged_step_tables.argtypes = [c_void] * 9 + [c_int] * 3 + [c_void] + [c_int] * 2
+            lib.vt_paged_step_tables.restype = c_int
+            lib.vt_tree_masks.argtypes = [c_void] * 5 + [c_int] * 3 + [c_void]
+            lib.vt_tree_masks.restype = c_int
+            lib.vt_norm_rope.argtypes = [c_void] * 5 + [c_int] * 5 + [c_float] * 2 + [c_long] * 3 + [c_void, c_int]
+            lib.vt_norm_rope.restype = c_int
+            tail = [c_int] * 8 + [c_float] * 2 + [c_long] * 5 + [c_void, c_int, c_int]
+            lib.vt_paged_kv_norm_append.argtypes = [c_void] * 13 + tail + [c_int]
+            lib.vt_paged_kv_norm_append.restype = c_int
+            lib.vt_paged_kv_norm_append_fp8.argtypes = [c_void] * 15 + tail
+            lib.vt_paged_kv_norm_append_fp8.restype = c_int
+            tail = [c_int] * 7 + [c_float, c_int, c_void, c_int, c_int]
+            lib.vt_paged_attn_prefill_tree.argtypes = [c_void] * 8 + tail + [c_int]
+            lib.vt_paged_attn_prefill_tree.restype = c_int
+            lib.vt_paged_attn_prefill_tree_fp8.argtypes = [c_void] * 10 + tail
+            lib.vt_paged_attn_prefill_tree_fp8.restype = c_int
+            lib.vt_paged_kv_keep_path.argtypes = [c_void] * 8 + [c_int] * 7 + [c_long] * 2 + [c_void] + [c_int] * 3
+            lib.vt_paged_kv_keep_path.restype = c_int
             lib.vt_paged_attn_last_plan.argtypes = [ctypes.POINTER(vt_plan)]
             lib.vt_paged_attn_last_plan.restype = c_int
             lib.vt_paged_attn_set_override.argtypes = [c_int, c_int]
@@ -262,6 +283,89 @@ def vt_paged_attn_prefill_fp8(out, q, k_cache, v_cache, k_scale, v_scale, q_star
 
 def vt_paged_attn_prefill_workspace_bytes(head_dim, dtype) -> int:
     return int(library().vt_paged_attn_prefill_workspace_bytes(head_dim, dtype))
+
+
+def vt_paged_step_tables(block_tables, context_lens, free_pages, counters, q_starts, positions, slots, keep_lens,
+                         new_lens, num_seqs, num_tokens, block_size, stream, max_blocks_per_seq, num_blocks) -> int:
+    """Raw call of the step's page tables; returns the status code."""
+    return library().vt_paged_step_tables(block_tables, context_lens, free_pages, counters, q_starts, positions,
+                                          slots, keep_lens, new_lens, num_seqs, num_tokens, block_size, stream,
+                                          max_blocks_per_seq, num_blocks)
+
+
+def vt_tree_masks(masks, positions, parents, q_starts, context_lens, num_seqs, num_tokens, mask_words, stream) -> int:
+    """Raw call of the drafted trees' masks; returns the status code."""
+    return library().vt_tree_masks(masks, positions, parents, q_starts, context_lens, num_seqs, num_tokens,
+                                   mask_words, stream)
+
+
+def vt_norm_rope(out, x, weight, positions, inv_freq, num_tokens, num_heads, head_dim, rot_dim, interleaved,
+                 amplitude, eps, x_stride, out_stride, weight_stride, stream, dtype) -> int:
+    """Raw call of the heads' norm and rotation; returns the status code."""
+    return library().vt_norm_rope(out, x, weight, positions, inv_freq, num_tokens, num_heads, head_dim, rot_dim,
+                                  int(interleaved), float(amplitude), float(eps), x_stride, out_stride,
+                                  weight_stride, stream, dtype)
+
+
+def vt_paged_kv_norm_append(k_cache, v_cache, q_out, k, v, q, k_weight, q_weight, q_starts, block_tables,
+                            context_lens, positions, inv_freq, num_seqs, num_tokens, num_q_heads, num_kv_heads,
+                            head_dim, block_size, rot_dim, interleaved, amplitude, eps, q_stride, k_stride, v_stride,
+                            q_weight_stride, k_weight_stride, stream, max_blocks_per_seq, num_blocks, dtype) -> int:
+    """Raw call of the append of normed queries and keys; returns the status code."""
+    return library().vt_paged_kv_norm_append(k_cache, v_cache, q_out, k, v, q, k_weight, q_weight, q_starts,
+                                             block_tables, context_lens, positions, inv_freq, num_seqs, num_tokens,
+                                             num_q_heads, num_kv_heads, head_dim, block_size, rot_dim,
+                                             int(interleaved), float(amplitude), float(eps), q_stride, k_stride,
+                                             v_stride, q_weight_stride, k_weight_stride, stream, max_blocks_per_seq,
+                                             num_blocks, dtype)
+
+
+def vt_paged_kv_norm_append_fp8(k_cache, v_cache, q_out, k, v, q, k_weight, q_weight, k_scale, v_scale, q_starts,
+                                block_tables, context_lens, positions, inv_freq, num_seqs, num_tokens, num_q_heads,
+                                num_kv_heads, head_dim, block_size, rot_dim, interleaved, amplitude, eps, q_stride,
+                                k_stride, v_stride, q_weight_stride, k_weight_stride, stream, max_blocks_per_seq,
+                                num_blocks) -> int:
+    """Raw call of the append of normed queries and keys to an FP8 (E4M3)
+    cache; returns the status code."""
+    return library().vt_paged_kv_norm_append_fp8(k_cache, v_cache, q_out, k, v, q, k_weight, q_weight, k_scale,
+                                                 v_scale, q_starts, block_tables, context_lens, positions, inv_freq,
+                                                 num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                                                 block_size, rot_dim, int(interleaved), float(amplitude), float(eps),
+                                                 q_stride, k_stride, v_stride, q_weight_stride, k_weight_stride,
+                                                 stream, max_blocks_per_seq, num_blocks)
+
+
+def vt_paged_attn_prefill_tree(out, q, k_cache, v_cache, masks, q_starts, block_tables, context_lens, num_seqs,
+                               num_tokens, mask_words, num_q_heads, num_kv_heads, head_dim, block_size, scale, window,
+                               stream, max_blocks_per_seq, num_blocks, dtype) -> int:
+    """Raw call of the drafted trees' attention; returns the status code."""
+    return library().vt_paged_attn_prefill_tree(out, q, k_cache, v_cache, masks, q_starts, block_tables,
+                                                context_lens, num_seqs, num_tokens, mask_words, num_q_heads,
+                                                num_kv_heads, head_dim, block_size, float(scale), int(window), stream,
+                                                max_blocks_per_seq, num_blocks, dtype)
+
+
+def vt_paged_attn_prefill_tree_fp8(out, q, k_cache, v_cache, k_scale, v_scale, masks, q_starts, block_tables,
+                                   context_lens, num_seqs, num_tokens, mask_words, num_q_heads, num_kv_heads,
+                                   head_dim, block_size, scale, window, stream, max_blocks_per_seq,
+                                   num_blocks) -> int:
+    """Raw call of the drafted trees' attention over an FP8 (E4M3) cache;
+    returns the status code."""
+    return library().vt_paged_attn_prefill_tree_fp8(out, q, k_cache, v_cache, k_scale, v_scale, masks, q_starts,
+                                                    block_tables, context_lens, num_seqs, num_tokens, mask_words,
+                                                    num_q_heads, num_kv_heads, head_dim, block_size, float(scale),
+                                                    int(window), stream, max_blocks_per_seq, num_blocks)
+
+
+def vt_paged_kv_keep_path(k_cache, v_cache, kept_lens, accepted, masks, q_starts, block_tables, context_lens,
+                          num_seqs, num_tokens, mask_words, num_layers, num_kv_heads, head_dim, block_size,
+                          k_layer_stride, v_layer_stride, stream, max_blocks_per_seq, num_blocks, dtype) -> int:
+    """Raw call that moves accepted branches to consecutive slots; returns the
+    status code."""
+    return library().vt_paged_kv_keep_path(k_cache, v_cache, kept_lens, accepted, masks, q_starts, block_tables,
+                                           context_lens, num_seqs, num_tokens, mask_words, num_layers, num_kv_heads,
+                                           head_dim, block_size, k_layer_stride, v_layer_stride, stream,
+                                           max_blocks_per_seq, num_blocks, dtype)
 
 
 def vt_paged_attn_last_plan() -> dict:
@@ -648,7 +752,7 @@ def rope(x, positions, inv_freq, interleaved: bool = False, amplitude: float = 1
 
 
 def _append(torch, k, v, k_cache, v_cache, scales, q_starts, block_tables, context_lens, q, q_out, positions,
-            inv_freq, interleaved, amplitude, stream):
+            inv_freq, interleaved, amplitude, stream, norm=None):
     index = _cuda_index("k", k)
     T, Hkv, D = k.shape
     fp8 = scales is not None
@@ -683,7 +787,20 @@ def _append(torch, k, v, k_cache, v_cache, scales, q_starts, block_tables, conte
     head = (k_cache.data_ptr(), v_cache.data_ptr(), out_ptr, k.data_ptr(), v.data_ptr(), q_ptr)
     rest = (q_starts.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), pos_ptr, freq, B, T, Hq, Hkv, D,
             shape[1], rot, 1 if interleaved else 0, amplitude, qs, ks, vs)
-    if fp8:
+    if norm is not None:
+        k_weight, q_weight, eps = norm
+        kw, kw_stride = _weight(torch, "k_weight", k_weight, Hkv, D, index)
+        qw, qw_stride = (None, 0) if q is None else _weight(torch, "q_weight", q_weight, Hq, D, index)
+        head += (kw, qw)
+        rest = rest[:14] + (eps,) + rest[14:] + (qw_stride, kw_stride)
+        if fp8:
+            _check_scales(torch, *scales, Hkv, index)
+            _launch(torch, index, stream, "vt_paged_kv_norm_append_fp8", library().vt_paged_kv_norm_append_fp8,
+                    head + (scales[0].data_ptr(), scales[1].data_ptr()) + rest, (max_blocks, shape[0]))
+        else:
+            _launch(torch, index, stream, "vt_paged_kv_norm_append", library().vt_paged_kv_norm_append, head + rest,
+                    (max_blocks, shape[0], code))
+    elif fp8:
         _check_scales(torch, *scales, Hkv, index)
         _launch(torch, index, stream, "vt_paged_kv_append_fp8", library().vt_paged_kv_append_fp8,
                 head + (scales[0].data_ptr(), scales[1].data_ptr()) + rest, (max_blocks, shape[0]))
@@ -718,7 +835,77 @@ def append_fp8(k, v, k_codes, v_codes, k_scale, v_scale, q_starts, block_tables,
                    block_tables, context_lens, q, q_out, positions, inv_freq, interleaved, amplitude, stream)
 
 
-def _prefill(torch, q, k_cache, v_cache, scales, q_starts, block_tables, context_lens, scale, window, out, stream):
+def _weight(torch, name, weight, H, D, index):
+    """(pointer, stride from head to head) of the norm's weights, [D] or [H][D]."""
+    if weight is None:
+        raise ValueError(f"{name} must be given")
+    _check_plain(name, weight, torch.float32, index)
+    shape = weight.shape
+    if len(shape) == 1 and shape[0] == D:
+        return weight.data_ptr(), 0
+    if len(shape) == 2 and shape[0] == H and shape[1] == D:
+        return weight.data_ptr(), D
+    raise ValueError(f"{name} must be [{D}] or [{H}][{D}], got {tuple(shape)}")
+
+
+def norm_rope(x, weight, positions=None, inv_freq=None, eps: float = 1e-6, interleaved: bool = False,
+              amplitude: float = 1.0, out=None, stream=None):
+    """RMS norm of each head's row, then ``rope``'s rotation, rounded once.
+
+    x [T][H][D] bf16 or fp32 (token stride free); weight float32 [D], or [H][D]
+    with a row for each head; y = x / sqrt(mean(x^2) + eps) * weight is turned
+    by positions [T] int32 and inv_freq (without inv_freq it is not turned).
+    Returns out [T][H][D] (allocated unless given; x itself works in place).
+    Asynchronous on ``stream``, whose memory an allocated result is."""
+    torch = _t()
+    index = _cuda_index("x", x)
+    io = x.dtype
+    code = _io_code(torch, io)
+    T, H, D = x.shape
+    x_stride = _row_stride("x", x, T, H, D, io, index)
+    w, w_stride = _weight(torch, "weight", weight, H, D, index)
+    freq, rot = _check_freq(torch, inv_freq, index)
+    pos = None
+    if positions is not None:
+        _check_plain("positions", positions, torch.int32, index)
+        if positions.numel() != T:
+            raise ValueError("positions must be [tokens]")
+        pos = positions.data_ptr()
+    elif rot:
+        raise ValueError("inv_freq needs positions")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=io, device=x.device) if stream is None else \
+            _empty_on(torch, (T, H, D), io, index, stream)
+    out_stride = _row_stride("out", out, T, H, D, io, index)
+    _launch(torch, index, stream, "vt_norm_rope", library().vt_norm_rope,
+            (out.data_ptr(), x.data_ptr(), w, pos, freq, T, H, D, rot, 1 if interleaved else 0, amplitude, eps,
+             x_stride, out_stride, w_stride), (code,))
+    return out
+
+
+def norm_append(k, v, k_weight, k_cache, v_cache, q_starts, block_tables, context_lens, q=None, q_weight=None,
+                eps: float = 1e-6, q_out=None, positions=None, inv_freq=None, interleaved: bool = False,
+                amplitude: float = 1.0, stream=None):
+    """``append`` of queries and keys that are normed first (``norm_rope``), in
+    the same pass: k_weight float32 [D] or [Hkv][D], q_weight [D] or [Hq][D]
+    where q is given.  Values are not normed."""
+    return _append(_t(), k, v, k_cache, v_cache, None, q_starts, block_tables, context_lens, q, q_out, positions,
+                   inv_freq, interleaved, amplitude, stream, (k_weight, q_weight, eps))
+
+
+def norm_append_fp8(k, v, k_weight, k_codes, v_codes, k_scale, v_scale, q_starts, block_tables, context_lens, q=None,
+                    q_weight=None, eps: float = 1e-6, q_out=None, positions=None, inv_freq=None,
+                    interleaved: bool = False, amplitude: float = 1.0, stream=None):
+    """``norm_append`` into an FP8 (E4M3) cache of codes with a scale per kv
+    head (rows bf16; codes uint8 or torch.float8_e4m3fn)."""
+    torch = _t()
+    return _append(torch, k, v, _codes(torch, k_codes), _codes(torch, v_codes), (k_scale, v_scale), q_starts,
+                   block_tables, context_lens, q, q_out, positions, inv_freq, interleaved, amplitude, stream,
+                   (k_weight, q_weight, eps))
+
+
+def _prefill(torch, q, k_cache, v_cache, scales, q_starts, block_tables, context_lens, scale, window, out, stream,
+             masks=None):
     index = _cuda_index("q", q)
     if q.dim() != 3:
         raise ValueError("q must be [tokens][heads][head_dim]")
@@ -743,7 +930,17 @@ def _prefill(torch, q, k_cache, v_cache, scales, q_starts, block_tables, context
     head = (out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr())
     rest = (q_starts.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), B, T, Hq, shape[2], D, shape[1],
             scale, window)
-    if fp8:
+    if masks is not None:
+        words = _check_masks(torch, masks, T, index)
+        rest = (masks.data_ptr(),) + rest[:5] + (words,) + rest[5:]
+        if fp8:
+            _check_scales(torch, *scales, shape[2], index)
+            _launch(torch, index, stream, "vt_paged_attn_prefill_tree_fp8", library().vt_paged_attn_prefill_tree_fp8,
+                    head + (scales[0].data_ptr(), scales[1].data_ptr()) + rest, (max_blocks, shape[0]))
+        else:
+            _launch(torch, index, stream, "vt_paged_attn_prefill_tree", library().vt_paged_attn_prefill_tree,
+                    head + rest, (max_blocks, shape[0], code))
+    elif fp8:
         _check_scales(torch, *scales, shape[2], index)
         _launch(torch, index, stream, "vt_paged_attn_prefill_fp8", library().vt_paged_attn_prefill_fp8,
                 head + (scales[0].data_ptr(), scales[1].data_ptr()) + rest, (max_blocks, shape[0]))
@@ -773,3 +970,172 @@ def prefill_fp8(q, k_codes, v_codes, k_scale, v_scale, q_starts, block_tables, c
     torch = _t()
     return _prefill(torch, q, _codes(torch, k_codes), _codes(torch, v_codes), (k_scale, v_scale), q_starts,
                     block_tables, context_lens, scale, window, out, stream)
+
+
+def _check_masks(torch, masks, T, index):
+    """Words of a row of masks [T][words]."""
+    _check_plain("masks", masks, torch.int32, index)
+    shape = masks.shape
+    if len(shape) != 2 or shape[0] != T:
+        raise ValueError(f"masks must be [{T}][words], got {tuple(shape)}")
+    return shape[1]
+
+
+def prefill_tree(q, k_cache, v_cache, masks, q_starts, block_tables, context_lens, scale=None, window: int = 0,
+                 out=None, stream=None):
+    """Attention of trees of drafted tokens over the paged cache (which holds
+    their keys and values already, see ``append`` and ``norm_append``).
+
+    As ``prefill``, but a row sees every token before its sequence's first new
+    one, and new token i where bit i of its mask is set (masks int32
+    [T][words], see ``tree_masks``); with a window the last ``window`` of
+    those.  A row that sees nothing is 0."""
+    return _prefill(_t(), q, k_cache, v_cache, None, q_starts, block_tables, context_lens, scale, window, out, stream,
+                    masks)
+
+
+def prefill_tree_fp8(q, k_codes, v_codes, k_scale, v_scale, masks, q_starts, block_tables, context_lens, scale=None,
+                     window: int = 0, out=None, stream=None):
+    """``prefill_tree`` over an FP8 (E4M3) cache (q and out bf16; codes uint8 or
+    torch.float8_e4m3fn with a float32 scale per kv head)."""
+    torch = _t()
+    return _prefill(torch, q, _codes(torch, k_codes), _codes(torch, v_codes), (k_scale, v_scale), q_starts,
+                    block_tables, context_lens, scale, window, out, stream, masks)
+
+
+def tree_masks(parents, q_starts, context_lens, words=None, masks=None, positions=None, stream=None):
+    """Masks and positions of trees of drafted tokens, from each one's parent.
+
+    parents [T] int32: the place within its sequence's rows of the token that
+    a row follows (less than its own), -1 where it follows the context.
+    q_starts and context_lens as for ``append``, the drafted tokens counted in.
+    Returns (masks [T][words] int32, positions [T] int32): bit i of a row's
+    mask says that it sees its sequence's i-th new token (itself and those it
+    follows), and its position is the context's end plus the number it follows.
+    ``words`` (32 tokens each, 32 at most) is read off masks where they are
+    given.  Rows behind the last sequence are not written.  Asynchronous on
+    ``stream``, whose memory allocated results are."""
+    torch = _t()
+    index = _cuda_index("parents", parents)
+    int32 = torch.int32
+    _check_plain("parents", parents, int32, index)
+    _check_plain("q_starts", q_starts, int32, index)
+    _check_plain("context_lens", context_lens, int32, index)
+    if parents.dim() != 1 or q_starts.numel() != context_lens.numel() + 1:
+        raise ValueError("parents must be [tokens] and q_starts [num_seqs + 1]")
+    T = parents.shape[0]
+    if masks is None:
+        if words is None:
+            raise ValueError("give words or masks")
+        masks = torch.empty((T, words), dtype=int32, device=parents.device) if stream is None else \
+            _empty_on(torch, (T, words), int32, index, stream)
+    elif words is not None and masks.shape[-1] != words:
+        raise ValueError("masks must be [tokens][words]")
+    words = _check_masks(torch, masks, T, index)
+    if positions is None:
+        positions = torch.empty((T,), dtype=int32, device=parents.device) if stream is None else \
+            _empty_on(torch, (T,), int32, index, stream)
+    _check_plain("positions", positions, int32, index)
+    if positions.shape != (T,):
+        raise ValueError("positions must be [tokens]")
+    _launch(torch, index, stream, "vt_tree_masks", library().vt_tree_masks,
+            (masks.data_ptr(), positions.data_ptr(), parents.data_ptr(), q_starts.data_ptr(),
+             context_lens.data_ptr(), context_lens.numel(), T, words), ())
+    return masks, positions
+
+
+def step_tables(context_lens, new_lens, block_tables, free_pages, counters, num_tokens: int, keep_lens=None,
+                q_starts=None, positions=None, slots=None, stream=None):
+    """Page tables of the next step, on the GPU, from request lengths.
+
+    Sequence b keeps keep_lens[b] of its context_lens[b] tokens (all without
+    keep_lens) and gets new_lens[b] new ones: pages behind what it keeps go
+    back to the stack of free pages, pages for the new tokens come from its
+    top, and block_tables, context_lens, free_pages [num_blocks] and
+    counters [2] (pages on the stack, sequences refused) are updated in place.
+    Returns (q_starts [B + 1], positions [num_tokens], slots [num_tokens]),
+    allocated unless given: the rows of the packed batch, their positions and
+    their slots (page * 32 + place).  Sequences from the first on whose pages
+    or rows do not fit get none (vt_paged_step_tables).  Asynchronous on
+    ``stream``, whose memory allocated results are."""
+    torch = _t()
+    index = _cuda_index("context_lens", context_lens)
+    int32 = torch.int32
+    for name, t in (("context_lens", context_lens), ("new_lens", new_lens), ("block_tables", block_tables),
+                    ("free_pages", free_pages), ("counters", counters)):
+        _check_plain(name, t, int32, index)
+    B = context_lens.numel()
+    if new_lens.numel() != B or block_tables.dim() != 2 or block_tables.shape[0] != B or counters.numel() != 2:
+        raise ValueError("new_lens must be [num_seqs], block_tables [num_seqs][max_blocks] and counters [2]")
+    keep = None
+    if keep_lens is not None:
+        _check_plain("keep_lens", keep_lens, int32, index)
+        if keep_lens.numel() != B:
+            raise ValueError("keep_lens must be [num_seqs]")
+        keep = keep_lens.data_ptr()
+    out = []
+    for name, t, n in (("q_starts", q_starts, B + 1), ("positions", positions, num_tokens),
+                       ("slots", slots, num_tokens)):
+        if t is None:
+            t = torch.empty((n,), dtype=int32, device=context_lens.device) if stream is None else \
+                _empty_on(torch, (n,), int32, index, stream)
+        else:
+            _check_plain(name, t, int32, index)
+            if t.numel() != n:
+                raise ValueError(f"{name} must be [{n}]")
+        out.append(t)
+    _launch(torch, index, stream, "vt_paged_step_tables", library().vt_paged_step_tables,
+            (block_tables.data_ptr(), context_lens.data_ptr(), free_pages.data_ptr(), counters.data_ptr(),
+             out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), keep, new_lens.data_ptr(), B, num_tokens,
+             BLOCK_SIZE), (block_tables.shape[1], free_pages.numel()))
+    return tuple(out)
+
+
+def keep_path(accepted, masks, k_cache, v_cache, q_starts, block_tables, context_lens, kept_lens=None, stream=None):
+    """Moves each sequence's accepted branch to consecutive slots.
+
+    accepted [B] int32: the place within its sequence's rows of the last
+    accepted drafted token, -1 for none; the tokens its row of masks names
+    (``tree_masks``) go to the slots right behind the context they were
+    drafted for.  k_cache, v_cache [num_blocks][32][Hkv][D], or
+    [layers][num_blocks][32][Hkv][D] (layer stride free) for all layers in one
+    launch; bf16, fp32 or E4M3 codes.  Returns kept_lens [B] (allocated unless
+    given): the contexts that are left, ``step_tables``' keep_lens.
+    Asynchronous on ``stream``, whose memory an allocated result is."""
+    torch = _t()
+    index = _cuda_index("accepted", accepted)
+    int32 = torch.int32
+    if k_cache.dtype is torch.float8_e4m3fn or k_cache.dtype is torch.uint8:
+        k_cache, v_cache = _codes(torch, k_cache), _codes(torch, v_cache)
+        code, kv = VT_E4M3, torch.uint8
+    else:
+        kv = k_cache.dtype
+        code = _io_code(torch, kv)
+    shape = k_cache.shape
+    if len(shape) not in (4, 5) or v_cache.shape != shape:
+        raise ValueError("k_cache/v_cache must be [num_blocks][32][Hkv][head_dim], or layers of it")
+    layers = shape[0] if len(shape) == 5 else 1
+    strides = []
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check_plain(name, t[0] if len(shape) == 5 and layers else t, kv, index)
+        strides.append(t.stride(0) if layers > 1 else 0)
+    for name, t in (("accepted", accepted), ("q_starts", q_starts), ("block_tables", block_tables),
+                    ("context_lens", context_lens)):
+        _check_plain(name, t, int32, index)
+    B = context_lens.numel()
+    if accepted.numel() != B or q_starts.numel() != B + 1 or block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("accepted must be [num_seqs], q_starts [num_seqs + 1] and block_tables "
+                         "[num_seqs][max_blocks]")
+    words = _check_masks(torch, masks, masks.shape[0], index)
+    if kept_lens is None:
+        kept_lens = torch.empty((B,), dtype=int32, device=accepted.device) if stream is None else \
+            _empty_on(torch, (B,), int32, index, stream)
+    else:
+        _check_plain("kept_lens", kept_lens, int32, index)
+        if kept_lens.numel() != B:
+            raise ValueError("kept_lens must be [num_seqs]")
+    _launch(torch, index, stream, "vt_paged_kv_keep_path", library().vt_paged_kv_keep_path,
+            (k_cache.data_ptr(), v_cache.data_ptr(), kept_lens.data_ptr(), accepted.data_ptr(), masks.data_ptr(),
+             q_starts.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), B, masks.shape[0], words, layers,
+             shape[-2], shape[-1], shape[-3], strides[0], strides[1]), (block_tables.shape[1], shape[-4], code))
+    return kept_lens

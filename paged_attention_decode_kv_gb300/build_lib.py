@@ -29,10 +29,15 @@ SOURCES = [
     "decode_d256_f32.cu",
     "decode_e4m3.cu",
     "rope_append.cu",
+    "norm_append.cu",
+    "step_tables.cu",
+    "tree.cu",
     "prefill_api.cu",
     "prefill_simt.cu",
     "prefill_bf16.cu",
     "prefill_e4m3.cu",
+    "prefill_tree_bf16.cu",
+    "prefill_tree_e4m3.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -23,6 +23,8 @@ constexpr size_t kStatusBytes = 256;
 // one (of a search's probes, of a tile's end) stay in 32 bits.
 constexpr int kMaxTokens = 0x7fffffff - (1 << 20);
 
+constexpr int kMaxMaskWords = 32;  // of a drafted token's mask: 1024 of them a sequence
+
 struct Scratch {
   char* base = nullptr;
   size_t bytes = 0;

@@ -39,9 +39,18 @@ struct PrefillCall {
   cudaStream_t stream;
   int max_blocks, num_blocks;
   vt_dtype dtype;
+  // trees of drafted tokens
+  bool tree;
+  const int32_t* masks;
+  int mask_words;
 };
 
-const PrefillVariant* find_prefill(int head_dim, vt_dtype dtype) {
+const PrefillVariant* find_prefill(int head_dim, vt_dtype dtype, bool tree) {
+  if (tree) {
+    if (dtype == VT_F32) return tree_simt_variant(head_dim);
+    if (dtype == VT_BF16) return tree_bf16_variant(head_dim);
+    return tree_e4m3_variant(head_dim);
+  }
   if (dtype == VT_F32) return prefill_simt_variant(head_dim);
   if (dtype == VT_BF16) return prefill_bf16_variant(head_dim);
   return prefill_e4m3_variant(head_dim);
@@ -96,6 +105,7 @@ vt_status validate(const PrefillCall& c) {
   if (c.num_seqs < 0 || c.num_tokens < 0) return VT_ERR_INVALID_ARG;
   if (!c.out || !c.q || !c.k_cache || !c.v_cache || !c.q_starts || !c.block_tables || !c.context_lens)
     return VT_ERR_INVALID_ARG;
+  if (c.tree && (!c.masks || !aligned(c.masks, 4) || c.mask_words <= 0)) return VT_ERR_INVALID_ARG;
   if (c.out == c.q) return VT_ERR_INVALID_ARG;  // rows are read again after others' results are written
   if (c.dtype != VT_BF16 && c.dtype != VT_F32 && c.dtype != VT_E4M3) return VT_ERR_INVALID_ARG;
   if (c.dtype == VT_E4M3 && (!c.k_scale || !c.v_scale || !aligned(c.k_scale, 4) || !aligned(c.v_scale, 4)))
@@ -112,7 +122,8 @@ vt_status validate(const PrefillCall& c) {
   if (static_cast<long long>(c.num_blocks) * kPfPage > 0x7fffffffLL ||
       static_cast<long long>(c.max_blocks) * kPfPage > 0x7fffffffLL)
     return VT_ERR_UNSUPPORTED;
-  const PrefillVariant* v = find_prefill(c.head_dim, c.dtype);
+  if (c.tree && c.mask_words > kMaxMaskWords) return VT_ERR_UNSUPPORTED;
+  const PrefillVariant* v = find_prefill(c.head_dim, c.dtype, c.tree);
   if (!v || c.num_q_heads / c.num_kv_heads > v->tile_rows) return VT_ERR_UNSUPPORTED;
   return VT_OK;
 }
@@ -212,7 +223,7 @@ vt_status prefill(const PrefillCall& c) {
   if (c.num_seqs == 0 || c.num_tokens == 0) return VT_OK;
   vt_status st = validate(c);
   if (st != VT_OK) return st;
-  const PrefillVariant& v = *find_prefill(c.head_dim, c.dtype);
+  const PrefillVariant& v = *find_prefill(c.head_dim, c.dtype, c.tree);
   int dev = 0, per_sm = 0, source = 0, grid = 0, sms = 0;
   char* status = nullptr;
   char* base = nullptr;
@@ -250,6 +261,8 @@ vt_status prefill(const PrefillCall& c) {
   a.num_blocks = c.num_blocks;
   // (a window no context can fill is none, and no sum with it overflows)
   a.window = c.window > 0 && c.window < c.max_blocks * kPfPage ? c.window : 0;
+  a.masks = c.masks;
+  a.mask_words = c.mask_words;
   // (a hidden score is -inf, which a scale of 0 would turn into NaN: 1e-37 leaves any finite score at 0)
   a.scale_log2 = c.scale == 0.f ? 1e-37f : std::fabs(c.scale) * 1.4426950408889634f;
   a.neg_scale = c.scale < 0.f;
@@ -322,7 +335,7 @@ vt_status vt_paged_attn_prefill(void* out, const void* q, const void* k_cache, c
     return vt::prefill(vt::PrefillCall{out, q, k_cache, v_cache, nullptr, nullptr, q_starts, block_tables,
                                        context_lens, num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim,
                                        block_size, scale, window, reinterpret_cast<cudaStream_t>(stream),
-                                       max_blocks_per_seq, num_blocks, dtype});
+                                       max_blocks_per_seq, num_blocks, dtype, false, nullptr, 0});
   } catch (const std::bad_alloc&) {
     return VT_ERR_OOM;
   }
@@ -338,7 +351,41 @@ vt_status vt_paged_attn_prefill_fp8(void* out, const void* q, const void* k_cach
     return vt::prefill(vt::PrefillCall{out, q, k_cache, v_cache, k_scale, v_scale, q_starts, block_tables,
                                        context_lens, num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim,
                                        block_size, scale, window, reinterpret_cast<cudaStream_t>(stream),
-                                       max_blocks_per_seq, num_blocks, VT_E4M3});
+                                       max_blocks_per_seq, num_blocks, VT_E4M3, false, nullptr, 0});
+  } catch (const std::bad_alloc&) {
+    return VT_ERR_OOM;
+  }
+}
+
+vt_status vt_paged_attn_prefill_tree(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                     const int32_t* masks, const int32_t* q_starts, const int32_t* block_tables,
+                                     const int32_t* context_lens, int num_seqs, int num_tokens, int mask_words,
+                                     int num_q_heads, int num_kv_heads, int head_dim, int block_size, float scale,
+                                     int window, vt_stream_t stream, int max_blocks_per_seq, int num_blocks,
+                                     vt_dtype dtype) {
+  if (dtype == VT_E4M3) return VT_ERR_INVALID_ARG;
+  try {
+    return vt::prefill(vt::PrefillCall{out, q, k_cache, v_cache, nullptr, nullptr, q_starts, block_tables,
+                                       context_lens, num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                                       block_size, scale, window, reinterpret_cast<cudaStream_t>(stream),
+                                       max_blocks_per_seq, num_blocks, dtype, true, masks, mask_words});
+  } catch (const std::bad_alloc&) {
+    return VT_ERR_OOM;
+  }
+}
+
+vt_status vt_paged_attn_prefill_tree_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                         const float* k_scale, const float* v_scale, const int32_t* masks,
+                                         const int32_t* q_starts, const int32_t* block_tables,
+                                         const int32_t* context_lens, int num_seqs, int num_tokens, int mask_words,
+                                         int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                         float scale, int window, vt_stream_t stream, int max_blocks_per_seq,
+                                         int num_blocks) {
+  try {
+    return vt::prefill(vt::PrefillCall{out, q, k_cache, v_cache, k_scale, v_scale, q_starts, block_tables,
+                                       context_lens, num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                                       block_size, scale, window, reinterpret_cast<cudaStream_t>(stream),
+                                       max_blocks_per_seq, num_blocks, VT_E4M3, true, masks, mask_words});
   } catch (const std::bad_alloc&) {
     return VT_ERR_OOM;
   }
@@ -346,7 +393,7 @@ vt_status vt_paged_attn_prefill_fp8(void* out, const void* q, const void* k_cach
 
 size_t vt_paged_attn_prefill_workspace_bytes(int head_dim, vt_dtype dtype) {
   using namespace vt;
-  const PrefillVariant* v = find_prefill(head_dim, dtype);
+  const PrefillVariant* v = find_prefill(head_dim, dtype, false);
   if (!v) return 0;
   int dev = 0, per_sm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;

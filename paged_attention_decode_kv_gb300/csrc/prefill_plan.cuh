@@ -13,6 +13,10 @@
 // knowledge of lengths and no queue, and they balance causal tiles (whose
 // cost grows with their position) as well as long contexts with few rows.
 //
+// A tree of drafted tokens (TREE) is the same with spans of its own: a row sees
+// all tokens before the sequence's first new one, and of the new ones those
+// its mask names, so every tile's span ends with the context.
+//
 // Weights of a sequence's first K tiles have a closed form (sums of
 // arithmetic progressions, clipped where a window has not yet started), so a
 // CTA finds its first item by a scan over sequences and a binary search over
@@ -40,6 +44,8 @@ struct PrefillArgs {
   int num_seqs, num_tokens, num_q_heads, num_kv_heads, group;
   int max_blocks, num_blocks;
   int window;        // 0: none
+  const int* masks;  // trees: [num_tokens][mask_words], bit i of a row: it sees new token i of its sequence
+  int mask_words;
   float scale_log2;  // |scale| * log2(e); the sign is applied where the product is formed
   int neg_scale;
   int tile_tokens;   // new tokens of an item
@@ -81,6 +87,7 @@ __device__ __forceinline__ int pf_tiles_in(const PrefillArgs& a, int x) {
 // Token of a tile's row r.
 __device__ __forceinline__ int pf_token_of(const PrefillArgs& a, int r) { return r * a.group_mul >> 16; }
 
+template <bool TREE>
 __device__ __forceinline__ PfSeq pf_seq(const PrefillArgs& a, int b) {
   PfSeq s;
   const int r0 = a.q_starts[b], r1 = a.q_starts[b + 1];
@@ -88,6 +95,7 @@ __device__ __forceinline__ PfSeq pf_seq(const PrefillArgs& a, int b) {
   s.row0 = r0;
   s.n = (r0 >= 0 && r1 > r0 && r1 <= a.num_tokens) ? r1 - r0 : 0;
   s.bad = L < s.n || static_cast<long long>(L) > static_cast<long long>(a.max_blocks) * kPfPage;
+  if (TREE && s.n > 32ll * a.mask_words) s.bad = 1;
   s.p0 = s.bad ? 0 : L - s.n;
   s.tiles = s.n > 0 ? pf_tiles_in(a, s.n - 1) + 1 : 0;
   return s;
@@ -97,10 +105,12 @@ __device__ __forceinline__ long long pf_mul(int a, int b) { return static_cast<l
 
 // Weight of the first K of the sequence's tiles (one head).  (Products of two
 // 32-bit numbers and one 32-bit division: 64-bit ones are long code.)
+template <bool TREE>
 __device__ __forceinline__ long long pf_weight(const PrefillArgs& a, const PfSeq& s, int K) {
   const int T = a.tile_tokens;
   if (K <= 0) return 0;
   if (s.bad) return pf_mul(K, a.item_weight);
+  if (TREE) return pf_mul(K, s.p0 + s.n - (a.window > 0 ? max(0, s.p0 - a.window) : 0)) + pf_mul(K, a.item_weight);
   long long w = ((pf_mul(K, K) + K) >> 1) * T + pf_mul(K, s.p0) + pf_mul(K, a.item_weight);
   if (K == s.tiles) w -= pf_mul(T, K) - s.n;
   if (a.window > 0) {
@@ -117,7 +127,7 @@ struct PfItem {
   int b, vh, tile;
   int row0;          // packed row of the tile's first token
   int ntok;          // tokens of the tile
-  int pos0;          // position of its first token
+  int pos0;          // position of its first token; of a tree, of the last token that every row sees
   int head, part;    // kv head, part of V's columns
   int lo;            // first attended key, rounded down to a page
   int lo_exact;      // first attended key
@@ -130,6 +140,7 @@ struct PfItem {
 };
 
 // Walks a CTA's share.  Uniform over the threads that use it together, whole warps.
+template <bool TREE = false>
 struct PfWalk {
   long long x, end;       // weights: next item's part starts at x
   long long item_x;       // weight where the current item starts
@@ -152,13 +163,13 @@ struct PfWalk {
   // The next sequence with rows.  In a padded batch many may have none, and
   // one after the other would cost a memory latency each: 32 at a time.
   __device__ __forceinline__ void next_sequence(const PrefillArgs& a) {
-    if (++b < a.num_seqs) s = pf_seq(a, b);
+    if (++b < a.num_seqs) s = pf_seq<TREE>(a, b);
 #pragma unroll 1
     while (b < a.num_seqs && s.tiles == 0) {
       const int at = b + 1 + static_cast<int>(threadIdx.x & 31);
-      const unsigned with_rows = __ballot_sync(0xffffffffu, at < a.num_seqs && pf_seq(a, at).tiles > 0);
+      const unsigned with_rows = __ballot_sync(0xffffffffu, at < a.num_seqs && pf_seq<TREE>(a, at).tiles > 0);
       b += with_rows ? __ffs(with_rows) : 32;
-      if (with_rows) s = pf_seq(a, b);
+      if (with_rows) s = pf_seq<TREE>(a, b);
     }
     if (b >= a.num_seqs) x = end;
   }
@@ -168,7 +179,7 @@ struct PfWalk {
     while (x < end) {
       long long W = 0;  // of the item: the difference of two sums (a loop: one copy of the code)
 #pragma unroll 1
-      for (int i = 0; i < 2; ++i) W = pf_weight(a, s, tile + i) - W;
+      for (int i = 0; i < 2; ++i) W = pf_weight<TREE>(a, s, tile + i) - W;
       it.b = b;
       it.vh = vh;
       it.tile = tile;
@@ -176,9 +187,9 @@ struct PfWalk {
       it.part = vh & (a.v_parts - 1);
       it.row0 = s.row0 + tile * a.tile_tokens;
       it.ntok = min(a.tile_tokens, s.n - tile * a.tile_tokens);
-      it.pos0 = s.p0 + tile * a.tile_tokens;
+      it.pos0 = TREE ? s.p0 - 1 : s.p0 + tile * a.tile_tokens;
       it.L = s.p0 + s.n;
-      it.hi = it.pos0 + it.ntok;
+      it.hi = TREE ? it.L : it.pos0 + it.ntok;
       it.lo_exact = a.window > 0 ? max(0, it.pos0 - a.window + 1) : 0;
       it.lo = it.lo_exact & ~(kPfPage - 1);
       it.nkv = s.bad ? 0 : (it.hi - it.lo + kPfBlock - 1) >> 7;
@@ -237,7 +248,8 @@ __host__ __device__ __forceinline__ long long pf_share_weight(long long total, u
 }
 
 // The share of this CTA in a total weight; false if it has none.
-__device__ __forceinline__ bool pf_share(const PrefillArgs& a, long long total, PfWalk& w) {
+template <bool TREE>
+__device__ __forceinline__ bool pf_share(const PrefillArgs& a, long long total, PfWalk<TREE>& w) {
   w.heads = a.num_kv_heads * a.v_parts;
   w.ctas = static_cast<int>(pf_share_count(total, a.min_weight, a.long_total, gridDim.x));
   w.cta = blockIdx.x;
@@ -252,16 +264,17 @@ __device__ __forceinline__ bool pf_share(const PrefillArgs& a, long long total, 
 
 // The item that holds weight w.x, in sequence b whose items start at weight
 // `start`.  By one whole warp: 32 tiles are weighed at a time.
-__device__ __forceinline__ void pf_locate(const PrefillArgs& a, int b, long long start, int lane, PfWalk& w) {
+template <bool TREE>
+__device__ __forceinline__ void pf_locate(const PrefillArgs& a, int b, long long start, int lane, PfWalk<TREE>& w) {
   w.b = b;
-  w.s = pf_seq(a, b);
+  w.s = pf_seq<TREE>(a, b);
   int lo = 0, hi = w.s.tiles, step = w.s.tiles;  // first the head (weight of all tiles), then the tile: W(0) = 0
   long long at_lo = 0;
   w.vh = -1;
 #pragma unroll 1
   do {
     const int K = min(lo + (lane + 1) * step, hi);
-    const long long m = pf_weight(a, w.s, K);
+    const long long m = pf_weight<TREE>(a, w.s, K);
     if (w.vh < 0) {
       for (w.vh = 0; w.x - start >= m; start += m) ++w.vh;
     } else {
@@ -289,7 +302,8 @@ __device__ __forceinline__ long long pf_warp_scan(long long x, int lane) {
 // The CTA's share, by one whole warp: each lane sums the weights of a run of
 // consecutive sequences, a scan over lanes gives the total and the run that
 // holds the share's start, and the warp looks through that run.
-__device__ __forceinline__ void pf_begin(const PrefillArgs& a, int lane, PfWalk& w) {
+template <bool TREE>
+__device__ __forceinline__ void pf_begin(const PrefillArgs& a, int lane, PfWalk<TREE>& w) {
   const int heads = a.num_kv_heads * a.v_parts;
   const int run = static_cast<int>((static_cast<unsigned>(a.num_seqs) + 31u) >> 5);
   int from = lane * run, to = min(from + run, a.num_seqs);
@@ -300,8 +314,8 @@ __device__ __forceinline__ void pf_begin(const PrefillArgs& a, int lane, PfWalk&
     long long mine = 0;
 #pragma unroll 1
     for (int b = from; b < to; ++b) {
-      const PfSeq s = pf_seq(a, b);
-      mine += heads * pf_weight(a, s, s.tiles);
+      const PfSeq s = pf_seq<TREE>(a, b);
+      mine += heads * pf_weight<TREE>(a, s, s.tiles);
     }
     const long long inc = before + pf_warp_scan(mine, lane);
     if (depth == 0 && !pf_share(a, __shfl_sync(0xffffffffu, inc, 31), w)) return;
@@ -316,6 +330,50 @@ __device__ __forceinline__ void pf_begin(const PrefillArgs& a, int lane, PfWalk&
     from = min(first + lane * step, last);
     to = min(from + step, last);
   }
+}
+
+// ---- trees
+// The mask of packed row `row`.
+__device__ __forceinline__ const int* tree_mask(const PrefillArgs& a, int row) {
+  return a.masks + static_cast<long long>(row) * a.mask_words;
+}
+
+// Word i of a mask of a sequence with n new tokens.
+__device__ __forceinline__ unsigned tree_word(const int* mask, int i, int n) {
+  const int left = n - 32 * i;
+  if (left <= 0) return 0u;
+  const unsigned w = static_cast<unsigned>(mask[i]);
+  return left < 32 ? w & ((1u << left) - 1u) : w;
+}
+
+// The first key a row's window takes in: of the tokens the row may see (those
+// before `base`, then the new ones its mask names) it sees the last `window`.
+__device__ __forceinline__ int tree_from(const PrefillArgs& a, const int* mask, int n, int base) {
+  if (a.window == 0) return 0;
+  int count = 0;
+#pragma unroll 1
+  for (int i = 0; 32 * i < n; ++i) count += __popc(tree_word(mask, i, n));
+  int skip = count - a.window;  // new tokens before the window
+  if (skip < 0) return max(0, base + skip);
+#pragma unroll 1
+  for (int i = 0;; ++i) {
+    unsigned w = tree_word(mask, i, n);
+    const int c = __popc(w);
+    if (skip < c) {
+      for (; skip > 0; --skip) w &= w - 1u;
+      return base + 32 * i + __ffs(w) - 1;
+    }
+    skip -= c;
+  }
+}
+
+// Which of the keys k .. k + 31 a row sees: bit by bit.
+__device__ __forceinline__ unsigned tree_seen(const int* mask, int n, int base, int from, int k) {
+  const int ahead = k - base, i = ahead >> 5;  // (rounded down)
+  const unsigned lo = i < 0 ? ~0u : tree_word(mask, i, n);
+  const unsigned hi = i + 1 < 0 ? ~0u : tree_word(mask, i + 1, n);
+  const int before = from - k;
+  return __funnelshift_r(lo, hi, ahead & 31) & (before <= 0 ? ~0u : before > 31 ? 0u : ~0u << before);
 }
 
 }  // namespace vt

@@ -15,8 +15,11 @@
 // finite do weights of 0 branch around it: 182 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math_constants.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "decode_kernel.cuh"  // ex2, smem_addr
 #include "packed.cuh"
@@ -59,7 +62,7 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, bool vali
                : "memory");
 }
 
-template <int D>
+template <int D, bool TREE>
 __global__ void __launch_bounds__(kSimtThreads<D>) prefill_simt_kernel(const PrefillArgs a) {
   extern __shared__ char raw[];
   SimtSmem<D>& s = *reinterpret_cast<SimtSmem<D>*>(raw);
@@ -67,7 +70,7 @@ __global__ void __launch_bounds__(kSimtThreads<D>) prefill_simt_kernel(const Pre
   const int ty = tid >> 4, tx = tid & 15;  // rows NR ty ...; keys tx + 16 e; columns 4 tx + 64 c
   constexpr int NC = D / 64, NR = 1024 / kSimtThreads<D>, NK = 4;
   if (tid == 0) a.splits[blockIdx.x].pieces = 0;
-  PfWalk w;
+  PfWalk<TREE> w;
   pf_begin(a, tid & 31, w);  // each warp for itself
   PfItem it;
   const float scale = a.neg_scale ? -a.scale_log2 : a.scale_log2;
@@ -80,12 +83,18 @@ __global__ void __launch_bounds__(kSimtThreads<D>) prefill_simt_kernel(const Pre
     const int rows = it.ntok * a.group;
     float m[NR], l[NR];
     float2 o[NR][NC][2];  // columns 4 tx + 64 c, +1 and +2, +3
-    int pos[NR];
+    int pos[NR];          // trees: the first key of the row's window
+    const int base = it.pos0 + 1, drafted = it.L - base;  // trees
+    unsigned some = 0;    // trees: rows that have seen a key
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       m[i] = -CUDART_INF_F;
       l[i] = 0.f;
-      pos[i] = it.pos0 + min(pf_token_of(a, ty * NR + i), it.ntok - 1);
+      const int tok = min(pf_token_of(a, ty * NR + i), it.ntok - 1);
+      if constexpr (TREE)
+        pos[i] = it.bad ? 0 : tree_from(a, tree_mask(a, it.row0 + tok), drafted, base);
+      else
+        pos[i] = it.pos0 + tok;
 #pragma unroll
       for (int c = 0; c < NC; ++c) o[i][c][0] = o[i][c][1] = make_float2(0.f, 0.f);
     }
@@ -155,11 +164,20 @@ __global__ void __launch_bounds__(kSimtThreads<D>) prefill_simt_kernel(const Pre
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
         float x[NK], top = -CUDART_INF_F;
-        const int at = t0 + tx, upto = min(pos[i], last - 1) - at;
-        const int from = a.window > 0 ? pos[i] - a.window + 1 - at : 0;
+        const int at = t0 + tx, upto = (TREE ? last - 1 : min(pos[i], last - 1)) - at;
+        const int from = !TREE && a.window > 0 ? pos[i] - a.window + 1 - at : 0;
+        unsigned of_row[2] = {~0u, ~0u};
+        if constexpr (TREE) {
+          if (t0 + kSimtKeys > base || (a.window > 0 && t0 < it.hi - a.window)) {
+            const int* mask = tree_mask(a, it.row0 + min(pf_token_of(a, ty * NR + i), it.ntok - 1));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) of_row[h] = tree_seen(mask, drafted, base, pos[i], t0 + 32 * h);
+          }
+          some |= (of_row[0] | of_row[1]) != 0u ? 1u << i : 0u;  // (bits past the last key are not set)
+        }
 #pragma unroll
         for (int e = 0; e < NK; ++e) {
-          const bool seen = 16 * e <= upto && 16 * e >= from;
+          const bool seen = 16 * e <= upto && (TREE ? (of_row[e / 2] >> (tx + 16 * (e & 1)) & 1u) != 0u : 16 * e >= from);
           x[e] = seen ? (y[i][e].x + y[i][e].y) * scale : -CUDART_INF_F;
           top = fmaxf(top, x[e]);
         }
@@ -263,6 +281,7 @@ __global__ void __launch_bounds__(kSimtThreads<D>) prefill_simt_kernel(const Pre
       if (r >= rows) continue;
       float* dst;
       float mul = 1.f;
+      if (TREE && m[i] == -CUDART_INF_F && (some >> i & 1u)) m[i] = -FLT_MAX;  // seen, if only scores of -inf
       if (split) {
         dst = a.part + (slot * kSimtRows + r) * D;
         if (tx == 0) a.ml[slot * kSimtRows + r] = make_float2(bad ? CUDART_NAN_F : m[i], l[i]);
@@ -270,7 +289,7 @@ __global__ void __launch_bounds__(kSimtThreads<D>) prefill_simt_kernel(const Pre
         const int t = pf_token_of(a, r), g = r - t * a.group;
         dst = static_cast<float*>(a.out) +
               (static_cast<long long>(it.row0 + t) * a.num_q_heads + it.head * a.group + g) * D;
-        mul = bad ? CUDART_NAN_F : 1.f / l[i];
+        mul = bad ? CUDART_NAN_F : TREE && m[i] == -CUDART_INF_F ? 0.f : 1.f / l[i];
       }
 #pragma unroll
       for (int c = 0; c < NC; ++c)
@@ -280,16 +299,16 @@ __global__ void __launch_bounds__(kSimtThreads<D>) prefill_simt_kernel(const Pre
   }
 }
 
-template <int D>
+template <int D, bool TREE>
 struct SimtVariant {
   static cudaError_t launch(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const PrefillArgs& a, int grid,
                             cudaStream_t stream) {
-    prefill_simt_kernel<D><<<grid, kSimtThreads<D>, sizeof(SimtSmem<D>), stream>>>(a);
+    prefill_simt_kernel<D, TREE><<<grid, kSimtThreads<D>, sizeof(SimtSmem<D>), stream>>>(a);
     return cudaGetLastError();
   }
   static PrefillVariant info() {
     return PrefillVariant{kSimtThreads<D>, kSimtRows, kSimtRows, D, 0, 1, 128, sizeof(SimtSmem<D>),
-                          reinterpret_cast<const void*>(&prefill_simt_kernel<D>), &launch};
+                          reinterpret_cast<const void*>(&prefill_simt_kernel<D, TREE>), &launch};
   }
 };
 
@@ -304,7 +323,7 @@ struct SimtVariant {
 constexpr int kCombineThreads = 256;
 constexpr int kCombineRows = 32;  // rows of a block
 
-template <typename T, int COLS>
+template <typename T, int COLS, bool TREE>
 __global__ void __launch_bounds__(kCombineThreads)
     prefill_combine_kernel(const PrefillArgs a, int rows, int tile_rows, int head_dim) {
   grid_dependency_wait();
@@ -362,7 +381,8 @@ __global__ void __launch_bounds__(kCombineThreads)
       }
     }
   }
-  const float inv = bad ? CUDART_NAN_F : 1.f / l;
+  // (a tree's row that sees no key is 0)
+  const float inv = bad ? CUDART_NAN_F : TREE && m == -CUDART_INF_F ? 0.f : 1.f / l;
   T* dst = static_cast<T*>(a.out) +
            (static_cast<long long>(sp.row0 + tok) * a.num_q_heads + sp.head * a.group + g) * head_dim +
            sp.part * COLS + 4 * lane;
@@ -380,8 +400,14 @@ __global__ void __launch_bounds__(kCombineThreads)
 }  // namespace
 
 const PrefillVariant* prefill_simt_variant(int head_dim) {
-  static const PrefillVariant table[] = {SimtVariant<64>::info(), SimtVariant<128>::info(),
-                                         SimtVariant<256>::info()};
+  static const PrefillVariant table[] = {SimtVariant<64, false>::info(), SimtVariant<128, false>::info(),
+                                         SimtVariant<256, false>::info()};
+  return head_dim == 64 ? &table[0] : head_dim == 128 ? &table[1] : head_dim == 256 ? &table[2] : nullptr;
+}
+
+const PrefillVariant* tree_simt_variant(int head_dim) {
+  static const PrefillVariant table[] = {SimtVariant<64, true>::info(), SimtVariant<128, true>::info(),
+                                         SimtVariant<256, true>::info()};
   return head_dim == 64 ? &table[0] : head_dim == 128 ? &table[1] : head_dim == 256 ? &table[2] : nullptr;
 }
 
@@ -398,13 +424,15 @@ cudaError_t launch_prefill_combine(const PrefillArgs& a, int grid, int rows, int
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (dtype_out == 0)
-    return cols == 64    ? cudaLaunchKernelEx(&cfg, prefill_combine_kernel<__nv_bfloat16, 64>, a, rows, tile_rows, head_dim)
-           : cols == 128 ? cudaLaunchKernelEx(&cfg, prefill_combine_kernel<__nv_bfloat16, 128>, a, rows, tile_rows, head_dim)
-                         : cudaLaunchKernelEx(&cfg, prefill_combine_kernel<__nv_bfloat16, 256>, a, rows, tile_rows, head_dim);
-  return cols == 64    ? cudaLaunchKernelEx(&cfg, prefill_combine_kernel<float, 64>, a, rows, tile_rows, head_dim)
-         : cols == 128 ? cudaLaunchKernelEx(&cfg, prefill_combine_kernel<float, 128>, a, rows, tile_rows, head_dim)
-                       : cudaLaunchKernelEx(&cfg, prefill_combine_kernel<float, 256>, a, rows, tile_rows, head_dim);
+  auto go = [&](auto tree, auto zero) {
+    using T = decltype(zero);
+    constexpr bool kTree = decltype(tree)::value;
+    return cols == 64    ? cudaLaunchKernelEx(&cfg, prefill_combine_kernel<T, 64, kTree>, a, rows, tile_rows, head_dim)
+           : cols == 128 ? cudaLaunchKernelEx(&cfg, prefill_combine_kernel<T, 128, kTree>, a, rows, tile_rows, head_dim)
+                         : cudaLaunchKernelEx(&cfg, prefill_combine_kernel<T, 256, kTree>, a, rows, tile_rows, head_dim);
+  };
+  if (a.masks) return dtype_out == 0 ? go(std::true_type(), __nv_bfloat16()) : go(std::true_type(), float());
+  return dtype_out == 0 ? go(std::false_type(), __nv_bfloat16()) : go(std::false_type(), float());
 }
 
 }  // namespace vt

@@ -45,6 +45,7 @@
 // too and given back to the rows that do attend to them at the end.
 #pragma once
 
+#include <float.h>
 #include <math_constants.h>
 
 #include "decode_kernel.cuh"
@@ -54,8 +55,9 @@
 
 namespace vt {
 
-template <bool FP8, int D, int NT, int DV, int KCW, int NSK, int VK, int NSV, int NSW = 1>
+template <bool FP8, int D, int NT, int DV, int KCW, int NSK, int VK, int NSV, int NSW = 1, bool TREE = false>
 struct TcConfig {
+  static constexpr bool kTree = TREE;                  // trees of drafted tokens, else causal
   static constexpr bool kFp8 = FP8;                    // E4M3 codes in the cache, else bf16
   static constexpr int kD = D, kNT = NT, kDV = DV;
   static constexpr int kElem = FP8 ? 1 : 2;            // bytes of a cached element
@@ -133,13 +135,37 @@ constexpr float kLazy = 8.f;
 
 enum : int { kItemBad = 1, kItemFix = 2 };
 
+// An item of a tree whose rows are one tile's: both tiles hold them and take
+// every other block of keys, and the epilogue joins their sums.  One tile alone
+// waits for its softmax and its products in turn (2900 cycles a block, 64 KB of
+// bf16 or 32 KB of codes at head_dim 128), two of them overlap.
+template <typename C>
+__device__ __forceinline__ bool in_turns(const PfItem& it, int tile_toks) {
+  return C::kTree && C::kNT == 2 && it.ntok <= tile_toks;
+}
+
 // Key blocks [jb, je) of this piece that tile t of the item takes part in.
 struct TileSpan {
   int jb, je;
   int tok0, ntok;  // the tile's tokens
 };
+template <typename C>
 __device__ __forceinline__ TileSpan tile_span(const PrefillArgs& a, const PfItem& it, int t, int tile_toks) {
   TileSpan s;
+  if constexpr (C::kTree) {
+    if (in_turns<C>(it, tile_toks)) {
+      s.tok0 = 0;
+      s.ntok = it.ntok;
+      s.jb = it.kb0 + t;
+      s.je = it.kb1 > s.jb ? s.jb + ((it.kb1 - 1 - s.jb) & ~1) + 1 : s.jb;
+    } else {
+      s.tok0 = t * tile_toks;
+      s.ntok = max(0, min(tile_toks, it.ntok - s.tok0));
+      s.jb = it.kb0;
+      s.je = s.ntok > 0 ? it.kb1 : it.kb0;
+    }
+    return s;
+  }
   s.tok0 = t * tile_toks;
   s.ntok = max(0, min(tile_toks, it.ntok - s.tok0));
   const int first = it.pos0 + s.tok0;
@@ -181,8 +207,8 @@ struct Ring {
 // has tokens and whatever the context is (a walk over a whole context of 30000
 // keys took longer than a bounded wait of 8 million cycles).  A warp looks at 32
 // of them at a time.  (All threads of a warp together; rare, so compact.)
-template <bool FP8>
-__device__ __forceinline__ void add_taken_values(const PrefillArgs& a, const PfItem& it, int head_dim, int pos, int cols,
+template <bool FP8, typename Sees>
+__device__ __forceinline__ void add_taken_values(const PrefillArgs& a, const PfItem& it, int head_dim, Sees sees, int cols,
                                               uint32_t o) {
   const int lane = threadIdx.x & 31;
   const int first = max(it.lo_exact, it.lo + it.kb0 * kPfBlock);
@@ -214,7 +240,7 @@ __device__ __forceinline__ void add_taken_values(const PrefillArgs& a, const PfI
       for (; taken; taken &= taken - 1) {
         const int i = __ffs(taken) - 1, key = t0 + i;
         const float y = __shfl_sync(0xffffffffu, x, i);
-        if (key <= pos && (a.window == 0 || key > pos - a.window)) add += y;
+        if (sees(key)) add += y;
       }
     }
     uint32_t sum;
@@ -351,7 +377,7 @@ struct TcRole {
 // --------------------------------------------------------------------- loader
 template <typename C>
 __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                          const PrefillArgs& a, TcSmem<C>& s, PfWalk& w, int lane) {
+                                          const PrefillArgs& a, TcSmem<C>& s, PfWalk<C::kTree>& w, int lane) {
   TcRole<C> role{a, s, lane};
   Ring<C::kStagesK> rk;
   Ring<C::kStagesV> rv;
@@ -422,7 +448,7 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
     if (!role.wait(&s.item_empty[items % C::kItems], (items / C::kItems) ^ 1u, kStatusEmpty)) break;
     if (!more) it.b = -1;
     if (lane < C::kNT) {
-      const TileSpan sp = tile_span(a, it, lane, tile_toks);
+      const TileSpan sp = tile_span<C>(a, it, lane, tile_toks);
       s.spans[items % C::kItems][lane] = make_int4(sp.jb, sp.je, sp.tok0, sp.ntok);
       if (lane == 0) s.items[items % C::kItems] = it;
     }
@@ -496,9 +522,13 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
   const int tile_toks = a.tile_tokens / C::kNT;
   PfItem it{};
 
+  // Whether block j is one of this issuer's.
+  auto takes = [&](int j, const TileSpan& sp) {
+    return j >= sp.jb && j < sp.je && !(in_turns<C>(it, tile_toks) && ((j - sp.jb) & 1));
+  };
   // S(buf) = Q K^T for block j's keys: the MMAs of chunk c and what follows them.  One lane.
   auto qk_issue = [&](int j, int buf, int c, const TileSpan& sp) {
-    const bool active = j >= sp.jb && j < sp.je;
+    const bool active = takes(j, sp);
     if (active) {
       const int keys = min(kPfBlock, it.hi - (it.lo + j * kPfBlock));
       const uint32_t idesc = (FP8 ? umma_idesc_e4m3(0)
@@ -576,7 +606,8 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
   };
   // k-steps of block j that the tile's rows need
   auto steps_of = [&](int j, const TileSpan& sp) {
-    return (min(it.pos0 + sp.tok0 + sp.ntok - (it.lo + j * kPfBlock), kPfBlock) + KS - 1) / KS;
+    const int end = C::kTree ? it.hi : it.pos0 + sp.tok0 + sp.ntok;
+    return (min(end - (it.lo + j * kPfBlock), kPfBlock) + KS - 1) / KS;
   };
   constexpr int kHalf = kPfBlock / 2 / KS;  // k-steps of half a block
   const uint32_t idesc_pv = umma_idesc_f16(!FP8, C::kDV, true);
@@ -639,7 +670,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
         for (int j = it.kb0 - 1; j < it.kb1 && role.live; ++j) {  // P V of block j, then Q K^T of block j + 1
           // What can be waited for ahead of the weights is: after them this
           // thread only issues.
-          const bool mine = j >= it.kb0, active = j >= sp.jb && j < sp.je, next = j + 1 < it.kb1;
+          const bool mine = j >= it.kb0, active = takes(j, sp), next = j + 1 < it.kb1;
           if (mine && !v_here(needs_prep(a, it, j), flags)) break;
           if (next && !role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) break;
           if (active && j == sp.jb && !role.wait(&s.o_free[t], no ^ 1u, kStatusSync)) break;
@@ -873,6 +904,17 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
   for (; role.item(items, it); ++items) {
     const TileSpan sp = role.span(items, t);
     const int pos = it.pos0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1);
+    // trees: the row's mask, the first key of its window, and whether it has seen a key
+    const int base = it.pos0 + 1, drafted = it.L - base;
+    const int* mask = nullptr;
+    int first_key = 0;
+    bool some = false;
+    if constexpr (C::kTree) {
+      if (!it.bad) {
+        mask = tree_mask(a, it.row0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1));
+        first_key = tree_from(a, mask, drafted, base);
+      }
+    }
     float m = -CUDART_INF_F, l = 0.f;
     float scale = a.scale_log2;  // from a score in tensor memory to the log2 domain
     if constexpr (FP8) {
@@ -951,22 +993,30 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
         mbar_arrive(&s.q_full[t]);
       }
     }
-    for (int j = sp.jb; j < sp.je; ++j, ++blocks) {
+    for (int j = sp.jb; j < sp.je; j += in_turns<C>(it, tile_toks) ? 2 : 1, ++blocks) {
       const int buf = NT == 2 ? t : static_cast<int>(blocks & 1u);
       const uint32_t tS = tmem + lane_base + buf * 128;
       if (!role.wait(&s.s_full[buf], NT == 2 ? blocks : blocks >> 1, kStatusSync)) break;
       tc_fence_after();
       const int k0 = it.lo + j * kPfBlock;
       // rows see keys (pos - window, pos]; block columns [from, upto]
-      if (k0 + kPfBlock > it.pos0 + sp.tok0 + 1 ||
-          (a.window > 0 && k0 < it.pos0 + sp.tok0 + sp.ntok - a.window)) {
+      if (C::kTree ? needs_prep(a, it, j)
+                   : k0 + kPfBlock > it.pos0 + sp.tok0 + 1 ||
+                         (a.window > 0 && k0 < it.pos0 + sp.tok0 + sp.ntok - a.window)) {
         const int upto = pos - k0, from = a.window > 0 ? pos - a.window + 1 - k0 : 0;
 #pragma unroll 1
         for (int q = 0; q < kPfBlock; q += 32) {
-          if (__all_sync(0xffffffffu, upto - q >= 31 && from - q <= 0)) continue;  // all seen
-          const int last = upto - q, first = from - q;
-          const uint32_t seen = (last < 0 ? 0u : last >= 31 ? ~0u : (2u << last) - 1u) &
-                                (first <= 0 ? ~0u : first > 31 ? 0u : ~0u << first);
+          uint32_t seen;
+          if constexpr (C::kTree) {
+            seen = tree_seen(mask, drafted, base, first_key, k0 + q);
+            some |= seen != 0u;
+            if (__all_sync(0xffffffffu, seen == ~0u)) continue;
+          } else {
+            if (__all_sync(0xffffffffu, upto - q >= 31 && from - q <= 0)) continue;  // all seen
+            const int last = upto - q, first = from - q;
+            seen = (last < 0 ? 0u : last >= 31 ? ~0u : (2u << last) - 1u) &
+                   (first <= 0 ? ~0u : first > 31 ? 0u : ~0u << first);
+          }
           float x[32];
           tmem_ld32(tS + q, reinterpret_cast<uint32_t*>(x));
           tmem_wait_ld();
@@ -976,6 +1026,8 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
           tmem_st32(tS + q, reinterpret_cast<const uint32_t*>(x));
         }
         tmem_wait_st();
+      } else if (C::kTree) {
+        some = true;
       }
       // The second half of the scores is read twice, for the maximum and for the
       // weights: a row of 128 has no room beside them, and the loop over halves
@@ -1073,6 +1125,8 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
     if (!role.live) break;
 
     if (!role.wait(&s.l_free[t], items ^ 1u, kStatusSync)) break;
+    // (a row that sees no key has -inf for its maximum, one whose scores are all -inf the least number: 0 and NaN)
+    if (C::kTree && some && m == -CUDART_INF_F) m = -FLT_MAX;
     s.ml[t][row] = make_float2(m, l);
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.l_full[t]);
@@ -1096,14 +1150,15 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
   PfItem it{};
   uint32_t items = 0, no = 0;  // no: parity of a tile's accumulators in bit t
   for (; role.item(items, it); ++items) {
+    const bool joined = in_turns<C>(it, tile_toks);  // the other tile holds sums of the same rows
 #pragma unroll 1
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < (joined ? 1 : NT); ++t) {
       const uint32_t tO = tmem + lane_base + C::kTmemO + t * DV;
       const TileSpan sp = role.span(items, t);
       const bool valid = tok < tile_toks && tok < sp.ntok;
       const int pos = it.pos0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1);
       if (!role.wait(&s.l_full[t], items, kStatusSync)) break;
-      const float m = s.ml[t][row].x, l = s.ml[t][row].y;
+      float m = s.ml[t][row].x, l = s.ml[t][row].y;
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.l_free[t]);
       const bool any = sp.je > sp.jb;  // O holds sums of this tile
@@ -1113,7 +1168,39 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
         no ^= 1u << t;
         tc_fence_after();
         flags = s.flags[t];
-        if (flags & kItemFix) add_taken_values<FP8>(a, it, D, pos, DV, tO);
+      }
+      float f0 = 1.f, f1 = 0.f;  // weights of the tiles' sums
+      bool any_other = false;
+      if (joined) {
+        if (!role.wait(&s.l_full[NT - 1], items, kStatusSync)) break;
+        const float2 ml = s.ml[NT - 1][row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.l_free[NT - 1]);
+        const TileSpan other = role.span(items, NT - 1);
+        any_other = other.je > other.jb;
+        if (any_other) {
+          if (!role.wait(&s.o_full[NT - 1], no >> (NT - 1), kStatusSync)) break;
+          no ^= 1u << (NT - 1);
+          tc_fence_after();
+          flags |= s.flags[NT - 1];
+        }
+        const float top = fmaxf(m, ml.x), ref = top == -CUDART_INF_F ? 0.f : top;
+        f0 = ex2(m - ref);
+        f1 = ex2(ml.x - ref);
+        l = f0 * l + f1 * ml.y;
+        m = top;
+      }
+      if (flags & kItemFix) {
+        if constexpr (C::kTree) {
+          const int* mask = tree_mask(a, it.row0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1));
+          const int base = it.pos0 + 1, drafted = it.L - base, first_key = tree_from(a, mask, drafted, base);
+          auto sees = [&](int key) { return (tree_seen(mask, drafted, base, first_key, key) & 1u) != 0u; };
+          add_taken_values<FP8>(a, it, D, sees, DV, tO);
+          if (any_other) add_taken_values<FP8>(a, it, D, sees, DV, tO + DV);  // (one of the two weights may be 0)
+        } else {
+          add_taken_values<FP8>(
+              a, it, D, [&](int key) { return key <= pos && (a.window == 0 || key > pos - a.window); }, DV, tO);
+        }
       }
       const bool split = it.kb0 > 0 || it.pieces > 0;
       if (it.pieces > 0 && t == 0 && row == 0)
@@ -1121,12 +1208,14 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
       const long long rec = (2ll * blockIdx.x + (it.kb0 > 0 ? 1 : 0)) * (NT * 128) + t * 128 + row;
       const bool bad = it.bad || (flags & kItemBad);
       const float vs = FP8 ? a.v_scale[it.head] : 1.f;
-      const float mul = split ? vs : bad ? CUDART_NAN_F : vs / l;
+      float mul = split ? vs : bad ? CUDART_NAN_F : vs / l;
+      const bool none = C::kTree && m == -CUDART_INF_F;  // this row saw no key
+      if (none && !bad) mul = 0.f;
       if (split && valid) a.ml[rec] = make_float2(bad ? CUDART_NAN_F : m, l);
       // Rows go out four lanes to a row: a lane's 16-byte pieces of its own row
       // are exchanged within groups of four, so that a store touches eight rows
       // of 64 bytes and not 32 of 16 (which took 7000 cycles an item).
-      const bool put = valid && !(split && l == 0.f);  // (the combine reads no sums of a row without weight)
+      const bool put = valid && !(split && (C::kTree ? none : l == 0.f));  // (the combine reads no sums of a row without weight)
       char* const to = split ? reinterpret_cast<char*>(a.part) : static_cast<char*>(a.out);
       const long long mine = split ? rec * DV * 4
                                    : ((static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads +
@@ -1147,7 +1236,17 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] *= mul;
+        for (int e = 0; e < 32; ++e) o[e] *= C::kTree ? mul * f0 : mul;
+        if (any_other) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float z[16];
+            tmem_ld16(tO + DV + (c & ~31) + 16 * h, reinterpret_cast<uint32_t*>(z));
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[16 * h + e] += z[e] * (mul * f1);
+          }
+        }
         if (split) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -1173,6 +1272,7 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.o_free[t]);
       }
+      if (any_other && lane == 0) mbar_arrive(&s.o_free[NT - 1]);
     }
     if (!role.live) break;
     role.item_done(items);
@@ -1235,7 +1335,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     prefetch_tensormap(&tv);
   }
   tc_fence_before();
-  PfWalk w;
+  PfWalk<C::kTree> w;
   if (warp == kLoader) pf_begin(a, lane, w);
   __syncthreads();
   tc_fence_after();
