@@ -522,13 +522,9 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
   const int tile_toks = a.tile_tokens / C::kNT;
   PfItem it{};
 
-  // Whether block j is one of this issuer's.
-  auto takes = [&](int j, const TileSpan& sp) {
-    return j >= sp.jb && j < sp.je && !(in_turns<C>(it, tile_toks) && ((j - sp.jb) & 1));
-  };
   // S(buf) = Q K^T for block j's keys: the MMAs of chunk c and what follows them.  One lane.
   auto qk_issue = [&](int j, int buf, int c, const TileSpan& sp) {
-    const bool active = takes(j, sp);
+    const bool active = j >= sp.jb && j < sp.je;
     if (active) {
       const int keys = min(kPfBlock, it.hi - (it.lo + j * kPfBlock));
       const uint32_t idesc = (FP8 ? umma_idesc_e4m3(0)
@@ -650,6 +646,70 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
     if (j == sp.je - 1) finish(flags);
   };
 
+  // An item whose blocks the tiles take in turn: this issuer's own, every other
+  // one.  The other's stages are passed over, in order (a wait tells phases
+  // apart by parity only) and released at once: the loader need not wait for
+  // this tile's products.  Nothing but this tile's own softmax and its own
+  // stages stands before its products, and what can be waited for is waited for
+  // while the first half of P V runs.
+  auto alternate = [&](const TileSpan& sp, int& flags) {
+    auto pass_k = [&] {
+      if (!role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) return false;
+      if (lane == 0) mbar_arrive(&s.k_empty[rk.stage]);
+      rk.next();
+      return true;
+    };
+    auto pass_v = [&](int j) {
+      if constexpr (FP8) {
+        if (!role.wait(&s.w_full[rv.stage], rv.phase, kStatusFull)) return false;
+      } else {
+        if (!role.wait(&s.v_full[rv.stage], rv.phase, kStatusFull)) return false;
+        // (its preparation is over before the stage is filled again)
+        if (needs_prep(a, it, j)) vphase ^= 1u << rv.stage;
+      }
+      if (lane == 0) mbar_arrive(v_free());
+      rv.next();
+      return true;
+    };
+    int v = it.kb0;  // the next V stage
+    if (t == 1 && !pass_k()) return;
+    if (sp.je > sp.jb) {
+      if (!role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) return;
+      tc_fence_after();
+      if (elect_one()) qk_issue(sp.jb, t, 0, sp);
+      __syncwarp();
+      rk.next();
+    }
+#pragma unroll 1
+    for (int j = sp.jb; j < sp.je; j += 2) {
+      if (v < j && !pass_v(v)) return;
+      if (!v_here(needs_prep(a, it, j), flags)) return;
+      if (j == sp.jb && !role.wait(&s.o_free[t], no ^ 1u, kStatusSync)) return;
+      const int steps = steps_of(j, sp);
+      const uint32_t vb = umma_desc_lo(v_addr(), C::kPBlockBytes);
+      if (!role.wait(&s.p_ready[0][t], np[0], kStatusSync)) return;
+      tc_fence_after();
+      if (elect_one()) pv_steps(t, 0, min(steps, kHalf), vb, j > sp.jb);
+      __syncwarp();
+      const bool next = j + 2 < it.kb1;
+      if (j + 1 < it.kb1 && !pass_k()) return;
+      if (next && !role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) return;
+      if (!role.wait(&s.p_ready[1][t], np[0]++, kStatusSync)) return;
+      tc_fence_after();
+      if (elect_one()) {
+        pv_steps(t, kHalf, steps, vb + ((kHalf * KS * 128) >> 4), 1u);
+        umma_commit(v_free());
+        if (next) qk_issue(j + 2, t, 0, sp);
+      }
+      __syncwarp();
+      rv.next();
+      v = j + 1;
+      if (next) rk.next();
+      if (!next) finish(flags);
+    }
+    if (v < it.kb1) pass_v(v);
+  };
+
   for (; role.item(items, it); ++items) {
     if (it.kb1 > it.kb0) {
       const TileSpan sp = role.span(items, t);
@@ -666,11 +726,17 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs& a, TcSmem<C>& s, ui
         // softmax, in step.  The turn passes when all is issued: passed a few
         // MMAs earlier, the two tiles' products mix again (8192-token prompt
         // 2 % slower).
+        if (in_turns<C>(it, tile_toks)) {
+          alternate(sp, flags);
+          if (!role.live) break;
+          role.item_done(items);
+          continue;
+        }
         const bool both = it.ntok > tile_toks;
         for (int j = it.kb0 - 1; j < it.kb1 && role.live; ++j) {  // P V of block j, then Q K^T of block j + 1
           // What can be waited for ahead of the weights is: after them this
           // thread only issues.
-          const bool mine = j >= it.kb0, active = takes(j, sp), next = j + 1 < it.kb1;
+          const bool mine = j >= it.kb0, active = j >= sp.jb && j < sp.je, next = j + 1 < it.kb1;
           if (mine && !v_here(needs_prep(a, it, j), flags)) break;
           if (next && !role.wait(&s.k_full[rk.stage], rk.phase, kStatusFull)) break;
           if (active && j == sp.jb && !role.wait(&s.o_free[t], no ^ 1u, kStatusSync)) break;
