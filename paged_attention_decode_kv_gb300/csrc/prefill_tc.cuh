@@ -903,37 +903,59 @@ __device__ __forceinline__ void tc_widen(const PrefillArgs& a, TcSmem<C>& s, int
         bool fix = false;
         constexpr int kRowPieces = C::kDV / 16;  // 16 codes each
         constexpr int kPieces = C::kRow / 16;    // of a swizzled block's row
-#pragma unroll 2
-        for (int p = tid; p < end * kRowPieces; p += 128) {
-          const int slot = p / kRowPieces, piece = p % kRowPieces;
-          const int cb = piece / kPieces, ch = piece % kPieces;
-          const int swz = C::kRow == 128 ? ch ^ (slot & 7) : ch ^ ((slot >> 1) & 3);
-          uint4 x = *reinterpret_cast<const uint4*>(src + cb * C::kVBlockBytes + slot * C::kRow + swz * 16);
-          if (prepare) {
-            const int t = k0 + slot;
-            if (t < it.lo_exact || t >= it.hi) {
-              x = make_uint4(0, 0, 0, 0);
-            } else if (t > it.pos0 || (a.window > 0 && t < it.hi - a.window)) {
-              const uint32_t m = (carries<true>(x.x) | carries<true>(x.y) | carries<true>(x.z) | carries<true>(x.w)) &
-                                 kCarry<true>;
-              if (m) {
-                fix = true;
-                x.x &= ~not_finite<true>(x.x), x.y &= ~not_finite<true>(x.y);
-                x.z &= ~not_finite<true>(x.z), x.w &= ~not_finite<true>(x.w);
-              }
+        auto take_out = [&](uint4& x, int slot) {
+          const int t = k0 + slot;
+          if (t < it.lo_exact || t >= it.hi) {
+            x = make_uint4(0, 0, 0, 0);
+          } else if (t > it.pos0 || (a.window > 0 && t < it.hi - a.window)) {
+            const uint32_t m = (carries<true>(x.x) | carries<true>(x.y) | carries<true>(x.z) | carries<true>(x.w)) &
+                               kCarry<true>;
+            if (m) {
+              fix = true;
+              x.x &= ~not_finite<true>(x.x), x.y &= ~not_finite<true>(x.y);
+              x.z &= ~not_finite<true>(x.z), x.w &= ~not_finite<true>(x.w);
             }
           }
+        };
+        auto widen = [&](const uint4& x, unsigned char* row, int at0, int at1, int odd) {
           uint4 y[2];
           e4m3x4_to_f16(x.x, y[0].x, y[0].y);
           e4m3x4_to_f16(x.y, y[0].z, y[0].w);
           e4m3x4_to_f16(x.z, y[1].x, y[1].y);
           e4m3x4_to_f16(x.w, y[1].z, y[1].w);
-          // two 16-byte pieces of a 128-byte row of 64 columns; the lanes of
-          // every other block store them the other way round (no bank conflicts)
-          unsigned char* row = dst + (piece >> 2) * C::kPBlockBytes + slot * 128;
-          const int at = (piece & 3) * 2, odd = (piece >> 2) & 1;
-          *reinterpret_cast<uint4*>(row + (((at + odd) ^ (slot & 7)) << 4)) = odd ? y[1] : y[0];
-          *reinterpret_cast<uint4*>(row + (((at + (odd ^ 1)) ^ (slot & 7)) << 4)) = odd ? y[0] : y[1];
+          *reinterpret_cast<uint4*>(row + at0) = odd ? y[1] : y[0];
+          *reinterpret_cast<uint4*>(row + at1) = odd ? y[0] : y[1];
+        };
+        // A thread's pieces lie a whole number of swizzle atoms apart, so they
+        // differ by a stride only.  Two 16-byte pieces of f16 go to a 128-byte
+        // row of 64 columns; the lanes of every other block store them the
+        // other way round (no bank conflicts).
+        const int piece = tid % kRowPieces, slot0 = tid / kRowPieces;
+        const int cb = piece / kPieces, ch = piece % kPieces;
+        const int swz = C::kRow == 128 ? ch ^ (slot0 & 7) : ch ^ ((slot0 >> 1) & 3);
+        const unsigned char* from = src + cb * C::kVBlockBytes + slot0 * C::kRow + swz * 16;
+        unsigned char* to = dst + (piece >> 2) * C::kPBlockBytes + slot0 * 128;
+        const int at = (piece & 3) * 2, odd = (piece >> 2) & 1;
+        const int at0 = ((at + odd) ^ (slot0 & 7)) << 4, at1 = ((at + (odd ^ 1)) ^ (slot0 & 7)) << 4;
+        constexpr int kStep = 128 / kRowPieces;  // slots
+        static_assert(kStep % 8 == 0, "whole atoms");
+        constexpr int kAhead = 4;
+#pragma unroll 1
+        for (int slot = slot0; slot < end; slot += kAhead * kStep) {
+          uint4 x[kAhead];
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u)
+            if (slot + u * kStep < end) x[u] = *reinterpret_cast<const uint4*>(from + u * kStep * C::kRow);
+          if (prepare) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+              if (slot + u * kStep < end) take_out(x[u], slot + u * kStep);
+          }
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u)
+            if (slot + u * kStep < end) widen(x[u], to + u * kStep * 128, at0, at1, odd);
+          from += kAhead * kStep * C::kRow;
+          to += kAhead * kStep * 128;
         }
         fix = __any_sync(0xffffffffu, fix);
         const bool bad = s.stage_bad[rv.stage] != 0;
