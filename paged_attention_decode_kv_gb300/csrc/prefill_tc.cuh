@@ -375,37 +375,98 @@ struct TcRole {
 };
 
 // --------------------------------------------------------------------- loader
+// A sequence's block-table row, 64 entries of it at a time, two a lane; the next
+// 32 are on their way while those before are used.
+struct PageIds {
+  int window = -1, now = 0, next = 0;  // entries 32 window + lane, and the 32 after them
+  __device__ __forceinline__ int load(const PrefillArgs& a, int b, int w, int lane) const {
+    const int at = 32 * w + lane;
+    return at < a.max_blocks ? a.block_tables[static_cast<long long>(b) * a.max_blocks + at] : 0;
+  }
+  __device__ __forceinline__ void start(const PrefillArgs& a, int b, int p, int lane) {
+    window = p >> 5;
+    now = load(a, b, window, lane);
+    next = load(a, b, window + 1, lane);
+  }
+  // Entry p + i, i < 32 the lane's own; p does not decrease.
+  __device__ __forceinline__ int get(const PrefillArgs& a, int b, int p, int i, int lane) {
+    if (p >> 5 != window) {
+      ++window;
+      now = next;
+      next = load(a, b, window + 1, lane);
+    }
+    const int x = __shfl_sync(0xffffffffu, now, (p + i) & 31), y = __shfl_sync(0xffffffffu, next, (p + i) & 31);
+    return (p + i) >> 5 == window ? x : y;
+  }
+};
+
+// Codes take half the time of bf16 to arrive, and one warp that looks up pages,
+// asks for them and waits for free stages takes 2000 cycles a block of a tree's
+// few rows: a second one fetches V.
+template <typename C>
+constexpr bool kTwoLoaders = C::kTree && C::kFp8;
+
+template <typename C>
+struct TcLoadV {
+  Ring<C::kStagesV> ring;
+  long long stages = 0;
+  // Block j of the item, whose pages lane i % 4 holds the i-th of.
+  __device__ __forceinline__ void operator()(const CUtensorMap& tv, const PrefillArgs& a, TcSmem<C>& s, TcRole<C>& role,
+                                             const PfItem& it, int j, int of_block, int lane) {
+    constexpr int kPages = C::kVK / kPfPage;  // of a stage
+    const int n = v_stages<C>(it, j);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int k0 = it.lo + j * kPfBlock + i * C::kVK;
+      const int pages = min(C::kVK, it.hi - k0 + kPfPage - 1) / kPfPage;
+      int page = kPages == 4 ? of_block : __shfl_sync(0xffffffffu, of_block, i * kPages + lane % kPages);
+      const bool use = lane % kPages < pages && lane < kPages * C::kVBlocks;
+      const bool bad = use && (page < 0 || page >= a.num_blocks);
+      const bool any_bad = __any_sync(0xffffffffu, bad);
+      if (bad) page = 0;
+      if (!role.wait(&s.v_empty[ring.stage], ring.phase ^ 1u, kStatusEmpty)) return;
+      if (lane == 0) {
+        s.stage_bad[ring.stage] = any_bad;
+        mbar_arrive_expect_tx(&s.v_full[ring.stage], pages * C::kVBlocks * kPfPage * C::kRow);
+      }
+      __syncwarp();
+      if (use)
+        tma_load_4d(s.v[ring.stage] + (lane / kPages) * C::kVBlockBytes + (lane % kPages) * kPfPage * C::kRow, &tv, 0,
+                    page * kPfPage, it.part * C::kVBlocks + lane / kPages, it.head, &s.v_full[ring.stage]);
+      ++stages;
+      ring.next();
+    }
+  }
+  // Lets this CTA's copies land before it exits.
+  __device__ __forceinline__ void drain(TcSmem<C>& s, TcRole<C>& role) {
+#pragma unroll 1
+    for (long long k = 1; k <= (stages < C::kStagesV ? stages : C::kStagesV); ++k)
+      role.drain(&s.v_full[(stages - k) % C::kStagesV], static_cast<uint32_t>((stages - k) / C::kStagesV));
+  }
+};
+
 template <typename C>
 __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                           const PrefillArgs& a, TcSmem<C>& s, PfWalk<C::kTree>& w, int lane) {
   TcRole<C> role{a, s, lane};
   Ring<C::kStagesK> rk;
-  Ring<C::kStagesV> rv;
+  TcLoadV<C> load_v;
   uint32_t nq = 0, used = 0, items = 0;  // nq: parity of a tile's Q loads in bit 16 t
-  long long nk = 0, nv = 0;
+  long long nk = 0;
   int blocks = 0;
   const int tile_toks = a.tile_tokens / C::kNT;
-  int ids = 0, ids_at = -1;  // 32 table entries, one a lane, from page index ids_at
+  PageIds ids;
   PfItem it{};
-  // This lane's box of a stage whose first page is the item's page p0: page
-  // p0 + box % pages, column block box / pages.
-  auto read_ids = [&](int p0) {
-    if (ids_at < 0 || p0 < ids_at || p0 + 4 > ids_at + 32) {
-      ids_at = max(0, p0 - 4);  // K runs a block ahead of V
-      const int at = ids_at + lane;
-      ids = at < a.max_blocks ? a.block_tables[static_cast<long long>(it.b) * a.max_blocks + at] : 0;
-    }
-  };
-  auto page_of = [&](int p0, int i) {
-    read_ids(p0);
-    return __shfl_sync(0xffffffffu, ids, p0 - ids_at + i);
-  };
+  // Pages of the last block of K asked for and of the one before; this lane's
+  // box of a stage has page lane % 4, column block lane / 4.
+  int last = 0, before = 0;
   auto load_k = [&](int j) {
     const int k0 = it.lo + j * kPfBlock;
     const int pages = min(kPfBlock, it.hi - k0 + kPfPage - 1) / kPfPage;  // those that hold keys of the item
-    int page = page_of(k0 / kPfPage, lane & 3);
+    before = last;
+    int page = last = ids.get(a, it.b, k0 / kPfPage, lane & 3, lane);
     const bool use = (lane & 3) < pages && lane < 4 * C::kKBlocks;
-    if (page < 0 || page >= a.num_blocks) page = 0;  // (load_v reports it)
+    if (page < 0 || page >= a.num_blocks) page = 0;  // (who loads V reports it)
 #pragma unroll 1
     for (int c = 0; c < C::kKChunks; ++c) {
       if (!role.wait(&s.k_empty[rk.stage], rk.phase ^ 1u, kStatusEmpty)) return;
@@ -416,31 +477,6 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
                     page * kPfPage, c * C::kKBlocks + (lane >> 2), it.head, &s.k_full[rk.stage]);
       ++nk;
       rk.next();
-    }
-  };
-  auto load_v = [&](int j) {
-    constexpr int kPages = C::kVK / kPfPage;  // of a stage
-    const int stages = v_stages<C>(it, j);
-#pragma unroll 1
-    for (int i = 0; i < stages; ++i) {
-      const int k0 = it.lo + j * kPfBlock + i * C::kVK;
-      const int pages = min(C::kVK, it.hi - k0 + kPfPage - 1) / kPfPage;
-      int page = page_of((it.lo + j * kPfBlock) / kPfPage, i * kPages + lane % kPages);
-      const bool use = lane % kPages < pages && lane < kPages * C::kVBlocks;
-      const bool bad = use && (page < 0 || page >= a.num_blocks);
-      const bool any_bad = __any_sync(0xffffffffu, bad);
-      if (bad) page = 0;
-      if (!role.wait(&s.v_empty[rv.stage], rv.phase ^ 1u, kStatusEmpty)) return;
-      if (lane == 0) {
-        s.stage_bad[rv.stage] = any_bad;
-        mbar_arrive_expect_tx(&s.v_full[rv.stage], pages * C::kVBlocks * kPfPage * C::kRow);
-      }
-      __syncwarp();
-      if (use)
-        tma_load_4d(s.v[rv.stage] + (lane / kPages) * C::kVBlockBytes + (lane % kPages) * kPfPage * C::kRow, &tv, 0,
-                    page * kPfPage, it.part * C::kVBlocks + lane / kPages, it.head, &s.v_full[rv.stage]);
-      ++nv;
-      rv.next();
     }
   };
   while (role.live) {
@@ -455,8 +491,7 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.item_full[items % C::kItems]);
     if (!more) break;
-    ids_at = -1;
-    if (it.kb1 > it.kb0) read_ids((it.lo + it.kb0 * kPfBlock) / kPfPage);  // on their way while Q is asked for
+    if (it.kb1 > it.kb0) ids.start(a, it.b, (it.lo + it.kb0 * kPfBlock) / kPfPage, lane);  // on their way while Q is asked for
 #pragma unroll 1
     for (int t = 0; t < C::kNT && !C::kFp8; ++t) {
       const TileSpan sp = role.span(items, t);
@@ -476,7 +511,8 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
     }
 #pragma unroll 1
     for (int j = it.kb0 - 1; j < it.kb1 && role.live; ++j) {  // K of block j + 1, then V of block j
-      if (j + 1 < it.kb1) {
+      const bool next = j + 1 < it.kb1;
+      if (next) {
         if (static_cast<int>(blockIdx.x) == a.withhold_cta && blocks >= a.withhold_block) {
           role.live = false;  // test hook: an issuer's wait for this block runs out
           break;
@@ -484,21 +520,37 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
         ++blocks;
         load_k(j + 1);
       }
-      if (role.live && j >= it.kb0) load_v(j);
+      if (!kTwoLoaders<C> && role.live && j >= it.kb0) load_v(tv, a, s, role, it, j, next ? before : last, lane);
     }
     ++items;
   }
   if (!role.live) {
-    // let this CTA's copies land before it exits
 #pragma unroll 1
     for (long long k = 1; k <= (nk < C::kStagesK ? nk : C::kStagesK); ++k)
       role.drain(&s.k_full[(nk - k) % C::kStagesK], static_cast<uint32_t>((nk - k) / C::kStagesK));
-#pragma unroll 1
-    for (long long k = 1; k <= (nv < C::kStagesV ? nv : C::kStagesV); ++k)
-      role.drain(&s.v_full[(nv - k) % C::kStagesV], static_cast<uint32_t>((nv - k) / C::kStagesV));
+    load_v.drain(s, role);
     for (int t = 0; t < C::kNT; ++t)
       if (used >> t & 1u) role.drain(&s.q_full[t], (nq >> (16 * t)) ^ 1u);
   }
+}
+
+// The second loader: V.
+template <typename C>
+__device__ __forceinline__ void tc_loader_v(const CUtensorMap& tv, const PrefillArgs& a, TcSmem<C>& s, int lane) {
+  TcRole<C> role{a, s, lane};
+  TcLoadV<C> load_v;
+  PageIds ids;
+  PfItem it{};
+  uint32_t items = 0;
+  for (; role.item(items, it); ++items) {
+    if (it.kb1 > it.kb0) ids.start(a, it.b, (it.lo + it.kb0 * kPfBlock) / kPfPage, lane);
+#pragma unroll 1
+    for (int j = it.kb0; j < it.kb1 && role.live; ++j)
+      load_v(tv, a, s, role, it, j, ids.get(a, it.b, (it.lo + j * kPfBlock) / kPfPage, lane & 3, lane), lane);
+    if (!role.live) break;
+    role.item_done(items);
+  }
+  if (!role.live) load_v.drain(s, role);
 }
 
 // --------------------------------------------------------------------- MMA issue
@@ -1412,7 +1464,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     for (int i = 0; i < C::kItems; ++i) {
       mbar_init(&s.item_full[i], 1);
-      mbar_init(&s.item_empty[i], (C::kFp8 ? 10 : 7) + 4 * NT);  // every warp but the loader
+      mbar_init(&s.item_empty[i], (C::kFp8 ? 10 : 7) + (kTwoLoaders<C> ? 1 : 0) + 4 * NT);  // every warp but the loader
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1442,6 +1494,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       tc_loader<C>(tq, tk, tv, a, s, w, lane);
     } else if (warp == kPrep) {
       if constexpr (!C::kFp8) tc_prepare<C>(a, s, lane);
+      if constexpr (kTwoLoaders<C>) tc_loader_v<C>(tv, a, s, lane);
     } else {
       tc_issuer<C>(a, s, tmem, warp - kIssuer, lane);
     }
