@@ -38,6 +38,7 @@ SOURCES = [
     "prefill_e4m3.cu",
     "prefill_tree_bf16.cu",
     "prefill_tree_e4m3.cu",
+    "tree_combine.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

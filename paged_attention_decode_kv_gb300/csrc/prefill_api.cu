@@ -297,7 +297,10 @@ vt_status prefill(const PrefillCall& c) {
   }
   e = v.launch(tq, tk, tv, a, grid, c.stream);
   if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
-  e = launch_prefill_combine(a, grid, v.rows, v.tile_rows, v.cols, c.head_dim, c.dtype == VT_F32 ? 1 : 0, c.stream);
+  if (c.tree && v.tensor_cores)
+    e = launch_tree_combine(a, grid, v.rows, v.cols, c.head_dim, sms, c.stream);
+  else
+    e = launch_prefill_combine(a, grid, v.rows, v.tile_rows, v.cols, c.head_dim, c.dtype == VT_F32 ? 1 : 0, c.stream);
   if (e != cudaSuccess) return cuda_fail(e, "prefill combine launch");
 
   vt_plan& r = g_last_plan;

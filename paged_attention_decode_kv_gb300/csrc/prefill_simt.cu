@@ -431,7 +431,7 @@ cudaError_t launch_prefill_combine(const PrefillArgs& a, int grid, int rows, int
            : cols == 128 ? cudaLaunchKernelEx(&cfg, prefill_combine_kernel<T, 128, kTree>, a, rows, tile_rows, head_dim)
                          : cudaLaunchKernelEx(&cfg, prefill_combine_kernel<T, 256, kTree>, a, rows, tile_rows, head_dim);
   };
-  if (a.masks) return dtype_out == 0 ? go(std::true_type(), __nv_bfloat16()) : go(std::true_type(), float());
+  if (a.masks) return go(std::true_type(), float());  // (trees with bf16 results: tree_combine.cu)
   return dtype_out == 0 ? go(std::false_type(), __nv_bfloat16()) : go(std::false_type(), float());
 }
 

@@ -1355,21 +1355,11 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
       // Rows go out four lanes to a row: a lane's 16-byte pieces of its own row
       // are exchanged within groups of four, so that a store touches eight rows
       // of 64 bytes and not 32 of 16 (which took 7000 cycles an item).
-      const bool put = valid && !(split && (C::kTree ? none : l == 0.f));  // (the combine reads no sums of a row without weight)
-      char* const to = split ? reinterpret_cast<char*>(a.part) : static_cast<char*>(a.out);
-      const long long mine = split ? rec * DV * 4
-                                   : ((static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads +
-                                       it.head * a.group + g) * D + it.part * DV) * 2;
-      long long at[4];  // byte offsets of the group's rows; -1: not written
-#pragma unroll
-      for (int r = 0; r < 4; ++r) at[r] = __shfl_sync(0xffffffffu, put ? mine : -1ll, (lane & ~3) + r);
-      // 64 bytes of a row at a time: 32 bf16 or 16 fp32 columns, from 32 columns read
-#pragma unroll 1
-      for (int c = 0; c < DV; c += split ? 16 : 32) {
-        float o[32];
-        uint4 x[4];
+      // 32 columns of the row, weighed and joined.
+      float o[32];
+      auto columns = [&](int c) {
         if (any) {
-          tmem_ld32(tO + (c & ~31), reinterpret_cast<uint32_t*>(o));
+          tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
           tmem_wait_ld();
         } else {
 #pragma unroll
@@ -1381,31 +1371,62 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float z[16];
-            tmem_ld16(tO + DV + (c & ~31) + 16 * h, reinterpret_cast<uint32_t*>(z));
+            tmem_ld16(tO + DV + c + 16 * h, reinterpret_cast<uint32_t*>(z));
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[16 * h + e] += z[e] * (mul * f1);
           }
         }
-        if (split) {
+      };
+      if (C::kTree && split) {
+        // A tree's partials lie four columns of the tile's 128 rows after
+        // another: a warp's stores are whole lines as they are.
+        float4* to = reinterpret_cast<float4*>(a.part + (rec - row) * DV) + row;
+#pragma unroll 1
+        for (int c = 0; c < DV; c += 32) {
+          columns(c);
+          if (valid && !none) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float f[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = c & 16 ? o[16 + 4 * e + i] : o[4 * e + i];
-            x[e] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+            for (int e = 0; e < 8; ++e)
+              to[(c / 4 + e) * 128] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                              pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+          __syncwarp();  // the next load of tensor memory is the whole warp's
         }
-        transpose4(x, lane);
+      } else {
+        const bool by_rows = !C::kTree && split;
+        const bool put = valid && !(by_rows && l == 0.f);  // (the combine reads no sums of a row without weight)
+        char* const to = by_rows ? reinterpret_cast<char*>(a.part) : static_cast<char*>(a.out);
+        const long long mine = by_rows ? rec * DV * 4
+                                     : ((static_cast<long long>(it.row0 + sp.tok0 + tok) * a.num_q_heads +
+                                         it.head * a.group + g) * D + it.part * DV) * 2;
+        long long at[4];  // byte offsets of the group's rows; -1: not written
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (at[r] >= 0) *reinterpret_cast<uint4*>(to + at[r] + c * (split ? 4 : 2) + 16 * (lane & 3)) = x[r];
-        __syncwarp();  // the next load of tensor memory is the whole warp's
+        for (int r = 0; r < 4; ++r) at[r] = __shfl_sync(0xffffffffu, put ? mine : -1ll, (lane & ~3) + r);
+        // 64 bytes of a row at a time: 32 bf16 or 16 fp32 columns, from 32 columns read
+#pragma unroll 1
+        for (int c = 0; c < DV; c += by_rows ? 16 : 32) {
+          uint4 x[4];
+          columns(c & ~31);
+          if (by_rows) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float f[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) f[i] = c & 16 ? o[16 + 4 * e + i] : o[4 * e + i];
+              x[e] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+          }
+          transpose4(x, lane);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (at[r] >= 0) *reinterpret_cast<uint4*>(to + at[r] + c * (by_rows ? 4 : 2) + 16 * (lane & 3)) = x[r];
+          __syncwarp();  // the next load of tensor memory is the whole warp's
+        }
       }
       if (any) {
         tc_fence_before();

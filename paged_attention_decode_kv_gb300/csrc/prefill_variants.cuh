@@ -35,4 +35,8 @@ const PrefillVariant* tree_e4m3_variant(int head_dim);
 cudaError_t launch_prefill_combine(const PrefillArgs& a, int grid, int rows, int tile_rows, int cols, int head_dim,
                                    int dtype_out, cudaStream_t stream);
 
+// The same for trees on tensor cores (bf16 results), whose partials lie four columns of a tile's 128 rows after another.
+cudaError_t launch_tree_combine(const PrefillArgs& a, int ctas, int rows, int cols, int head_dim, int num_sms,
+                                cudaStream_t stream);
+
 }  // namespace vt
