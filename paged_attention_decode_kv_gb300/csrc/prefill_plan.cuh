@@ -346,34 +346,55 @@ __device__ __forceinline__ unsigned tree_word(const int* mask, int i, int n) {
   return left < 32 ? w & ((1u << left) - 1u) : w;
 }
 
-// The first key a row's window takes in: of the tokens the row may see (those
-// before `base`, then the new ones its mask names) it sees the last `window`.
-__device__ __forceinline__ int tree_from(const PrefillArgs& a, const int* mask, int n, int base) {
-  if (a.window == 0) return 0;
-  int count = 0;
-#pragma unroll 1
-  for (int i = 0; 32 * i < n; ++i) count += __popc(tree_word(mask, i, n));
-  int skip = count - a.window;  // new tokens before the window
-  if (skip < 0) return max(0, base + skip);
-#pragma unroll 1
-  for (int i = 0;; ++i) {
-    unsigned w = tree_word(mask, i, n);
-    const int c = __popc(w);
-    if (skip < c) {
-      for (; skip > 0; --skip) w &= w - 1u;
-      return base + 32 * i + __ffs(w) - 1;
-    }
-    skip -= c;
-  }
-}
+// What a row of a tree sees.  The first words of its mask are read when the row
+// is taken up, long before they are needed (a load takes 2400 cycles while all
+// SMs read keys and values).
+struct TreeRow {
+  const int* mask = nullptr;
+  int n = 0;        // new tokens of its sequence
+  int base = 0;     // position of the first
+  int from = 0;     // the first key its window takes in
+  unsigned w0 = 0, w1 = 0;
 
-// Which of the keys k .. k + 31 a row sees: bit by bit.
-__device__ __forceinline__ unsigned tree_seen(const int* mask, int n, int base, int from, int k) {
-  const int ahead = k - base, i = ahead >> 5;  // (rounded down)
-  const unsigned lo = i < 0 ? ~0u : tree_word(mask, i, n);
-  const unsigned hi = i + 1 < 0 ? ~0u : tree_word(mask, i + 1, n);
-  const int before = from - k;
-  return __funnelshift_r(lo, hi, ahead & 31) & (before <= 0 ? ~0u : before > 31 ? 0u : ~0u << before);
-}
+  __device__ __forceinline__ unsigned word(int i) const { return i == 0 ? w0 : i == 1 ? w1 : tree_word(mask, i, n); }
+
+  // Packed row `row` of a sequence with n new tokens from position `base` on.
+  __device__ __forceinline__ void take(const PrefillArgs& a, int row, int n_, int base_) {
+    mask = tree_mask(a, row);
+    n = n_;
+    base = base_;
+    w0 = tree_word(mask, 0, n);
+    w1 = tree_word(mask, 1, n);
+    from = 0;
+    if (a.window > 0) from = window_start(a.window);
+  }
+  // Of the tokens the row may see (those before `base`, then the new ones its
+  // mask names) it sees the last `window`.
+  __device__ __forceinline__ int window_start(int window) const {
+    int count = 0;
+#pragma unroll 1
+    for (int i = 0; 32 * i < n; ++i) count += __popc(word(i));
+    int skip = count - window;  // new tokens before the window
+    if (skip < 0) return max(0, base + skip);
+#pragma unroll 1
+    for (int i = 0;; ++i) {
+      unsigned w = word(i);
+      const int c = __popc(w);
+      if (skip < c) {
+        for (; skip > 0; --skip) w &= w - 1u;
+        return base + 32 * i + __ffs(w) - 1;
+      }
+      skip -= c;
+    }
+  }
+  // Which of the keys k .. k + 31 it sees: bit by bit.
+  __device__ __forceinline__ unsigned seen(int k) const {
+    const int ahead = k - base, i = ahead >> 5;  // (rounded down)
+    const unsigned lo = i < 0 ? ~0u : word(i);
+    const unsigned hi = i + 1 < 0 ? ~0u : word(i + 1);
+    const int before = from - k;
+    return __funnelshift_r(lo, hi, ahead & 31) & (before <= 0 ? ~0u : before > 31 ? 0u : ~0u << before);
+  }
+};
 
 }  // namespace vt

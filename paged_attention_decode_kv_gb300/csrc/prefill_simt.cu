@@ -91,10 +91,12 @@ __global__ void __launch_bounds__(kSimtThreads<D>) prefill_simt_kernel(const Pre
       m[i] = -CUDART_INF_F;
       l[i] = 0.f;
       const int tok = min(pf_token_of(a, ty * NR + i), it.ntok - 1);
-      if constexpr (TREE)
-        pos[i] = it.bad ? 0 : tree_from(a, tree_mask(a, it.row0 + tok), drafted, base);
-      else
-        pos[i] = it.pos0 + tok;
+      pos[i] = TREE ? 0 : it.pos0 + tok;
+      if (TREE && !it.bad && a.window > 0) {
+        TreeRow r;
+        r.take(a, it.row0 + tok, drafted, base);
+        pos[i] = r.from;
+      }
 #pragma unroll
       for (int c = 0; c < NC; ++c) o[i][c][0] = o[i][c][1] = make_float2(0.f, 0.f);
     }
@@ -169,9 +171,15 @@ __global__ void __launch_bounds__(kSimtThreads<D>) prefill_simt_kernel(const Pre
         unsigned of_row[2] = {~0u, ~0u};
         if constexpr (TREE) {
           if (t0 + kSimtKeys > base || (a.window > 0 && t0 < it.hi - a.window)) {
-            const int* mask = tree_mask(a, it.row0 + min(pf_token_of(a, ty * NR + i), it.ntok - 1));
+            TreeRow r;
+            r.mask = tree_mask(a, it.row0 + min(pf_token_of(a, ty * NR + i), it.ntok - 1));
+            r.n = drafted;
+            r.base = base;
+            r.from = pos[i];
+            r.w0 = tree_word(r.mask, 0, drafted);
+            r.w1 = tree_word(r.mask, 1, drafted);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) of_row[h] = tree_seen(mask, drafted, base, pos[i], t0 + 32 * h);
+            for (int h = 0; h < 2; ++h) of_row[h] = r.seen(t0 + 32 * h);
           }
           some |= (of_row[0] | of_row[1]) != 0u ? 1u << i : 0u;  // (bits past the last key are not set)
         }

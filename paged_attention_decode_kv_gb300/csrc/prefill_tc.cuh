@@ -492,6 +492,17 @@ __device__ __forceinline__ void tc_loader(const CUtensorMap& tq, const CUtensorM
     if (lane == 0) mbar_arrive(&s.item_full[items % C::kItems]);
     if (!more) break;
     if (it.kb1 > it.kb0) ids.start(a, it.b, (it.lo + it.kb0 * kPfBlock) / kPfPage, lane);  // on their way while Q is asked for
+    if constexpr (C::kTree && C::kFp8) {
+      // Q's rows, which the softmax threads read when they get to the item, into L2
+      const int lines = a.group * C::kD / 64;  // of 128 bytes, of a token
+#pragma unroll 1
+      for (int i = lane; i < it.ntok * lines; i += 32) {
+        const int tok = i / lines;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            static_cast<const char*>(a.q) +
+            (static_cast<long long>(it.row0 + tok) * a.num_q_heads + it.head * a.group) * C::kD * 2 + (i - tok * lines) * 128));
+      }
+    }
 #pragma unroll 1
     for (int t = 0; t < C::kNT && !C::kFp8; ++t) {
       const TileSpan sp = role.span(items, t);
@@ -1044,16 +1055,12 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
   for (; role.item(items, it); ++items) {
     const TileSpan sp = role.span(items, t);
     const int pos = it.pos0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1);
-    // trees: the row's mask, the first key of its window, and whether it has seen a key
-    const int base = it.pos0 + 1, drafted = it.L - base;
-    const int* mask = nullptr;
-    int first_key = 0;
+    // trees: what the row sees, and whether it has seen a key
+    TreeRow tree;
     bool some = false;
     if constexpr (C::kTree) {
-      if (!it.bad) {
-        mask = tree_mask(a, it.row0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1));
-        first_key = tree_from(a, mask, drafted, base);
-      }
+      if (!it.bad)
+        tree.take(a, it.row0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1), it.L - it.pos0 - 1, it.pos0 + 1);
     }
     float m = -CUDART_INF_F, l = 0.f;
     float scale = a.scale_log2;  // from a score in tensor memory to the log2 domain
@@ -1066,7 +1073,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
       if (sp.je > sp.jb) {
         const float ks = a.k_scale[it.head] * (a.neg_scale ? -1.f : 1.f);
         constexpr int kLanes = D / 16, kRows = 32 / kLanes, kSteps = kLanes;  // lanes of a row, rows of a step
-        constexpr int kAhead = 2;                                             // steps of a batch of loads
+        constexpr int kAhead = C::kTree ? 4 : 2;                              // steps of a batch of loads
         const int piece = lane % kLanes;
         const int blk = piece / (ROW / 16), ch = piece % (ROW / 16);
         uint4 in[kAhead][2], next[kAhead][2];
@@ -1148,7 +1155,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
         for (int q = 0; q < kPfBlock; q += 32) {
           uint32_t seen;
           if constexpr (C::kTree) {
-            seen = tree_seen(mask, drafted, base, first_key, k0 + q);
+            seen = tree.seen(k0 + q);
             some |= seen != 0u;
             if (__all_sync(0xffffffffu, seen == ~0u)) continue;
           } else {
@@ -1291,6 +1298,7 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
   uint32_t items = 0, no = 0;  // no: parity of a tile's accumulators in bit t
   for (; role.item(items, it); ++items) {
     const bool joined = in_turns<C>(it, tile_toks);  // the other tile holds sums of the same rows
+    const float vs = FP8 ? a.v_scale[it.head] : 1.f;  // (here: the load is under way while sums are waited for)
 #pragma unroll 1
     for (int t = 0; t < (joined ? 1 : NT); ++t) {
       const uint32_t tO = tmem + lane_base + C::kTmemO + t * DV;
@@ -1332,9 +1340,9 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
       }
       if (flags & kItemFix) {
         if constexpr (C::kTree) {
-          const int* mask = tree_mask(a, it.row0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1));
-          const int base = it.pos0 + 1, drafted = it.L - base, first_key = tree_from(a, mask, drafted, base);
-          auto sees = [&](int key) { return (tree_seen(mask, drafted, base, first_key, key) & 1u) != 0u; };
+          TreeRow tree;
+          tree.take(a, it.row0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1), it.L - it.pos0 - 1, it.pos0 + 1);
+          auto sees = [&](int key) { return (tree.seen(key) & 1u) != 0u; };
           add_taken_values<FP8>(a, it, D, sees, DV, tO);
           if (any_other) add_taken_values<FP8>(a, it, D, sees, DV, tO + DV);  // (one of the two weights may be 0)
         } else {
@@ -1347,14 +1355,10 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
         a.splits[blockIdx.x] = PrefillSplit{it.pieces, it.row0, it.ntok, it.head, it.part};
       const long long rec = (2ll * blockIdx.x + (it.kb0 > 0 ? 1 : 0)) * (NT * 128) + t * 128 + row;
       const bool bad = it.bad || (flags & kItemBad);
-      const float vs = FP8 ? a.v_scale[it.head] : 1.f;
       float mul = split ? vs : bad ? CUDART_NAN_F : vs / l;
       const bool none = C::kTree && m == -CUDART_INF_F;  // this row saw no key
       if (none && !bad) mul = 0.f;
       if (split && valid) a.ml[rec] = make_float2(bad ? CUDART_NAN_F : m, l);
-      // Rows go out four lanes to a row: a lane's 16-byte pieces of its own row
-      // are exchanged within groups of four, so that a store touches eight rows
-      // of 64 bytes and not 32 of 16 (which took 7000 cycles an item).
       // 32 columns of the row, weighed and joined.
       float o[32];
       auto columns = [&](int c) {
