@@ -13,6 +13,7 @@
 
 #include "../../include/vt_paged_attn.h"
 #include "host_state.cuh"
+#include "packed.cuh"
 
 namespace vt {
 namespace {
@@ -337,32 +338,73 @@ __device__ __forceinline__ Token look_up(const RopeArgs& a, int t, int lane, int
   return token_of(a, t, b);
 }
 
-// x / rms(x) * weight of a head's row of 16 U elements, 16 of them in each of
-// its U lanes: 8 at off0 and 8 at off1.
-template <int U>
-__device__ __forceinline__ void norm16(float (&x0)[8], float (&x1)[8], const float* weight, int off0, int off1,
-                                       float eps, unsigned lanes) {
-  float sum = 0.f;
+// Norm and rotation of 16 elements of a head's row, of which a lane has 8 pairs:
+// with s = 1 / rms(x) (over the U lanes that share the row), weights w and an
+// angle's (c, n) = (cos, sin),
+//   y_a = s (x_a (c w_a) - x_b (n w_b)),   y_b = s (x_b (c w_b) + x_a (n w_a)).
+// The products of weights and angles are those of a token and of all heads with
+// the same weights; they are formed once for them.
+struct NormTurn {
+  float2 own[8];    // c w of elements 2 i, 2 i + 1 (x0's, then x1's)
+  float2 other[8];  // what their partners are multiplied by, with its sign
+
+  // Half layout: x0[e] turns with x1[e]; interleaved: neighbours turn with each other.
+  template <bool INTER>
+  __device__ __forceinline__ void form(const float* weight, int off0, int off1, const float2 (&cs)[8]) {
+    float w[16];
+    load8(weight + off0, *reinterpret_cast<float(*)[8]>(w));
+    load8(weight + off1, *reinterpret_cast<float(*)[8]>(w + 8));
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sum += x0[e] * x0[e] + x1[e] * x1[e];
-#pragma unroll
-  for (int d = 1; d < U; d <<= 1) sum += __shfl_xor_sync(lanes, sum, d);
-  const float inv = rsqrtf(sum * (1.f / (16 * U)) + eps);
-  float w0[8], w1[8];
-  load8(weight + off0, w0);
-  load8(weight + off1, w1);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x0[e] *= inv * w0[e];
-    x1[e] *= inv * w1[e];
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (INTER) {
+        own[i] = make_float2(w[2 * i] * cs[i].x, w[2 * i + 1] * cs[i].x);
+        other[i] = make_float2(-w[2 * i + 1] * cs[i].y, w[2 * i] * cs[i].y);
+      } else {
+        const int e = 2 * (i & 3), p = i < 4 ? 8 : 0;  // partners: the other half's elements
+        own[i] = make_float2(w[2 * i] * cs[e].x, w[2 * i + 1] * cs[e + 1].x);
+        other[i] = make_float2(w[p + e] * cs[e].y, w[p + e + 1] * cs[e + 1].y);
+        if (i < 4) other[i] = make_float2(-other[i].x, -other[i].y);
+      }
+    }
   }
-}
+  // A lane whose elements are not turned: own alone.
+  __device__ __forceinline__ void form(const float* weight, int off0, int off1) {
+    float w[16];
+    load8(weight + off0, *reinterpret_cast<float(*)[8]>(w));
+    load8(weight + off1, *reinterpret_cast<float(*)[8]>(w + 8));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) own[i] = make_float2(w[2 * i], w[2 * i + 1]);
+  }
+  template <bool INTER, int U>
+  __device__ __forceinline__ void apply(const float2 (&x)[8], float2 (&y)[8], bool turns, float eps,
+                                        unsigned lanes) const {
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i & 1] = fma2(x[i], x[i], sum[i & 1]);
+    const float2 both = add2(sum[0], sum[1]);
+    float total = both.x + both.y;
+#pragma unroll
+    for (int d = 1; d < U; d <<= 1) total += __shfl_xor_sync(lanes, total, d);
+    const float inv = rsqrtf(total * (1.f / (16 * U)) + eps);
+    const float2 inv2 = make_float2(inv, inv);
+    if (turns) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 partner = INTER ? make_float2(x[i].y, x[i].x) : x[i ^ 4];
+        y[i] = mul2(inv2, fma2(partner, other[i], mul2(x[i], own[i])));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = mul2(inv2, mul2(x[i], own[i]));
+    }
+  }
+};
 
 // U lanes to a head's row of 16 U elements (U = 4 to 32, a power of two), 16 |
 // rot_dim.  The work is units of `unit` rounds of R heads, nb of them a token;
 // a warp takes consecutive ones, `per` or (the first `extra` warps) per + 1.
 template <typename T, typename KV, bool APPEND, bool INTER, int U, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads) rope_warp_kernel(const RopeArgs a, int nb, int unit, int warps, long long per, int extra) {
+__global__ void __launch_bounds__(kRopeThreads, NORM ? 2 : 1) rope_warp_kernel(const RopeArgs a, int nb, int unit, int warps, long long per, int extra) {
   constexpr int R = 32 / U;                // heads of a round
   constexpr int NP = U >= 4 ? U / 4 : 1;   // pairs a lane forms: pairs NP lane ..
   constexpr int P = sizeof(T) == 2 ? 4 : 2;  // rounds in flight
@@ -429,32 +471,59 @@ __global__ void __launch_bounds__(kRopeThreads) rope_warp_kernel(const RopeArgs 
     float2 mine[NP], cs[8];
 #pragma unroll
     for (int i = 0; i < NP; ++i) mine[i] = cos_sin(frac[i], k.position, a.amplitude);
+    auto angles = [&] {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int from = (8 * u + e) / NP;
-      cs[e].x = __shfl_sync(0xffffffffu, mine[e % NP].x, from);
-      cs[e].y = __shfl_sync(0xffffffffu, mine[e % NP].y, from);
-    }
+      for (int e = 0; e < 8; ++e) {
+        const int from = (8 * u + e) / NP;
+        cs[e].x = __shfl_sync(0xffffffffu, mine[e % NP].x, from);
+        cs[e].y = __shfl_sync(0xffffffffu, mine[e % NP].y, from);
+      }
+    };
+    if constexpr (!NORM) angles();
+    NormTurn turn;
+    const float* held = nullptr;  // whose weights the turn is made of
 #pragma unroll 1
     for (int h0 = first; h0 < last; h0 += P * R) {
       if (h0 != first) fetch(t, h0);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         const int head = h0 + i * R + r;
+        const bool is_v = APPEND && head >= a.q_heads + a.kv_heads;
+        if constexpr (NORM) {
+          const float* weight = held;
+          if (head < last && !is_v)
+            weight = !APPEND || head < a.q_heads ? a.q_weight + head * a.q_weight_stride
+                                                 : a.k_weight + (head - a.q_heads) * a.k_weight_stride;
+          if (__any_sync(0xffffffffu, weight != held)) {
+            angles();  // (the whole warp's; they are not kept beside the turn)
+            if (weight) {
+              if (turns)
+                turn.form<INTER>(weight, off0, off1, cs);
+              else
+                turn.form(weight, off0, off1);
+            }
+            held = weight;
+          }
+        }
         if (head >= last) continue;
         float x0[8], x1[8], y0[8], y1[8];
         load8(reinterpret_cast<const T*>(&raw[i].v[0]), x0);
         load8(reinterpret_cast<const T*>(&raw[i].v[sizeof(T) / 2]), x1);
-        const bool is_v = APPEND && head >= a.q_heads + a.kv_heads;
-        if constexpr (NORM) {
-          if (!is_v) {
-            const float* weight = !APPEND || head < a.q_heads ? a.q_weight + head * a.q_weight_stride
-                                                              : a.k_weight + (head - a.q_heads) * a.k_weight_stride;
-            // (the head's lanes: others of the warp may be past the last head)
-            norm16<U>(x0, x1, weight, off0, off1, a.eps, U == 32 ? ~0u : ((1u << (U & 31)) - 1u) << (r * U));
+        if (NORM && !is_v) {
+          float2 x[8], y[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = make_float2(x0[2 * e], x0[2 * e + 1]);
+            x[4 + e] = make_float2(x1[2 * e], x1[2 * e + 1]);
           }
-        }
-        if (turns && !is_v) {
+          // (the head's lanes: others of the warp may be past the last head)
+          turn.apply<INTER, U>(x, y, turns, a.eps, U == 32 ? ~0u : ((1u << (U & 31)) - 1u) << (r * U));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y0[2 * e] = y[e].x, y0[2 * e + 1] = y[e].y;
+            y1[2 * e] = y[4 + e].x, y1[2 * e + 1] = y[4 + e].y;
+          }
+        } else if (turns && !is_v) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             if constexpr (INTER) {  // pairs (2e, 2e + 1) of the 16 elements
