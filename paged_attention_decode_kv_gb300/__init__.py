@@ -839,11 +839,12 @@ def _weight(torch, name, weight, H, D, index):
     """(pointer, stride from head to head) of the norm's weights, [D] or [H][D]."""
     if weight is None:
         raise ValueError(f"{name} must be given")
-    _check_plain(name, weight, torch.float32, index)
     shape = weight.shape
-    if len(shape) == 1 and shape[0] == D:
+    if not (weight.dtype is torch.float32 and weight.get_device() == index and weight.is_contiguous()):
+        _check_plain(name, weight, torch.float32, index)
+    if shape == (D,):
         return weight.data_ptr(), 0
-    if len(shape) == 2 and shape[0] == H and shape[1] == D:
+    if shape == (H, D):
         return weight.data_ptr(), D
     raise ValueError(f"{name} must be [{D}] or [{H}][{D}], got {tuple(shape)}")
 
@@ -1032,16 +1033,23 @@ def tree_masks(parents, q_starts, context_lens, words=None, masks=None, position
     elif words is not None and masks.shape[-1] != words:
         raise ValueError("masks must be [tokens][words]")
     words = _check_masks(torch, masks, T, index)
-    if positions is None:
-        positions = torch.empty((T,), dtype=int32, device=parents.device) if stream is None else \
-            _empty_on(torch, (T,), int32, index, stream)
-    _check_plain("positions", positions, int32, index)
-    if positions.shape != (T,):
-        raise ValueError("positions must be [tokens]")
+    positions = _int32_out(torch, "positions", positions, T, index, stream)
     _launch(torch, index, stream, "vt_tree_masks", library().vt_tree_masks,
             (masks.data_ptr(), positions.data_ptr(), parents.data_ptr(), q_starts.data_ptr(),
              context_lens.data_ptr(), context_lens.numel(), T, words), ())
     return masks, positions
+
+
+def _int32_out(torch, name, t, n, index, stream):
+    """An int32 result [n], allocated unless given."""
+    if t is None:
+        return torch.empty((n,), dtype=torch.int32, device=index) if stream is None else \
+            _empty_on(torch, (n,), torch.int32, index, stream)
+    if not (t.dtype is torch.int32 and t.get_device() == index and t.is_contiguous()):
+        _check_plain(name, t, torch.int32, index)
+    if t.numel() != n:
+        raise ValueError(f"{name} must be [{n}]")
+    return t
 
 
 def step_tables(context_lens, new_lens, block_tables, free_pages, counters, num_tokens: int, keep_lens=None,
@@ -1061,11 +1069,17 @@ def step_tables(context_lens, new_lens, block_tables, free_pages, counters, num_
     torch = _t()
     index = _cuda_index("context_lens", context_lens)
     int32 = torch.int32
-    for name, t in (("context_lens", context_lens), ("new_lens", new_lens), ("block_tables", block_tables),
-                    ("free_pages", free_pages), ("counters", counters)):
-        _check_plain(name, t, int32, index)
-    B = context_lens.numel()
-    if new_lens.numel() != B or block_tables.dim() != 2 or block_tables.shape[0] != B or counters.numel() != 2:
+    # (in line what _check_plain says of each)
+    if not (new_lens.get_device() == block_tables.get_device() == free_pages.get_device() == counters.get_device()
+            == index and context_lens.dtype is int32 and new_lens.dtype is int32 and block_tables.dtype is int32
+            and free_pages.dtype is int32 and counters.dtype is int32 and context_lens.is_contiguous()
+            and new_lens.is_contiguous() and block_tables.is_contiguous() and free_pages.is_contiguous()
+            and counters.is_contiguous()):
+        for name, t in (("context_lens", context_lens), ("new_lens", new_lens), ("block_tables", block_tables),
+                        ("free_pages", free_pages), ("counters", counters)):
+            _check_plain(name, t, int32, index)
+    B, table = context_lens.numel(), block_tables.shape
+    if new_lens.numel() != B or len(table) != 2 or table[0] != B or counters.numel() != 2:
         raise ValueError("new_lens must be [num_seqs], block_tables [num_seqs][max_blocks] and counters [2]")
     keep = None
     if keep_lens is not None:
@@ -1073,22 +1087,14 @@ def step_tables(context_lens, new_lens, block_tables, free_pages, counters, num_
         if keep_lens.numel() != B:
             raise ValueError("keep_lens must be [num_seqs]")
         keep = keep_lens.data_ptr()
-    out = []
-    for name, t, n in (("q_starts", q_starts, B + 1), ("positions", positions, num_tokens),
-                       ("slots", slots, num_tokens)):
-        if t is None:
-            t = torch.empty((n,), dtype=int32, device=context_lens.device) if stream is None else \
-                _empty_on(torch, (n,), int32, index, stream)
-        else:
-            _check_plain(name, t, int32, index)
-            if t.numel() != n:
-                raise ValueError(f"{name} must be [{n}]")
-        out.append(t)
+    q_starts = _int32_out(torch, "q_starts", q_starts, B + 1, index, stream)
+    positions = _int32_out(torch, "positions", positions, num_tokens, index, stream)
+    slots = _int32_out(torch, "slots", slots, num_tokens, index, stream)
     _launch(torch, index, stream, "vt_paged_step_tables", library().vt_paged_step_tables,
             (block_tables.data_ptr(), context_lens.data_ptr(), free_pages.data_ptr(), counters.data_ptr(),
-             out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), keep, new_lens.data_ptr(), B, num_tokens,
-             BLOCK_SIZE), (block_tables.shape[1], free_pages.numel()))
-    return tuple(out)
+             q_starts.data_ptr(), positions.data_ptr(), slots.data_ptr(), keep, new_lens.data_ptr(), B, num_tokens,
+             BLOCK_SIZE), (table[1], free_pages.numel()))
+    return q_starts, positions, slots
 
 
 def keep_path(accepted, masks, k_cache, v_cache, q_starts, block_tables, context_lens, kept_lens=None, stream=None):
@@ -1115,27 +1121,30 @@ def keep_path(accepted, masks, k_cache, v_cache, q_starts, block_tables, context
     if len(shape) not in (4, 5) or v_cache.shape != shape:
         raise ValueError("k_cache/v_cache must be [num_blocks][32][Hkv][head_dim], or layers of it")
     layers = shape[0] if len(shape) == 5 else 1
-    strides = []
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check_plain(name, t[0] if len(shape) == 5 and layers else t, kv, index)
-        strides.append(t.stride(0) if layers > 1 else 0)
-    for name, t in (("accepted", accepted), ("q_starts", q_starts), ("block_tables", block_tables),
-                    ("context_lens", context_lens)):
-        _check_plain(name, t, int32, index)
-    B = context_lens.numel()
-    if accepted.numel() != B or q_starts.numel() != B + 1 or block_tables.dim() != 2 or block_tables.shape[0] != B:
+    strides = (0, 0)
+    if len(shape) == 5 and layers:
+        _check_plain("k_cache", k_cache[0], kv, index)
+        _check_plain("v_cache", v_cache[0], kv, index)
+        if layers > 1:
+            strides = (k_cache.stride(0), v_cache.stride(0))
+    else:
+        _check_plain("k_cache", k_cache, kv, index)
+        _check_plain("v_cache", v_cache, kv, index)
+    if not (q_starts.get_device() == block_tables.get_device() == context_lens.get_device() == index
+            and accepted.dtype is int32 and q_starts.dtype is int32 and block_tables.dtype is int32
+            and context_lens.dtype is int32 and accepted.is_contiguous() and q_starts.is_contiguous()
+            and block_tables.is_contiguous() and context_lens.is_contiguous()):
+        for name, t in (("accepted", accepted), ("q_starts", q_starts), ("block_tables", block_tables),
+                        ("context_lens", context_lens)):
+            _check_plain(name, t, int32, index)
+    B, table = context_lens.numel(), block_tables.shape
+    if accepted.numel() != B or q_starts.numel() != B + 1 or len(table) != 2 or table[0] != B:
         raise ValueError("accepted must be [num_seqs], q_starts [num_seqs + 1] and block_tables "
                          "[num_seqs][max_blocks]")
     words = _check_masks(torch, masks, masks.shape[0], index)
-    if kept_lens is None:
-        kept_lens = torch.empty((B,), dtype=int32, device=accepted.device) if stream is None else \
-            _empty_on(torch, (B,), int32, index, stream)
-    else:
-        _check_plain("kept_lens", kept_lens, int32, index)
-        if kept_lens.numel() != B:
-            raise ValueError("kept_lens must be [num_seqs]")
+    kept_lens = _int32_out(torch, "kept_lens", kept_lens, B, index, stream)
     _launch(torch, index, stream, "vt_paged_kv_keep_path", library().vt_paged_kv_keep_path,
             (k_cache.data_ptr(), v_cache.data_ptr(), kept_lens.data_ptr(), accepted.data_ptr(), masks.data_ptr(),
              q_starts.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), B, masks.shape[0], words, layers,
-             shape[-2], shape[-1], shape[-3], strides[0], strides[1]), (block_tables.shape[1], shape[-4], code))
+             shape[-2], shape[-1], shape[-3], strides[0], strides[1]), (table[1], shape[-4], code))
     return kept_lens
