@@ -1123,10 +1123,13 @@ def keep_path(accepted, masks, k_cache, v_cache, q_starts, block_tables, context
     layers = shape[0] if len(shape) == 5 else 1
     strides = (0, 0)
     if len(shape) == 5 and layers:
-        _check_plain("k_cache", k_cache[0], kv, index)
-        _check_plain("v_cache", v_cache[0], kv, index)
-        if layers > 1:
-            strides = (k_cache.stride(0), v_cache.stride(0))
+        inner = (shape[2] * shape[3] * shape[4], shape[3] * shape[4], shape[4], 1)
+        strides = k_cache.stride(), v_cache.stride()
+        if not (k_cache.get_device() == v_cache.get_device() == index and v_cache.dtype is kv
+                and strides[0][1:] == inner and strides[1][1:] == inner):
+            _check_plain("k_cache", k_cache[0], kv, index)  # (a view of one layer takes 3 us)
+            _check_plain("v_cache", v_cache[0], kv, index)
+        strides = (strides[0][0], strides[1][0]) if layers > 1 else (0, 0)
     else:
         _check_plain("k_cache", k_cache, kv, index)
         _check_plain("v_cache", v_cache, kv, index)

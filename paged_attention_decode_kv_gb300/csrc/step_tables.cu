@@ -28,6 +28,7 @@ constexpr int kPage = 32;
 constexpr int kThreads = 1024;
 constexpr int kCtas = 8;           // of the cluster
 constexpr int kMaxSeqs = 16384;    // 12 bytes of shared memory each
+constexpr int kRowsAhead = 4;      // rows whose searches and loads a thread has under way
 
 struct TablesArgs {
   int* block_tables;
@@ -134,16 +135,17 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(const TablesArgs 
   }
   const int on_stack = max(0, min(a.counters[0], cap));
 
-  // pages given back in all: they lie on top of the stack
-  Sums total{0, 0, 0};
-  for (int b0 = 0; b0 < B; b0 += kThreads) {
+  // pages given back in all: they lie on top of the stack (with one sequence a
+  // thread the sums below say it at once)
+  long long given = 0;
+  for (int b0 = 0; b0 < B && B > kThreads; b0 += kThreads) {
     const Ask q = ask_of(a, b0 + tid);
     Sums sum;
     block_scan(Sums{q.have - q.kept, 0, 0}, of_warp, sum);
-    total = total + sum;
+    given += sum.given;
   }
-  const long long top = on_stack + total.given;                // of the stack with them
-  const int avail = static_cast<int>(top < cap ? top : cap);   // (more than the pool has: such pages are not kept)
+  long long top = on_stack + given;  // of the stack with them
+  int avail = on_stack;              // pages to take
 
   Sums before{0, 0, 0};
   for (int b0 = 0; b0 < B; b0 += kThreads) {
@@ -153,6 +155,8 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(const TablesArgs 
     const Sums mine{q.have - q.kept, q.need, q.rows};
     const Sums end = before + block_scan(mine, of_warp, sum);
     before = before + sum;
+    if (B <= kThreads) top = on_stack + sum.given;
+    avail = static_cast<int>(top < cap ? top : cap);  // (more than the pool has: such pages are not kept)
     const long long big = 0x7fffffff;
     if (b < B) {
       row_start[b] = static_cast<int>(min(big, end.rows - q.rows));
@@ -189,26 +193,35 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(const TablesArgs 
     a.q_starts[b] = row_start[min(b, out)];
     if (b < B) a.context_lens[b] = keep[b] + (b < out ? row_start[b + 1] - row_start[b] : 0);
   }
-  for (int i = thread; i < rows; i += threads) {
-    int lo = 0, hi = out;  // row_start[lo] <= i, row_start[hi] > i
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (row_start[mid] <= i)
-        lo = mid;
-      else
-        hi = mid;
+  int first_step = 1;  // of a search: the power of two below out
+  while (2 * first_step < out) first_step *= 2;
+#pragma unroll 1
+  for (int i0 = thread; i0 < rows; i0 += kRowsAhead * threads) {
+    int lo[kRowsAhead] = {}, page[kRowsAhead], pos[kRowsAhead];
+#pragma unroll 1
+    for (int d = first_step; d > 0; d >>= 1)  // the last sequence whose rows begin at or before i
+#pragma unroll
+      for (int u = 0; u < kRowsAhead; ++u)
+        if (lo[u] + d < out && row_start[lo[u] + d] <= i0 + u * threads) lo[u] += d;
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u) {
+      const int i = i0 + u * threads;
+      if (i >= rows) continue;
+      const int k = keep[lo[u]], kept = pages_of(k);
+      pos[u] = k + (i - row_start[lo[u]]);
+      const int p = pos[u] / kPage;
+      page[u] = p >= kept ? __ldcg(a.free_pages + (avail - 1 - (page_start[lo[u]] + (p - kept))))
+                          : a.block_tables[static_cast<long long>(lo[u]) * a.max_blocks + p];
     }
-    const int k = keep[lo], pos = k + (i - row_start[lo]), p = pos / kPage, kept = pages_of(k);
-    int* const entry = a.block_tables + static_cast<long long>(lo) * a.max_blocks + p;
-    int page;
-    if (p >= kept) {
-      page = __ldcg(a.free_pages + (avail - 1 - (page_start[lo] + (p - kept))));
-      if (pos % kPage == 0) *entry = page;
-    } else {
-      page = *entry;
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u) {
+      const int i = i0 + u * threads;
+      if (i >= rows) continue;
+      // (a position on a page's first slot is behind the tokens kept: a page that was taken)
+      if (pos[u] % kPage == 0) a.block_tables[static_cast<long long>(lo[u]) * a.max_blocks + pos[u] / kPage] = page[u];
+      if (a.positions) a.positions[i] = pos[u];
+      if (a.slots) a.slots[i] = page[u] >= 0 && page[u] < cap ? page[u] * kPage + pos[u] % kPage : -1;
     }
-    if (a.positions) a.positions[i] = pos;
-    if (a.slots) a.slots[i] = page >= 0 && page < cap ? page * kPage + pos % kPage : -1;
   }
   if (thread == 0) {
     const int taken = out < B ? page_start[out] : static_cast<int>(before.need);

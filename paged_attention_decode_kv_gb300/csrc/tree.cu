@@ -54,8 +54,8 @@ struct MasksArgs {
 constexpr int kChunk = 8;  // words of a row that a thread holds
 
 __global__ void tree_masks_kernel(const MasksArgs a) {
-  extern __shared__ unsigned bits[];                              // [words][threads]
-  const int threads = blockDim.x, j = threadIdx.x;
+  extern __shared__ unsigned bits[];  // [words][threads + 1] (a row's words in different banks)
+  const int j = threadIdx.x, threads = blockDim.x + 1;
   int* const up = reinterpret_cast<int*>(bits + a.words * threads);  // [threads]
   const Rows r = rows_of(a.q_starts, a.context_lens, blockIdx.x, a.num_tokens);
   if (r.n == 0 || r.n > 32 * a.words || r.L < r.n) return;
@@ -79,15 +79,16 @@ __global__ void tree_masks_kernel(const MasksArgs a) {
     }
     up[j] = parent = next;
   }
-  if (!live) return;
-  int seen = 0;
-  int* const to = a.masks + static_cast<long long>(r.row0 + j) * a.words;
-  for (int w = 0; w < a.words; ++w) {
-    const unsigned x = bits[w * threads + j];
-    seen += __popc(x);
-    to[w] = static_cast<int>(x);
+  int* const to = a.masks + static_cast<long long>(r.row0) * a.words;
+  for (int i = j; i < r.n * a.words; i += blockDim.x) {
+    const int row = i / a.words, w = i - row * a.words;
+    to[i] = static_cast<int>(bits[w * threads + row]);
   }
-  if (a.positions) a.positions[r.row0 + j] = r.L - r.n + seen - 1;
+  if (live && a.positions) {
+    int seen = 0;
+    for (int w = 0; w < a.words; ++w) seen += __popc(bits[w * threads + j]);
+    a.positions[r.row0 + j] = r.L - r.n + seen - 1;
+  }
 }
 
 // ------------------------------------------------------------------- accepted branches
@@ -122,6 +123,18 @@ __global__ void __launch_bounds__(kKeepThreads) keep_path_kernel(const KeepArgs 
   const int base = r.L - r.n, took = a.accepted[b];
   const bool any = whole && took >= 0 && took < r.n;
   if (tid < 32) {  // the branch, by one warp: a lane a word
+    // the block table from the first new token's page on, 33 pages at most, while the mask is on its way
+    const int* const table = a.block_tables + static_cast<long long>(b) * a.max_blocks;
+    const int page0 = base / kPage, pages = (r.L - 1) / kPage - page0 + 1;
+    int page = -1, page32 = -1;
+    if (any) {
+      if (lane < pages) page = table[page0 + lane];
+      if (pages > 32) page32 = table[page0 + 32];
+    }
+    auto page_of = [&](int token) {
+      const int i = token / kPage - page0, p = __shfl_sync(0xffffffffu, page, i & 31);
+      return i < 32 ? p : page32;
+    };
     unsigned x = 0;
     if (any && lane < a.words) {
       x = static_cast<unsigned>(a.masks[static_cast<long long>(r.row0 + took) * a.words + lane]);
@@ -141,18 +154,15 @@ __global__ void __launch_bounds__(kKeepThreads) keep_path_kernel(const KeepArgs 
     for (; x; x &= x - 1u, ++rank) from[rank] = 32 * lane + __ffs(x) - 1;
     __syncwarp();
     // slots; tokens that are in their place already, and those of pages out of range, stay out
-    const int* const table = a.block_tables + static_cast<long long>(b) * a.max_blocks;
     int at = 0;
     for (int r0 = 0; r0 < all; r0 += 32) {
-      const int i = r0 + lane;
+      const int i = r0 + lane, f = i < all ? from[i] : 0;
+      const int ts = base + f, tt = base + (i < all ? i : 0);
+      const int ps = page_of(ts), pt = page_of(tt);
       int source = -1, target = -1;
-      if (i < all && from[i] != i) {
-        const int ts = base + from[i], tt = base + i;
-        const int ps = table[ts / kPage], pt = table[tt / kPage];
-        if (ps >= 0 && ps < a.num_blocks && pt >= 0 && pt < a.num_blocks) {
-          source = ps * kPage + ts % kPage;
-          target = pt * kPage + tt % kPage;
-        }
+      if (i < all && f != i && ps >= 0 && ps < a.num_blocks && pt >= 0 && pt < a.num_blocks) {
+        source = ps * kPage + ts % kPage;
+        target = pt * kPage + tt % kPage;
       }
       const unsigned moves = __ballot_sync(0xffffffffu, source >= 0);
       if (source >= 0) {
@@ -186,6 +196,8 @@ __global__ void __launch_bounds__(kKeepThreads) keep_path_kernel(const KeepArgs 
 
 using namespace vt::host;
 
+size_t masks_smem(int words) { return sizeof(int) * (32 * static_cast<size_t>(words) + 1) * (words + 1); }
+
 vt_status tree_masks(const MasksArgs& a, int num_seqs, cudaStream_t stream) {
   if (num_seqs < 0 || a.num_tokens < 0) return VT_ERR_INVALID_ARG;
   if (num_seqs == 0 || a.num_tokens == 0) return VT_OK;
@@ -199,7 +211,7 @@ vt_status tree_masks(const MasksArgs& a, int num_seqs, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   const int threads = 32 * a.words;
-  const size_t smem = sizeof(int) * threads * (static_cast<size_t>(a.words) + 1);
+  const size_t smem = masks_smem(a.words);
   if (smem > 48 * 1024) {
     std::lock_guard<std::mutex> lock(g_mutex);
     DeviceState& ds = device_state(dev);
@@ -210,7 +222,7 @@ vt_status tree_masks(const MasksArgs& a, int num_seqs, cudaStream_t stream) {
     for (auto& p : ds.occupancy) known |= p.first == func;
     if (!known) {
       e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(sizeof(int)) * 32 * kMaxWords * (kMaxWords + 1));
+                               static_cast<int>(masks_smem(kMaxWords)));
       if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
       ds.occupancy.emplace_back(func, 1);
     }
