@@ -275,6 +275,9 @@ vt_status prefill(const PrefillCall& c) {
   a.group_mul = (65535 + a.group) / a.group;  // (128 rows x an excess below 128 stay below 2^16)
   a.v_parts = c.head_dim / v.cols;
   a.item_weight = v.item_weight;
+  a.one_tile = v.tensor_cores && v.rows > v.tile_rows ? v.tile_rows / a.group : 0;
+  a.one_weight = v.one_weight;
+  a.one_mul = ~0ull / static_cast<unsigned>(v.one_weight) + 1;
   const bool set = g_override_min_units > 0;
   a.min_weight = kPfBlock * (set ? std::min(g_override_min_units, 1 << 20) : 1);
   const long long items = (static_cast<long long>(c.num_tokens) / a.tile_tokens + c.num_seqs) * c.num_kv_heads * a.v_parts;

@@ -53,6 +53,10 @@ struct PrefillArgs {
   int group_mul;     // r / group = r * group_mul >> 16 for 0 <= r <= 128
   int v_parts;       // items that share a (kv head, tile), each with a part of V's columns
   int item_weight;   // an item's fixed cost in tokens
+  // Trees: new tokens up to which an item is one tile's.  A block of such an item weighs one_weight, where one of
+  // two tiles weighs kPfBlock; x / one_weight is the high word of x * one_mul.
+  int one_tile, one_weight;
+  unsigned long long one_mul;
   int min_weight;    // least share of a CTA, whole kPfBlocks (every cut of an item then takes a block)
   long long long_total;  // total weight above which it doubles
   // Partials: record s (2 for each CTA: 2c an item's head piece, 2c + 1 a later piece) holds `rows` rows of
@@ -110,7 +114,12 @@ __device__ __forceinline__ long long pf_weight(const PrefillArgs& a, const PfSeq
   const int T = a.tile_tokens;
   if (K <= 0) return 0;
   if (s.bad) return pf_mul(K, a.item_weight);
-  if (TREE) return pf_mul(K, s.p0 + s.n - (a.window > 0 ? max(0, s.p0 - a.window) : 0)) + pf_mul(K, a.item_weight);
+  if (TREE) {
+    const int span = s.p0 + s.n - (a.window > 0 ? max(0, s.p0 - a.window) : 0);
+    long long w = pf_mul(K, span) + pf_mul(K, a.item_weight);
+    if (K == s.tiles && s.n - (K - 1) * T <= a.one_tile) w -= span - (pf_mul(span, a.one_weight) >> 7);
+    return w;
+  }
   long long w = ((pf_mul(K, K) + K) >> 1) * T + pf_mul(K, s.p0) + pf_mul(K, a.item_weight);
   if (K == s.tiles) w -= pf_mul(T, K) - s.n;
   if (a.window > 0) {
@@ -154,9 +163,13 @@ struct PfWalk {
   __device__ __forceinline__ long long share(unsigned c) const { return c >= static_cast<unsigned>(ctas) ? total : quot * c; }
 
   // kb(r): block boundary nearest to weight r of an item.
-  __device__ __forceinline__ static int cut(const PrefillArgs& a, long long r, long long W, int nkv) {
+  __device__ __forceinline__ static int cut(const PrefillArgs& a, long long r, long long W, int nkv, int ntok) {
     if (r >= W) return nkv;
-    const long long k = (r - a.item_weight + kPfBlock / 2) >> 7;
+    long long k = (r - a.item_weight + kPfBlock / 2) >> 7;
+    if (TREE && ntok <= a.one_tile) {
+      const long long x = r - a.item_weight + (a.one_weight >> 1);
+      k = x < 0 ? 0 : static_cast<long long>(__umul64hi(static_cast<unsigned long long>(x), a.one_mul));
+    }
     return k < 0 ? 0 : (k > nkv ? nkv : static_cast<int>(k));
   }
 
@@ -197,15 +210,15 @@ struct PfWalk {
       it.pieces = 0;
       const long long ra = x - item_x, rb = end - item_x;
       const bool whole_end = rb >= W;
-      it.kb0 = ra <= 0 ? 0 : cut(a, ra, W, it.nkv);
-      it.kb1 = whole_end ? it.nkv : cut(a, rb, W, it.nkv);
+      it.kb0 = ra <= 0 ? 0 : cut(a, ra, W, it.nkv, it.ntok);
+      it.kb1 = whole_end ? it.nkv : cut(a, rb, W, it.nkv, it.ntok);
       if (it.kb0 == 0 && it.kb1 < it.nkv && it.kb1 > 0) {
         // the head piece of a split item: count the cuts inside it
         it.pieces = 1;
 #pragma unroll 1
         for (unsigned c = cta + 1;; ++c) {
           const long long e = share(c) - item_x;
-          if ((e >= W ? it.nkv : cut(a, e, W, it.nkv)) >= it.nkv) break;
+          if ((e >= W ? it.nkv : cut(a, e, W, it.nkv, it.ntok)) >= it.nkv) break;
           ++it.pieces;
         }
       }

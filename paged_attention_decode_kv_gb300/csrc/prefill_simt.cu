@@ -315,7 +315,7 @@ struct SimtVariant {
     return cudaGetLastError();
   }
   static PrefillVariant info() {
-    return PrefillVariant{kSimtThreads<D>, kSimtRows, kSimtRows, D, 0, 1, 128, sizeof(SimtSmem<D>),
+    return PrefillVariant{kSimtThreads<D>, kSimtRows, kSimtRows, D, 0, 1, 128, kPfBlock, sizeof(SimtSmem<D>),
                           reinterpret_cast<const void*>(&prefill_simt_kernel<D, TREE>), &launch};
   }
 };

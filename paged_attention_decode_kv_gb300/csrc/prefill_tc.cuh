@@ -130,6 +130,18 @@ struct TcSmem {
 template <bool FP8>
 constexpr int kItemWeight = FP8 ? 384 : 192;
 
+// A tree's items.  Its rows are few, so that what an item costs beside its
+// blocks weighs more, and the blocks of an item of one tile, which the tiles
+// take in turn, cost less than those that both tiles take: 64 trees of 24 to 64
+// tokens (32 q / 8 kv heads of 128) over contexts to 8000 take 227 us with 384
+// and 104, 239 with 192 and 128, 278 with 384 and 72; of 8 to 60 tokens 155 us
+// at head_dim 64 with 384 and 72, 185 with 384 and 128, and over codes 199 with
+// 640 and 76, 250 with 384 and 128.
+template <typename C>
+constexpr int kTreeItemWeight = C::kFp8 ? 640 : C::kNT == 2 ? 384 : 192;
+template <typename C>
+constexpr int kTreeOneWeight = C::kFp8 ? 76 : C::kD == 64 ? 72 : 104;
+
 // Weights are 2^(score - m) with m at most kLazy below the largest score.
 constexpr float kLazy = 8.f;
 
@@ -1557,7 +1569,8 @@ struct TcVariant {
     return cudaGetLastError();
   }
   static PrefillVariant info() {
-    return PrefillVariant{C::kThreads, C::kNT * 128, 128, C::kDV, 1, C::kStagesK + C::kStagesV, kItemWeight<C::kFp8>, smem,
+    return PrefillVariant{C::kThreads, C::kNT * 128, 128, C::kDV, 1, C::kStagesK + C::kStagesV,
+                          C::kTree ? kTreeItemWeight<C> : kItemWeight<C::kFp8>, kTreeOneWeight<C>, smem,
                           reinterpret_cast<const void*>(&prefill_tc_kernel<C>), &launch};
   }
 };

@@ -16,6 +16,7 @@ struct PrefillVariant {
   int tensor_cores;
   int stages;
   int item_weight;  // an item's fixed cost in tokens (PrefillArgs)
+  int one_weight;   // of a block of a one-tile item of a tree
   size_t smem_bytes;
   const void* func;
   cudaError_t (*launch)(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PrefillArgs& a,

@@ -25,7 +25,7 @@ namespace vt {
 namespace {
 
 constexpr int kPage = 32;
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
 constexpr int kCtas = 8;           // of the cluster
 constexpr int kMaxSeqs = 16384;    // 12 bytes of shared memory each
 constexpr int kRowsAhead = 4;      // rows whose searches and loads a thread has under way
@@ -102,13 +102,13 @@ __device__ __forceinline__ Sums block_scan(Sums x, Sums (&of_warp)[kThreads / 32
   if (lane == 31) of_warp[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    Sums y = of_warp[lane];
+    Sums y = lane < kThreads / 32 ? of_warp[lane] : Sums{0, 0, 0};
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const Sums o = shift_up(y, d);
       if (lane >= d) y = y + o;
     }
-    of_warp[lane] = y;
+    if (lane < kThreads / 32) of_warp[lane] = y;
   }
   __syncthreads();
   total = of_warp[kThreads / 32 - 1];
