@@ -1519,9 +1519,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   const uint32_t tmem = s.tmem;
   // A softmax thread holds a row of 128 scores; with two tiles registers move
   // to it from the other warpgroups (512 x 128 = 128 x (96 + 96) + 256 x 160;
-  // with widening 640 x 96 >= 128 x 3 x 72 + 256 x 128).
+  // with widening 640 x 96 >= 128 x 3 x 72 + 256 x 128, and for trees 128 x 3 x 64 + 256 x 144: 149 -> 147 us).
   constexpr bool kMove = NT == 2;
-  constexpr int kFew = C::kFp8 ? 72 : 96, kMany = C::kFp8 ? 128 : 160;
+  constexpr int kFew = C::kFp8 ? (C::kTree ? 64 : 72) : 96, kMany = C::kFp8 ? (C::kTree ? 144 : 128) : 160;
   if (warp >= kWiden) {
     if constexpr (kMove) regs_dec<kFew>();
     if constexpr (C::kFp8) tc_widen<C>(a, s, tid - kWiden * 32);
