@@ -660,3 +660,151 @@ def check_row(out, q, token_rows, kw, inv, dtype, scales, window):
         # the score, shows as a part of the weights no larger than this)
         slack = {"f32": 2.0 ** -14, "bf16": 2.0 ** -6, "e4m3": 2.0 ** -4}[dtype]
         assert ((out[h].double() - p @ v[:, h // group]).abs() <= slack * (reach + reach.mean())).all()
+
+
+# ------------------------------------------------------------------- what calls meet
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 256), ("f32", 64), ("e4m3", 128)])
+@pytest.mark.parametrize("window", [7, 40])
+def test_windows_pass_over_what_is_not_finite(dev, dtype, D, window):
+    """NaN before a row's window, drafted or not, is not its."""
+    new, ctx = [20, 20], [300, 45]
+    batch = make_batch(new, ctx, 8, 2, D, dtype, seed=21)
+    rows = [[list(range(j + 1)) for j in range(n)] for n in new]
+    spots = [(0, ctx[0] - new[0] - window + 2), (1, ctx[1] - new[1] + 1)]  # seen by a chain's first rows only
+    for b, t in spots:
+        batch.v_cache[int(batch.block_tables[b, t // PAGE]), t % PAGE, 1, 5] = 0x7f if dtype == "e4m3" else float("nan")
+    for grid in (0, 3):
+        got = run(batch, pack(rows, 1, 40), window=window, grid=grid, blocks=1 if grid else 0)
+        torch.cuda.synchronize()
+        for b, t in spots:
+            base = ctx[b] - new[b]
+            for j in range(new[b]):
+                seen = (list(range(base)) + [base + i for i in range(j + 1)])[-window:]
+                bad = torch.isnan(got[b * 20 + j])
+                assert bool(bad[4:, 5].all()) == (t in seen), (b, j)
+                bad[4:, 5] = False
+                assert not bad.any()
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f32", 64)])
+def test_starts_and_contexts_that_are_none(dev, dtype, D):
+    """Row starts that decrease, are below 0 or pass the rows are sequences without rows; contexts past the table NaN."""
+    batch = make_batch([4, 5, 6], [40, 70, 64], 8, 2, D, dtype, seed=22, pad=1)
+    rows = [[[j] for j in range(n)] for n in batch.new]
+    masks = pack(rows, 1, 16)
+    out = torch.full_like(batch.q, 3.0)
+    for starts in ([0, 4, 9, 40], [-5, 4, 9, 15], [0, 9, 4, 15], [15, 9, 4, 0]):
+        q_starts = torch.tensor(starts, **I32)
+        vt.prefill_tree(batch.q, batch.k_cache, batch.v_cache, masks, q_starts, batch.block_tables,
+                        batch.context_lens, out=out)
+        kept = vt.keep_path(torch.zeros(3, **I32), masks, batch.k_cache.clone(), batch.v_cache.clone(), q_starts,
+                            batch.block_tables, batch.context_lens)
+        assert [k for k, s, e in zip(kept.tolist(), starts, starts[1:]) if not (0 <= s < e <= 16)] == \
+            [L for L, s, e in zip(batch.ctx, starts, starts[1:]) if not (0 <= s < e <= 16)]
+    assert vt.vt_paged_attn_device_status() == 0
+    lens = torch.tensor([40, 10 ** 9, -3], **I32)
+    got = vt.prefill_tree(batch.q, batch.k_cache, batch.v_cache, masks, batch.q_starts, batch.block_tables, lens)
+    assert torch.isfinite(got[:4]).all() and torch.isnan(got[4:15]).all()
+    kept = vt.keep_path(torch.zeros(3, **I32), masks, batch.k_cache.clone(), batch.v_cache.clone(), batch.q_starts,
+                        batch.block_tables, lens)
+    assert kept.tolist() == [37, 10 ** 9, -3]
+
+
+def test_batches_without_rows(dev):
+    batch = make_batch([0, 0], [40, 33], 4, 2, 64, "bf16")
+    masks = torch.zeros((0, 2), **I32)
+    assert run(batch, masks).shape == (0, 4, 64)
+    k, v = batch.k_cache.clone(), batch.v_cache.clone()
+    kept = vt.keep_path(torch.tensor([0, -1], **I32), masks, k, v, batch.q_starts, batch.block_tables,
+                        batch.context_lens)
+    assert kept.tolist() == [40, 33] and torch.equal(k.view(torch.int16), batch.k_cache.view(torch.int16))
+    empty = torch.zeros(0, **I32)
+    kept = vt.keep_path(empty, masks, k, v, torch.zeros(1, **I32), torch.zeros((0, 3), **I32), empty)
+    assert kept.shape == (0,)
+
+
+def test_calls_at_once_on_two_streams(dev):
+    """Operators without a workspace run side by side."""
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    new, ctx = [30, 64, 5], [500, 900, 64]
+    states = []
+    for i in range(2):
+        batch = make_batch(new, ctx, 2, 2, 128, "bf16", seed=30 + i)
+        parents = [random_parents(n, 5, random.Random(i)) for n in new]
+        flat = torch.tensor([p for seq in parents for p in seq], **I32)
+        states.append((batch, parents, flat, torch.zeros((99, 2), **I32), torch.zeros(99, **I32)))
+    torch.cuda.synchronize()
+    kept = []
+    for _ in range(5):
+        for s, (batch, parents, flat, masks, positions) in zip(sides, states):
+            vt.tree_masks(flat, batch.q_starts, batch.context_lens, masks=masks, positions=positions, stream=s)
+    for s, (batch, parents, flat, masks, positions) in zip(sides, states):
+        with torch.cuda.stream(s):
+            k, v, took = batch.k_cache.clone(), batch.v_cache.clone(), torch.tensor([29, 63, 4], **I32)
+            kept.append((k, v, vt.keep_path(took, masks, k, v, batch.q_starts, batch.block_tables, batch.context_lens)))
+    torch.cuda.synchronize()
+    for (batch, parents, flat, masks, positions), (k, v, lens) in zip(states, kept):
+        rows = [[branch(p, j) for j in range(n)] for p, n in zip(parents, new)]
+        assert torch.equal(masks, pack(rows, 2, 99))
+        want, (wk, wv) = kept_by_hand(batch, rows, [29, 63, 4], (batch.k_cache, batch.v_cache))
+        assert lens.tolist() == want
+        assert torch.equal(k.view(torch.int16), wk.view(torch.int16))
+        assert torch.equal(v.view(torch.int16), wv.view(torch.int16))
+
+
+FIRST = """
+import torch, paged_attention_decode_kv_gb300 as vt
+i32 = dict(dtype=torch.int32, device="cuda")
+lens, new = torch.tensor([5, 0], **i32), torch.tensor([3, 40], **i32)
+tables, free, counters = torch.tensor([[4, 0], [0, 0]], **i32), torch.arange(5, **i32), torch.tensor([4, 0], **i32)
+parents, starts = torch.tensor([j - 1 for n in (3, 40) for j in range(n)], **i32), torch.tensor([0, 3, 43], **i32)
+masks = torch.zeros((43, 32), **i32)
+k, v = torch.zeros((2, 5, 32, 2, 64), dtype=torch.bfloat16, device="cuda").unbind()
+x = torch.ones((43, 2, 64), dtype=torch.bfloat16, device="cuda")
+w = torch.ones(64, device="cuda")
+inv, _ = vt.rope_frequencies(64)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    q_starts, positions, slots = vt.step_tables(lens, new, tables, free, counters, 43)
+    vt.tree_masks(parents, q_starts, lens, masks=masks, positions=positions)
+    q = vt.norm_append(x, x, w, k, v, q_starts, tables, lens, q=x, q_weight=w, positions=positions, inv_freq=inv)
+    kept = vt.keep_path(starts[:2], masks, k, v, q_starts, tables, lens)
+    try:
+        vt.prefill_tree(q, k, v, masks, q_starts, tables, lens)
+        raise SystemExit("a first prefill inside a capture allocates")
+    except vt.VtError as e:
+        assert e.status == vt.VT_ERR_SCRATCH_LIMIT, e
+g.replay()
+torch.cuda.synchronize()
+assert lens.tolist() == [8, 40] and q_starts.tolist() == [0, 3, 43], (lens, q_starts)
+assert positions.tolist() == [5, 6, 7, *range(40)]
+assert slots.tolist() == [4 * 32 + 5, 4 * 32 + 6, 4 * 32 + 7] + [3 * 32 + i for i in range(32)] + [2 * 32 + i for i in range(8)]
+assert masks[42, 0].item() == -1 and masks[42, 1].item() == 255
+assert kept.tolist() == [6, 4], kept
+assert torch.isfinite(q).all() and (v[4, 5:8] == 1).all() and (v[3] == 1).all()
+print("fine")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture(dev):
+    """Nothing of the step but the attention allocates, so it can be captured at once; the attention refuses."""
+    import subprocess
+    import sys
+    from pathlib import Path
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=Path(__file__).resolve().parents[1], capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("fine"), r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_many_items_of_both_kinds(dev, dtype, D):
+    """Trees of one tile and of two in one batch, in shares that cut them anywhere."""
+    rng = random.Random(D)
+    new = [rng.randint(1, 64) for _ in range(40)]
+    ctx = [n + rng.randint(0, 700) for n in new]
+    batch = make_batch(new, ctx, 8, 2, D, dtype, seed=D)
+    rows = tree_rows(new, 4, D)
+    masks = pack(rows, 2, sum(new))
+    for grid in (0, 11, 97):
+        check(batch, rows, run(batch, masks, grid=grid, blocks=1 if grid else 0))
