@@ -663,12 +663,15 @@ def _check_scales(torch, k_scale, v_scale, heads, index):
         raise TypeError("k_scale and v_scale must be float32 [num_kv_heads]")
 
 
-def _codes(torch, t):
-    if t.dtype == torch.float8_e4m3fn:
-        t = t.view(torch.uint8)
-    if t.dtype != torch.uint8:
-        raise TypeError("the caches must be uint8 or float8_e4m3fn E4M3 codes")
-    return t
+def _codes(torch, k, v):
+    """Caches of codes, of one type (whose name does not matter: a view takes 3 us)."""
+    dtype = k.dtype
+    if dtype is v.dtype and (dtype is torch.float8_e4m3fn or dtype is torch.uint8):
+        return k, v
+    for t in (k, v):
+        if t.dtype is not torch.float8_e4m3fn and t.dtype is not torch.uint8:
+            raise TypeError("the caches must be uint8 or float8_e4m3fn E4M3 codes")
+    return k.view(torch.uint8), v.view(torch.uint8)
 
 
 def _check_freq(torch, inv_freq, index):
@@ -831,7 +834,7 @@ def append_fp8(k, v, k_codes, v_codes, k_scale, v_scale, q_starts, block_tables,
     """``append`` into an FP8 (E4M3) cache of codes with a scale per kv head
     (rows bf16; codes uint8 or torch.float8_e4m3fn)."""
     torch = _t()
-    return _append(torch, k, v, _codes(torch, k_codes), _codes(torch, v_codes), (k_scale, v_scale), q_starts,
+    return _append(torch, k, v, *_codes(torch, k_codes, v_codes), (k_scale, v_scale), q_starts,
                    block_tables, context_lens, q, q_out, positions, inv_freq, interleaved, amplitude, stream)
 
 
@@ -900,7 +903,7 @@ def norm_append_fp8(k, v, k_weight, k_codes, v_codes, k_scale, v_scale, q_starts
     """``norm_append`` into an FP8 (E4M3) cache of codes with a scale per kv
     head (rows bf16; codes uint8 or torch.float8_e4m3fn)."""
     torch = _t()
-    return _append(torch, k, v, _codes(torch, k_codes), _codes(torch, v_codes), (k_scale, v_scale), q_starts,
+    return _append(torch, k, v, *_codes(torch, k_codes, v_codes), (k_scale, v_scale), q_starts,
                    block_tables, context_lens, q, q_out, positions, inv_freq, interleaved, amplitude, stream,
                    (k_weight, q_weight, eps))
 
@@ -969,7 +972,7 @@ def prefill_fp8(q, k_codes, v_codes, k_scale, v_scale, q_starts, block_tables, c
     """``prefill`` over an FP8 (E4M3) cache (q and out bf16; codes uint8 or
     torch.float8_e4m3fn with a float32 scale per kv head)."""
     torch = _t()
-    return _prefill(torch, q, _codes(torch, k_codes), _codes(torch, v_codes), (k_scale, v_scale), q_starts,
+    return _prefill(torch, q, *_codes(torch, k_codes, v_codes), (k_scale, v_scale), q_starts,
                     block_tables, context_lens, scale, window, out, stream)
 
 
@@ -1000,7 +1003,7 @@ def prefill_tree_fp8(q, k_codes, v_codes, k_scale, v_scale, masks, q_starts, blo
     """``prefill_tree`` over an FP8 (E4M3) cache (q and out bf16; codes uint8 or
     torch.float8_e4m3fn with a float32 scale per kv head)."""
     torch = _t()
-    return _prefill(torch, q, _codes(torch, k_codes), _codes(torch, v_codes), (k_scale, v_scale), q_starts,
+    return _prefill(torch, q, *_codes(torch, k_codes, v_codes), (k_scale, v_scale), q_starts,
                     block_tables, context_lens, scale, window, out, stream, masks)
 
 
@@ -1112,11 +1115,11 @@ def keep_path(accepted, masks, k_cache, v_cache, q_starts, block_tables, context
     index = _cuda_index("accepted", accepted)
     int32 = torch.int32
     if k_cache.dtype is torch.float8_e4m3fn or k_cache.dtype is torch.uint8:
-        k_cache, v_cache = _codes(torch, k_cache), _codes(torch, v_cache)
-        code, kv = VT_E4M3, torch.uint8
+        k_cache, v_cache = _codes(torch, k_cache, v_cache)
+        code = VT_E4M3
     else:
-        kv = k_cache.dtype
-        code = _io_code(torch, kv)
+        code = _io_code(torch, k_cache.dtype)
+    kv = k_cache.dtype
     shape = k_cache.shape
     if len(shape) not in (4, 5) or v_cache.shape != shape:
         raise ValueError("k_cache/v_cache must be [num_blocks][32][Hkv][head_dim], or layers of it")

@@ -663,6 +663,23 @@ def check_row(out, q, token_rows, kw, inv, dtype, scales, window):
 
 
 # ------------------------------------------------------------------- what calls meet
+def test_codes_under_either_name(dev):
+    """E4M3 codes as uint8, as float8_e4m3fn, or one of each."""
+    batch = make_batch([9, 40], [200, 60], 8, 2, 128, "e4m3", seed=20)
+    rows = tree_rows(batch.new, 3, 20)
+    masks = pack(rows, 2, 49)
+    want = run(batch, masks)
+    k8, v8 = batch.k_cache.view(torch.float8_e4m3fn), batch.v_cache.view(torch.float8_e4m3fn)
+    where = (masks, batch.q_starts, batch.block_tables, batch.context_lens)
+    for k, v in ((k8, v8), (k8, batch.v_cache), (batch.k_cache, v8)):
+        assert torch.equal(vt.prefill_tree_fp8(batch.q, k, v, batch.k_scale, batch.v_scale, *where), want)
+        was = batch.k_cache.clone()
+        kept = vt.keep_path(torch.tensor([0, 0], **I32), masks, k, v, *where[1:])
+        assert kept.tolist() == [192, 21] and torch.equal(was, batch.k_cache)
+    with pytest.raises(TypeError):
+        vt.prefill_tree_fp8(batch.q, k8, batch.v_cache.view(torch.int8), batch.k_scale, batch.v_scale, *where)
+
+
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 256), ("f32", 64), ("e4m3", 128)])
 @pytest.mark.parametrize("window", [7, 40])
 def test_windows_pass_over_what_is_not_finite(dev, dtype, D, window):
