@@ -6,10 +6,15 @@
 // (rope_append.cu).  Everything is fp32 and rounded once, to the storage type
 // or the code: between norm and rotation nothing is rounded.
 //
-// What bounds it: as without the norm, every element is read and written once.
-// A row's elements are in its lanes' registers when its sum of squares is
-// formed, so the norm costs log2 of those lanes in shuffles and the weights'
-// loads, which the caches serve.
+// What bounds it: as without the norm, every element is read and written once,
+// and here also issue: a lane's 16 elements cost some 170 instructions.  A row's
+// elements are in its lanes' registers when its sum of squares is formed, so the
+// norm costs log2 of those lanes in shuffles; weights and angles are multiplied
+// once a token for all heads that share the weights, and products are taken two
+// at a time.  Measured: 11583 tokens of 64 + 8 + 8 heads of 128 into E4M3 pages
+// 86 us, 0.77 of the copy rate (91 with weights and angles multiplied in one
+// after the other); 128 tokens of 32 + 8 + 8 5.2 us from a graph.  Fetching a
+// round's successor behind it, across tokens, took 107 us.
 #include "rope_append.cuh"
 
 extern "C" {

@@ -9,7 +9,7 @@
 // 227 us where 8 x 4 took 204: 1263 tokens over contexts of up to 972, 16 q / 8
 // kv heads of 128.)  At that tile the bound is dependent latency, not the loads:
 // two warps a scheduler, the FMA pipe 57 % busy, the load pipe 22 %, and `wait`
-// the first stall; at head_dim 128 its 255 registers spill 76 bytes.  Q, K and V
+// the first stall; at head_dim 128 its 255 registers spill 72 bytes.  Q, K and V
 // come by asynchronous copies; at head_dim 128 P lies over K's tile.  Values are
 // looked at only in tiles that some row sees in part, and only if one is not
 // finite do weights of 0 branch around it: 182 us.

@@ -11,7 +11,10 @@
 // pages put on the stack and pages taken from it, a search for each row's
 // sequence), not its few bytes.  So it is one launch of one cluster: every CTA
 // forms all sums for itself, in shared memory, and the cluster's barrier is all
-// that is waited for.
+// that is waited for.  Measured, calls in a row from a graph: 256 sequences with
+// one new token each 5.0 us, 33 thousand prompt tokens beside 40 sequences that
+// end 7.7 (four CTAs 10.6, CTAs of 256 threads 11.7, one row a thread at a time
+// 9.3; the launch alone takes 2.5).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -7,16 +7,18 @@
 // sequence, a thread a row, and the steps end when no row has an ancestor
 // left (log2 of the deepest branch; following parents one by one costs a
 // branch's length in dependent loads).  A row's position is the context's end
-// plus its ancestors.  What bounds it: those steps' latency; long batches the
-// masks' bytes.
+// plus its ancestors.  What bounds it: those steps' latency, and of many blocks
+// the launch: 64 trees of 24 to 64 tokens 3.3 us from a graph, 256 of 200 to 256
+// (2.3 MB) 5.9, with words stored row by row 6.8.
 //
 // Accepted branches.  Bit i_r, the r-th in ascending order, of the accepted
 // row's mask names the token whose rows go to place r behind the context.
 // i_r >= r, and i_r' > r for r' > r, so rows moved in ascending order never
 // overwrite one that is still to be read: a thread takes 16 bytes of a row
 // (of keys or values, of a layer) and walks the branch, a few loads in flight.
-// What bounds it: the launch, and latency: lengths, the mask, the block
-// table, the rows.
+// What bounds it: the launch, and latency: lengths, the mask with the block
+// table, the rows: 8 branches in one layer 2.8 us from a graph, 64 in 16 layers
+// (24.5 MB read and written) 7.5 on caches out of L2, 5.2 on the same ones again.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
