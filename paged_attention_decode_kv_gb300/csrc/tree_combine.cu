@@ -110,7 +110,8 @@ __global__ void __launch_bounds__(kThreads) tree_combine_kernel(const PrefillArg
         for (int i = 0; i < kFlight; ++i) {
           const float f = ex2(ml[i].x - ref);
           l += f * ml[i].y;
-          if (f == 0.f) continue;  // nothing attended there, nothing written
+          if (ml[i].x == -CUDART_INF_F) continue;  // nothing attended there, nothing written (a weight of 0 still
+                                                   // makes NaN of a value that is not finite)
           o[0] += f * x[i][0].x, o[1] += f * x[i][0].y, o[2] += f * x[i][0].z, o[3] += f * x[i][0].w;
           o[4] += f * x[i][1].x, o[5] += f * x[i][1].y, o[6] += f * x[i][1].z, o[7] += f * x[i][1].w;
         }

@@ -7,6 +7,7 @@ fp32 products and a sum, 2^-23 of w, within what is left of its 2^-12.
 """
 from __future__ import annotations
 
+import math
 import random
 
 import pytest
@@ -309,6 +310,28 @@ def test_scores_of_minus_infinity(dev, dtype, D):
         v = batch.v_cache[page, 0, 0].expand(4, D)
         assert torch.isnan(got[1]).all() and (got[3] == 0).all()
         assert torch.equal(got[0], v) and torch.equal(got[2], v)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("e4m3", 128)])
+def test_values_that_are_not_finite_keep_through_weights_that_underflow(dev, dtype, D):
+    """The first key's value is not finite and its weight, over 200 powers of 2 below the last key's, is 0 in 32 bits:
+    the rows are not finite, in one piece or in several."""
+    batch = make_batch([3], [2000], 8, 2, D, dtype, seed=8)
+    batch.q.abs_().add_(0.1)
+    table = batch.block_tables[0]
+    batch.v_cache[int(table[0]), 0, 0, 3] = 0x7f if dtype == "e4m3" else float("inf")
+    batch.k_cache[int(table[1996 // PAGE]), 1996 % PAGE] = 0x7e if dtype == "e4m3" else 8.0
+    rows = [[[0], [0, 1], [0, 2]]]
+    scale = 8 * D ** -0.5
+    k = batch.dense("k")[0]
+    scores = torch.einsum("thd,hld->thl", batch.q.double(), k.repeat_interleave(4, 0)) * scale
+    assert ((scores[..., 1996] - scores[..., 0]) / math.log(2) > 200).all()
+    for grid in (1, 5):
+        got = run(batch, pack(rows, 1, 3), scale=scale, grid=grid, blocks=1)
+        torch.cuda.synchronize()
+        assert not torch.isfinite(got[:, :4, 3]).any()
+        got[:, :4, 3] = 0
+        assert torch.isfinite(got).all()
 
 
 def test_bits_past_the_rows_are_not_looked_at(dev):
