@@ -838,11 +838,15 @@ def append_fp8(k, v, k_codes, v_codes, k_scale, v_scale, q_starts, block_tables,
                    block_tables, context_lens, q, q_out, positions, inv_freq, interleaved, amplitude, stream)
 
 
+def _given(name, t):
+    if t is None:
+        raise ValueError(f"{name} must be given")
+    return t
+
+
 def _weight(torch, name, weight, H, D, index):
     """(pointer, stride from head to head) of the norm's weights, [D] or [H][D]."""
-    if weight is None:
-        raise ValueError(f"{name} must be given")
-    shape = weight.shape
+    shape = _given(name, weight).shape
     if not (weight.dtype is torch.float32 and weight.get_device() == index and weight.is_contiguous()):
         _check_plain(name, weight, torch.float32, index)
     if shape == (D,):
@@ -995,7 +999,7 @@ def prefill_tree(q, k_cache, v_cache, masks, q_starts, block_tables, context_len
     [T][words], see ``tree_masks``); with a window the last ``window`` of
     those.  A row that sees nothing is 0."""
     return _prefill(_t(), q, k_cache, v_cache, None, q_starts, block_tables, context_lens, scale, window, out, stream,
-                    masks)
+                    _given("masks", masks))
 
 
 def prefill_tree_fp8(q, k_codes, v_codes, k_scale, v_scale, masks, q_starts, block_tables, context_lens, scale=None,
@@ -1004,7 +1008,7 @@ def prefill_tree_fp8(q, k_codes, v_codes, k_scale, v_scale, masks, q_starts, blo
     torch.float8_e4m3fn with a float32 scale per kv head)."""
     torch = _t()
     return _prefill(torch, q, *_codes(torch, k_codes, v_codes), (k_scale, v_scale), q_starts,
-                    block_tables, context_lens, scale, window, out, stream, masks)
+                    block_tables, context_lens, scale, window, out, stream, _given("masks", masks))
 
 
 def tree_masks(parents, q_starts, context_lens, words=None, masks=None, positions=None, stream=None):

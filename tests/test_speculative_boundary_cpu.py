@@ -172,3 +172,18 @@ def test_wrappers_refuse_host_tensors():
         vt.norm_append_fp8(kv, kv, w, cache, cache.clone(), ones, ones, i32, table, i32[:1])  # not codes
     with pytest.raises(ValueError, match="CUDA"):
         vt.keep_path(i32[:1], i32[:, None], cache, cache.clone(), i32, table, i32[:1])
+
+
+def test_wrappers_refuse_trees_without_masks():
+    """(which would be a causal chunk's rows)"""
+    torch = pytest.importorskip("torch")
+    i32 = torch.zeros((2,), dtype=torch.int32)
+    table = torch.zeros((1, 2), dtype=torch.int32)
+    x = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
+    cache = torch.zeros((3, 32, 2, 64), dtype=torch.bfloat16)
+    codes = torch.zeros((3, 32, 2, 64), dtype=torch.uint8)
+    ones = torch.ones((2,))
+    with pytest.raises(ValueError, match="masks must be given"):
+        vt.prefill_tree(x, cache, cache.clone(), None, i32, table, i32[:1])
+    with pytest.raises(ValueError, match="masks must be given"):
+        vt.prefill_tree_fp8(x, codes, codes.clone(), ones, ones, None, i32, table, i32[:1])
