@@ -12,9 +12,7 @@
 // norm costs log2 of those lanes in shuffles; weights and angles are multiplied
 // once a token for all heads that share the weights, and products are taken two
 // at a time.  Measured: 11583 tokens of 64 + 8 + 8 heads of 128 into E4M3 pages
-// 86 us, 0.77 of the copy rate (91 with weights and angles multiplied in one
-// after the other); 128 tokens of 32 + 8 + 8 5.2 us from a graph.  Fetching a
-// round's successor behind it, across tokens, took 107 us.
+// 77.7 us, 0.86 of the copy rate; 128 tokens of 32 + 8 + 8 4.7 us from a graph.
 #include "rope_append.cuh"
 
 extern "C" {

@@ -400,17 +400,32 @@ struct NormTurn {
   }
 };
 
+// Threads of a block of the kernels whose warps go their own ways: with the norm
+// four blocks of 128 an SM (128 tokens of 32 + 8 + 8 heads 4.7 us, in blocks of 256 5.1).
+template <bool NORM>
+constexpr int kWarpThreads = NORM ? 128 : kRopeThreads;
+
+// CACHED: through L1, for lanes whose 16 bytes are every other ones (a sector is asked for twice).
+template <bool CACHED>
+__device__ __forceinline__ void copy16_async(void* smem, const void* global) {
+  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+  if constexpr (CACHED)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to), "l"(global) : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(global) : "memory");
+}
+
 // U lanes to a head's row of 16 U elements (U = 4 to 32, a power of two), 16 |
 // rot_dim.  The work is units of `unit` rounds of R heads, nb of them a token;
 // a warp takes consecutive ones, `per` or (the first `extra` warps) per + 1.
 template <typename T, typename KV, bool APPEND, bool INTER, int U, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads, NORM ? 2 : 1) rope_warp_kernel(const RopeArgs a, int nb, int unit, int warps, long long per, int extra) {
+__global__ void __launch_bounds__(kWarpThreads<NORM>, NORM ? 4 : 1) rope_warp_kernel(const RopeArgs a, int nb, int unit, int warps, long long per, int extra) {
   constexpr int R = 32 / U;                // heads of a round
   constexpr int NP = U >= 4 ? U / 4 : 1;   // pairs a lane forms: pairs NP lane ..
   constexpr int P = sizeof(T) == 2 ? 4 : 2;  // rounds in flight
   constexpr int D = 16 * U;
   const int lane = threadIdx.x & 31;
-  const int warp = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  const int warp = blockIdx.x * (kWarpThreads<NORM> / 32) + (threadIdx.x >> 5);
   if (warp >= warps) return;
   long long todo = per + (warp < extra ? 1 : 0);
   const long long from = warp * per + min(warp, extra);
@@ -566,6 +581,180 @@ __global__ void __launch_bounds__(kRopeThreads, NORM ? 2 : 1) rope_warp_kernel(c
   }
 }
 
+// The same with the norm, for many units a warp.  A row's elements come through
+// shared memory, each lane its own, two units ahead and across tokens: the
+// registers that would hold them hold the turn.  11583 tokens of 64 + 8 + 8 heads
+// of 128 into E4M3 pages take 77.7 us, with the kernel above 86 (two rounds' code
+// side by side 79, units of two rounds 80, 24 warps an SM with 80 registers 93).
+// Few units are gone before that pays, and there rounds side by side hide each
+// other's latencies: 3000 tokens of 16 + 4 + 4 heads of 256, 3.7 units a warp,
+// 16.9 with this kernel and 16.2 with that one.
+constexpr int kRing = 3;      // units of a warp in shared memory
+constexpr int kRingFrom = 5;  // units a warp
+
+template <typename T, typename KV, bool APPEND, bool INTER, int U>
+__global__ void __launch_bounds__(kWarpThreads<true>, 4) norm_ring_kernel(const RopeArgs a, int nb, int unit, int warps,
+                                                                    long long per, int extra) {
+  constexpr int R = 32 / U;                // heads of a round
+  constexpr int NP = U >= 4 ? U / 4 : 1;   // pairs a lane forms: pairs NP lane ..
+  constexpr int N = sizeof(T) / 2;         // 16-byte vectors of 8 elements
+  constexpr int D = 16 * U;
+  constexpr bool kCached = INTER || N > 1;
+  extern __shared__ float4 ring[];         // [warps][kRing][unit][2 N][32]
+  const int lane = threadIdx.x & 31;
+  const int warp = blockIdx.x * (kWarpThreads<true> / 32) + (threadIdx.x >> 5);
+  if (warp >= warps) return;
+  float4* const own = ring + (threadIdx.x >> 5) * kRing * unit * 2 * N * 32 + lane;
+  long long todo = per + (warp < extra ? 1 : 0);
+  const long long from = warp * per + min(warp, extra);
+  int t = static_cast<int>(from / nb);
+  int part = static_cast<int>(from - static_cast<long long>(t) * nb);
+  const int heads = a.q_heads + (APPEND ? 2 * a.kv_heads : 0);
+  const int u = lane & (U - 1), r = lane / U;
+  const int half = a.rot_dim >> 1;
+  const bool turns = u < (a.rot_dim >> 4);  // else this lane's elements are normed only
+  const int off0 = turns && !INTER ? 8 * u : 16 * u, off1 = turns && !INTER ? half + off0 : off0 + 8;
+
+  // The unit after the last one asked for.
+  int next_t = t, next_part = part;
+  long long ahead = todo;
+  int into = 0;
+  auto ask = [&] {
+    if (ahead > 0) {
+      const int first = next_part * unit * R;
+      float4* to = own + into * unit * 2 * N * 32;
+#pragma unroll 1
+      for (int i = 0, head = first + r; i < unit && head < heads; ++i, head += R, to += 2 * N * 32) {
+        const T* p;
+        if (!APPEND || head < a.q_heads)
+          p = static_cast<const T*>(a.q) + next_t * a.q_stride + static_cast<long long>(head) * D;
+        else if (head < a.q_heads + a.kv_heads)
+          p = static_cast<const T*>(a.k) + next_t * a.k_stride + static_cast<long long>(head - a.q_heads) * D;
+        else
+          p = static_cast<const T*>(a.v) + next_t * a.v_stride +
+              static_cast<long long>(head - a.q_heads - a.kv_heads) * D;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          copy16_async<kCached>(to + k * 32, p + off0 + k * (8 / N));
+          copy16_async<kCached>(to + (N + k) * 32, p + off1 + k * (8 / N));
+        }
+      }
+      --ahead;
+      if (++next_part == nb) {
+        next_part = 0;
+        ++next_t;
+      }
+      into = into == kRing - 1 ? 0 : into + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int i = 0; i < kRing - 1; ++i) ask();
+
+  unsigned long long frac[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) frac[i] = NP * lane + i < half ? turn_fraction(a.inv_freq[NP * lane + i]) : 0ull;
+  int b = -1, slot = 0;
+  bool fresh = true;  // a token whose place and angles are not known
+  Token k{0, 1, -1};
+  float2 mine[NP];
+  NormTurn turn;
+  const float* held = nullptr;  // whose weights the turn is made of
+#pragma unroll 1
+  for (; todo > 0; --todo) {
+    ask();  // (into the slot that was read last)
+    if (fresh) {
+      if constexpr (APPEND)
+        k = look_up(a, t, lane, b);
+      else
+        k.position = a.rot_dim ? a.positions[t] : 0;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) mine[i] = cos_sin(frac[i], k.position, a.amplitude);
+      held = nullptr;
+      fresh = false;
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+    const float4* raw = own + slot * unit * 2 * N * 32;
+    const int first = part * unit * R, last = k.live ? min(first + unit * R, heads) : first;
+#pragma unroll 1
+    for (int h0 = first; h0 < last; h0 += R, raw += 2 * N * 32) {
+      const int head = h0 + r;
+      const bool is_v = APPEND && head >= a.q_heads + a.kv_heads;
+      const float* weight = held;
+      if (head < last && !is_v)
+        weight = !APPEND || head < a.q_heads ? a.q_weight + head * a.q_weight_stride
+                                             : a.k_weight + (head - a.q_heads) * a.k_weight_stride;
+      if (__any_sync(0xffffffffu, weight != held)) {
+        float2 cs[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int holder = (8 * u + e) / NP;
+          cs[e].x = __shfl_sync(0xffffffffu, mine[e % NP].x, holder);
+          cs[e].y = __shfl_sync(0xffffffffu, mine[e % NP].y, holder);
+        }
+        if (weight) {
+          if (turns)
+            turn.form<INTER>(weight, off0, off1, cs);
+          else
+            turn.form(weight, off0, off1);
+        }
+        held = weight;
+      }
+      if (head >= last) continue;
+      float4 v[2 * N];
+#pragma unroll
+      for (int i = 0; i < 2 * N; ++i) v[i] = raw[32 * i];
+      float x0[8], x1[8], y0[8], y1[8];
+      load8(reinterpret_cast<const T*>(v), x0);
+      load8(reinterpret_cast<const T*>(v + N), x1);
+      if (!is_v) {
+        float2 x[8], y[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = make_float2(x0[2 * e], x0[2 * e + 1]);
+          x[4 + e] = make_float2(x1[2 * e], x1[2 * e + 1]);
+        }
+        // (the head's lanes: others of the warp may be past the last head)
+        turn.apply<INTER, U>(x, y, turns, a.eps, U == 32 ? ~0u : ((1u << (U & 31)) - 1u) << (r * U));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y0[2 * e] = y[e].x, y0[2 * e + 1] = y[e].y;
+          y1[2 * e] = y[4 + e].x, y1[2 * e + 1] = y[4 + e].y;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y0[e] = x0[e];
+          y1[e] = x1[e];
+        }
+      }
+      if (!APPEND || head < a.q_heads) {
+        if (k.live == 2) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y0[e] = y1[e] = __int_as_float(0x7fffffff);
+        }
+        T* dst = static_cast<T*>(a.q_out) + t * a.q_out_stride + static_cast<long long>(head) * D;
+        store8(dst + off0, y0, 1.f);
+        store8(dst + off1, y1, 1.f);
+      } else if constexpr (APPEND) {
+        if (k.slot >= 0) {
+          const int h = head - a.q_heads - (is_v ? a.kv_heads : 0);
+          KV* dst = static_cast<KV*>(is_v ? a.v_cache : a.k_cache) + (k.slot * a.kv_heads + h) * D;
+          const float scale = sizeof(KV) == 1 ? (is_v ? a.v_scale : a.k_scale)[h] : 1.f;
+          store8(dst + off0, y0, scale);
+          store8(dst + off1, y1, scale);
+        }
+      }
+    }
+    slot = slot == kRing - 1 ? 0 : slot + 1;
+    if (++part == nb) {
+      part = 0;
+      ++t;
+      fresh = true;
+    }
+  }
+}
+
 // With the norm, any head_dim and rot_dim: a warp a head's row, which it reads
 // twice (for its sum of squares and to turn it), a lane a pair.
 template <typename T, typename KV, bool APPEND, bool INTER>
@@ -641,11 +830,24 @@ bool launch_rope_warps(const RopeArgs& a, int interleaved, int num_sms, cudaStre
   const int unit = a.num_tokens * rounds >= 2 * kFlight * want ? kFlight : 1;
   const long long nb = (rounds + unit - 1) / unit, total = a.num_tokens * nb;
   const long long warps = total < want ? total : want;
-  const unsigned blocks = static_cast<unsigned>((warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32));
+  auto blocks = [&](int threads) { return static_cast<unsigned>((warps + threads / 32 - 1) / (threads / 32)); };
   auto go = [&](auto inter, auto units) {
-    rope_warp_kernel<T, KV, APPEND, decltype(inter)::value, decltype(units)::value, NORM>
-        <<<blocks, kRopeThreads, 0, stream>>>(a, static_cast<int>(nb), unit, static_cast<int>(warps), total / warps,
-                                              static_cast<int>(total % warps));
+    constexpr bool kInter = decltype(inter)::value;
+    constexpr int kUnits = decltype(units)::value;
+    const long long per = total / warps;
+    const int extra = static_cast<int>(total % warps);
+    if constexpr (NORM) {
+      static_assert(sizeof(T) * kWarpThreads<true> * kRing * kFlight * 16 <= 48 * 1024, "what a launch may ask for as it is");
+      if (unit > 1 && per >= kRingFrom) {
+        norm_ring_kernel<T, KV, APPEND, kInter, kUnits>
+            <<<blocks(kWarpThreads<true>), kWarpThreads<true>, 16 * kWarpThreads<true> * sizeof(T) * kRing * unit, stream>>>(
+                a, static_cast<int>(nb), unit, static_cast<int>(warps), per, extra);
+        return;
+      }
+    }
+    rope_warp_kernel<T, KV, APPEND, kInter, kUnits, NORM>
+        <<<blocks(kWarpThreads<NORM>), kWarpThreads<NORM>, 0, stream>>>(a, static_cast<int>(nb), unit,
+                                                                       static_cast<int>(warps), per, extra);
   };
   auto with = [&](auto inter) {
     if (U == 4) go(inter, std::integral_constant<int, 4>());

@@ -234,6 +234,49 @@ def test_append_invalid_device_data(dev, rot):
     assert torch.equal(fresh.view(torch.int16), kc.view(torch.int16))
 
 
+# Batches of so many units a warp (152 SMs, 16 warps each, units of four bf16 or two fp32 rounds of 512 elements) that
+# rows come through shared memory ahead of their turn; heads that fill neither rounds nor units.
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H,D,rot", [(6203, 17, 128, 128), (6200, 17, 128, 48), (6211, 33, 64, 64), (6201, 9, 256, 0),
+                                       (4203, 9, 512, 32)])
+def test_norm_rope_long(dev, T, H, D, rot, dtype, interleaved, per_head):
+    inv = vt.rope_frequencies(rot, 10000.0)[0] if rot else None
+    g = torch.Generator().manual_seed(T + D)
+    positions = torch.randint(-5000, 200000, (T,), generator=g, dtype=torch.int32).to(dev)
+    x = rows(T, H, D, dtype, dev, extra=2)
+    w = weights(H, D, per_head, dev)
+    got = vt.norm_rope(x, w, positions if rot else None, inv, eps=1e-5, interleaved=interleaved, amplitude=1.25)
+    check_rows(got, *expected(x, w, 1e-5, positions, inv, interleaved, 1.25))
+    assert vt.norm_rope(x, w, positions if rot else None, inv, eps=1e-5, interleaved=interleaved, amplitude=1.25,
+                        out=x) is x
+    assert torch.equal(x, got)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype,D,q_heads,kv_heads", [
+    ("bf16", 64, 25, 4), ("bf16", 128, 9, 4), ("bf16", 256, 5, 2), ("bf16", 512, 3, 1), ("f32", 64, 25, 4),
+    ("f32", 128, 9, 4), ("f32", 256, 5, 2), ("e4m3", 64, 25, 4), ("e4m3", 128, 9, 4), ("e4m3", 256, 5, 2)])
+def test_append_long(dev, dtype, D, q_heads, kv_heads, interleaved):
+    """Long batches, whose last sequence's context is shorter than its rows, with padding rows behind."""
+    new, ctx = [4100, 0, 1, 2099, 3], [4100, 5, 77, 2500, 64]
+    batch = make_batch(new, ctx, q_heads, kv_heads, D, dtype, seed=D, pad=4)
+    batch.context_lens[4] = 2
+    live = sum(new[:4])
+    q, k, v, qw, kw, inv, kc, vc, out = run_append(batch, kv_heads, D, dev, q_heads, D if interleaved else D // 2,
+                                                   interleaved, per_head=interleaved)
+    assert torch.isnan(out[live:live + 3]).all() and (out[live + 3:] == 7).all()
+    again = q.contiguous()
+    scales = (batch.k_scale, batch.v_scale) if dtype == "e4m3" else ()
+    (vt.norm_append_fp8 if scales else vt.norm_append)(
+        k, v, kw, batch.k_cache.clone(), batch.v_cache.clone(), *scales, batch.q_starts, batch.block_tables,
+        batch.context_lens, q=again, q_weight=qw, q_out=again, inv_freq=inv, interleaved=interleaved, eps=1e-6)
+    assert torch.equal(again[:live], out[:live])
+    batch.new, batch.ctx, batch.q_starts = new[:4], ctx[:4], batch.q_starts[:5]
+    check_append(batch, q, k, v, qw, kw, inv, kc, vc, out[:live], interleaved=interleaved)
+
+
 def test_captured_on_a_stream(dev):
     batch = make_batch([1, 2, 3], [30, 60, 90], 8, 2, 128, "bf16")
     side = torch.cuda.Stream()
