@@ -776,9 +776,10 @@ def _append(torch, k, v, k_cache, v_cache, scales, q_starts, block_tables, conte
         if q_out is None:
             q_out = torch.empty((T, Hq, D), dtype=io, device=q.device) if stream is None else \
                 _empty_on(torch, (T, Hq, D), io, index, stream)
-        _check_plain("q_out", q_out, io, index)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must be shaped like q")
+        else:
+            _check_plain("q_out", q_out, io, index)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must be shaped like q")
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
@@ -789,13 +790,15 @@ def _append(torch, k, v, k_cache, v_cache, scales, q_starts, block_tables, conte
         pos_ptr = positions.data_ptr()
     head = (k_cache.data_ptr(), v_cache.data_ptr(), out_ptr, k.data_ptr(), v.data_ptr(), q_ptr)
     rest = (q_starts.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), pos_ptr, freq, B, T, Hq, Hkv, D,
-            shape[1], rot, 1 if interleaved else 0, amplitude, qs, ks, vs)
-    if norm is not None:
+            shape[1], rot, 1 if interleaved else 0, amplitude)
+    if norm is None:
+        rest += (qs, ks, vs)
+    else:
         k_weight, q_weight, eps = norm
         kw, kw_stride = _weight(torch, "k_weight", k_weight, Hkv, D, index)
         qw, qw_stride = (None, 0) if q is None else _weight(torch, "q_weight", q_weight, Hq, D, index)
         head += (kw, qw)
-        rest = rest[:14] + (eps,) + rest[14:] + (qw_stride, kw_stride)
+        rest += (eps, qs, ks, vs, qw_stride, kw_stride)
         if fp8:
             _check_scales(torch, *scales, Hkv, index)
             _launch(torch, index, stream, "vt_paged_kv_norm_append_fp8", library().vt_paged_kv_norm_append_fp8,
@@ -803,7 +806,8 @@ def _append(torch, k, v, k_cache, v_cache, scales, q_starts, block_tables, conte
         else:
             _launch(torch, index, stream, "vt_paged_kv_norm_append", library().vt_paged_kv_norm_append, head + rest,
                     (max_blocks, shape[0], code))
-    elif fp8:
+        return q_out
+    if fp8:
         _check_scales(torch, *scales, Hkv, index)
         _launch(torch, index, stream, "vt_paged_kv_append_fp8", library().vt_paged_kv_append_fp8,
                 head + (scales[0].data_ptr(), scales[1].data_ptr()) + rest, (max_blocks, shape[0]))
