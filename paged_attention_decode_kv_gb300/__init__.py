@@ -678,7 +678,8 @@ def _check_freq(torch, inv_freq, index):
     """(pointer, rot_dim) of a frequency table, or of none."""
     if inv_freq is None:
         return None, 0
-    _check_plain("inv_freq", inv_freq, torch.float64, index)
+    if not (inv_freq.dtype is torch.float64 and inv_freq.get_device() == index and inv_freq.is_contiguous()):
+        _check_plain("inv_freq", inv_freq, torch.float64, index)
     n = inv_freq.numel()
     return (inv_freq.data_ptr(), 2 * n) if n else (None, 0)
 
@@ -701,11 +702,12 @@ def _io_code(torch, dtype):
 def _launch(torch, index, stream, where, call, before, after):
     """call(*before, stream handle, *after) with the tensors' device current;
     raises VtError."""
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream_on(torch, index, stream)
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
-            status = call(*before, _stream_on(torch, index, stream), *after)
+            status = call(*before, handle, *after)
     else:
-        status = call(*before, _stream_on(torch, index, stream), *after)
+        status = call(*before, handle, *after)
     if status != VT_OK:
         _check(status, where)
 
@@ -986,7 +988,8 @@ def prefill_fp8(q, k_codes, v_codes, k_scale, v_scale, q_starts, block_tables, c
 
 def _check_masks(torch, masks, T, index):
     """Words of a row of masks [T][words]."""
-    _check_plain("masks", masks, torch.int32, index)
+    if not (masks.dtype is torch.int32 and masks.get_device() == index and masks.is_contiguous()):
+        _check_plain("masks", masks, torch.int32, index)
     shape = masks.shape
     if len(shape) != 2 or shape[0] != T:
         raise ValueError(f"masks must be [{T}][words], got {tuple(shape)}")
@@ -1030,12 +1033,15 @@ def tree_masks(parents, q_starts, context_lens, words=None, masks=None, position
     torch = _t()
     index = _cuda_index("parents", parents)
     int32 = torch.int32
-    _check_plain("parents", parents, int32, index)
-    _check_plain("q_starts", q_starts, int32, index)
-    _check_plain("context_lens", context_lens, int32, index)
-    if parents.dim() != 1 or q_starts.numel() != context_lens.numel() + 1:
+    if not (q_starts.get_device() == context_lens.get_device() == index and parents.dtype is int32
+            and q_starts.dtype is int32 and context_lens.dtype is int32 and parents.is_contiguous()
+            and q_starts.is_contiguous() and context_lens.is_contiguous()):
+        for name, t in (("parents", parents), ("q_starts", q_starts), ("context_lens", context_lens)):
+            _check_plain(name, t, int32, index)
+    shape, B = parents.shape, context_lens.numel()
+    if len(shape) != 1 or q_starts.numel() != B + 1:
         raise ValueError("parents must be [tokens] and q_starts [num_seqs + 1]")
-    T = parents.shape[0]
+    T = shape[0]
     if masks is None:
         if words is None:
             raise ValueError("give words or masks")
@@ -1047,7 +1053,7 @@ def tree_masks(parents, q_starts, context_lens, words=None, masks=None, position
     positions = _int32_out(torch, "positions", positions, T, index, stream)
     _launch(torch, index, stream, "vt_tree_masks", library().vt_tree_masks,
             (masks.data_ptr(), positions.data_ptr(), parents.data_ptr(), q_starts.data_ptr(),
-             context_lens.data_ptr(), context_lens.numel(), T, words), ())
+             context_lens.data_ptr(), B, T, words), ())
     return masks, positions
 
 
@@ -1094,7 +1100,8 @@ def step_tables(context_lens, new_lens, block_tables, free_pages, counters, num_
         raise ValueError("new_lens must be [num_seqs], block_tables [num_seqs][max_blocks] and counters [2]")
     keep = None
     if keep_lens is not None:
-        _check_plain("keep_lens", keep_lens, int32, index)
+        if not (keep_lens.dtype is int32 and keep_lens.get_device() == index and keep_lens.is_contiguous()):
+            _check_plain("keep_lens", keep_lens, int32, index)
         if keep_lens.numel() != B:
             raise ValueError("keep_lens must be [num_seqs]")
         keep = keep_lens.data_ptr()
