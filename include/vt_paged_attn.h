@@ -579,6 +579,32 @@ VT_API vt_status vt_paged_kv_keep_path(void* k_cache, void* v_cache, int32_t* ke
                                        long long k_layer_stride, long long v_layer_stride, vt_stream_t stream,
                                        int max_blocks_per_seq, int num_blocks, vt_dtype dtype);
 
+/*
+ * vt_call -- any of the speculative step's operators above, its arguments in
+ * 8-byte slots: for callers whose foreign-function interface costs by the
+ * argument.
+ *
+ *   args  args[0].i a vt_op, args[1].i the number of arguments that follow, then the operator's arguments in their
+ *         order: pointers, integers and vt_dtype as i, float as f.
+ * Returns what the operator returns; VT_ERR_INVALID_ARG where the operator is none, the number is not its number of
+ * arguments, or an int's value is outside an int's range.
+ */
+typedef enum vt_op {
+  VT_OP_STEP_TABLES = 1,
+  VT_OP_TREE_MASKS = 2,
+  VT_OP_NORM_ROPE = 3,
+  VT_OP_NORM_APPEND = 4,
+  VT_OP_NORM_APPEND_FP8 = 5,
+  VT_OP_PREFILL_TREE = 6,
+  VT_OP_PREFILL_TREE_FP8 = 7,
+  VT_OP_KEEP_PATH = 8,
+} vt_op;
+typedef union vt_arg {
+  long long i;
+  double f;
+} vt_arg;
+VT_API vt_status vt_call(const vt_arg* args);
+
 /* What the last successful decode or prefill call on this host thread
  * launched (a prefill: group_tile is the query rows of a work item, subgroups
  * 1, min_units_per_cta in 128-key blocks, q_len 0). */

@@ -10,6 +10,7 @@ fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import struct
 import threading
 from pathlib import Path
 
@@ -130,6 +131,8 @@ def library() -> ctypes.CDLL:
             lib.vt_paged_attn_prefill_tree_fp8.restype = c_int
             lib.vt_paged_kv_keep_path.argtypes = [c_void] * 8 + [c_int] * 7 + [c_long] * 2 + [c_void] + [c_int] * 3
             lib.vt_paged_kv_keep_path.restype = c_int
+            lib.vt_call.argtypes = [ctypes.c_char_p]
+            lib.vt_call.restype = c_int
             lib.vt_paged_attn_last_plan.argtypes = [ctypes.POINTER(vt_plan)]
             lib.vt_paged_attn_last_plan.restype = c_int
             lib.vt_paged_attn_set_override.argtypes = [c_int, c_int]
@@ -677,11 +680,11 @@ def _codes(torch, k, v):
 def _check_freq(torch, inv_freq, index):
     """(pointer, rot_dim) of a frequency table, or of none."""
     if inv_freq is None:
-        return None, 0
+        return 0, 0
     if not (inv_freq.dtype is torch.float64 and inv_freq.get_device() == index and inv_freq.is_contiguous()):
         _check_plain("inv_freq", inv_freq, torch.float64, index)
     n = inv_freq.numel()
-    return (inv_freq.data_ptr(), 2 * n) if n else (None, 0)
+    return (inv_freq.data_ptr(), 2 * n) if n else (0, 0)
 
 
 def _cuda_index(name, t):
@@ -708,6 +711,29 @@ def _launch(torch, index, stream, where, call, before, after):
             status = call(*before, handle, *after)
     else:
         status = call(*before, handle, *after)
+    if status != VT_OK:
+        _check(status, where)
+
+
+# vt_call's arguments: the operator, their number, and each operator's own (the stream's handle among them).
+_TAIL = "8q2d8q"
+_STEP_TABLES, _TREE_MASKS = (1, 15, struct.Struct("17q")), (2, 9, struct.Struct("11q"))
+_NORM_ROPE = 3, 17, struct.Struct("12q2d5q")
+_NORM_APPEND, _NORM_APPEND_FP8 = (4, 32, struct.Struct("15q" + _TAIL + "q")), (5, 33, struct.Struct("17q" + _TAIL))
+_PREFILL_TREE, _PREFILL_TREE_FP8 = (6, 21, struct.Struct("17qd5q")), (7, 22, struct.Struct("19qd4q"))
+_KEEP_PATH = 8, 21, struct.Struct("23q")
+
+
+def _launch_packed(torch, index, stream, where, op, before, after):
+    """``_launch`` through vt_call (0 for a null pointer): ctypes takes 0.1 us an argument."""
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream_on(torch, index, stream)
+    number, count, layout = op
+    args = layout.pack(number, count, *before, handle, *after)
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            status = library().vt_call(args)
+    else:
+        status = library().vt_call(args)
     if status != VT_OK:
         _check(status, where)
 
@@ -771,7 +797,7 @@ def _append(torch, k, v, k_cache, v_cache, scales, q_starts, block_tables, conte
         raise ValueError("k_cache/v_cache must be [num_blocks][32][Hkv][head_dim] matching k")
     freq, rot = _check_freq(torch, inv_freq, index)
     Hq = qs = 0
-    q_ptr = out_ptr = pos_ptr = None
+    q_ptr = out_ptr = pos_ptr = 0
     if q is not None:
         Hq = q.shape[1]
         qs = _row_stride("q", q, T, Hq, D, io, index)
@@ -798,16 +824,16 @@ def _append(torch, k, v, k_cache, v_cache, scales, q_starts, block_tables, conte
     else:
         k_weight, q_weight, eps = norm
         kw, kw_stride = _weight(torch, "k_weight", k_weight, Hkv, D, index)
-        qw, qw_stride = (None, 0) if q is None else _weight(torch, "q_weight", q_weight, Hq, D, index)
+        qw, qw_stride = (0, 0) if q is None else _weight(torch, "q_weight", q_weight, Hq, D, index)
         head += (kw, qw)
         rest += (eps, qs, ks, vs, qw_stride, kw_stride)
         if fp8:
             _check_scales(torch, *scales, Hkv, index)
-            _launch(torch, index, stream, "vt_paged_kv_norm_append_fp8", library().vt_paged_kv_norm_append_fp8,
-                    head + (scales[0].data_ptr(), scales[1].data_ptr()) + rest, (max_blocks, shape[0]))
+            _launch_packed(torch, index, stream, "vt_paged_kv_norm_append_fp8", _NORM_APPEND_FP8,
+                           head + (scales[0].data_ptr(), scales[1].data_ptr()) + rest, (max_blocks, shape[0]))
         else:
-            _launch(torch, index, stream, "vt_paged_kv_norm_append", library().vt_paged_kv_norm_append, head + rest,
-                    (max_blocks, shape[0], code))
+            _launch_packed(torch, index, stream, "vt_paged_kv_norm_append", _NORM_APPEND, head + rest,
+                           (max_blocks, shape[0], code))
         return q_out
     if fp8:
         _check_scales(torch, *scales, Hkv, index)
@@ -879,7 +905,7 @@ def norm_rope(x, weight, positions=None, inv_freq=None, eps: float = 1e-6, inter
     x_stride = _row_stride("x", x, T, H, D, io, index)
     w, w_stride = _weight(torch, "weight", weight, H, D, index)
     freq, rot = _check_freq(torch, inv_freq, index)
-    pos = None
+    pos = 0
     if positions is not None:
         _check_plain("positions", positions, torch.int32, index)
         if positions.numel() != T:
@@ -891,9 +917,9 @@ def norm_rope(x, weight, positions=None, inv_freq=None, eps: float = 1e-6, inter
         out = torch.empty((T, H, D), dtype=io, device=x.device) if stream is None else \
             _empty_on(torch, (T, H, D), io, index, stream)
     out_stride = _row_stride("out", out, T, H, D, io, index)
-    _launch(torch, index, stream, "vt_norm_rope", library().vt_norm_rope,
-            (out.data_ptr(), x.data_ptr(), w, pos, freq, T, H, D, rot, 1 if interleaved else 0, amplitude, eps,
-             x_stride, out_stride, w_stride), (code,))
+    _launch_packed(torch, index, stream, "vt_norm_rope", _NORM_ROPE,
+                   (out.data_ptr(), x.data_ptr(), w, pos, freq, T, H, D, rot, 1 if interleaved else 0, amplitude, eps,
+                    x_stride, out_stride, w_stride), (code,))
     return out
 
 
@@ -949,11 +975,11 @@ def _prefill(torch, q, k_cache, v_cache, scales, q_starts, block_tables, context
         rest = (masks.data_ptr(),) + rest[:5] + (words,) + rest[5:]
         if fp8:
             _check_scales(torch, *scales, shape[2], index)
-            _launch(torch, index, stream, "vt_paged_attn_prefill_tree_fp8", library().vt_paged_attn_prefill_tree_fp8,
-                    head + (scales[0].data_ptr(), scales[1].data_ptr()) + rest, (max_blocks, shape[0]))
+            _launch_packed(torch, index, stream, "vt_paged_attn_prefill_tree_fp8", _PREFILL_TREE_FP8,
+                           head + (scales[0].data_ptr(), scales[1].data_ptr()) + rest, (max_blocks, shape[0]))
         else:
-            _launch(torch, index, stream, "vt_paged_attn_prefill_tree", library().vt_paged_attn_prefill_tree,
-                    head + rest, (max_blocks, shape[0], code))
+            _launch_packed(torch, index, stream, "vt_paged_attn_prefill_tree", _PREFILL_TREE,
+                           head + rest, (max_blocks, shape[0], code))
     elif fp8:
         _check_scales(torch, *scales, shape[2], index)
         _launch(torch, index, stream, "vt_paged_attn_prefill_fp8", library().vt_paged_attn_prefill_fp8,
@@ -1051,9 +1077,9 @@ def tree_masks(parents, q_starts, context_lens, words=None, masks=None, position
         raise ValueError("masks must be [tokens][words]")
     words = _check_masks(torch, masks, T, index)
     positions = _int32_out(torch, "positions", positions, T, index, stream)
-    _launch(torch, index, stream, "vt_tree_masks", library().vt_tree_masks,
-            (masks.data_ptr(), positions.data_ptr(), parents.data_ptr(), q_starts.data_ptr(),
-             context_lens.data_ptr(), B, T, words), ())
+    _launch_packed(torch, index, stream, "vt_tree_masks", _TREE_MASKS,
+                   (masks.data_ptr(), positions.data_ptr(), parents.data_ptr(), q_starts.data_ptr(),
+                    context_lens.data_ptr(), B, T, words), ())
     return masks, positions
 
 
@@ -1098,7 +1124,7 @@ def step_tables(context_lens, new_lens, block_tables, free_pages, counters, num_
     B, table = context_lens.numel(), block_tables.shape
     if new_lens.numel() != B or len(table) != 2 or table[0] != B or counters.numel() != 2:
         raise ValueError("new_lens must be [num_seqs], block_tables [num_seqs][max_blocks] and counters [2]")
-    keep = None
+    keep = 0
     if keep_lens is not None:
         if not (keep_lens.dtype is int32 and keep_lens.get_device() == index and keep_lens.is_contiguous()):
             _check_plain("keep_lens", keep_lens, int32, index)
@@ -1108,10 +1134,10 @@ def step_tables(context_lens, new_lens, block_tables, free_pages, counters, num_
     q_starts = _int32_out(torch, "q_starts", q_starts, B + 1, index, stream)
     positions = _int32_out(torch, "positions", positions, num_tokens, index, stream)
     slots = _int32_out(torch, "slots", slots, num_tokens, index, stream)
-    _launch(torch, index, stream, "vt_paged_step_tables", library().vt_paged_step_tables,
-            (block_tables.data_ptr(), context_lens.data_ptr(), free_pages.data_ptr(), counters.data_ptr(),
-             q_starts.data_ptr(), positions.data_ptr(), slots.data_ptr(), keep, new_lens.data_ptr(), B, num_tokens,
-             BLOCK_SIZE), (table[1], free_pages.numel()))
+    _launch_packed(torch, index, stream, "vt_paged_step_tables", _STEP_TABLES,
+                   (block_tables.data_ptr(), context_lens.data_ptr(), free_pages.data_ptr(), counters.data_ptr(),
+                    q_starts.data_ptr(), positions.data_ptr(), slots.data_ptr(), keep, new_lens.data_ptr(), B,
+                    num_tokens, BLOCK_SIZE), (table[1], free_pages.numel()))
     return q_starts, positions, slots
 
 
@@ -1164,8 +1190,8 @@ def keep_path(accepted, masks, k_cache, v_cache, q_starts, block_tables, context
                          "[num_seqs][max_blocks]")
     words = _check_masks(torch, masks, masks.shape[0], index)
     kept_lens = _int32_out(torch, "kept_lens", kept_lens, B, index, stream)
-    _launch(torch, index, stream, "vt_paged_kv_keep_path", library().vt_paged_kv_keep_path,
-            (k_cache.data_ptr(), v_cache.data_ptr(), kept_lens.data_ptr(), accepted.data_ptr(), masks.data_ptr(),
-             q_starts.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), B, masks.shape[0], words, layers,
-             shape[-2], shape[-1], shape[-3], strides[0], strides[1]), (table[1], shape[-4], code))
+    _launch_packed(torch, index, stream, "vt_paged_kv_keep_path", _KEEP_PATH,
+                   (k_cache.data_ptr(), v_cache.data_ptr(), kept_lens.data_ptr(), accepted.data_ptr(), masks.data_ptr(),
+                    q_starts.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), B, masks.shape[0], words,
+                    layers, shape[-2], shape[-1], shape[-3], strides[0], strides[1]), (table[1], shape[-4], code))
     return kept_lens

@@ -39,6 +39,7 @@ SOURCES = [
     "prefill_tree_bf16.cu",
     "prefill_tree_e4m3.cu",
     "tree_combine.cu",
+    "call.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -187,3 +187,60 @@ def test_wrappers_refuse_trees_without_masks():
         vt.prefill_tree(x, cache, cache.clone(), None, i32, table, i32[:1])
     with pytest.raises(ValueError, match="masks must be given"):
         vt.prefill_tree_fp8(x, codes, codes.clone(), ones, ones, None, i32, table, i32[:1])
+
+
+# ------------------------------------------------------------------- arguments in slots
+def packed(op, values, count=None):
+    import struct
+    slots = [op, len(values) if count is None else count, *values]
+    return vt.library().vt_call(struct.pack("".join("d" if isinstance(v, float) else "q" for v in slots), *slots))
+
+
+CALLS = {1: (vt.vt_paged_step_tables, TABLES), 2: (vt.vt_tree_masks, MASKS), 3: (vt.vt_norm_rope, NORM),
+         4: (vt.vt_paged_kv_norm_append, APPEND), 5: (vt.vt_paged_kv_norm_append_fp8, APPEND),
+         6: (vt.vt_paged_attn_prefill_tree, TREE), 7: (vt.vt_paged_attn_prefill_tree_fp8, TREE),
+         8: (vt.vt_paged_kv_keep_path, KEEP)}
+
+
+def slots_of(op, **over):
+    import inspect
+    function, args = CALLS[op]
+    args = dict(args, **SCALES, **over)
+    return [0 if args[name] is None else args[name] for name in inspect.signature(function).parameters]
+
+
+@pytest.mark.parametrize("op", sorted(CALLS))
+def test_packed_calls(op):
+    """Each argument arrives in its place: what is refused for one of them alone is refused here, too."""
+    import inspect
+    function, args = CALLS[op]
+    names = list(inspect.signature(function).parameters)
+    number = {1: "num_seqs", 2: "num_seqs", 3: "num_tokens", 4: "num_tokens", 5: "num_tokens", 6: "num_tokens",
+              7: "num_tokens", 8: "num_seqs"}[op]
+    if op != 1:                                                      # (no tokens, nothing to do, whatever else)
+        assert packed(op, slots_of(op, **{number: 0})) == vt.VT_OK
+    assert packed(op, slots_of(op, **{number: -1})) == BAD
+    assert packed(op, slots_of(op, **{number: 0x7ff00000})) == NOT
+    for name in ("block_size", "mask_words", "head_dim"):
+        if name in names:
+            assert packed(op, slots_of(op, **{name: 1 << 40})) == BAD        # no int
+            assert packed(op, slots_of(op, **{name: -(1 << 32) + 32})) == BAD
+    for name in ("eps", "scale"):
+        if name in names:
+            assert packed(op, slots_of(op, **{name: float("nan")})) == BAD
+    for name in ("weight_stride", "q_weight_stride", "k_weight_stride"):
+        if name in names:
+            assert packed(op, slots_of(op, **{name: 130})) == BAD
+    for name in names:
+        if name in ("q_starts", "context_lens", "new_lens", "free_pages", "masks", "weight", "k_weight", "accepted"):
+            assert packed(op, slots_of(op, **{name: args.get(name, 0x1000) + 1})) == BAD
+    if names[-1] == "dtype":
+        assert packed(op, slots_of(op, dtype=9)) == BAD
+    values = slots_of(op)
+    assert packed(op, values[:-1]) == BAD and packed(op, values + [0]) == BAD
+    assert packed(op, values, count=len(values) + 1) == BAD
+
+
+def test_packed_calls_of_nothing():
+    assert packed(0, []) == BAD and packed(9, [0, 0]) == BAD and packed(-1, []) == BAD
+    assert vt.library().vt_call(None) == BAD
