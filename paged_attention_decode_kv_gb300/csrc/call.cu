@@ -1,8 +1,8 @@
 // Operators called with one pointer to their arguments.
 //
 // A call through a foreign-function interface costs by the argument (Python's
-// ctypes 0.1 us each, and these operators have 10 to 36); packed into 8-byte
-// slots first, 35 cost 0.8 us in all.
+// ctypes 0.1 us each, and these operators have 9 to 33); packed into 8-byte
+// slots first, 32 cost 1 us in all.
 #include <limits.h>
 
 #include <type_traits>
