@@ -27,7 +27,7 @@ EXPORTED = ("vt_paged_attn_decode", "vt_paged_attn_decode_noalloc", "vt_paged_at
             "vt_paged_attn_prefill", "vt_paged_attn_prefill_fp8", "vt_paged_attn_prefill_workspace_bytes",
             "vt_paged_step_tables", "vt_tree_masks", "vt_norm_rope", "vt_paged_kv_norm_append",
             "vt_paged_kv_norm_append_fp8", "vt_paged_attn_prefill_tree", "vt_paged_attn_prefill_tree_fp8",
-            "vt_paged_kv_keep_path",
+            "vt_paged_kv_keep_path", "vt_call",
             "vt_paged_attn_last_plan",
             "vt_paged_attn_set_override", "vt_paged_attn_set_overlap", "vt_paged_attn_set_segment_cost",
             "vt_paged_attn_set_workspace", "vt_paged_attn_set_test_wait",
@@ -369,6 +369,12 @@ def vt_paged_kv_keep_path(k_cache, v_cache, kept_lens, accepted, masks, q_starts
                                            context_lens, num_seqs, num_tokens, mask_words, num_layers, num_kv_heads,
                                            head_dim, block_size, k_layer_stride, v_layer_stride, stream,
                                            max_blocks_per_seq, num_blocks, dtype)
+
+
+def vt_call(args) -> int:
+    """Raw call of an operator by its arguments in 8-byte slots (bytes, see
+    vt_op and vt_arg); returns the status code."""
+    return library().vt_call(args)
 
 
 def vt_paged_attn_last_plan() -> dict:
