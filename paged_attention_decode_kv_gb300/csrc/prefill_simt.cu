@@ -363,13 +363,14 @@ __global__ void __launch_bounds__(kCombineThreads)
   constexpr int U = COLS >= 256 ? 1 : 256 / COLS;  // pieces whose loads are in flight together
 #pragma unroll 1
   for (int p0 = 0; p0 < sp.pieces; p0 += U) {
-    float f[U];
+    float f[U], mk[U];
     float4 x[U][N];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      f[u] = 0.f;
+      mk[u] = -CUDART_INF_F;
       if (p0 + u < sp.pieces) {
         const float2 ml = a.ml[record(p0 + u)];
+        mk[u] = ml.x;
         f[u] = ex2(ml.x - mb);
         l += f[u] * ml.y;
         const float* src = a.part + record(p0 + u) * COLS + 4 * lane;
@@ -379,7 +380,8 @@ __global__ void __launch_bounds__(kCombineThreads)
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (f[u] == 0.f) continue;  // nothing attended there, nothing written
+      // (nothing attended there, nothing written; a weight of 0 still makes NaN of a value that is not finite)
+      if (mk[u] == -CUDART_INF_F) continue;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         o[e].x += f[u] * x[u][e].x;

@@ -13,6 +13,8 @@ sum |q k| with 2^-24 each, the output up to n of them.
 """
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
@@ -714,3 +716,24 @@ def test_rows_past_two_billion_elements(dev):
     out.zero_()
     vt.append(k, k, cache[0], cache[1], starts, table, lens, q=q, q_out=out, inv_freq=inv)
     assert torch.equal(out, q)
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_weights_that_underflow_between_pieces_keep_what_is_not_finite(dev, dtype, D):
+    """The first key's value is not finite and its weight, over 200 powers of 2 below another key's, is 0 in 32 bits:
+    the rows are not finite, in one piece or in several."""
+    batch = make_batch([3], [2000], 8, 2, D, dtype, seed=8)
+    batch.q.abs_().add_(0.1)
+    table = batch.block_tables[0]
+    batch.v_cache[int(table[0]), 0, 0, 3] = 0x7f if dtype == "e4m3" else float("inf")
+    batch.k_cache[int(table[1990 // 32]), 1990 % 32] = 0x7e if dtype == "e4m3" else 8.0
+    scale = 8 * D ** -0.5
+    k = batch.dense("k")[0]
+    scores = torch.einsum("thd,hld->thl", batch.q.double(), k.repeat_interleave(4, 0)) * scale
+    assert ((scores[..., 1990] - scores[..., 0]) / math.log(2) > 200).all()
+    for grid in (1, 2, 5, 16):
+        got = run(batch, scale=scale, grid=grid, blocks=1)
+        torch.cuda.synchronize()
+        assert not torch.isfinite(got[:, :4, 3]).any()
+        got[:, :4, 3] = 0
+        assert torch.isfinite(got).all()

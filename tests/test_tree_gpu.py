@@ -848,3 +848,29 @@ def test_many_items_of_both_kinds(dev, dtype, D):
     masks = pack(rows, 2, sum(new))
     for grid in (0, 11, 97):
         check(batch, rows, run(batch, masks, grid=grid, blocks=1 if grid else 0))
+
+
+# ------------------------------------------------------------------- values that are not finite, by how work is cut
+def not_finite(dtype, value):
+    return 0x7f if dtype == "e4m3" else value
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_weights_that_underflow_between_pieces_keep_what_is_not_finite(dev, dtype, D):
+    """As the test of weights that underflow, with the pieces of every type joined: what a row sees and is not finite
+    is so in the result, however the work was cut."""
+    batch = make_batch([3], [2000], 8, 2, D, dtype, seed=8)
+    batch.q.abs_().add_(0.1)
+    table = batch.block_tables[0]
+    batch.v_cache[int(table[0]), 0, 0, 3] = not_finite(dtype, float("inf"))
+    batch.k_cache[int(table[1990 // PAGE]), 1990 % PAGE] = 0x7e if dtype == "e4m3" else 8.0
+    scale = 8 * D ** -0.5
+    k = batch.dense("k")[0]
+    scores = torch.einsum("thd,hld->thl", batch.q.double(), k.repeat_interleave(4, 0)) * scale
+    assert ((scores[..., 1990] - scores[..., 0]) / math.log(2) > 200).all()
+    for grid in (1, 2, 5, 16):
+        got = run(batch, pack([[[0], [0, 1], [0, 2]]], 1, 3), scale=scale, grid=grid, blocks=1)
+        torch.cuda.synchronize()
+        assert not torch.isfinite(got[:, :4, 3]).any()
+        got[:, :4, 3] = 0
+        assert torch.isfinite(got).all()
