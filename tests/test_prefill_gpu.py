@@ -737,3 +737,32 @@ def test_weights_that_underflow_between_pieces_keep_what_is_not_finite(dev, dtyp
         assert not torch.isfinite(got[:, :4, 3]).any()
         got[:, :4, 3] = 0
         assert torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_weights_that_underflow_within_a_block_keep_what_is_not_finite(dev, dtype, D, window):
+    """Among keys that only some rows see, a value that is not finite and whose weight is 0 in 32 bits: the rows that
+    see it are not finite, the others are."""
+    new, L = 20, 100
+    batch = make_batch([new], [L], 8, 2, D, dtype, seed=9)
+    batch.q.abs_().add_(0.1)
+    table = batch.block_tables[0]
+    spots = [(90, 3)] + ([(45, 5)] if window else [])
+    for t, col in spots:
+        batch.v_cache[int(table[t // 32]), t % 32, 0, col] = 0x7f if dtype == "e4m3" else float("inf")
+    batch.k_cache[int(table[60 // 32]), 60 % 32] = 0x7e if dtype == "e4m3" else 8.0   # which every row sees
+    scale = 8 * D ** -0.5
+    k = batch.dense("k")[0]
+    scores = torch.einsum("thd,hld->thl", batch.q.double(), k.repeat_interleave(4, 0)) * scale
+    for t, _ in spots:
+        assert ((scores[..., 60] - scores[..., t]) / math.log(2) > 200).all()
+    got = run(batch, scale=scale, window=window)
+    torch.cuda.synchronize()
+    p = torch.arange(L - new, L, device=got.device)
+    for t, col in spots:
+        sees = (t <= p) & (t > p - window) if window else t <= p
+        assert sees.any() and not sees.all()
+        assert not torch.isfinite(got[sees][:, :4, col]).any()
+        got[sees, :4, col] = 0
+    assert torch.isfinite(got).all()

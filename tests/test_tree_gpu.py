@@ -874,3 +874,34 @@ def test_weights_that_underflow_between_pieces_keep_what_is_not_finite(dev, dtyp
         assert not torch.isfinite(got[:, :4, 3]).any()
         got[:, :4, 3] = 0
         assert torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_weights_that_underflow_within_a_block_keep_what_is_not_finite(dev, dtype, D, window):
+    """Among keys that only some rows see, a value that is not finite and whose weight is 0 in 32 bits: the rows that
+    see it are not finite, the others are."""
+    new, L = 20, 100
+    batch = make_batch([new], [L], 8, 2, D, dtype, seed=9)
+    batch.q.abs_().add_(0.1)
+    rows = [[0], [0, 1], [0, 2], [3]] + [list(range(4, j + 1)) for j in range(4, new)]
+    table = batch.block_tables[0]
+    base = L - new
+    spots = [(base, 3), (base + 6, 7)] + ([(45, 5)] if window else [])
+    for t, col in spots:
+        batch.v_cache[int(table[t // PAGE]), t % PAGE, 0, col] = not_finite(dtype, float("inf"))
+    batch.k_cache[int(table[60 // PAGE]), 60 % PAGE] = 0x7e if dtype == "e4m3" else 8.0   # which every row sees
+    scale = 8 * D ** -0.5
+    k = batch.dense("k")[0]
+    scores = torch.einsum("thd,hld->thl", batch.q.double(), k.repeat_interleave(4, 0)) * scale
+    for t, _ in spots:
+        assert ((scores[..., 60] - scores[..., t]) / math.log(2) > 200).all()
+    seen = [(list(range(base)) + [base + i for i in r])[-window:] for r in rows]
+    got = run(batch, pack([rows], 1, new), scale=scale, window=window)
+    torch.cuda.synchronize()
+    for t, col in spots:
+        sees = torch.tensor([t in s for s in seen], device=got.device)
+        assert sees.any() and not sees.all()
+        assert not torch.isfinite(got[sees][:, :4, col]).any()
+        got[sees, :4, col] = 0
+    assert torch.isfinite(got).all()
