@@ -1366,9 +1366,11 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
         if constexpr (C::kTree) {
           TreeRow tree;
           tree.take(a, it.row0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1), it.L - it.pos0 - 1, it.pos0 + 1);
+          // (to the sums of the tile whose weight is 1: the other's may be 0, and 0 * inf is NaN)
+          const bool other = f1 > f0;
           auto sees = [&](int key) { return (tree.seen(key) & 1u) != 0u; };
-          add_taken_values<FP8>(a, it, D, sees, DV, tO);
-          if (any_other) add_taken_values<FP8>(a, it, D, sees, DV, tO + DV);  // (one of the two weights may be 0)
+          add_taken_values<FP8>(a, it, D, [&](int key) { return !other && sees(key); }, DV, tO);
+          if (any_other) add_taken_values<FP8>(a, it, D, [&](int key) { return other && sees(key); }, DV, tO + DV);
         } else {
           add_taken_values<FP8>(
               a, it, D, [&](int key) { return key <= pos && (a.window == 0 || key > pos - a.window); }, DV, tO);

@@ -905,3 +905,28 @@ def test_weights_that_underflow_within_a_block_keep_what_is_not_finite(dev, dtyp
         assert not torch.isfinite(got[sees][:, :4, col]).any()
         got[sees, :4, col] = 0
     assert torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("window", [0, 60])
+@pytest.mark.parametrize("grid", [0, 1, 2, 5])
+@pytest.mark.parametrize("dtype,D", [k for k in KINDS if k[0] != "e4m3"])
+def test_infinities_keep_their_sign(dev, dtype, D, grid, window):
+    """Infinite values are infinities of their sign in the rows that see them, NaN where a row sees both signs, and
+    nothing elsewhere: with items of one tile and of two, rows that see keys in one of two blocks only, and an
+    infinity every row sees."""
+    new, ctx = [20, 50, 9, 33], [130, 140, 400, 33]
+    batch = make_batch(new, ctx, 8, 2, D, dtype, seed=14)
+    rows = tree_rows(new, 4, 14)
+    inf = float("inf")
+    for b, t, col, value in ((0, 114, 3, inf), (0, 114, 4, -inf), (0, 112, 5, inf), (0, 129, 5, -inf), (0, 5, 6, -inf),
+                             (0, 108, 7, inf), (0, 109, 7, -inf), (1, 100, 3, inf), (1, 138, 4, inf), (1, 91, 5, -inf), (2, 100, 3, inf),
+                             (2, 395, 4, -inf), (2, 398, 5, inf), (3, 4, 3, inf), (3, 4, 4, -inf),
+                             (3, 32, 5, -inf)):
+        batch.v_cache[int(batch.block_tables[b, t // PAGE]), t % PAGE, 0, col] = value
+    got = run(batch, pack(rows, 2, sum(new)), window=window, grid=grid, blocks=1 if grid else 0)
+    check(batch, rows, got, window=window, finite=False)
+    ref = tree_attention(batch, rows, D ** -0.5, window)[0]
+    some = ~torch.isfinite(ref)
+    assert torch.equal(got[some].double().nan_to_num(7.0), ref[some].nan_to_num(7.0))
+    for what in (ref == inf, ref == -inf, torch.isnan(ref)):
+        assert what.any()
