@@ -12,7 +12,8 @@
 // the first stall; at head_dim 128 its 255 registers spill 72 bytes.  Q, K and V
 // come by asynchronous copies; at head_dim 128 P lies over K's tile.  Values are
 // looked at only in tiles that some row sees in part, and only if one is not
-// finite do rows branch around the keys they do not see: 182 us.
+// finite do rows branch around the keys they do not see: 178 us (183 where causal weights are -0
+// for those keys, too).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kSimtThreads<D>) prefill_simt_kernel(const Pre
         for (int e = 0; e < NK; ++e) {
           const float p = ex2(x[e] - mb);
           sum += p;
-          ps[ty * NR + i][tx + 16 * e] = seen[e] ? p : -0.f;
+          ps[ty * NR + i][tx + 16 * e] = TREE && !seen[e] ? -0.f : p;
         }
 #pragma unroll
         for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -220,8 +221,9 @@ __global__ void __launch_bounds__(kSimtThreads<D>) prefill_simt_kernel(const Pre
         asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncthreads();
       // Where some row sees only part of the keys, and a value is not finite,
-      // keys that a row does not see (their weights are -0) take no part: 0 times
-      // such a value would be NaN.  Those it sees do, if with a weight of 0.
+      // keys that a row does not see (of a tree, those whose weight is -0) take no
+      // part: 0 times such a value would be NaN.  Those it sees do, if with a weight
+      // of 0.
       const int keys = min(kSimtKeys, last - t0);
       bool apart = false;
       if (t0 + kSimtKeys > it.pos0 + 1 || (a.window > 0 && t0 < it.hi - a.window)) {
@@ -245,7 +247,8 @@ __global__ void __launch_bounds__(kSimtThreads<D>) prefill_simt_kernel(const Pre
             const float4 v = load4(&s.v[t][4 * tx + 64 * c]);
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
-              if (__float_as_int(pe[i]) >= 0) {
+              const int after = t0 + t - pos[i];
+              if (TREE ? __float_as_int(pe[i]) >= 0 : after <= 0 && (a.window == 0 || after > -a.window)) {
                 o[i][c][0] = fma2(make_float2(pe[i], pe[i]), make_float2(v.x, v.y), o[i][c][0]);
                 o[i][c][1] = fma2(make_float2(pe[i], pe[i]), make_float2(v.z, v.w), o[i][c][1]);
               }
