@@ -225,56 +225,6 @@ struct Ring {
   }
 };
 
-// Adds the values that preparation took out to a row's sums, in tensor memory
-// from column 0 of `o` on: they are not finite, so neither is the result.  They
-// lie among the keys that only some rows see, as many at either end as the item
-// has tokens and whatever the context is (a walk over a whole context of 30000
-// keys took longer than a bounded wait of 8 million cycles).  A warp looks at 32
-// of them at a time.  (All threads of a warp together; rare, so compact.)
-template <bool FP8, typename Sees>
-__device__ __forceinline__ void add_taken_values(const PrefillArgs& a, const PfItem& it, int head_dim, Sees sees, int cols,
-                                              uint32_t o) {
-  const int lane = threadIdx.x & 31;
-  const int first = max(it.lo_exact, it.lo + it.kb0 * kPfBlock);
-  const int last = min(it.hi, it.lo + it.kb1 * kPfBlock);
-  // before `early` some rows' windows have not begun, from `late` on are some rows' later tokens
-  const int early = a.window > 0 ? min(last, max(first, it.hi - a.window)) : first;
-  const int late = min(last, max(early, it.pos0 + 1));
-#pragma unroll 1
-  for (int c = 0; c < cols; ++c) {
-    float add = 0.f;
-#pragma unroll 1
-    for (int t0 = first; t0 < last; t0 += 32) {
-      if (t0 >= early && t0 < late) t0 = late;
-      const int t = t0 + lane;
-      float x = 0.f;
-      if (t < last && (t < early || t >= late)) {
-        const int page = a.block_tables[static_cast<long long>(it.b) * a.max_blocks + t / kPfPage];
-        if (page >= 0 && page < a.num_blocks) {
-          const long long at = ((static_cast<long long>(page) * kPfPage + t % kPfPage) * a.num_kv_heads + it.head) *
-                                   head_dim + it.part * cols + c;
-          if constexpr (FP8)
-            x = (static_cast<const uint8_t*>(a.v_cache)[at] & 0x7f) == 0x7f ? CUDART_NAN_F : 0.f;
-          else
-            x = __bfloat162float(static_cast<const __nv_bfloat16*>(a.v_cache)[at]);
-        }
-      }
-      unsigned taken = __ballot_sync(0xffffffffu, !isfinite(x));
-#pragma unroll 1
-      for (; taken; taken &= taken - 1) {
-        const int i = __ffs(taken) - 1, key = t0 + i;
-        const float y = __shfl_sync(0xffffffffu, x, i);
-        if (sees(key)) add += y;
-      }
-    }
-    uint32_t sum;
-    tmem_ld1(o + c, sum);
-    tmem_wait_ld();
-    tmem_st1(o + c, __float_as_uint(__uint_as_float(sum) + add));
-    tmem_wait_st();
-  }
-}
-
 // A word whose elements that are not finite (exponents of all ones; the E4M3
 // codes 0x7f and 0xff) carry into the bits of kCarry, and all ones in their place.
 template <bool FP8>
@@ -287,6 +237,75 @@ template <bool FP8>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   const uint32_t m = carries<FP8>(w) & kCarry<FP8>;
   return FP8 ? (m >> 7) * 0xffu : (m >> 15) * 0xffffu;
+}
+
+// Adds the values that preparation took out to a row's sums, in tensor memory
+// from column 0 of `o` on (or, of a row that two tiles hold and where `other` says
+// so, of the second one's, `cols` columns on): they are not finite, so neither is
+// the result.  They lie among the keys that only some rows see: as many at either
+// end as the item has tokens, of a tree as its sequence has drafted ones (up to
+// 32 mask_words), and whatever the context is (a walk over a whole context of
+// 30000 keys took longer than a bounded wait of 8 million cycles, and so did 1024
+// drafted ones a column at a time).  A warp looks at 8 bytes of 32 of them at a
+// time; `sees` says which of the 32 from a key on this thread's row sees.  (All
+// threads of a warp together; rare, so compact.  With a key's columns in the
+// inner loop its registers spill, and chunks over codes took 0.5 % longer.)
+template <bool FP8, typename Sees>
+__device__ __forceinline__ void add_taken_values(const PrefillArgs& a, const PfItem& it, int head_dim, Sees sees, int cols,
+                                              uint32_t o, bool two, bool other) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kBits = FP8 ? 8 : 16, kPer = 64 / kBits;  // of an element; columns of 8 bytes
+  const int first = max(it.lo_exact, it.lo + it.kb0 * kPfBlock);
+  const int last = min(it.hi, it.lo + it.kb1 * kPfBlock);
+  // before `early` some rows' windows have not begun, from `late` on are some rows' later tokens
+  const int early = a.window > 0 ? min(last, max(first, it.hi - a.window)) : first;
+  const int late = min(last, max(early, it.pos0 + 1));
+#pragma unroll 1
+  for (int c0 = 0; c0 < cols; c0 += kPer) {
+    uint32_t found = 0;  // a byte a column: the row sees +inf, -inf, NaN there (codes: a bit, NaN)
+#pragma unroll 1
+    for (int t0 = first; t0 < last; t0 += 32) {
+      if (t0 >= early && t0 < late) t0 = late;
+      const int t = t0 + lane;
+      uint2 x = make_uint2(0, 0);
+      if (t < last && (t < early || t >= late)) {
+        const int page = a.block_tables[static_cast<long long>(it.b) * a.max_blocks + t / kPfPage];
+        if (page >= 0 && page < a.num_blocks)
+          x = *reinterpret_cast<const uint2*>(
+              static_cast<const unsigned char*>(a.v_cache) +
+              (((static_cast<long long>(page) * kPfPage + t % kPfPage) * a.num_kv_heads + it.head) * head_dim +
+               it.part * cols + c0) * (kBits / 8));
+      }
+      if (!__any_sync(0xffffffffu, (carries<FP8>(x.x) | carries<FP8>(x.y)) & kCarry<FP8>)) continue;
+      const unsigned seen = sees(t0);
+#pragma unroll 1
+      for (int e = 0; e < kPer; ++e) {
+        if constexpr (FP8) {
+          if (seen & __ballot_sync(0xffffffffu, (x.x & 0x7fu) == 0x7fu)) found |= 1u << e;
+        } else {
+          if (seen & __ballot_sync(0xffffffffu, (x.x & 0xffffu) == 0x7f80u)) found |= 1u << 8 * e;
+          if (seen & __ballot_sync(0xffffffffu, (x.x & 0xffffu) == 0xff80u)) found |= 2u << 8 * e;
+          if (seen & __ballot_sync(0xffffffffu, (x.x & 0x7fffu) > 0x7f80u)) found |= 4u << 8 * e;
+        }
+        x = make_uint2(__funnelshift_r(x.x, x.y, kBits), x.y >> kBits);
+      }
+    }
+    if (!__any_sync(0xffffffffu, found)) continue;
+#pragma unroll 1
+    for (int e = 0; e < kPer; ++e, found >>= FP8 ? 1 : 8) {
+      const uint32_t f = FP8 ? (found & 1u) * 4u : found & 7u;
+      const float add = f == 0u ? 0.f : f == 1u ? CUDART_INF_F : f == 2u ? -CUDART_INF_F : CUDART_NAN_F;
+#pragma unroll 1
+      for (int i = 0; i <= static_cast<int>(two); ++i) {
+        const uint32_t at = o + c0 + e + i * cols;
+        uint32_t sum;
+        tmem_ld1(at, sum);
+        tmem_wait_ld();
+        tmem_st1(at, __float_as_uint(__uint_as_float(sum) + (other == (i != 0) ? add : 0.f)));
+        tmem_wait_st();
+      }
+    }
+  }
 }
 
 // Two floats as E4M3 terms, hi + lo: lo is the rest that hi leaves, itself
@@ -1367,13 +1386,15 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
           TreeRow tree;
           tree.take(a, it.row0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1), it.L - it.pos0 - 1, it.pos0 + 1);
           // (to the sums of the tile whose weight is 1: the other's may be 0, and 0 * inf is NaN)
-          const bool other = f1 > f0;
-          auto sees = [&](int key) { return (tree.seen(key) & 1u) != 0u; };
-          add_taken_values<FP8>(a, it, D, [&](int key) { return !other && sees(key); }, DV, tO);
-          if (any_other) add_taken_values<FP8>(a, it, D, [&](int key) { return other && sees(key); }, DV, tO + DV);
-        } else {
           add_taken_values<FP8>(
-              a, it, D, [&](int key) { return key <= pos && (a.window == 0 || key > pos - a.window); }, DV, tO);
+              a, it, D, [&](int k) { return tree.seen(k); }, DV, tO, any_other, any_other && f1 > f0);
+        } else {
+          auto sees = [&](int k) {  // keys (pos - window, pos]
+            const int upto = pos - k, from = a.window > 0 ? upto - a.window + 1 : 0;
+            return (upto < 0 ? 0u : upto >= 31 ? ~0u : (2u << upto) - 1u) &
+                   (from <= 0 ? ~0u : from > 31 ? 0u : ~0u << from);
+          };
+          add_taken_values<FP8>(a, it, D, sees, DV, tO, false, false);
         }
       }
       const bool split = it.kb0 > 0 || it.pieces > 0;

@@ -930,3 +930,29 @@ def test_infinities_keep_their_sign(dev, dtype, D, grid, window):
     assert torch.equal(got[some].double().nan_to_num(7.0), ref[some].nan_to_num(7.0))
     for what in (ref == inf, ref == -inf, torch.isnan(ref)):
         assert what.any()
+
+
+@pytest.mark.parametrize("window", [0, 200, 1100])
+@pytest.mark.parametrize("dtype,D", [k for k in KINDS if k[0] != "f32"])
+def test_a_large_tree_of_values_that_are_not_finite(dev, dtype, D, window):
+    """What they cost is a look at each new token's values an item, whatever the number of those that are not finite:
+    no wait takes more than 8 million cycles."""
+    new, L = 1024, 1400
+    batch = make_batch([new], [L], 4, 2, D, dtype, seed=15)
+    rows = tree_rows([new], 3, 15)
+    rows[0] = [r if j % 5 else [] for j, r in enumerate(rows[0])]   # rows that see the context alone
+    base = L - new
+    spots = torch.arange(base if not window else base - 100, L, device=dev)
+    pages_, at = batch.block_tables[0, spots // PAGE].long(), spots % PAGE
+    batch.v_cache[pages_, at] = not_finite(dtype, float("nan"))
+    vt.vt_paged_attn_set_test_wait(8_000_000, -1, -1)
+    got = run(batch, pack(rows, 32, new), window=window, grid=4, blocks=8)
+    vt.vt_paged_attn_set_test_wait(0, -1, -1)
+    torch.cuda.synchronize()
+    assert vt.vt_paged_attn_device_status() == 0
+    first = int(spots[0])
+    hit = torch.tensor([max((list(range(base)) + [base + i for i in r])[-window:]) >= first for r in rows[0]], device=dev)
+    assert hit.any()
+    assert torch.isnan(got[hit]).all() and torch.isfinite(got[~hit]).all()
+    if not window:
+        assert not hit.all()
