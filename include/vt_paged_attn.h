@@ -409,7 +409,8 @@ VT_API vt_status vt_paged_attn_prefill_fp8(void* out, const void* q, const void*
                                            int block_size, float scale, int window, vt_stream_t stream,
                                            int max_blocks_per_seq, int num_blocks);
 
-/* Bytes of workspace a prefill call with this head_dim and cache type uses on the current device (0: not taken). */
+/* Bytes of workspace a prefill call with this head_dim and cache type, causal or of trees, uses at most on the current
+ * device (0: not taken). */
 VT_API size_t vt_paged_attn_prefill_workspace_bytes(int head_dim, vt_dtype dtype);
 
 /*

@@ -399,16 +399,23 @@ vt_status vt_paged_attn_prefill_tree_fp8(void* out, const void* q, const void* k
 
 size_t vt_paged_attn_prefill_workspace_bytes(int head_dim, vt_dtype dtype) {
   using namespace vt;
-  const PrefillVariant* v = find_prefill(head_dim, dtype, false);
-  if (!v) return 0;
-  int dev = 0, per_sm = 0;
+  if (!find_prefill(head_dim, dtype, false)) return 0;
+  int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   try {
     std::lock_guard<std::mutex> lock(g_mutex);
     DeviceState& ds = device_state(dev);
-    if (prepare_device(dev, ds) != VT_OK || prepare(ds, *v, &per_sm) != VT_OK) return 0;
-    const int grid = g_override_grid > 0 ? g_override_grid : ds.num_sms * per_sm;
-    return kStatusBytes + scratch_bytes(*v, grid);
+    if (prepare_device(dev, ds) != VT_OK) return 0;
+    size_t need = 0;
+    for (const bool tree : {false, true}) {  // (each has an occupancy of its own)
+      const PrefillVariant* v = find_prefill(head_dim, dtype, tree);
+      int per_sm = 0;
+      if (!v) continue;
+      if (prepare(ds, *v, &per_sm) != VT_OK) return 0;
+      const int grid = g_override_grid > 0 ? g_override_grid : ds.num_sms * per_sm;
+      need = std::max(need, kStatusBytes + scratch_bytes(*v, grid));
+    }
+    return need;
   } catch (const std::bad_alloc&) {
     return 0;
   }

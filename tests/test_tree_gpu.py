@@ -956,3 +956,19 @@ def test_a_large_tree_of_values_that_are_not_finite(dev, dtype, D, window):
     assert torch.isnan(got[hit]).all() and torch.isfinite(got[~hit]).all()
     if not window:
         assert not hit.all()
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_the_workspace_asked_for_holds_a_call(dev, dtype, D):
+    """Of trees and of causal chunks, beside what was asked for and not a byte behind it."""
+    batch = make_batch([20, 50], [700, 900], 8, 2, D, dtype, seed=16)
+    rows = tree_rows(batch.new, 4, 16)
+    masks = pack(rows, 2, 70)
+    n = vt.vt_paged_attn_prefill_workspace_bytes(D, {"bf16": vt.VT_BF16, "f32": vt.VT_F32, "e4m3": vt.VT_E4M3}[dtype])
+    area = torch.full((n + 4096,), 7, dtype=torch.uint8, device=dev)
+    area[:n] = 0
+    vt.vt_paged_attn_set_workspace(area.data_ptr(), n)
+    check(batch, rows, run(batch, masks))
+    plan = vt.vt_paged_attn_last_plan()
+    assert plan["scratch_source"] == 1 and plan["workspace_bytes"] <= n
+    assert (area[n:] == 7).all()
