@@ -467,7 +467,7 @@ VT_API vt_status vt_paged_step_tables(int32_t* block_tables, int32_t* context_le
  *
  *   masks      [num_tokens][mask_words] int32, out.
  *   positions  [num_tokens] int32, out, may be NULL: context_lens[b] - n_b + the number of tokens the row follows.
- *   parents    [num_tokens] int32, not overlapping the outputs.
+ *   parents    [num_tokens] int32.  The outputs overlap neither the inputs nor each other.
  *   mask_words 1 to 32 (else VT_ERR_UNSUPPORTED).
  * Rows of a sequence with more than 32 * mask_words rows, or with fewer context tokens than rows, and those behind
  * the last sequence are left as they were.  num_seqs or num_tokens 0 is a no-op.  Needs no workspace.

@@ -207,7 +207,10 @@ vt_status tree_masks(const MasksArgs& a, int num_seqs, cudaStream_t stream) {
   if (!aligned(a.masks, 4) || !aligned(a.positions, 4) || !aligned(a.parents, 4) || !aligned(a.q_starts, 4) ||
       !aligned(a.context_lens, 4))
     return VT_ERR_INVALID_ARG;
-  if (a.parents == a.masks || a.parents == a.positions) return VT_ERR_INVALID_ARG;
+  // (other blocks, and other threads of a block, still read what would be written)
+  for (const int* out : {a.masks, a.positions})
+    if (out && (out == a.parents || out == a.q_starts || out == a.context_lens)) return VT_ERR_INVALID_ARG;
+  if (a.masks == a.positions) return VT_ERR_INVALID_ARG;
   if (a.words > kMaxWords || num_seqs > kMaxTokens || a.num_tokens > kMaxTokens) return VT_ERR_UNSUPPORTED;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -247,8 +250,8 @@ vt_status keep_path(KeepArgs a, int num_seqs, int num_kv_heads, int head_dim, in
     return VT_ERR_INVALID_ARG;
   if (a.layers > 0 && (!a.k_cache || !a.v_cache)) return VT_ERR_INVALID_ARG;
   // (other blocks of the sequence still read what would be written)
-  if (a.kept_lens == a.context_lens || a.kept_lens == a.accepted || a.kept_lens == a.q_starts)
-    return VT_ERR_INVALID_ARG;
+  for (const int* in : {a.context_lens, a.accepted, a.q_starts, a.block_tables, a.masks})
+    if (a.kept_lens == in) return VT_ERR_INVALID_ARG;
   if (!aligned(a.k_cache, 16) || !aligned(a.v_cache, 16) || !aligned(a.kept_lens, 4) || !aligned(a.accepted, 4) ||
       !aligned(a.masks, 4) || !aligned(a.q_starts, 4) || !aligned(a.block_tables, 4) || !aligned(a.context_lens, 4))
     return VT_ERR_INVALID_ARG;

@@ -244,3 +244,15 @@ def test_packed_calls(op):
 def test_packed_calls_of_nothing():
     assert packed(0, []) == BAD and packed(9, [0, 0]) == BAD and packed(-1, []) == BAD
     assert vt.library().vt_call(None) == BAD
+
+
+@pytest.mark.parametrize("out", ["masks", "positions"])
+@pytest.mark.parametrize("other", ["parents", "q_starts", "context_lens", "masks"])
+def test_tree_masks_refuse_outputs_that_are_read(out, other):
+    if out != other:
+        assert vt.vt_tree_masks(**dict(MASKS, **{out: MASKS[other]})) == BAD
+
+
+@pytest.mark.parametrize("other", ["context_lens", "accepted", "q_starts", "block_tables", "masks"])
+def test_keep_path_refuses_lengths_that_are_read(other):
+    assert vt.vt_paged_kv_keep_path(**dict(KEEP, kept_lens=KEEP[other])) == BAD
