@@ -1105,7 +1105,10 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
       if (!it.bad)
         tree.take(a, it.row0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1), it.L - it.pos0 - 1, it.pos0 + 1);
     }
-    float m = -CUDART_INF_F, l = 0.f;
+    // A warp's rows move their maxima together, which shows in the last bits.  Rows
+    // without a query of a tree's item (others' and padding) have no say; of a
+    // causal one's those of a tile that its tokens do not fill are queries of 0.
+    float m = !C::kTree || tok < sp.ntok ? -CUDART_INF_F : CUDART_INF_F, l = 0.f;
     float scale = a.scale_log2;  // from a score in tensor memory to the log2 domain
     if constexpr (FP8) {
       // Q as two E4M3 terms in the layout TMA gives K.  (The previous item's last
@@ -1539,6 +1542,15 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       mbar_init(&s.item_empty[i], (C::kFp8 ? 10 : 7) + (kTwoLoaders<C> ? 1 : 0) + 4 * NT);  // every warp but the loader
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if constexpr (!C::kFp8 && !C::kTree) {
+    const int first = a.tile_tokens / NT * a.group;
+    if (__builtin_expect(first < 128 && warp < kLoader, 0)) {  // rows that no token of a tile fills, which TMA never writes
+      const int pieces = (128 - first) * 8;                    // 16 bytes each
+      for (int i = tid; i < NT * (C::kD / 64) * pieces; i += kLoader * 32)
+        *reinterpret_cast<uint4*>(s.q[0] + (i / pieces * 128 + first) * 128 + i % pieces * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_shared();
+    }
   }
   if (warp == kIssuer) tmem_alloc(&s.tmem, 512);
   if (warp == kLoader && lane == 0) {

@@ -766,3 +766,20 @@ def test_weights_that_underflow_within_a_block_keep_what_is_not_finite(dev, dtyp
         assert not torch.isfinite(got[sees][:, :4, col]).any()
         got[sees, :4, col] = 0
     assert torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("group", [24, 7, 127])
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_shared_memory_left_by_earlier_calls_does_not_show(dev, dtype, D, group):
+    """To the bit, where groups do not fill a tile's 128 rows."""
+    if dtype == "f32" and group > 64:
+        pytest.skip("fp32 has 64 rows")
+    batch = make_batch([3, 9, 2], [2500, 1800, 900], group, 1, D, dtype, seed=40)
+    other = make_batch([64], [700], 16, 2, D, dtype, seed=41)
+    results = []
+    for scale in (0.0, 1.0, 6.0, 40.0):
+        other.q.mul_(0).add_(1).mul_(scale)
+        run(other)
+        results.append(run(batch))
+    for got in results[1:]:
+        assert torch.equal(got.view(torch.uint8), results[0].view(torch.uint8))

@@ -972,3 +972,27 @@ def test_the_workspace_asked_for_holds_a_call(dev, dtype, D):
     plan = vt.vt_paged_attn_last_plan()
     assert plan["scratch_source"] == 1 and plan["workspace_bytes"] <= n
     assert (area[n:] == 7).all()
+
+
+@pytest.mark.parametrize("group", [24, 7, 127, 4])
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_a_row_depends_on_its_own_sequence_alone(dev, dtype, D, group):
+    """To the bit: not on what an earlier call left in shared memory where groups do not fill a tile's 128 rows, nor on
+    other sequences' queries, nor on what lies in rows behind the last one."""
+    if dtype == "f32" and group > 64:
+        pytest.skip("fp32 has 64 rows")
+    new, ctx = [3, 9, 2], [2500, 1800, 900]
+    batch = make_batch(new, ctx, group, 1, D, dtype, seed=40, pad=9)
+    rows = tree_rows(new, 3, 40)
+    masks = pack(rows, 1, sum(new) + 9)
+    other = make_batch([64], [700], 16, 2, D, dtype, seed=41)
+    chain = pack([[list(range(j + 1)) for j in range(64)]], 2, 64)
+    results = []
+    for scale in (0.0, 1.0, 6.0, 40.0):
+        other.q.mul_(0).add_(1).mul_(scale)
+        run(other, chain)
+        batch.q[3:12] = torch.randn((9, group, D), generator=torch.Generator().manual_seed(int(scale))) * scale
+        batch.q[14:] = scale
+        results.append(run(batch, masks)[[0, 1, 2, 12, 13]])
+    for got in results[1:]:
+        assert torch.equal(got.view(torch.uint8), results[0].view(torch.uint8))
