@@ -239,20 +239,19 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   return FP8 ? (m >> 7) * 0xffu : (m >> 15) * 0xffffu;
 }
 
-// Adds the values that preparation took out to a row's sums, in tensor memory
-// from column 0 of `o` on (or, of a row that two tiles hold and where `other` says
-// so, of the second one's, `cols` columns on): they are not finite, so neither is
-// the result.  They lie among the keys that only some rows see: as many at either
-// end as the item has tokens, of a tree as its sequence has drafted ones (up to
-// 32 mask_words), and whatever the context is (a walk over a whole context of
-// 30000 keys took longer than a bounded wait of 8 million cycles, and so did 1024
-// drafted ones a column at a time).  A warp looks at 8 bytes of 32 of them at a
-// time; `sees` says which of the 32 from a key on this thread's row sees.  (All
-// threads of a warp together; rare, so compact.  With a key's columns in the
-// inner loop its registers spill, and chunks over codes took 0.5 % longer.)
+// Adds the values that preparation took out to the sums of a row that `takes`
+// them, in tensor memory from column 0 of `o` on: they are not finite, so neither
+// is the result.  They lie among the keys that only some rows see: as many at
+// either end as the item has tokens, of a tree as its sequence has drafted ones
+// (up to 32 mask_words), and whatever the context is (a walk over a whole context
+// of 30000 keys took longer than a bounded wait of 8 million cycles, and so did
+// 1024 drafted ones a column at a time).  A warp looks at 8 bytes of 32 of them at
+// a time; `sees` says which of the 32 from a key on this thread's row sees.  (All
+// threads of a warp together; rare, so compact.  With a key's columns in the inner
+// loop its registers spill, and chunks over codes took 0.5 % longer.)
 template <bool FP8, typename Sees>
 __device__ __forceinline__ void add_taken_values(const PrefillArgs& a, const PfItem& it, int head_dim, Sees sees, int cols,
-                                              uint32_t o, bool two, bool other) {
+                                              uint32_t o, bool takes) {
   const int lane = threadIdx.x & 31;
   constexpr int kBits = FP8 ? 8 : 16, kPer = 64 / kBits;  // of an element; columns of 8 bytes
   const int first = max(it.lo_exact, it.lo + it.kb0 * kPfBlock);
@@ -295,15 +294,11 @@ __device__ __forceinline__ void add_taken_values(const PrefillArgs& a, const PfI
     for (int e = 0; e < kPer; ++e, found >>= FP8 ? 1 : 8) {
       const uint32_t f = FP8 ? (found & 1u) * 4u : found & 7u;
       const float add = f == 0u ? 0.f : f == 1u ? CUDART_INF_F : f == 2u ? -CUDART_INF_F : CUDART_NAN_F;
-#pragma unroll 1
-      for (int i = 0; i <= static_cast<int>(two); ++i) {
-        const uint32_t at = o + c0 + e + i * cols;
-        uint32_t sum;
-        tmem_ld1(at, sum);
-        tmem_wait_ld();
-        tmem_st1(at, __float_as_uint(__uint_as_float(sum) + (other == (i != 0) ? add : 0.f)));
-        tmem_wait_st();
-      }
+      uint32_t sum;
+      tmem_ld1(o + c0 + e, sum);
+      tmem_wait_ld();
+      tmem_st1(o + c0 + e, __float_as_uint(__uint_as_float(sum) + (takes ? add : 0.f)));
+      tmem_wait_st();
     }
   }
 }
@@ -1106,9 +1101,11 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
         tree.take(a, it.row0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1), it.L - it.pos0 - 1, it.pos0 + 1);
     }
     // A warp's rows move their maxima together, which shows in the last bits.  Rows
-    // without a query of a tree's item (others' and padding) have no say; of a
-    // causal one's those of a tile that its tokens do not fill are queries of 0.
-    float m = !C::kTree || tok < sp.ntok ? -CUDART_INF_F : CUDART_INF_F, l = 0.f;
+    // that no token of a tile can fill are queries of 0 (so are those behind an
+    // item's last token over codes); in a bf16 tree's item neither they nor those
+    // behind the last token, other sequences' and padding, have a say.
+    const float lazy = C::kTree && !FP8 && tok >= sp.ntok ? CUDART_INF_F : kLazy;
+    float m = -CUDART_INF_F, l = 0.f;
     float scale = a.scale_log2;  // from a score in tensor memory to the log2 domain
     if constexpr (FP8) {
       // Q as two E4M3 terms in the layout TMA gives K.  (The previous item's last
@@ -1249,7 +1246,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs& a, TcSmem<C>& s, u
         for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], z[60 + e]);
         most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
       }
-      if (__any_sync(0xffffffffu, most > m + kLazy)) {
+      if (__any_sync(0xffffffffu, most > m + lazy)) {
         const float mn = fmaxf(m, most);
         const float keep = m == -CUDART_INF_F ? 0.f : ex2(m - mn);
         if (j > sp.jb) {
@@ -1389,15 +1386,17 @@ __device__ __forceinline__ void tc_epilogue(const PrefillArgs& a, TcSmem<C>& s, 
           TreeRow tree;
           tree.take(a, it.row0 + sp.tok0 + min(tok, max(sp.ntok, 1) - 1), it.L - it.pos0 - 1, it.pos0 + 1);
           // (to the sums of the tile whose weight is 1: the other's may be 0, and 0 * inf is NaN)
-          add_taken_values<FP8>(
-              a, it, D, [&](int k) { return tree.seen(k); }, DV, tO, any_other, any_other && f1 > f0);
+#pragma unroll 1
+          for (int i = 0; i <= static_cast<int>(any_other); ++i)
+            add_taken_values<FP8>(
+                a, it, D, [&](int k) { return tree.seen(k); }, DV, tO + i * DV, (f1 > f0) == (i != 0));
         } else {
           auto sees = [&](int k) {  // keys (pos - window, pos]
             const int upto = pos - k, from = a.window > 0 ? upto - a.window + 1 : 0;
             return (upto < 0 ? 0u : upto >= 31 ? ~0u : (2u << upto) - 1u) &
                    (from <= 0 ? ~0u : from > 31 ? 0u : ~0u << from);
           };
-          add_taken_values<FP8>(a, it, D, sees, DV, tO, false, false);
+          add_taken_values<FP8>(a, it, D, sees, DV, tO, true);
         }
       }
       const bool split = it.kb0 > 0 || it.pieces > 0;
