@@ -371,7 +371,10 @@ VT_API vt_status vt_paged_kv_append_fp8(void* k_cache, void* v_cache, void* q_ou
  * V (8 bits of each; vt_paged_attn_decode and vt_paged_attn_decode_multi keep 16, so the same rows are closer to the
  * exact value there).  fp32 runs on CUDA cores.
  *
- * The values of slots outside [0, context_lens[b]) of a sequence's pages are never used, whatever they hold.
+ * The values of slots outside [0, context_lens[b]) of a sequence's pages are never used, whatever they hold.  A value
+ * that is not finite reaches every row that sees its key, whatever its weight, and no other row: that column is then
+ * the infinity, NaN where infinities of both signs or a NaN are seen (or where the infinity's weight is 0 in 32 bits).
+ * The same call on the same data gives the same bits.
  * Invalid device data never faults: rows of a sequence with a context outside [n_b, max_blocks_per_seq * 32] are
  * NaN, and so are rows that attend to a page whose id is outside [0, num_blocks) (other rows of that sequence may be
  * too).  q_starts below 0, that decrease or pass num_tokens are read as sequences without rows.
@@ -438,6 +441,11 @@ VT_API size_t vt_paged_attn_prefill_workspace_bytes(int head_dim, vt_dtype dtype
  * A sequence does not grow where k + n > max_blocks_per_seq * 32, and from the first other one on whose pages the
  * stack or whose rows num_tokens does not hold, none does: such sequences are left with k tokens and no rows.  One
  * whose lengths are none (L or k negative, k > L, L > max_blocks_per_seq * 32, n < 0) is left as it is, without rows.
+ *
+ * Rows lie as they were granted: behind a sequence that got fewer than it asked for, those of later ones begin
+ * earlier than the lengths asked for say.  Tokens, parents or projections that the caller packed by those lengths
+ * would then belong to other sequences, which no operator behind can notice: a caller that packs ahead asks only for
+ * what fits, or looks at counters[1] or q_starts first.
  *
  *   block_tables  [num_seqs][max_blocks_per_seq] int32, in and out; entries behind a context are left as they were.
  *   context_lens  [num_seqs] int32, in and out.
@@ -533,7 +541,8 @@ VT_API vt_status vt_paged_kv_norm_append_fp8(void* k_cache, void* v_cache, void*
  * sees nothing is 0.
  *
  *   masks       [num_tokens][mask_words] int32, 1 <= mask_words <= 32 (else VT_ERR_UNSUPPORTED).
- * Rows of a sequence with more than 32 * mask_words rows are NaN.  The other arguments, limits, arithmetic, invalid
+ * Rows of a sequence with more than 32 * mask_words rows are NaN.  For given lengths a row depends, to the bit, on its
+ * own sequence alone.  The other arguments, limits, arithmetic, invalid
  * device data and workspace (vt_paged_attn_prefill_workspace_bytes) as for vt_paged_attn_prefill and
  * vt_paged_attn_prefill_fp8.
  */

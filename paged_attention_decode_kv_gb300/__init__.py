@@ -1113,8 +1113,11 @@ def step_tables(context_lens, new_lens, block_tables, free_pages, counters, num_
     Returns (q_starts [B + 1], positions [num_tokens], slots [num_tokens]),
     allocated unless given: the rows of the packed batch, their positions and
     their slots (page * 32 + place).  Sequences from the first on whose pages
-    or rows do not fit get none (vt_paged_step_tables).  Asynchronous on
-    ``stream``, whose memory allocated results are."""
+    or rows do not fit get none, nor do those with a table too short or
+    lengths that are none (counters[1] of them in all): rows lie as granted, so
+    what was packed by the lengths asked for is then out of place
+    (vt_paged_step_tables).  Asynchronous on ``stream``, whose memory
+    allocated results are."""
     torch = _t()
     index = _cuda_index("context_lens", context_lens)
     int32 = torch.int32

@@ -12,7 +12,13 @@
 // norm costs log2 of those lanes in shuffles; weights and angles are multiplied
 // once a token for all heads that share the weights, and products are taken two
 // at a time.  Measured: 11583 tokens of 64 + 8 + 8 heads of 128 into E4M3 pages
-// 77.7 us, 0.86 of the copy rate; 128 tokens of 32 + 8 + 8 4.7 us from a graph.
+// 77.7 us, 0.86 of the copy rate; 128 tokens of 32 + 8 + 8 4.7 us from a graph
+// (fp32 5.1); 8191 tokens of 32 + 8 + 8 37.1, in fp32 66.6.  With weights per head
+// the products of weights and angles are formed for every round of heads: 44.8 and,
+// of the E4M3 batch, 104.  Rows that lanes do not divide (a rotation of 34 of 128)
+// take 180: a warp a row, read twice an element at a time, its angles formed for
+// every head.  Of the short batches' kernel, held to 128 registers, the variants of
+// head_dim 512 spill 36 to 84 bytes and those of 256 up to 28.
 #include "rope_append.cuh"
 
 extern "C" {

@@ -9,11 +9,11 @@
 // 227 us where 8 x 4 took 204: 1263 tokens over contexts of up to 972, 16 q / 8
 // kv heads of 128.)  At that tile the bound is dependent latency, not the loads:
 // two warps a scheduler, the FMA pipe 57 % busy, the load pipe 22 %, and `wait`
-// the first stall; at head_dim 128 its 255 registers spill 72 bytes.  Q, K and V
-// come by asynchronous copies; at head_dim 128 P lies over K's tile.  Values are
-// looked at only in tiles that some row sees in part, and only if one is not
-// finite do rows branch around the keys they do not see: 178 us (183 where causal weights are -0
-// for those keys, too).
+// the first stall; at head_dim 128 its 255 registers spill 16 bytes (of trees 44).
+// Q, K and V come by asynchronous copies; at head_dim 128 P lies over K's tile.
+// Values are looked at only in tiles that some row sees in part, and only if one is
+// not finite do rows branch around the keys they do not see: 178 us (with a mark on
+// causal rows' hidden weights, as trees have it, 183).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>

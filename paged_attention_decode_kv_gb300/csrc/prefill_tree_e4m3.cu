@@ -1,5 +1,6 @@
 // Tensor-core attention of trees of drafted tokens over FP8 (E4M3) caches: the
-// prefill's kernel with a mask for each row.
+// prefill's kernel with a mask for each row.  The two-tile variants spill 56
+// (head_dim 64) and 52 bytes a thread.
 #include "prefill_tc.cuh"
 
 namespace vt {
